@@ -26,8 +26,13 @@ from ._abi import GemmError, DT, ACT, ROW, COL
 _TORCH_DT = {torch.float16: "f16", torch.bfloat16: "bf16", torch.float32: "f32",
              torch.float8_e4m3fn: "e4m3", torch.float8_e5m2: "e5m2"}
 
+from .mx import MxPlan, MxTensor, mx_dequantize, mx_empty, mx_gemm, mx_quantize
+from .norm import rmsnorm, rmsnorm_backward, rmsnorm_backward_workspace
+
 __all__ = ["Plan", "gemm", "gemm_dact", "gemm_create", "gemm_run", "plan_grid", "configs", "tune", "fastdivmod_params",
-           "fastdivmod_check", "check_cu_seqlens", "tuned_config", "GemmError", "library_path"]
+           "fastdivmod_check", "check_cu_seqlens", "tuned_config", "GemmError", "library_path",
+           "MxTensor", "MxPlan", "mx_empty", "mx_quantize", "mx_dequantize", "mx_gemm",
+           "rmsnorm", "rmsnorm_backward", "rmsnorm_backward_workspace"]
 
 
 def library_path():

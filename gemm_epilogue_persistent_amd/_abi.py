@@ -10,6 +10,9 @@ OK, INVALID_ARG, UNSUPPORTED, ALIGNMENT, HIP_ERROR, NO_MEMORY = range(6)
 DT = {"none": 0, "f16": 1, "bf16": 2, "f32": 3, "e4m3": 4, "e5m2": 5}
 ROW, COL = 0, 1
 ACT = {"none": 0, "relu": 1, "relu_sq": 2, "gelu_tanh": 3, "silu": 4}
+MX_FORMAT = {"e2m1": 0, "e4m3": 1}
+MX_TILE = {"auto": 0, "256": 1, "128": 2, "64": 3, "rows32": 4, "rows16": 5}
+MX_HEADER = os.path.join(os.path.dirname(HERE), "include", "mx_mi355x.h")
 
 
 class GemmDesc(ctypes.Structure):
@@ -35,6 +38,29 @@ class GemmDesc(ctypes.Structure):
 class GemmArgs(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("A", "B", "C", "D", "PostAct", "alpha_dev", "beta_dev",
                                                "cu_seqlens_m", "cu_seqlens_k", "a_idx", "tile_counters")]
+
+
+class MxGemmDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("M", "N", "K", "groups", "a_format", "b_format", "c", "d", "post",
+                                              "act", "tile")] + [
+        (n, ctypes.c_int64) for n in ("ldc", "ldd", "ldp")]
+
+
+class MxGemmArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("a_codes", "a_scales", "b_codes", "b_scales", "C", "D", "PostAct",
+                                               "cu_seqlens_m")]
+
+
+class RmsnormArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("rows", "cols", "type", "q_format")] + [("eps", ctypes.c_float)] + [
+        (n, ctypes.c_void_p) for n in ("x", "residual", "weight", "h_out", "y", "q_codes", "q_scales", "rstd")] + [
+        (n, ctypes.c_int64) for n in ("ldx", "ldr", "ldh", "ldy")]
+
+
+class RmsnormBackwardArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("rows", "cols", "type")] + [
+        (n, ctypes.c_void_p) for n in ("dy", "h", "weight", "rstd", "dres", "dx", "dw", "workspace")] + [
+        (n, ctypes.c_int64) for n in ("workspace_bytes", "lddy", "ldh", "lddres", "lddx")]
 
 
 class GemmError(RuntimeError):
@@ -80,6 +106,28 @@ def load():
         lib.gemm_fastdivmod_params.argtypes = [u32, ctypes.POINTER(u32), ctypes.POINTER(u32)]
         lib.gemm_fastdivmod_check.restype = ctypes.c_int
         lib.gemm_fastdivmod_check.argtypes = [u32, u32, u32, vp, vp]
+        lib.mx_code_bytes.restype = i64
+        lib.mx_code_bytes.argtypes = [i64, i64, i32]
+        lib.mx_scale_bytes.restype = i64
+        lib.mx_scale_bytes.argtypes = [i64, i64]
+        lib.mx_quantize.restype = ctypes.c_int
+        lib.mx_quantize.argtypes = [i32, i32, vp, i32, i64, i32, i32, vp, vp, vp]
+        lib.mx_dequantize.restype = ctypes.c_int
+        lib.mx_dequantize.argtypes = [i32, i32, i32, vp, vp, vp, i32, i64, vp]
+        lib.rmsnorm_forward.restype = ctypes.c_int
+        lib.rmsnorm_forward.argtypes = [ctypes.POINTER(RmsnormArgs), vp]
+        lib.rmsnorm_backward.restype = ctypes.c_int
+        lib.rmsnorm_backward.argtypes = [ctypes.POINTER(RmsnormBackwardArgs), vp]
+        lib.rmsnorm_backward_workspace.restype = i64
+        lib.rmsnorm_backward_workspace.argtypes = [i32, i32]
+        lib.mx_gemm_create.restype = ctypes.c_int
+        lib.mx_gemm_create.argtypes = [ctypes.POINTER(MxGemmDesc), ctypes.POINTER(vp)]
+        lib.mx_gemm_run.restype = ctypes.c_int
+        lib.mx_gemm_run.argtypes = [vp, ctypes.POINTER(MxGemmArgs), vp]
+        lib.mx_gemm_destroy.restype = ctypes.c_int
+        lib.mx_gemm_destroy.argtypes = [vp]
+        lib.mx_gemm_plan_tile.restype = ctypes.c_int
+        lib.mx_gemm_plan_tile.argtypes = [vp, i32, ctypes.POINTER(i32)]
         lib.gemm_status_string.restype = ctypes.c_char_p
         lib.gemm_status_string.argtypes = [ctypes.c_int]
         lib.gemm_last_error.restype = ctypes.c_char_p

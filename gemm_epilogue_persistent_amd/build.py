@@ -18,6 +18,9 @@ LIB = os.path.join(HERE, "libgemm_mi355x.so")
 # one unit per (operand type, epilogue kind, varlen mode) family of kernels
 UNITS = ["plan.cpp", "gemm_api.hip"] + [
     f"inst_{op}_{fam}.hip" for op in ("f16", "bf16", "fp8") for fam in ("fwd", "vm", "vk", "dact", "dact_vm")]
+# block-scaled (MX) operators and the fused RMS norm
+UNITS += [os.path.join("mx", u) for u in ["mx_plan.cpp", "mx_api.hip", "mx_quant.hip", "rmsnorm.hip"] + [
+    f"mx_inst_{a}_{b}_{v}.hip" for a in ("e2m1", "e4m3") for b in ("e2m1", "e4m3") for v in ("dense", "vm")]]
 
 
 def hipcc() -> str:

@@ -1,0 +1,104 @@
+// mx_gemm_run (C ABI): the launch of an MX product.
+#include <atomic>
+
+#include "mx_gemm.hpp"
+#include "mx_plan.hpp"
+
+namespace gep {
+gemm_status fail(gemm_status st, const char* fmt, ...);
+void clear_error();
+
+#define GEP_MX_DECLARE(FA, FB)                                                              \
+  template <> hipError_t mx_launch<FA, FB, false>(int32_t, const MxParams&, dim3, hipStream_t); \
+  template <> hipError_t mx_launch<FA, FB, true>(int32_t, const MxParams&, dim3, hipStream_t);
+GEP_MX_DECLARE(MX_E2M1, MX_E2M1)
+GEP_MX_DECLARE(MX_E2M1, MX_E4M3)
+GEP_MX_DECLARE(MX_E4M3, MX_E2M1)
+GEP_MX_DECLARE(MX_E4M3, MX_E4M3)
+
+template <bool VM>
+static hipError_t launch(const mx_gemm_desc& d, int32_t tile, const MxParams& p, dim3 g, hipStream_t s) {
+  if (d.a_format == MX_E2M1)
+    return d.b_format == MX_E2M1 ? mx_launch<MX_E2M1, MX_E2M1, VM>(tile, p, g, s) : mx_launch<MX_E2M1, MX_E4M3, VM>(tile, p, g, s);
+  return d.b_format == MX_E2M1 ? mx_launch<MX_E4M3, MX_E2M1, VM>(tile, p, g, s) : mx_launch<MX_E4M3, MX_E4M3, VM>(tile, p, g, s);
+}
+
+constexpr int32_t kRasterG = 8;
+
+// Compute units of the current device, looked up once per device.
+static gemm_status compute_units(int32_t* cus) {
+  static std::atomic<int32_t> cache[64];
+  int dev = 0, n = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return fail(GEMM_ERR_HIP, "hipGetDevice: %s", hipGetErrorString(e));
+  const bool cached = dev >= 0 && dev < 64;
+  if (cached && (n = cache[dev].load(std::memory_order_relaxed)) > 0) {
+    *cus = n;
+    return GEMM_OK;
+  }
+  e = hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev);
+  if (e != hipSuccess || n <= 0) return fail(GEMM_ERR_HIP, "hipDeviceGetAttribute: %s", hipGetErrorString(e));
+  if (cached) cache[dev].store(n, std::memory_order_relaxed);
+  *cus = n;
+  return GEMM_OK;
+}
+
+}  // namespace gep
+
+using namespace gep;
+
+extern "C" gemm_status mx_gemm_run(const mx_gemm_plan* plan, const mx_gemm_args* a, void* stream) {
+  if (!plan || !a) return fail(GEMM_ERR_INVALID_ARG, "mx_gemm_run: NULL plan or args");
+  const mx_gemm_desc& d = plan->d;
+  if (d.M == 0 || d.N == 0) { clear_error(); return GEMM_OK; }
+  if (d.K > 0 && (!a->a_codes || !a->a_scales || ((!a->b_codes || !a->b_scales))))
+    return fail(GEMM_ERR_INVALID_ARG, "mx_gemm_run: A and B are required");
+  if ((d.c != GEMM_DT_NONE) != (a->C != nullptr)) return fail(GEMM_ERR_INVALID_ARG, "mx_gemm_run: C must be given iff the plan has a C type");
+  if ((d.d != GEMM_DT_NONE) != (a->D != nullptr)) return fail(GEMM_ERR_INVALID_ARG, "mx_gemm_run: D must be given iff the plan has a D type");
+  if ((d.post != GEMM_DT_NONE) != (a->PostAct != nullptr)) return fail(GEMM_ERR_INVALID_ARG, "mx_gemm_run: PostAct must be given iff the plan has a PostAct type");
+  if ((d.groups > 0) != (a->cu_seqlens_m != nullptr)) return fail(GEMM_ERR_INVALID_ARG, "mx_gemm_run: cu_seqlens_m must be given iff the plan is grouped");
+  for (const void* p : {a->a_codes, a->a_scales, a->b_codes, a->b_scales, a->C, (const void*)a->D, (const void*)a->PostAct})
+    if ((uintptr_t)p & 15) return fail(GEMM_ERR_ALIGNMENT, "mx_gemm_run: pointers must be 16-byte aligned");
+  if ((uintptr_t)a->cu_seqlens_m & 3) return fail(GEMM_ERR_ALIGNMENT, "mx_gemm_run: cu_seqlens_m not 4-byte aligned");
+  int32_t cus = 0;
+  const gemm_status st = compute_units(&cus);
+  if (st != GEMM_OK) return st;
+
+  const int32_t tile = mx_choose_tile(*plan, cus);
+  int32_t bm, bn;
+  mx_tile_extent(tile, &bm, &bn);
+  MxParams p{};
+  KParams& k = p.k;
+  k.A = a->a_codes; k.B = a->b_codes; k.C = a->C; k.D = a->D; k.Post = a->PostAct;
+  k.lda = plan->lda; k.ldb = plan->ldb; k.ldc = d.ldc; k.ldd = d.ldd; k.ldp = d.ldp;
+  k.a_bytes = plan->a_bytes; k.b_bytes = plan->b_bytes;
+  k.M = d.M; k.N = d.N; k.K = d.K; k.L = d.groups;
+  k.cu_seqlens = a->cu_seqlens_m;
+  k.c_dt = d.c; k.d_dt = d.d; k.p_dt = d.post; k.act = d.act;
+  p.sa = (const uint8_t*)a->a_scales; p.sb = (const uint8_t*)a->b_scales;
+  p.sa_bytes = plan->sa_bytes; p.sb_bytes = plan->sb_bytes;
+  p.nsb = (d.K + 511) / 512;
+  p.steps = (d.K + 127) / 128;
+  const int64_t tm = mx_row_blocks(*plan, bm), tn = (d.N + bn - 1) / bn;
+  dim3 grid;
+  if (tile == MX_TILE_256 || tile == MX_TILE_128) {
+    k.tm = (int32_t)tm;
+    k.tn = (int32_t)tn;
+    k.T = (int32_t)(tm * tn);  // (grouped: the kernel counts its tiles itself)
+    const int32_t cap = tile == MX_TILE_256 ? cus : 2 * cus;
+    k.P = k.T < cap ? k.T : cap;
+    k.log2G = 3;
+    k.xcd_remap = 1;
+    k.fd_Gtn = make_fastdiv((uint32_t)(kRasterG * tn));
+    for (int w = 1; w < kRasterG; ++w) k.fd_tail[w] = make_fastdiv((uint32_t)w);
+    grid = dim3((unsigned)k.P);
+  } else {
+    if (tm > 65535) return fail(GEMM_ERR_UNSUPPORTED, "mx_gemm_run: too many rows for the tile asked for");
+    grid = dim3((unsigned)tn, (unsigned)tm);
+  }
+  hipStream_t s = (hipStream_t)stream;
+  const hipError_t e = d.groups ? launch<true>(d, tile, p, grid, s) : launch<false>(d, tile, p, grid, s);
+  if (e != hipSuccess) return fail(GEMM_ERR_HIP, "mx_gemm_run launch: %s", hipGetErrorString(e));
+  clear_error();
+  return GEMM_OK;
+}

@@ -1,0 +1,747 @@
+// Products of MX operands with a fused epilogue for gfx950 (mx_gemm_* of the public header):
+//   D = A x B^T + C,  PostAct = act(A x B^T + C)
+//
+// v_mfma_scale_f32_16x16x128_f8f6f4 multiplies 16 x 128 by 128 x 16 blocks in either element
+// type per operand and applies one scale byte per 32 values of K to each of them, so the scales
+// cost no vector arithmetic: A[m, k] = a 2^(sa - 127), and each block of 32 contributes
+// 2^(sa + sb - 254) sum a b to the fp32 accumulator. Lane l holds row l % 16 of a fragment:
+// E2M1 its 32 codes of K block l / 16 (16 bytes), E4M3 the 16-byte chunks l / 16 and l / 16 + 4
+// of the row's 128 bytes; the scale it supplies is that of row l % 16, K block l / 16 (the same
+// for both types; checked on the hardware element by element).
+//
+// Two kernels:
+//   MxRing   large problems. 256x256 outputs per workgroup of 8 waves, or 128x128 of 4: both
+//            operands go through LDS (global -> LDS transfers, two stages), persistent tile loop.
+//   MxDirect few rows. 16x16 to 64x64 outputs per workgroup, whose waves share out K and read
+//            their fragments from global memory themselves; one join in LDS at the end.
+#pragma once
+#include "../gemm_kernel.hpp"
+#include "mx_common.hpp"
+
+namespace gep {
+
+// Kernel arguments. k: sizes, output pointers and strides, raster constants; lda / ldb are the
+// operands' row pitches in bytes.
+struct MxParams {
+  KParams k;
+  const uint8_t *sa, *sb;  // scales
+  int64_t sa_bytes, sb_bytes;  // their extents (sb: of one group)
+  int32_t nsb;             // scale tiles along K (512 values each)
+  int32_t steps;           // MFMA steps of 128 along K
+};
+
+enum MxTile : int32_t { MX_T_AUTO = 0, MX_T_256 = 1, MX_T_128 = 2, MX_T_64 = 3, MX_T_R32 = 4, MX_T_R16 = 5 };
+
+template <int FMT>
+struct MxFmt {
+  static constexpr bool k8 = FMT == MX_E4M3;
+  static constexpr int kCode = k8 ? 0 : 4;       // format field of the instruction
+  static constexpr int kStepBytes = k8 ? 128 : 64;  // bytes of a row per 128 values
+  static constexpr int kBlockBytes = k8 ? 32 : 16;
+};
+
+// The fragment registers of one 16 x 128 block (E2M1 uses the first four).
+template <int FMT>
+struct MxFrag {
+  i32x4 lo, hi;
+};
+template <>
+struct MxFrag<MX_E2M1> {
+  i32x4 lo;
+};
+template <int FMT>
+__device__ __forceinline__ i32x8 mx_regs(const MxFrag<FMT>& f) {
+  if constexpr (FMT == MX_E4M3) return __builtin_shufflevector(f.lo, f.hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  else return __builtin_shufflevector(f.lo, f.lo, 0, 1, 2, 3, -1, -1, -1, -1);
+}
+// B first, A second: a lane then holds 4 consecutive columns of one row (as in gemm_kernel.hpp).
+// OS: which byte of the scale registers applies.
+template <int FA, int FB, int OS = 0>
+__device__ __forceinline__ f32x4 mx_mma(const MxFrag<FB>& b, const MxFrag<FA>& a, f32x4 c, int sb, int sa) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mx_regs<FB>(b), mx_regs<FA>(a), c, MxFmt<FB>::kCode,
+                                                          MxFmt<FA>::kCode, OS, sb, OS, sa);
+}
+
+// ---- outputs: 8 consecutive columns of a row
+__device__ __forceinline__ void mx_load8(int dt, const char* p, float v[8]) {
+  if (dt == DT_F32) {
+    const f32x4 a = *(const f32x4*)p, b = *(const f32x4*)(p + 16);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = a[e], v[4 + e] = b[e];
+  } else {
+    const uint4 x = *(const uint4*)p;
+    unpack4_16(dt, uint2{x.x, x.y}, v);
+    unpack4_16(dt, uint2{x.z, x.w}, v + 4);
+  }
+}
+__device__ __forceinline__ void mx_store8(int dt, char* p, const float v[8]) {
+  if (dt == DT_F32) {
+    *(f32x4*)p = f32x4{v[0], v[1], v[2], v[3]};
+    *(f32x4*)(p + 16) = f32x4{v[4], v[5], v[6], v[7]};
+  } else {
+    const uint2 a = pack4_16(dt, v), b = pack4_16(dt, v + 4);
+    *(uint4*)p = uint4{a.x, a.y, b.x, b.y};
+  }
+}
+__device__ __forceinline__ void mx_act8(int act, float v[8]) {
+  switch (act) {
+    case ACT_RELU:
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = act_fn<ACT_RELU>(v[e]);
+      break;
+    case ACT_RELU_SQ:
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = act_fn<ACT_RELU_SQ>(v[e]);
+      break;
+    case ACT_GELU_TANH:
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = act_fn<ACT_GELU_TANH>(v[e]);
+      break;
+    case ACT_SILU:
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = act_fn<ACT_SILU>(v[e]);
+      break;
+    default: break;
+  }
+}
+// C, D and PostAct of row m, columns [n, n + 8) from the product v.
+__device__ __forceinline__ void mx_finish8(const KParams& p, int64_t m, int n, float v[8]) {
+  if (p.c_dt != DT_NONE) {
+    float c[8];
+    mx_load8(p.c_dt, (const char*)p.C + (m * p.ldc + n) * dt_bytes(p.c_dt), c);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] += c[e];
+  }
+  if (p.d_dt != DT_NONE) mx_store8(p.d_dt, (char*)p.D + (m * p.ldd + n) * dt_bytes(p.d_dt), v);
+  if (p.p_dt != DT_NONE) {
+    mx_act8(p.act, v);
+    mx_store8(p.p_dt, (char*)p.Post + (m * p.ldp + n) * dt_bytes(p.p_dt), v);
+  }
+}
+
+// One output tile of a grouped or dense problem.
+struct MxTileInfo {
+  int g, m0, n0, row_end;
+};
+
+// ------------------------------------------------------------------------------------
+// MxRing
+// ------------------------------------------------------------------------------------
+// A stage holds 128 bytes of K per row: one step (128 values) of an E4M3 operand, a pair of
+// steps (256 values) of an E2M1 one; each operand has two stages. The scales of four steps (16
+// bytes a row, in storage order) go through a two-stage ring of their own. The loop runs quads of
+// four steps; steps past K read zero codes.
+//
+// A step is kMI x kNI MFMAs, row by row. Two A fragments (block row r in register r & 1) and the
+// kNI B fragments are held; the A fragment of row r is read after row r - 2's last MFMA. The
+// barrier comes before the last row, when every wave has read its last fragment of the stage;
+// after it the next step's first fragments are read and the first half of the transfers into the
+// freed stage goes out; the second half follows at the head of the next step. (No barrier in
+// the middle of a pair when both operands are E2M1: neither stage changes.)
+template <int BM, int BN, int NW, int FA, int FB, bool VM>
+struct MxRing {
+  static constexpr int kThreads = NW * 64;
+  static constexpr int kWN = 64, kWavesN = BN / kWN, kWavesM = NW / kWavesN, kWM = BM / kWavesM;
+  static constexpr int kMI = kWM / 16, kNI = kWN / 16;
+  static constexpr int kABytes = BM * kRowBytes, kBBytes = BN * kRowBytes;
+  static constexpr int kBOff = 2 * kABytes, kSOff = kBOff + 2 * kBBytes, kSBytes = (BM + BN) * 16;
+  static constexpr int kLdsBytes = kSOff + 2 * kSBytes;
+  static constexpr int kVarlenLds = VM ? (kMaxVarlenGroups + 1 + kThreads + 1) * 4 : 0;
+  static constexpr int kInstrA = BM / 8 / NW, kInstrB = BN / 8 / NW;  // transfers (8 rows each) of a stage
+  static_assert((BM + BN) / 64 == NW, "one scale transfer (64 rows) a wave");
+  static_assert(kMI >= 4 && kMI % 2 == 0 && kNI == 4, "the fragment schedule below");
+  static constexpr int kN = kMI * kNI, kLastP = kN - kNI, kPrioP = kLastP / 2;
+  using A = MxFmt<FA>;
+  using B = MxFmt<FB>;
+
+  struct Loader {  // this lane's share of one operand's transfers
+    uint32_t off[4];
+    int32_t klim;  // bytes of a row past this lane's chunk
+  };
+  template <int N>
+  static __device__ __forceinline__ void init(Loader& l, int wave, int lane, int rows_valid, int ld, int row_bytes) {
+    const int c = (lane & 7) ^ kswz(wave * 8 + (lane >> 3));  // (the key repeats every 16 rows)
+#pragma unroll
+    for (int q = 0; q < N; ++q) {
+      const int row = (q * NW + wave) * 8 + (lane >> 3);
+      l.off[q] = row < rows_valid ? (uint32_t)(row * ld + c * 16) : kOOB;
+    }
+    l.klim = row_bytes - c * 16;
+  }
+  // Transfers [Q0, Q1) of the stage at `lds`: bytes [kb, kb + 128) of the rows. (kb is added to
+  // the lane's offset: the range check, which turns kOOB into zeros, is stated for that sum. An
+  // offset is below 2^31, so kOOB + kb does not wrap.)
+  template <int Q0, int Q1>
+  static __device__ __forceinline__ void dma(const Loader& l, __amdgpu_buffer_rsrc_t rs, int kb, GEP_LDS char* lds,
+                                             int wave) {
+    if constexpr (Q0 < Q1) {
+#if defined(__HIP_DEVICE_COMPILE__)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (GEP_LDS void*)(lds + (Q0 * NW + wave) * 1024), 16,
+                                               kb < l.klim ? l.off[Q0] + kb : kOOB, 0, 0, 0);
+#endif
+      dma<Q0 + 1, Q1>(l, rs, kb, lds, wave);
+    }
+  }
+
+  struct Src {
+    __amdgpu_buffer_rsrc_t a, b, s;
+    Loader la, lb;
+    uint32_t s_off;  // this lane's row in the wave's scale transfer
+    int32_t nsb;
+  };
+  static __device__ __forceinline__ void dma_scales(const Src& s, int quad, GEP_LDS char* smem, int stage, int wave) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(s.s, (GEP_LDS void*)(smem + kSOff + stage * kSBytes + wave * 1024), 16,
+                                             quad < s.nsb ? s.s_off + quad * 1024 : kOOB, 0, 0, 0);
+#endif
+  }
+
+  // Lane offsets (A: from the start of the ring; B and scales likewise).
+  struct Lane {
+    int a0, a1;  // E4M3: the two chunks; E2M1: steps 0 and 1 of a pair
+    int b0, b1;
+    int sa, sb;  // scale bytes, of the current scale stage
+  };
+  static __device__ __forceinline__ Lane lane_offsets(int lane, int wm0, int wn0) {
+    Lane o;
+    const int ra = wm0 + (lane & 15), rb = wn0 + (lane & 15), g = lane >> 4;
+    o.a0 = ra * kRowBytes + ((g ^ kswz(ra)) << 4);
+    o.b0 = kBOff + rb * kRowBytes + ((g ^ kswz(rb)) << 4);
+    o.a1 = o.a0 ^ 64;
+    o.b1 = o.b0 ^ 64;
+    o.sa = kSOff + ra * 16 + g;
+    o.sb = kSOff + (BM + rb) * 16 + g;
+    return o;
+  }
+  // Stage of an operand in step T of a quad.
+  template <int F>
+  static constexpr int stage(int t) { return F == MX_E4M3 ? (t & 1) : ((t >> 1) & 1); }
+  template <int F, int T>
+  static __device__ __forceinline__ MxFrag<F> read(const GEP_LDS char* smem, int stage_bytes, int r, int o0, int o1) {
+    const GEP_LDS char* p = smem + stage<F>(T) * stage_bytes + r * 16 * kRowBytes;
+    MxFrag<F> f;
+    if constexpr (F == MX_E4M3) {
+      f.lo = *(const GEP_LDS i32x4*)(p + o0);
+      f.hi = *(const GEP_LDS i32x4*)(p + o1);
+    } else {
+      f.lo = *(const GEP_LDS i32x4*)(p + ((T & 1) ? o1 : o0));
+    }
+    return f;
+  }
+  template <int T>
+  static __device__ __forceinline__ int read_scale(const GEP_LDS char* smem, int o, int r) {
+    return *(const GEP_LDS uint8_t*)(smem + o + r * 256 + T * 4);
+  }
+
+  struct Frags {
+    MxFrag<FA> a[2];
+    MxFrag<FB> b[kNI];
+    int sa[2], sb[kNI];
+  };
+  template <int T>
+  static __device__ __forceinline__ void read_a(Frags& f, const GEP_LDS char* smem, const Lane& o, int r, int so) {
+    f.a[r & 1] = read<FA, T>(smem, kABytes, r, o.a0, o.a1);
+    f.sa[r & 1] = read_scale<T>(smem, o.sa + so, r);
+  }
+  template <int T>
+  static __device__ __forceinline__ void read_b(Frags& f, const GEP_LDS char* smem, const Lane& o, int c, int so) {
+    f.b[c] = read<FB, T>(smem, kBBytes, c, o.b0, o.b1);
+    f.sb[c] = read_scale<T>(smem, o.sb + so, c);
+  }
+
+  static constexpr bool bar(int t) { return A::k8 || B::k8 || (t & 1); }
+  // rows whose A fragments are read after position p (row 1 after the first MFMA)
+  static constexpr int row_after(int p) {
+    if (p == 0) return 1;
+    return ((p + 1) % kNI == 0 && (p + 1) / kNI + 1 < kMI && (p + 1) / kNI >= 1) ? (p + 1) / kNI + 1 : 0;
+  }
+  static constexpr int reads(int t, int p) {  // LDS reads after position p
+    return (row_after(p) ? (A::k8 ? 3 : 2) : 0) + (p == kLastP ? (A::k8 ? 3 : 2) : 0) + (p >= kLastP ? (B::k8 ? 3 : 2) : 0);
+  }
+  // transfers after position p of step t: the second half of the next stage at the head (A at
+  // 0, 2, B at 4, 6; the next quad's scales at 8), the first half of the one after it in the last row
+  static constexpr bool head(bool k8, int t) { return k8 || !(t & 1); }
+  static constexpr bool tail(bool k8, int t) { return k8 || (t & 1); }
+  static constexpr int transfers(int t, int p) {
+    int n = 0;
+    if (p < 4 && p % 2 == 0) n += head(A::k8, t);
+    if (p >= 4 && p < 8 && p % 2 == 0) n += head(B::k8, t);
+    if (p == 8 && t == 0) n += 1;
+    if (p >= kLastP && p < kLastP + 2) n += tail(A::k8, t);
+    if (p >= kLastP + 2) n += tail(B::k8, t);
+    return n;
+  }
+  template <int T, int P, int E>
+  static __device__ __forceinline__ void sched() {
+    if constexpr (P < E) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      if constexpr (reads(T, P) > 0) __builtin_amdgcn_sched_group_barrier(0x100, reads(T, P), 0);
+      if constexpr (transfers(T, P) > 0) __builtin_amdgcn_sched_group_barrier(0x020, transfers(T, P), 0);
+      sched<T, P + 1, E>();
+    }
+  }
+
+  // Positions [P, E) of step T of quad q (so: its scale stage's offset; so_next: the next step's).
+  template <bool MM, int T, int P, int E>
+  static __device__ __forceinline__ void positions(f32x4 (&acc)[kMI][kNI], Frags& f, GEP_LDS char* smem, const Lane& o,
+                                                   const Src& s, int q, int so, int so_next, int wave) {
+    if constexpr (P < E) {
+      constexpr int NT = (T + 1) & 3;
+      if constexpr (MM) {
+        constexpr int r = P / kNI, c = P % kNI;
+        acc[r][c] = mx_mma<FA, FB>(f.b[c], f.a[r & 1], acc[r][c], f.sb[c], f.sa[r & 1]);
+        if constexpr (row_after(P) > 0) read_a<T>(f, smem, o, row_after(P), so);
+        if constexpr (P == kLastP) read_a<NT>(f, smem, o, 0, so_next);
+        if constexpr (P >= kLastP) read_b<NT>(f, smem, o, P - kLastP, so_next);
+      }
+      const int step = q * 4 + T;
+      // (slots: steps of an E4M3 operand, pairs of an E2M1 one, 128 bytes each)
+      if constexpr (P < 4 && P % 2 == 0 && head(A::k8, T)) {
+        constexpr int st = stage<FA>(A::k8 ? T : T + 1) ^ 1;
+        const int slot = (A::k8 ? step : step >> 1) + 1;
+        dma<kInstrA / 2 + P / 2 * (kInstrA / 4), kInstrA / 2 + (P / 2 + 1) * (kInstrA / 4)>(s.la, s.a, slot * 128, smem + st * kABytes, wave);
+      }
+      if constexpr (P >= 4 && P < 8 && P % 2 == 0 && head(B::k8, T)) {
+        constexpr int st = stage<FB>(B::k8 ? T : T + 1) ^ 1, u = (P - 4) / 2;
+        const int slot = (B::k8 ? step : step >> 1) + 1;
+        dma<kInstrB / 2 + u * (kInstrB / 4), kInstrB / 2 + (u + 1) * (kInstrB / 4)>(s.lb, s.b, slot * 128, smem + kBOff + st * kBBytes, wave);
+      }
+      if constexpr (P == 8 && T == 0) dma_scales(s, q + 1, smem, (q + 1) & 1, wave);
+      if constexpr (P >= kLastP && P < kLastP + 2 && tail(A::k8, T)) {
+        constexpr int u = P - kLastP;
+        const int slot = (A::k8 ? step : step >> 1) + 2;
+        dma<u * (kInstrA / 4), (u + 1) * (kInstrA / 4)>(s.la, s.a, slot * 128, smem + stage<FA>(T) * kABytes, wave);
+      }
+      if constexpr (P >= kLastP + 2 && tail(B::k8, T)) {
+        constexpr int u = P - kLastP - 2;
+        const int slot = (B::k8 ? step : step >> 1) + 2;
+        dma<u * (kInstrB / 4), (u + 1) * (kInstrB / 4)>(s.lb, s.b, slot * 128, smem + kBOff + stage<FB>(T) * kBBytes, wave);
+      }
+      positions<MM, T, P + 1, E>(acc, f, smem, o, s, q, so, so_next, wave);
+    }
+  }
+  static_assert(kInstrA == 4 && kInstrB == 4, "two transfers in each half of a stage");
+
+  template <bool MM, int T>
+  static __device__ __forceinline__ void step(f32x4 (&acc)[kMI][kNI], Frags& f, GEP_LDS char* smem, const Lane& lo,
+                                              const Src& s, int q, int wave) {
+    const int so = (q & 1) * kSBytes, so_next = T == 3 ? ((q + 1) & 1) * kSBytes : so;
+    // opaque offsets: stage and block-row offsets then fold into the reads' immediates
+    Lane o = lo;
+    asm volatile("" : "+v"(o.a0), "+v"(o.a1), "+v"(o.b0), "+v"(o.b1), "+v"(o.sa), "+v"(o.sb));
+    if constexpr (MM) {
+      __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_setprio(1);
+      __builtin_amdgcn_sched_barrier(0);
+      positions<true, T, 0, kPrioP>(acc, f, smem, o, s, q, so, so_next, wave);
+      sched<T, 0, kPrioP>();
+      __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_setprio(0);
+      __builtin_amdgcn_sched_barrier(0);
+      positions<true, T, kPrioP, kLastP>(acc, f, smem, o, s, q, so, so_next, wave);
+      sched<T, kPrioP, kLastP>();
+      if constexpr (bar(T)) dma_barrier();
+      positions<true, T, kLastP, kN>(acc, f, smem, o, s, q, so, so_next, wave);
+      sched<T, kLastP, kN>();
+      __builtin_amdgcn_sched_barrier(0);
+    } else {
+      positions<false, T, 0, kLastP>(acc, f, smem, o, s, q, so, so_next, wave);
+      if constexpr (bar(T)) dma_barrier();
+      positions<false, T, kLastP, kN>(acc, f, smem, o, s, q, so, so_next, wave);
+    }
+  }
+  template <bool MM>
+  static __device__ __forceinline__ void mainloop(f32x4 (&acc)[kMI][kNI], Frags& f, GEP_LDS char* smem, const Lane& o,
+                                                  const Src& s, int steps, int wave) {
+    for (int q = 0; q * 4 < steps; ++q) {
+      step<MM, 0>(acc, f, smem, o, s, q, wave);
+      step<MM, 1>(acc, f, smem, o, s, q, wave);
+      if (q * 4 + 2 < steps) {
+        step<MM, 2>(acc, f, smem, o, s, q, wave);
+        step<MM, 3>(acc, f, smem, o, s, q, wave);
+      }
+    }
+  }
+
+  // ---- epilogue: passes of 64 rows of the wave's block through its share of the idle ring, as
+  // fp32 rows of 64 columns, and back 8 columns a lane, so that C, D and PostAct are accessed 16
+  // bytes (or more) at a time and 128 bytes a row. Half-row chunks are XOR-swizzled by the row
+  // as in gemm_kernel.hpp's 16x16 epilogue.
+  static __device__ __forceinline__ int ebuf(int r, int c8, int hf) {
+    return r * 256 + hf * 128 + ((c8 ^ ((r & 3) | ((r >> 1) & 4))) << 4);
+  }
+  static __device__ __forceinline__ void epilogue(const KParams& p, const MxTileInfo& ti, const f32x4 (&acc)[kMI][kNI],
+                                                  GEP_LDS char* region, int lane, int wm0, int wn0) {
+    asm volatile("" : "+v"(lane));
+    const int row0 = ti.m0 + wm0, col0 = ti.n0 + wn0;
+    const int rl = lane >> 3, n = col0 + 8 * (lane & 7);
+#pragma unroll
+    for (int pass = 0; pass < kMI / 4; ++pass) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < kNI; ++j)
+          *(f32x4 GEP_LDS*)(region + ebuf(i * 16 + (lane & 15), 2 * j + (lane >> 5), (lane >> 4) & 1)) = acc[pass * 4 + i][j];
+      asm volatile("" ::: "memory");  // (LDS operations of a wave complete in order)
+#pragma unroll 1
+      for (int it = 0; it < 8; ++it) {
+        const int r = it * 8 + rl;
+        const int64_t m = row0 + pass * 64 + r;
+        const f32x4 x0 = *(const f32x4 GEP_LDS*)(region + ebuf(r, lane & 7, 0));
+        const f32x4 x1 = *(const f32x4 GEP_LDS*)(region + ebuf(r, lane & 7, 1));
+        float v[8] = {x0[0], x0[1], x0[2], x0[3], x1[0], x1[1], x1[2], x1[3]};
+        if (m < ti.row_end && n < p.N) mx_finish8(p, m, n, v);
+      }
+      asm volatile("" ::: "memory");
+    }
+  }
+
+  static __device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+  static __device__ __forceinline__ MxTileInfo decode(const MxParams& mp, int t, const int32_t* gstart) {
+    const KParams& p = mp.k;
+    MxTileInfo ti;
+    uint32_t mb, nb;
+    int row_base = 0;
+    if constexpr (VM) {
+      int lo = 0, hi = p.L - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (gstart[mid] <= t) lo = mid; else hi = mid - 1;
+      }
+      row_base = p.cu_seqlens[lo];
+      ti.row_end = p.cu_seqlens[lo + 1];
+      ti.g = lo;
+      raster(p, (uint32_t)(t - gstart[lo]), (uint32_t)((ti.row_end - row_base + BM - 1) / BM), (uint32_t)p.tn, p.fd_Gtn, mb, nb);
+    } else {
+      ti.g = 0;
+      ti.row_end = p.M;
+      raster(p, (uint32_t)t, (uint32_t)p.tm, (uint32_t)p.tn, p.fd_Gtn, mb, nb);
+    }
+    ti.g = uni(ti.g);
+    ti.m0 = uni(row_base + (int)mb * BM);
+    ti.n0 = uni((int)nb * BN);
+    ti.row_end = uni(ti.row_end);
+    return ti;
+  }
+
+  static __device__ __forceinline__ void run(const MxParams& mp) {
+    const KParams& p = mp.k;
+    __shared__ __attribute__((aligned(1024))) char smem_raw[kLdsBytes + kVarlenLds];
+    GEP_LDS char* smem = (GEP_LDS char*)smem_raw;
+    const int tid = threadIdx.x, lane_id = tid & 63;
+    const int wave = uni(tid >> 6);
+    // 8 waves: w and w + 4 share a SIMD and take the two row halves of a column block
+    const int wm0 = (wave / kWavesN) * kWM, wn0 = (wave % kWavesN) * kWN;
+
+    int T = p.T;
+    [[maybe_unused]] int32_t* gstart = nullptr;
+    if constexpr (VM) {
+      // tile offsets of the groups; an array that does not run 0 .. M without decreasing gives
+      // no tiles (see gemm_kernel.hpp: the flag shares the one LDS array)
+      gstart = (int32_t*)(smem_raw + kLdsBytes);
+      int32_t* part = gstart + kMaxVarlenGroups + 1;
+      volatile int32_t* s_bad = part + kThreads;
+      if (tid == 0) *s_bad = 0;
+      __syncthreads();
+      constexpr int kPer = kMaxVarlenGroups / kThreads;
+      int32_t local[kPer], sum = 0;
+      int bad = 0;
+#pragma unroll
+      for (int q = 0; q < kPer; ++q) {
+        const int g = tid * kPer + q;
+        int32_t tiles = 0;
+        if (g < p.L) {
+          const int c0 = p.cu_seqlens[g], c1 = p.cu_seqlens[g + 1];
+          bad |= c1 < c0 || (g == 0 && c0 != 0) || (g == p.L - 1 && c1 != p.M);
+          tiles = c1 > c0 ? (int)(((int64_t)c1 - c0 + BM - 1) / BM) * p.tn : 0;
+        }
+        local[q] = sum;
+        sum += tiles;
+      }
+      if (bad) *s_bad = 1;
+      part[tid] = sum;
+      __syncthreads();
+      bad = uni(*s_bad);
+      for (int off = 1; off < kThreads; off <<= 1) {
+        const int32_t add = tid >= off ? part[tid - off] : 0;
+        __syncthreads();
+        part[tid] += add;
+        __syncthreads();
+      }
+#pragma unroll
+      for (int q = 0; q < kPer; ++q) {
+        const int g = tid * kPer + q;
+        if (g < p.L) gstart[g] = part[tid] - sum + local[q];
+      }
+      T = uni(bad ? 0 : part[kThreads - 1]);
+      __syncthreads();
+    }
+    const int P = p.P;
+    const bool xq = p.xcd_remap && (P & 7) == 0;
+    const int bid = blockIdx.x;
+    const int b0 = xq ? (bid & 7) * (P >> 3) + (bid >> 3) : bid;
+
+    for (int t = b0; t < T; t += P) {
+      const MxTileInfo ti = decode(mp, t, gstart);
+      int lane = lane_id;
+      asm volatile("" : "+v"(lane));  // (lane offsets are not kept across the main loop)
+      Src s;
+      init<kInstrA>(s.la, wave, lane, ti.row_end - ti.m0, (int)p.lda, (int)p.lda);
+      init<kInstrB>(s.lb, wave, lane, p.N - ti.n0, (int)p.ldb, (int)p.ldb);
+      const int64_t ao = (int64_t)ti.m0 * p.lda, bo = (int64_t)ti.n0 * p.ldb;
+      s.a = make_rsrc((const char*)p.A + ao, p.a_bytes - ao);
+      s.b = make_rsrc((const char*)p.B + (int64_t)ti.g * p.b_bytes + bo, p.b_bytes - bo);
+      s.nsb = mp.nsb;
+      {
+        const bool is_a = wave < BM / 64;
+        const int first = is_a ? ti.m0 : ti.n0;  // row of the tile's first scale
+        const int i = (is_a ? wave : wave - BM / 64) * 64 + lane;  // row of the tile
+        const int64_t so = (int64_t)(first >> 6) * mp.nsb * 1024;
+        s.s = make_rsrc(is_a ? mp.sa + so : mp.sb + (int64_t)ti.g * mp.sb_bytes + so,
+                        (is_a ? mp.sa_bytes : mp.sb_bytes) - so);
+        const int rr = (first & 63) + i;
+        s.s_off = first + i < (is_a ? ti.row_end : p.N) ? (uint32_t)((rr >> 6) * mp.nsb * 1024 + (rr & 63) * 16) : kOOB;
+      }
+      const Lane o = lane_offsets(lane, wm0, wn0);
+      f32x4 acc[kMI][kNI];
+#pragma unroll
+      for (int i = 0; i < kMI; ++i)
+#pragma unroll
+        for (int j = 0; j < kNI; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+      // a wave whose rows all lie past the output only moves data
+      const bool idle = ti.m0 + wm0 >= ti.row_end;
+      lds_barrier();  // the previous tile's epilogue buffers are free
+      if (mp.steps > 0) {
+        dma<0, 4>(s.la, s.a, 0, smem, wave);
+        dma<0, 4>(s.lb, s.b, 0, smem + kBOff, wave);
+        dma_scales(s, 0, smem, 0, wave);
+        dma<0, 2>(s.la, s.a, 128, smem + kABytes, wave);
+        dma<0, 2>(s.lb, s.b, 128, smem + kBOff + kBBytes, wave);
+        dma_barrier();
+        Frags f;
+        if (idle) {
+          __builtin_amdgcn_s_setprio(0);
+          mainloop<false>(acc, f, smem, o, s, mp.steps, wave);
+        } else {
+          read_a<0>(f, smem, o, 0, 0);
+#pragma unroll
+          for (int c = 0; c < kNI; ++c) read_b<0>(f, smem, o, c, 0);
+          mainloop<true>(acc, f, smem, o, s, mp.steps, wave);
+        }
+      }
+      dma_barrier();  // transfers past K have landed and every wave has left the ring
+      if (!idle) epilogue(p, ti, acc, smem + wave * (kSOff / NW), lane, wm0, wn0);
+    }
+  }
+};
+
+// ------------------------------------------------------------------------------------
+// MxDirect
+// ------------------------------------------------------------------------------------
+// 16 MB x 16 NB outputs per workgroup of NW waves; wave w takes the scale tiles (512 values of
+// K) w, w + NW, ... and reads its fragments straight from global memory, D steps ahead. With one
+// row of activations the operand B is read once from HBM in 64-byte runs of 16 rows, and nothing
+// waits on a barrier. The waves' partial sums meet in LDS in a fixed order.
+template <int MB, int NB, int NW, int D, int FA, int FB, bool VM>
+struct MxDirect {
+  static constexpr int kBM = 16 * MB, kBN = 16 * NB;
+  static constexpr int kPitch = kBN + 4;  // floats of a row of partial sums
+  static constexpr int kPlane = kBM * kPitch;
+
+  struct Buf {
+    MxFrag<FA> a[MB];
+    MxFrag<FB> b[NB];
+  };
+  struct Src {
+    __amdgpu_buffer_rsrc_t a, b, sa, sb;
+    uint32_t ao[MB], bo[NB], sao[MB], sbo[NB];  // this lane's rows (kOOB past the operand)
+    int ka, kb;   // bytes of a row past the lane's first chunk
+    int nsb;
+  };
+  template <int F>
+  static __device__ __forceinline__ MxFrag<F> load(__amdgpu_buffer_rsrc_t rs, uint32_t off, int klim, int step) {
+    MxFrag<F> f;
+    const int kb = step * MxFmt<F>::kStepBytes;
+    f.lo = __builtin_amdgcn_raw_buffer_load_b128(rs, kb < klim ? off + kb : kOOB, 0, 0);
+    if constexpr (F == MX_E4M3) f.hi = __builtin_amdgcn_raw_buffer_load_b128(rs, kb + 64 < klim ? off + kb + 64 : kOOB, 0, 0);
+    return f;
+  }
+  static __device__ __forceinline__ void fetch(Buf& b, const Src& s, int step) {
+#pragma unroll
+    for (int j = 0; j < NB; ++j) b.b[j] = load<FB>(s.b, s.bo[j], s.kb, step);
+#pragma unroll
+    for (int i = 0; i < MB; ++i) b.a[i] = load<FA>(s.a, s.ao[i], s.ka, step);
+  }
+  struct Scales {
+    i32x4 a[MB], b[NB];
+  };
+  static __device__ __forceinline__ void fetch_scales(Scales& q, const Src& s, int tile) {
+#pragma unroll
+    for (int j = 0; j < NB; ++j) q.b[j] = __builtin_amdgcn_raw_buffer_load_b128(s.sb, tile < s.nsb ? s.sbo[j] + tile * 1024 : kOOB, 0, 0);
+#pragma unroll
+    for (int i = 0; i < MB; ++i) q.a[i] = __builtin_amdgcn_raw_buffer_load_b128(s.sa, tile < s.nsb ? s.sao[i] + tile * 1024 : kOOB, 0, 0);
+  }
+  // Byte t of the result: the lane's scale (byte l / 16 of word t) of step t.
+  static __device__ __forceinline__ int gather_scale(const i32x4& w, uint32_t sel) {
+    const uint32_t lo = __builtin_amdgcn_perm((uint32_t)w[1], (uint32_t)w[0], sel);
+    const uint32_t hi = __builtin_amdgcn_perm((uint32_t)w[3], (uint32_t)w[2], sel);
+    return (int)(lo | (hi << 16));
+  }
+
+  template <int T>
+  static __device__ __forceinline__ void step(f32x4 (&acc)[MB][NB], Buf (&buf)[D], const Src& s, const int (&sa)[MB],
+                                              const int (&sb)[NB], int tile) {
+    Buf& b = buf[T % D];
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      for (int j = 0; j < NB; ++j) acc[i][j] = mx_mma<FA, FB, T>(b.b[j], b.a[i], acc[i][j], sb[j], sa[i]);
+    // the step D further on, in this tile of scales or in the wave's next
+    fetch(b, s, T + D < 4 ? tile * 4 + T + D : (tile + NW) * 4 + T + D - 4);
+  }
+
+  static __device__ __forceinline__ void run(const MxParams& mp) {
+    const KParams& p = mp.k;
+    __shared__ __attribute__((aligned(16))) float sums[NW * kPlane];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int g = 0, m0 = blockIdx.y * kBM, row_end = p.M;
+    const int n0 = blockIdx.x * kBN;
+    if constexpr (VM) {
+      // the group of row block blockIdx.y: 64 groups a pass, one a lane; the whole array is
+      // checked (0 .. M, never decreasing)
+      int base = 0, found = 0, bad = 0;
+      const int want = blockIdx.y;
+      for (int g0 = 0; g0 < p.L; g0 += 64) {
+        const int gi = g0 + lane;
+        int c0 = 0, c1 = 0;
+        if (gi < p.L) {
+          c0 = p.cu_seqlens[gi];
+          c1 = p.cu_seqlens[gi + 1];
+          bad |= c1 < c0 || (gi == 0 && c0 != 0) || (gi == p.L - 1 && c1 != p.M);
+        }
+        const int tiles = c1 > c0 ? (int)(((int64_t)c1 - c0 + kBM - 1) / kBM) : 0;
+        int incl = tiles;
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) {
+          const int u = __shfl_up(incl, off);
+          if (lane >= off) incl += u;
+        }
+        const int first = base + incl - tiles;
+        const uint64_t hit = __ballot(want >= first && want < first + tiles);
+        if (hit) {
+          const int src = __ffsll((unsigned long long)hit) - 1;
+          g = g0 + src;
+          m0 = __shfl(c0, src) + (want - __shfl(first, src)) * kBM;
+          row_end = __shfl(c1, src);
+          found = 1;
+        }
+        base += __shfl(incl, 63);
+      }
+      if (__ballot(bad) || !found) return;  // (the same in every wave)
+      g = __builtin_amdgcn_readfirstlane(g);
+      m0 = __builtin_amdgcn_readfirstlane(m0);
+      row_end = __builtin_amdgcn_readfirstlane(row_end);
+    }
+    const int r = lane & 15, kg = lane >> 4;
+    Src s;
+    const int64_t ao = (int64_t)m0 * p.lda, bo = (int64_t)n0 * p.ldb;
+    s.a = make_rsrc((const char*)p.A + ao, p.a_bytes - ao);
+    s.b = make_rsrc((const char*)p.B + (int64_t)g * p.b_bytes + bo, p.b_bytes - bo);
+    const int64_t sao = (int64_t)(m0 >> 6) * mp.nsb * 1024, sbo = (int64_t)(n0 >> 6) * mp.nsb * 1024;
+    s.sa = make_rsrc(mp.sa + sao, mp.sa_bytes - sao);
+    s.sb = make_rsrc(mp.sb + (int64_t)g * mp.sb_bytes + sbo, mp.sb_bytes - sbo);
+    s.nsb = mp.nsb;
+    s.ka = (int)p.lda - kg * 16;
+    s.kb = (int)p.ldb - kg * 16;
+#pragma unroll
+    for (int i = 0; i < MB; ++i) {
+      const int row = i * 16 + r, q = (m0 & 63) + row;
+      s.ao[i] = m0 + row < row_end ? (uint32_t)(row * (int)p.lda + kg * 16) : kOOB;
+      s.sao[i] = m0 + row < row_end ? (uint32_t)((q >> 6) * mp.nsb * 1024 + (q & 63) * 16) : kOOB;
+    }
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      const int row = j * 16 + r, q = (n0 & 63) + row;
+      s.bo[j] = n0 + row < p.N ? (uint32_t)(row * (int)p.ldb + kg * 16) : kOOB;
+      s.sbo[j] = n0 + row < p.N ? (uint32_t)((q >> 6) * mp.nsb * 1024 + (q & 63) * 16) : kOOB;
+    }
+    f32x4 acc[MB][NB];
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      for (int j = 0; j < NB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    if (wave < mp.nsb) {
+      const uint32_t sel = (uint32_t)kg | ((uint32_t)(4 + kg) << 8) | 0x0C0C0000u;  // (0x0C: a zero byte)
+      Scales sc;
+      fetch_scales(sc, s, wave);
+      Buf buf[D];
+#pragma unroll
+      for (int t = 0; t < D; ++t) fetch(buf[t], s, wave * 4 + t);
+      for (int tile = wave; tile < mp.nsb; tile += NW) {
+        int sa[MB], sb[NB];
+#pragma unroll
+        for (int i = 0; i < MB; ++i) sa[i] = gather_scale(sc.a[i], sel);
+#pragma unroll
+        for (int j = 0; j < NB; ++j) sb[j] = gather_scale(sc.b[j], sel);
+        fetch_scales(sc, s, tile + NW);
+        step<0>(acc, buf, s, sa, sb, tile);
+        step<1>(acc, buf, s, sa, sb, tile);
+        step<2>(acc, buf, s, sa, sb, tile);
+        step<3>(acc, buf, s, sa, sb, tile);
+      }
+    }
+    // lane l of block (i, j) holds row l % 16, columns 4 (l / 16) + [0, 4)
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+        *(f32x4*)(sums + wave * kPlane + (i * 16 + r) * kPitch + j * 16 + kg * 4) = acc[i][j];
+    __syncthreads();
+    for (int u = tid; u < kBM * kBN / 8; u += NW * 64) {
+      const int row = u / (kBN / 8), col = u % (kBN / 8) * 8;
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = 0.f;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        const float* q = sums + w * kPlane + row * kPitch + col;
+        const f32x4 x = *(const f32x4*)q, y = *(const f32x4*)(q + 4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] += x[e], v[4 + e] += y[e];
+      }
+      if (m0 + row < row_end && n0 + col < p.N) mx_finish8(p, m0 + row, n0 + col, v);
+    }
+  }
+};
+
+template <int BM, int NW, int FA, int FB, bool VM>
+__global__ __launch_bounds__(NW * 64, (BM == 256 ? 1 : 2)) void mx_ring_kernel(const MxParams p) {
+  MxRing<BM, BM, NW, FA, FB, VM>::run(p);
+}
+template <int MB, int NB, int NW, int D, int FA, int FB, bool VM>
+__global__ __launch_bounds__(NW * 64) void mx_direct_kernel(const MxParams p) {
+  MxDirect<MB, NB, NW, D, FA, FB, VM>::run(p);
+}
+
+// Launch tile kind `tile` (an MxTile) of one pair of formats; grid: workgroups of a ring kernel, or
+// x (columns) by y (rows) of a direct one.
+template <int FA, int FB, bool VM>
+hipError_t mx_launch(int32_t tile, const MxParams& p, dim3 grid, hipStream_t s);
+
+#define GEP_MX_LAUNCH(FA, FB, VM)                                                                    \
+  template <>                                                                                        \
+  hipError_t mx_launch<FA, FB, VM>(int32_t tile, const MxParams& p, dim3 grid, hipStream_t s) {      \
+    switch (tile) {                                                                                  \
+      case MX_T_256: mx_ring_kernel<256, 8, FA, FB, VM><<<grid, 512, 0, s>>>(p); break;              \
+      case MX_T_128: mx_ring_kernel<128, 4, FA, FB, VM><<<grid, 256, 0, s>>>(p); break;              \
+      case MX_T_64: mx_direct_kernel<4, 4, 4, 2, FA, FB, VM><<<grid, 256, 0, s>>>(p); break;         \
+      case MX_T_R32: mx_direct_kernel<2, 2, 8, 2, FA, FB, VM><<<grid, 512, 0, s>>>(p); break;        \
+      case MX_T_R16: mx_direct_kernel<1, 1, 8, 4, FA, FB, VM><<<grid, 512, 0, s>>>(p); break;        \
+      default: return hipErrorInvalidValue;                                                          \
+    }                                                                                                \
+    return hipGetLastError();                                                                        \
+  }
+
+}  // namespace gep

@@ -1,0 +1,5 @@
+// MX product kernels: A E2M1, B E4M3, rows grouped by expert.
+#include "mx_gemm.hpp"
+namespace gep {
+GEP_MX_LAUNCH(MX_E2M1, MX_E4M3, true)
+}  // namespace gep

@@ -1,0 +1,261 @@
+// MX quantiser and its inverse (mx_quantize, mx_dequantize of the public header).
+//
+// Both are bound by memory: the input is read once, codes and scales (8.25 or 4.25 bits a value)
+// are written once, and a value costs about ten vector instructions.
+#include "mx_common.hpp"
+
+namespace gep {
+gemm_status fail(gemm_status st, const char* fmt, ...);
+void clear_error();
+
+namespace {
+
+constexpr int kThreads = 256;
+
+// ---- blocks along a row. A thread takes a chunk of 8 values (16 or 32 bytes), the four lanes of
+// a quad a block: the maximum crosses lanes by DPP, loads and stores are contiguous over the
+// wave. Chunks are numbered row by row over rows [r0, r0 + rows) (below 2^31 in one launch).
+template <typename T, int FMT>
+__global__ __launch_bounds__(kThreads) void quantize_rows_kernel(const T* x, int64_t ldx, int64_t r0, int cols, int nb,
+                                                                 int nsb, uint32_t n, FastDiv fd_cpr, uint8_t* codes,
+                                                                 uint8_t* scales) {
+  const uint32_t i = blockIdx.x * kThreads + threadIdx.x;
+  if (i >= n) return;  // (n is a multiple of 4: quads leave together)
+  uint32_t rr, ch;
+  fd_divmod(fd_cpr, i, rr, ch);
+  const int64_t r = r0 + rr;
+  float v[8];
+  load8_tail(x + r * ldx, (int)ch * 8, cols, v);
+  mx_store_chunk<FMT>(v, r, (int)ch, nb, nsb, codes, scales);
+}
+
+// ---- blocks along a column. A workgroup takes 128 rows (four blocks) by 256 bytes of columns:
+// the rows are read 16 bytes a lane into LDS; then each thread holds one dword column (two
+// 16-bit columns or one fp32 column) of one block in registers, the four lanes of a quad the
+// four blocks of a column, so that a quad writes 128 (E4M3) or 64 (E2M1) contiguous bytes of an
+// output row. Rows of LDS are 64 dwords; each block starts 16 dwords further, so the 16 dword
+// columns x 4 blocks that a wave reads lie in 64 distinct banks.
+constexpr int kTR = 128, kTB = kTR / kMxBlock;  // rows and blocks of a tile
+constexpr int kRowDw = 64, kSkewDw = 16;
+constexpr int kTileDw = kTR * kRowDw + kTB * kSkewDw;
+
+template <typename T, int FMT>
+__global__ __launch_bounds__(kThreads) void quantize_cols_kernel(const T* x, int64_t ldx, int rows, int cols, int nb,
+                                                                 int nsb, uint8_t* codes, uint8_t* scales) {
+  constexpr int kVec = 16 / (int)sizeof(T);     // elements of a 16-byte load
+  constexpr int kCols = 256 / (int)sizeof(T);   // columns of a tile
+  constexpr int kPer = 4 / (int)sizeof(T);      // columns of a dword
+  __shared__ __attribute__((aligned(16))) uint32_t tile[kTileDw];
+  const int tid = threadIdx.x;
+  const int r0 = blockIdx.y * kTR, c0 = blockIdx.x * kCols;
+  // 16 lanes a row, 16 rows a pass
+  uint4 in[kTR / 16];
+  const int lc = c0 + (tid & 15) * kVec;
+#pragma unroll
+  for (int q = 0; q < kTR / 16; ++q) {
+    const int r = r0 + q * 16 + (tid >> 4);
+    in[q] = uint4{0, 0, 0, 0};
+    if (r < rows) {
+      const T* p = x + (int64_t)r * ldx + lc;
+      if (lc + kVec <= cols) {
+        __builtin_memcpy(&in[q], (const void*)p, 16);
+      } else {
+        T e[kVec] = {};
+#pragma unroll
+        for (int k = 0; k < kVec; ++k)
+          if (lc + k < cols) e[k] = p[k];
+        __builtin_memcpy(&in[q], e, 16);
+      }
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < kTR / 16; ++q) {
+    const int r = q * 16 + (tid >> 4);
+    *(uint4*)(tile + r * kRowDw + (r / kMxBlock) * kSkewDw + (tid & 15) * 4) = in[q];
+  }
+  __syncthreads();
+  const int blk = tid & 3, dc = tid >> 2;  // block of the tile, dword column
+  const int b = blockIdx.y * kTB + blk;
+  const uint32_t* col = tile + blk * (kMxBlock * kRowDw + kSkewDw) + dc;
+  uint32_t w[kMxBlock];
+#pragma unroll
+  for (int i = 0; i < kMxBlock; ++i) w[i] = col[i * kRowDw];
+  if (b >= nb) return;
+#pragma unroll
+  for (int h = 0; h < kPer; ++h) {
+    const int c = c0 + dc * kPer + h;
+    if (c >= cols) break;
+    float v[kMxBlock];
+    uint32_t am = 0;
+#pragma unroll
+    for (int i = 0; i < kMxBlock; ++i) {
+      if constexpr (sizeof(T) == 4) {
+        v[i] = __uint_as_float(w[i]);
+      } else {
+        T e[2];
+        __builtin_memcpy(e, &w[i], 4);
+        v[i] = (float)e[h];
+      }
+      am = max(am, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+    }
+    float inv;
+    const uint32_t s = mx_scale<FMT>(am, inv);
+    uint32_t o[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint2 p = mx_codes8<FMT>(v + 8 * j, inv, s == 255u);
+      if constexpr (FMT == MX_E4M3) {
+        o[2 * j] = p.x;
+        o[2 * j + 1] = p.y;
+      } else {
+        o[j] = p.x;
+      }
+    }
+    if constexpr (FMT == MX_E4M3) {
+      uint4* dst = (uint4*)(codes + ((int64_t)c * nb + b) * 32);
+      dst[0] = uint4{o[0], o[1], o[2], o[3]};
+      dst[1] = uint4{o[4], o[5], o[6], o[7]};
+    } else {
+      *(uint4*)(codes + ((int64_t)c * nb + b) * 16) = uint4{o[0], o[1], o[2], o[3]};
+    }
+    scales[mx_scale_at(c, b, nsb)] = (uint8_t)s;
+    if (b == nb - 1)
+      for (int q = nb; q < nsb * kMxScaleBlocks; ++q) scales[mx_scale_at(c, q, nsb)] = 0;
+  }
+}
+
+// ---- values of the codes. A thread takes 8 codes (8 or 4 bytes) and writes 8 values.
+template <typename T, int FMT>
+__global__ __launch_bounds__(kThreads) void dequantize_kernel(const uint8_t* codes, const uint8_t* scales, int64_t r0,
+                                                              int k, int nb, int nsb, uint32_t n, FastDiv fd_cpr, T* out,
+                                                              int64_t ldo) {
+  const uint32_t i = blockIdx.x * kThreads + threadIdx.x;
+  if (i >= n) return;
+  uint32_t rr, ch;
+  fd_divmod(fd_cpr, i, rr, ch);
+  const int64_t r = r0 + rr;
+  const int s = scales[mx_scale_at(r, (int)ch >> 2, nsb)];
+  float v[8];
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  f32x2 p[4];
+  if constexpr (FMT == MX_E4M3) {
+    const uint2 w = *(const uint2*)(codes + (r * nb * 4 + ch) * 8);
+    p[0] = __builtin_amdgcn_cvt_pk_f32_fp8(w.x, false);
+    p[1] = __builtin_amdgcn_cvt_pk_f32_fp8(w.x, true);
+    p[2] = __builtin_amdgcn_cvt_pk_f32_fp8(w.y, false);
+    p[3] = __builtin_amdgcn_cvt_pk_f32_fp8(w.y, true);
+  } else {
+    const uint32_t w = *(const uint32_t*)(codes + (r * nb * 4 + ch) * 4);
+#if defined(__HIP_DEVICE_COMPILE__)
+    p[0] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.f, 0);
+    p[1] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.f, 1);
+    p[2] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.f, 2);
+    p[3] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.f, 3);
+#endif
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    v[e] = s == 255 ? __uint_as_float(0x7FC00000u) : __builtin_ldexpf(p[e >> 1][e & 1], s - 127);
+  store8_tail(out + r * ldo, (int)ch * 8, k, v);
+}
+
+// Launch `f(r0, n)` over ranges of rows whose chunks number below 2^31.
+template <typename F>
+void row_ranges(int32_t rows, uint32_t cpr, F&& f) {
+  const int64_t per = max((int64_t)1, (int64_t)0x7FFFFF00 / cpr);
+  for (int64_t r0 = 0; r0 < rows; r0 += per) f(r0, (uint32_t)(min((int64_t)rows - r0, per) * cpr));
+}
+
+constexpr int32_t kMaxExtent = 1 << 30;
+
+gemm_status check_matrix(const char* fn, int32_t rows, int32_t cols, int32_t type, int64_t ld, const char* name,
+                         const void* p) {
+  if (rows < 0 || cols < 0) return fail(GEMM_ERR_INVALID_ARG, "%s: negative size", fn);
+  if (rows > kMaxExtent || cols > kMaxExtent) return fail(GEMM_ERR_UNSUPPORTED, "%s: more than 2^30 rows or columns", fn);
+  const int es = type == GEMM_DT_F32 ? 4 : ((type == GEMM_DT_F16 || type == GEMM_DT_BF16) ? 2 : 0);
+  if (!es) return fail(GEMM_ERR_INVALID_ARG, "%s: %s must be F16, BF16 or F32", fn, name);
+  if (rows > 1 && ld < cols) return fail(GEMM_ERR_INVALID_ARG, "%s: leading dimension of %s below its columns", fn, name);
+  if (ld < 0 || ld > ((int64_t)1 << 48)) return fail(GEMM_ERR_UNSUPPORTED, "%s: leading dimension of %s outside [0, 2^48]", fn, name);
+  if (rows == 0 || cols == 0) return GEMM_OK;
+  if (!p) return fail(GEMM_ERR_INVALID_ARG, "%s: NULL %s", fn, name);
+  if ((uintptr_t)p % es) return fail(GEMM_ERR_ALIGNMENT, "%s: %s not aligned to its elements", fn, name);
+  return GEMM_OK;
+}
+gemm_status check_mx(const char* fn, int32_t format, const void* codes, const void* scales, bool empty) {
+  if (format != MX_E2M1 && format != MX_E4M3) return fail(GEMM_ERR_INVALID_ARG, "%s: unknown format %d", fn, format);
+  if (empty) return GEMM_OK;
+  if (!codes || !scales) return fail(GEMM_ERR_INVALID_ARG, "%s: NULL codes or scales", fn);
+  if ((uintptr_t)codes & 15) return fail(GEMM_ERR_ALIGNMENT, "%s: codes not 16-byte aligned", fn);
+  return GEMM_OK;
+}
+
+}  // namespace
+}  // namespace gep
+
+using namespace gep;
+
+extern "C" {
+
+gemm_status mx_quantize(int32_t rows, int32_t cols, const void* x, int32_t x_type, int64_t ldx, int32_t transpose,
+                        int32_t format, void* codes, void* scales, void* stream) {
+  const bool empty = rows == 0 || cols == 0;
+  gemm_status st = check_matrix("mx_quantize", rows, cols, x_type, ldx, "x", x);
+  if (st == GEMM_OK) st = check_mx("mx_quantize", format, codes, scales, empty);
+  if (st != GEMM_OK) return st;
+  if (transpose != 0 && transpose != 1) return fail(GEMM_ERR_INVALID_ARG, "mx_quantize: transpose must be 0 or 1");
+  clear_error();
+  if (empty) return GEMM_OK;
+  hipStream_t s = (hipStream_t)stream;
+  const int nb = ((transpose ? rows : cols) + kMxBlock - 1) / kMxBlock;
+  const int nsb = (nb + kMxScaleBlocks - 1) / kMxScaleBlocks;
+  uint8_t *qc = (uint8_t*)codes, *qs = (uint8_t*)scales;
+  with_type(x_type, [&](auto* t) {
+    using T = std::remove_pointer_t<decltype(t)>;
+    if (transpose) {
+      const int tc = 256 / (int)sizeof(T);
+      // (the grid's y extent is 16 bits: tall matrices go in ranges of whole scale tiles)
+      const int gy = (rows + kTR - 1) / kTR, gx = (cols + tc - 1) / tc;
+      if (gy > 65535) { st = fail(GEMM_ERR_UNSUPPORTED, "mx_quantize: more than 2^23 rows with transpose"); return; }
+      if (format == MX_E2M1) quantize_cols_kernel<T, MX_E2M1><<<dim3(gx, gy), kThreads, 0, s>>>((const T*)x, ldx, rows, cols, nb, nsb, qc, qs);
+      else quantize_cols_kernel<T, MX_E4M3><<<dim3(gx, gy), kThreads, 0, s>>>((const T*)x, ldx, rows, cols, nb, nsb, qc, qs);
+    } else {
+      const uint32_t cpr = (uint32_t)nb * 4;
+      row_ranges(rows, cpr, [&](int64_t r0, uint32_t n) {
+        const unsigned g = (n + kThreads - 1) / kThreads;
+        if (format == MX_E2M1) quantize_rows_kernel<T, MX_E2M1><<<g, kThreads, 0, s>>>((const T*)x, ldx, r0, cols, nb, nsb, n, make_fastdiv(cpr), qc, qs);
+        else quantize_rows_kernel<T, MX_E4M3><<<g, kThreads, 0, s>>>((const T*)x, ldx, r0, cols, nb, nsb, n, make_fastdiv(cpr), qc, qs);
+      });
+    }
+  });
+  if (st != GEMM_OK) return st;
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return fail(GEMM_ERR_HIP, "mx_quantize launch: %s", hipGetErrorString(e));
+  return GEMM_OK;
+}
+
+gemm_status mx_dequantize(int32_t rows, int32_t k, int32_t format, const void* codes, const void* scales, void* out,
+                          int32_t out_type, int64_t ldo, void* stream) {
+  const bool empty = rows == 0 || k == 0;
+  gemm_status st = check_matrix("mx_dequantize", rows, k, out_type, ldo, "out", out);
+  if (st == GEMM_OK) st = check_mx("mx_dequantize", format, codes, scales, empty);
+  if (st != GEMM_OK) return st;
+  clear_error();
+  if (empty) return GEMM_OK;
+  hipStream_t s = (hipStream_t)stream;
+  const int nb = (k + kMxBlock - 1) / kMxBlock, nsb = (nb + kMxScaleBlocks - 1) / kMxScaleBlocks;
+  const uint32_t cpr = (uint32_t)nb * 4;
+  const uint8_t *qc = (const uint8_t*)codes, *qs = (const uint8_t*)scales;
+  with_type(out_type, [&](auto* t) {
+    using T = std::remove_pointer_t<decltype(t)>;
+    row_ranges(rows, cpr, [&](int64_t r0, uint32_t n) {
+      const unsigned g = (n + kThreads - 1) / kThreads;
+      if (format == MX_E2M1) dequantize_kernel<T, MX_E2M1><<<g, kThreads, 0, s>>>(qc, qs, r0, k, nb, nsb, n, make_fastdiv(cpr), (T*)out, ldo);
+      else dequantize_kernel<T, MX_E4M3><<<g, kThreads, 0, s>>>(qc, qs, r0, k, nb, nsb, n, make_fastdiv(cpr), (T*)out, ldo);
+    });
+  });
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return fail(GEMM_ERR_HIP, "mx_dequantize launch: %s", hipGetErrorString(e));
+  return GEMM_OK;
+}
+
+}  // extern "C"
