@@ -24,69 +24,115 @@ __host__ __device__ __forceinline__ int64_t mx_scale_at(int64_t r, int b, int ns
          b % kMxScaleBlocks;
 }
 
-struct __attribute__((packed, aligned(2))) U16x8 { uint32_t w[4]; };  // 8 16-bit elements, any even address
-struct __attribute__((packed, aligned(4))) F32x8 { float w[8]; };
+// ---- chunks of 8 elements of a row of n elements of T (_Float16, __bf16 or float), at the
+// alignment of the element: rows of an odd length start anywhere, and gfx950 takes 16-byte
+// accesses at such addresses.
+struct __attribute__((packed, aligned(2))) Packed16 { uint32_t w[4]; };
+struct __attribute__((packed, aligned(4))) Packed32 { uint32_t w[8]; };
 
-// T: _Float16, __bf16 or float. Eight consecutive elements to and from fp32, at the alignment
-// of the element only: one (16-bit) or two (fp32) 16-byte accesses. Rows of an odd number of
-// elements start at any multiple of the element size; gfx950 takes such addresses.
+// The registers of a loaded chunk.
 template <typename T>
-__device__ __forceinline__ float to_f32(T v) { return (float)v; }
+struct Chunk {
+  static constexpr int kW = (int)sizeof(T) * 2;
+  uint32_t w[kW];
+};
 
+// Load elements [c, c + 8) of a row. The load itself has no branch, so that a thread's loads go out
+// together: a chunk that reaches past the end loads the row's last 8 elements instead, and unpack
+// moves them into place.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float v[8]) {
-  if constexpr (sizeof(T) == 4) {
-    const F32x8 x = *(const F32x8*)p;
+__device__ __forceinline__ Chunk<T> load_chunk(const T* row, int c, int n) {
+  Chunk<T> k;
+  if (n >= 8) {  // (the same in every thread)
+    const T* p = row + (c + 8 <= n ? c : n - 8);
+    if constexpr (sizeof(T) == 4) {
+      const Packed32 x = *(const Packed32*)p;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = x.w[e];
-  } else {
-    const U16x8 x = *(const U16x8*)p;
+      for (int i = 0; i < 8; ++i) k.w[i] = x.w[i];
+    } else {
+      const Packed16 x = *(const Packed16*)p;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      T h[2];
-      __builtin_memcpy(h, &x.w[i], 4);
-      v[2 * i] = (float)h[0];
-      v[2 * i + 1] = (float)h[1];
+      for (int i = 0; i < 4; ++i) k.w[i] = x.w[i];
     }
+  } else {
+    T e[8] = {};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c + i < n) e[i] = row[c + i];
+    __builtin_memcpy(k.w, e, sizeof(e));
   }
+  return k;
 }
 
+// The chunk as fp32.
 template <typename T>
-__device__ __forceinline__ void store8(T* p, const float v[8]) {
-  if constexpr (sizeof(T) == 4) {
-    F32x8 x;
+__device__ __forceinline__ void unpack(const Chunk<T>& k, float v[8]) {
+  T e[8];
+  __builtin_memcpy(e, k.w, sizeof(e));
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x.w[e] = v[e];
-    *(F32x8*)p = x;
-  } else {
-    U16x8 x;
+  for (int i = 0; i < 8; ++i) v[i] = (float)e[i];
+}
+// After load_chunk(row, c, n): a chunk that reaches past the end gets its elements into place, zeros
+// behind them. To be called once per loaded chunk, before unpack.
+template <typename T>
+__device__ __forceinline__ void settle(Chunk<T>& k, int c, int n) {
+  if (c + 8 > n && n >= 8) {
+    const int s = c + 8 - n;  // places to move down
+    T v[8];
+    __builtin_memcpy(v, k.w, sizeof(v));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      T h[2] = {(T)v[2 * i], (T)v[2 * i + 1]};
-      __builtin_memcpy(&x.w[i], h, 4);
+    for (int st = 4; st > 0; st >>= 1)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = (s & st) ? (e + st < 8 ? v[e + st] : (T)0.f) : v[e];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = s >= 8 ? (T)0.f : v[e];
+    __builtin_memcpy(k.w, v, sizeof(v));
+  }
+}
+// The chunk's registers as values the compiler knows nothing about: what is unpacked from them
+// after this is unpacked again, not kept in fp32 (twice the registers) from before.
+template <typename T>
+__device__ __forceinline__ void forget(Chunk<T>& k) {
+#pragma unroll
+  for (int i = 0; i < Chunk<T>::kW; ++i) asm volatile("" : "+v"(k.w[i]));
+}
+template <typename T>
+__device__ __forceinline__ void load8(const T* row, int c, int n, float v[8]) {
+  Chunk<T> k = load_chunk(row, c, n);
+  settle(k, c, n);
+  unpack(k, v);
+}
+// Eight values rounded to T.
+template <typename T>
+__device__ __forceinline__ Chunk<T> pack(const float v[8]) {
+  Chunk<T> k;
+  T e[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) e[i] = (T)v[i];
+  __builtin_memcpy(k.w, e, sizeof(e));
+  return k;
+}
+// Store a chunk of unshifted elements; those past the end of the row are not written.
+template <typename T>
+__device__ __forceinline__ void store_chunk(T* row, int c, int n, const Chunk<T>& k) {
+  if (c + 8 <= n) {
+    if constexpr (sizeof(T) == 4) {
+      Packed32 x;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x.w[i] = k.w[i];
+      *(Packed32*)(row + c) = x;
+    } else {
+      Packed16 x;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x.w[i] = k.w[i];
+      *(Packed16*)(row + c) = x;
     }
-    *(U16x8*)p = x;
-  }
-}
-
-// Elements [c, c + 8) of a row of n elements; those past the end read as zero / are not written.
-template <typename T>
-__device__ __forceinline__ void load8_tail(const T* row, int c, int n, float v[8]) {
-  if (c + 8 <= n) {
-    load8(row + c, v);
-  } else {
+  } else if (c < n) {
+    T e[8];
+    __builtin_memcpy(e, k.w, sizeof(e));
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = c + e < n ? (float)row[c + e] : 0.f;
-  }
-}
-template <typename T>
-__device__ __forceinline__ void store8_tail(T* row, int c, int n, const float v[8]) {
-  if (c + 8 <= n) {
-    store8(row + c, v);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (c + e < n) row[c + e] = (T)v[e];
+    for (int i = 0; i < 8; ++i)
+      if (c + i < n) row[c + i] = e[i];
   }
 }
 

@@ -132,12 +132,12 @@ struct MxTileInfo {
 // bytes a row, in storage order) go through a two-stage ring of their own. The loop runs quads of
 // four steps; steps past K read zero codes.
 //
-// A step is kMI x kNI MFMAs, row by row. Two A fragments (block row r in register r & 1) and the
-// kNI B fragments are held; the A fragment of row r is read after row r - 2's last MFMA. The
-// barrier comes before the last row, when every wave has read its last fragment of the stage;
-// after it the next step's first fragments are read and the first half of the transfers into the
-// freed stage goes out; the second half follows at the head of the next step. (No barrier in
-// the middle of a pair when both operands are E2M1: neither stage changes.)
+// A step is kMI x kNI MFMAs, row by row. kRA A fragments are held in a ring (block row r in r %
+// kRA; r is read after row r - kRA's last MFMA) and the kNI B fragments of the step, with kDB
+// those of the next step too. The barrier comes when every wave has read its last fragment of
+// the stage; after it the next step's first fragments are read and the first half of the
+// transfers into the freed stage goes out; the second half follows at the head of the next step.
+// (No barrier in the middle of a pair when both operands are E2M1: neither stage changes.)
 template <int BM, int BN, int NW, int FA, int FB, bool VM>
 struct MxRing {
   static constexpr int kThreads = NW * 64;
@@ -150,7 +150,15 @@ struct MxRing {
   static constexpr int kInstrA = BM / 8 / NW, kInstrB = BN / 8 / NW;  // transfers (8 rows each) of a stage
   static_assert((BM + BN) / 64 == NW, "one scale transfer (64 rows) a wave");
   static_assert(kMI >= 4 && kMI % 2 == 0 && kNI == 4, "the fragment schedule below");
-  static constexpr int kN = kMI * kNI, kLastP = kN - kNI, kPrioP = kLastP / 2;
+  static constexpr int kN = kMI * kNI, kLastP = kN - kNI;
+  static constexpr bool kDeep = FA == MX_E2M1 && FB == MX_E2M1;
+  static constexpr int kRA = kDeep ? 4 : 2;
+  static constexpr bool kDB = kDeep;
+  // the barrier's position: past the last read of the step's own fragments (and, without kDB,
+  // where the next step's fragments find free registers)
+  static constexpr int kBarP = !kDB ? kLastP : ((kMI - kRA) * kNI > kNI ? (kMI - kRA) * kNI : kNI);
+  static constexpr int kPrioP = (kBarP / 2 + 3) / 4 * 4;
+  static constexpr int kTailStep = (kN - kBarP) / 4;  // between the transfers after the barrier
   using A = MxFmt<FA>;
   using B = MxFmt<FB>;
 
@@ -234,48 +242,67 @@ struct MxRing {
   }
 
   struct Frags {
-    MxFrag<FA> a[2];
-    MxFrag<FB> b[kNI];
-    int sa[2], sb[kNI];
+    MxFrag<FA> a[kRA];
+    MxFrag<FB> b[kDB ? 2 : 1][kNI];
+    int sa[kRA], sb[kDB ? 2 : 1][kNI];
   };
+  static constexpr int bset(int t) { return kDB ? t & 1 : 0; }
   template <int T>
   static __device__ __forceinline__ void read_a(Frags& f, const GEP_LDS char* smem, const Lane& o, int r, int so) {
-    f.a[r & 1] = read<FA, T>(smem, kABytes, r, o.a0, o.a1);
-    f.sa[r & 1] = read_scale<T>(smem, o.sa + so, r);
+    f.a[r % kRA] = read<FA, T>(smem, kABytes, r, o.a0, o.a1);
+    f.sa[r % kRA] = read_scale<T>(smem, o.sa + so, r);
   }
   template <int T>
   static __device__ __forceinline__ void read_b(Frags& f, const GEP_LDS char* smem, const Lane& o, int c, int so) {
-    f.b[c] = read<FB, T>(smem, kBBytes, c, o.b0, o.b1);
-    f.sb[c] = read_scale<T>(smem, o.sb + so, c);
+    f.b[bset(T)][c] = read<FB, T>(smem, kBBytes, c, o.b0, o.b1);
+    f.sb[bset(T)][c] = read_scale<T>(smem, o.sb + so, c);
   }
 
   static constexpr bool bar(int t) { return A::k8 || B::k8 || (t & 1); }
-  // rows whose A fragments are read after position p (row 1 after the first MFMA)
-  static constexpr int row_after(int p) {
-    if (p == 0) return 1;
-    return ((p + 1) % kNI == 0 && (p + 1) / kNI + 1 < kMI && (p + 1) / kNI >= 1) ? (p + 1) / kNI + 1 : 0;
+  // What is read after position p: the A fragment of this step's row a_after (the rows past the ring's
+  // first kRA - 1), of the next step's row na_after, the next step's B fragment nb_after (-1: none).
+  static constexpr int a_after(int p) {
+    for (int r = kRA - 1; r < kMI; ++r)
+      if ((r == kRA - 1 ? 0 : (r - kRA + 1) * kNI - 1) == p) return r;
+    return -1;
   }
-  static constexpr int reads(int t, int p) {  // LDS reads after position p
-    return (row_after(p) ? (A::k8 ? 3 : 2) : 0) + (p == kLastP ? (A::k8 ? 3 : 2) : 0) + (p >= kLastP ? (B::k8 ? 3 : 2) : 0);
+  static constexpr int na_after(int p) {
+    for (int r = 0; r < kRA - 1; ++r) {
+      const int free = (kMI - kRA + r + 1) * kNI - 1;
+      if ((free > kBarP ? free : kBarP) == p) return r;
+    }
+    return -1;
+  }
+  static constexpr int nb_after(int p) {
+    for (int c = 0; c < kNI; ++c)
+      if ((kDB ? kBarP + 2 * c : kLastP + c) == p) return c;
+    return -1;
+  }
+  static_assert(kDB || kRA == 2, "a deeper ring reads the next step's rows before the last");
+  static constexpr int reads(int p) {  // LDS reads after position p
+    return (A::k8 ? 3 : 2) * ((a_after(p) >= 0) + (na_after(p) >= 0)) + (B::k8 ? 3 : 2) * (nb_after(p) >= 0);
   }
   // transfers after position p of step t: the second half of the next stage at the head (A at
-  // 0, 2, B at 4, 6; the next quad's scales at 8), the first half of the one after it in the last row
+  // 0, 2, B at 4, 6; the next quad's scales at 8), the first half of the one after it behind the
+  // barrier
   static constexpr bool head(bool k8, int t) { return k8 || !(t & 1); }
   static constexpr bool tail(bool k8, int t) { return k8 || (t & 1); }
+  static constexpr int tail_at(int p) {  // which of the four tail transfers (A, A, B, B), or -1
+    return p >= kBarP && (p - kBarP) % kTailStep == 0 ? (p - kBarP) / kTailStep : -1;
+  }
   static constexpr int transfers(int t, int p) {
     int n = 0;
     if (p < 4 && p % 2 == 0) n += head(A::k8, t);
     if (p >= 4 && p < 8 && p % 2 == 0) n += head(B::k8, t);
     if (p == 8 && t == 0) n += 1;
-    if (p >= kLastP && p < kLastP + 2) n += tail(A::k8, t);
-    if (p >= kLastP + 2) n += tail(B::k8, t);
+    if (tail_at(p) >= 0) n += tail_at(p) < 2 ? tail(A::k8, t) : tail(B::k8, t);
     return n;
   }
   template <int T, int P, int E>
   static __device__ __forceinline__ void sched() {
     if constexpr (P < E) {
       __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      if constexpr (reads(T, P) > 0) __builtin_amdgcn_sched_group_barrier(0x100, reads(T, P), 0);
+      if constexpr (reads(P) > 0) __builtin_amdgcn_sched_group_barrier(0x100, reads(P), 0);
       if constexpr (transfers(T, P) > 0) __builtin_amdgcn_sched_group_barrier(0x020, transfers(T, P), 0);
       sched<T, P + 1, E>();
     }
@@ -289,10 +316,10 @@ struct MxRing {
       constexpr int NT = (T + 1) & 3;
       if constexpr (MM) {
         constexpr int r = P / kNI, c = P % kNI;
-        acc[r][c] = mx_mma<FA, FB>(f.b[c], f.a[r & 1], acc[r][c], f.sb[c], f.sa[r & 1]);
-        if constexpr (row_after(P) > 0) read_a<T>(f, smem, o, row_after(P), so);
-        if constexpr (P == kLastP) read_a<NT>(f, smem, o, 0, so_next);
-        if constexpr (P >= kLastP) read_b<NT>(f, smem, o, P - kLastP, so_next);
+        acc[r][c] = mx_mma<FA, FB>(f.b[bset(T)][c], f.a[r % kRA], acc[r][c], f.sb[bset(T)][c], f.sa[r % kRA]);
+        if constexpr (a_after(P) >= 0) read_a<T>(f, smem, o, a_after(P), so);
+        if constexpr (na_after(P) >= 0) read_a<NT>(f, smem, o, na_after(P), so_next);
+        if constexpr (nb_after(P) >= 0) read_b<NT>(f, smem, o, nb_after(P), so_next);
       }
       const int step = q * 4 + T;
       // (slots: steps of an E4M3 operand, pairs of an E2M1 one, 128 bytes each)
@@ -307,15 +334,14 @@ struct MxRing {
         dma<kInstrB / 2 + u * (kInstrB / 4), kInstrB / 2 + (u + 1) * (kInstrB / 4)>(s.lb, s.b, slot * 128, smem + kBOff + st * kBBytes, wave);
       }
       if constexpr (P == 8 && T == 0) dma_scales(s, q + 1, smem, (q + 1) & 1, wave);
-      if constexpr (P >= kLastP && P < kLastP + 2 && tail(A::k8, T)) {
-        constexpr int u = P - kLastP;
+      constexpr int u = tail_at(P);
+      if constexpr (u >= 0 && u < 2 && tail(A::k8, T)) {
         const int slot = (A::k8 ? step : step >> 1) + 2;
         dma<u * (kInstrA / 4), (u + 1) * (kInstrA / 4)>(s.la, s.a, slot * 128, smem + stage<FA>(T) * kABytes, wave);
       }
-      if constexpr (P >= kLastP + 2 && tail(B::k8, T)) {
-        constexpr int u = P - kLastP - 2;
+      if constexpr (u >= 2 && tail(B::k8, T)) {
         const int slot = (B::k8 ? step : step >> 1) + 2;
-        dma<u * (kInstrB / 4), (u + 1) * (kInstrB / 4)>(s.lb, s.b, slot * 128, smem + kBOff + stage<FB>(T) * kBBytes, wave);
+        dma<(u - 2) * (kInstrB / 4), (u - 1) * (kInstrB / 4)>(s.lb, s.b, slot * 128, smem + kBOff + stage<FB>(T) * kBBytes, wave);
       }
       positions<MM, T, P + 1, E>(acc, f, smem, o, s, q, so, so_next, wave);
     }
@@ -338,16 +364,16 @@ struct MxRing {
       __builtin_amdgcn_sched_barrier(0);
       __builtin_amdgcn_s_setprio(0);
       __builtin_amdgcn_sched_barrier(0);
-      positions<true, T, kPrioP, kLastP>(acc, f, smem, o, s, q, so, so_next, wave);
-      sched<T, kPrioP, kLastP>();
+      positions<true, T, kPrioP, kBarP>(acc, f, smem, o, s, q, so, so_next, wave);
+      sched<T, kPrioP, kBarP>();
       if constexpr (bar(T)) dma_barrier();
-      positions<true, T, kLastP, kN>(acc, f, smem, o, s, q, so, so_next, wave);
-      sched<T, kLastP, kN>();
+      positions<true, T, kBarP, kN>(acc, f, smem, o, s, q, so, so_next, wave);
+      sched<T, kBarP, kN>();
       __builtin_amdgcn_sched_barrier(0);
     } else {
-      positions<false, T, 0, kLastP>(acc, f, smem, o, s, q, so, so_next, wave);
+      positions<false, T, 0, kBarP>(acc, f, smem, o, s, q, so, so_next, wave);
       if constexpr (bar(T)) dma_barrier();
-      positions<false, T, kLastP, kN>(acc, f, smem, o, s, q, so, so_next, wave);
+      positions<false, T, kBarP, kN>(acc, f, smem, o, s, q, so, so_next, wave);
     }
   }
   template <bool MM>
@@ -524,7 +550,8 @@ struct MxRing {
           __builtin_amdgcn_s_setprio(0);
           mainloop<false>(acc, f, smem, o, s, mp.steps, wave);
         } else {
-          read_a<0>(f, smem, o, 0, 0);
+#pragma unroll
+          for (int r = 0; r < kRA - 1; ++r) read_a<0>(f, smem, o, r, 0);
 #pragma unroll
           for (int c = 0; c < kNI; ++c) read_b<0>(f, smem, o, c, 0);
           mainloop<true>(acc, f, smem, o, s, mp.steps, wave);

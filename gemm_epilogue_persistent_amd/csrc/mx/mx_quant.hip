@@ -25,7 +25,7 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(const T* x, int
   fd_divmod(fd_cpr, i, rr, ch);
   const int64_t r = r0 + rr;
   float v[8];
-  load8_tail(x + r * ldx, (int)ch * 8, cols, v);
+  load8(x + r * ldx, (int)ch * 8, cols, v);
   mx_store_chunk<FMT>(v, r, (int)ch, nb, nsb, codes, scales);
 }
 
@@ -35,25 +35,31 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(const T* x, int
 // four blocks of a column, so that a quad writes 128 (E4M3) or 64 (E2M1) contiguous bytes of an
 // output row. Rows of LDS are 64 dwords; each block starts 16 dwords further, so the 16 dword
 // columns x 4 blocks that a wave reads lie in 64 distinct banks.
-constexpr int kTR = 128, kTB = kTR / kMxBlock;  // rows and blocks of a tile
-constexpr int kRowDw = 64, kSkewDw = 16;
-constexpr int kTileDw = kTR * kRowDw + kTB * kSkewDw;
-
-template <typename T, int FMT>
-__global__ __launch_bounds__(kThreads) void quantize_cols_kernel(const T* x, int64_t ldx, int rows, int cols, int nb,
-                                                                 int nsb, uint8_t* codes, uint8_t* scales) {
+template <typename T, int FMT, int kTB, int kRowDw>
+__global__ __launch_bounds__(kTB* kRowDw) void quantize_cols_kernel(const T* x, int64_t ldx, int rows, int cols, int nb,
+                                                                 int nsb, uint32_t tiles, FastDiv fd_ty, uint8_t* codes,
+                                                                 uint8_t* scales) {
   constexpr int kVec = 16 / (int)sizeof(T);     // elements of a 16-byte load
-  constexpr int kCols = 256 / (int)sizeof(T);   // columns of a tile
+  constexpr int kCols = kRowDw * 4 / (int)sizeof(T);   // columns of a tile
+  constexpr int kTR = kTB * kMxBlock, kSkewDw = 64 / kTB;
+  constexpr int kTileDw = kTR * kRowDw + kTB * kSkewDw;
+  constexpr int kLR = kRowDw / 4;                // lanes of a row
+  constexpr int kRP = kTB * kRowDw / kLR;       // rows of a pass
   constexpr int kPer = 4 / (int)sizeof(T);      // columns of a dword
   __shared__ __attribute__((aligned(16))) uint32_t tile[kTileDw];
   const int tid = threadIdx.x;
-  const int r0 = blockIdx.y * kTR, c0 = blockIdx.x * kCols;
-  // 16 lanes a row, 16 rows a pass
-  uint4 in[kTR / 16];
-  const int lc = c0 + (tid & 15) * kVec;
+  // Workgroups go to the eight XCDs in turn; each XCD takes a run of tiles down the rows, so that
+  // the lines of the output that two tiles share are put together in one L2.
+  const uint32_t per = (tiles + 7) >> 3, tile_id = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+  if (tile_id >= tiles) return;
+  uint32_t bx, by;
+  fd_divmod(fd_ty, tile_id, bx, by);
+  const int r0 = (int)by * kTR, c0 = (int)bx * kCols;
+  uint4 in[kTR / kRP];
+  const int lc = c0 + (tid % kLR) * kVec;
 #pragma unroll
-  for (int q = 0; q < kTR / 16; ++q) {
-    const int r = r0 + q * 16 + (tid >> 4);
+  for (int q = 0; q < kTR / kRP; ++q) {
+    const int r = r0 + q * kRP + tid / kLR;
     in[q] = uint4{0, 0, 0, 0};
     if (r < rows) {
       const T* p = x + (int64_t)r * ldx + lc;
@@ -69,13 +75,13 @@ __global__ __launch_bounds__(kThreads) void quantize_cols_kernel(const T* x, int
     }
   }
 #pragma unroll
-  for (int q = 0; q < kTR / 16; ++q) {
-    const int r = q * 16 + (tid >> 4);
-    *(uint4*)(tile + r * kRowDw + (r / kMxBlock) * kSkewDw + (tid & 15) * 4) = in[q];
+  for (int q = 0; q < kTR / kRP; ++q) {
+    const int r = q * kRP + tid / kLR;
+    *(uint4*)(tile + r * kRowDw + (r / kMxBlock) * kSkewDw + (tid % kLR) * 4) = in[q];
   }
   __syncthreads();
-  const int blk = tid & 3, dc = tid >> 2;  // block of the tile, dword column
-  const int b = blockIdx.y * kTB + blk;
+  const int blk = tid % kTB, dc = tid / kTB;  // block of the tile, dword column
+  const int b = (int)by * kTB + blk;
   const uint32_t* col = tile + blk * (kMxBlock * kRowDw + kSkewDw) + dc;
   uint32_t w[kMxBlock];
 #pragma unroll
@@ -156,7 +162,7 @@ __global__ __launch_bounds__(kThreads) void dequantize_kernel(const uint8_t* cod
 #pragma unroll
   for (int e = 0; e < 8; ++e)
     v[e] = s == 255 ? __uint_as_float(0x7FC00000u) : __builtin_ldexpf(p[e >> 1][e & 1], s - 127);
-  store8_tail(out + r * ldo, (int)ch * 8, k, v);
+  store_chunk(out + r * ldo, (int)ch * 8, k, pack<T>(v));
 }
 
 // Launch `f(r0, n)` over ranges of rows whose chunks number below 2^31.
@@ -212,12 +218,13 @@ gemm_status mx_quantize(int32_t rows, int32_t cols, const void* x, int32_t x_typ
   with_type(x_type, [&](auto* t) {
     using T = std::remove_pointer_t<decltype(t)>;
     if (transpose) {
-      const int tc = 256 / (int)sizeof(T);
-      // (the grid's y extent is 16 bits: tall matrices go in ranges of whole scale tiles)
-      const int gy = (rows + kTR - 1) / kTR, gx = (cols + tc - 1) / tc;
-      if (gy > 65535) { st = fail(GEMM_ERR_UNSUPPORTED, "mx_quantize: more than 2^23 rows with transpose"); return; }
-      if (format == MX_E2M1) quantize_cols_kernel<T, MX_E2M1><<<dim3(gx, gy), kThreads, 0, s>>>((const T*)x, ldx, rows, cols, nb, nsb, qc, qs);
-      else quantize_cols_kernel<T, MX_E4M3><<<dim3(gx, gy), kThreads, 0, s>>>((const T*)x, ldx, rows, cols, nb, nsb, qc, qs);
+      constexpr int kTB = 4, kRowDw = 64, tc = kRowDw * 4 / (int)sizeof(T);
+      const int64_t ty = (nb + kTB - 1) / kTB, tx = ((int64_t)cols + tc - 1) / tc;
+      if (ty * tx > 0x7FFFFF00) { st = fail(GEMM_ERR_UNSUPPORTED, "mx_quantize: more than 2^31 tiles"); return; }
+      const uint32_t tiles = (uint32_t)(ty * tx), grid = (tiles + 7) / 8 * 8;
+      const FastDiv fd = make_fastdiv((uint32_t)ty);
+      if (format == MX_E2M1) quantize_cols_kernel<T, MX_E2M1, kTB, kRowDw><<<grid, kTB * kRowDw, 0, s>>>((const T*)x, ldx, rows, cols, nb, nsb, tiles, fd, qc, qs);
+      else quantize_cols_kernel<T, MX_E4M3, kTB, kRowDw><<<grid, kTB * kRowDw, 0, s>>>((const T*)x, ldx, rows, cols, nb, nsb, tiles, fd, qc, qs);
     } else {
       const uint32_t cpr = (uint32_t)nb * 4;
       row_ranges(rows, cpr, [&](int64_t r0, uint32_t n) {

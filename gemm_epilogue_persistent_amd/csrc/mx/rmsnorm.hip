@@ -48,13 +48,9 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
   return v;
 }
 
-// The type's rounding of h, so that the statistics see the stored values.
-template <typename T>
-__device__ __forceinline__ float round_to(float v) { return (float)(T)v; }
-
 template <typename T, int FMT>
 __device__ __forceinline__ void norm_store(const NormParams& p, int64_t row, int ch, const float y[8]) {
-  if (p.y) store8_tail((T*)p.y + row * p.ldy, ch * 8, p.cols, y);
+  if (p.y) store_chunk((T*)p.y + row * p.ldy, ch * 8, p.cols, pack<T>(y));
   if (p.codes && ch < p.nb * 4) mx_store_chunk<FMT>(y, row, ch, p.nb, p.nsb, p.codes, p.scales);
 }
 template <typename T>
@@ -63,47 +59,63 @@ __device__ __forceinline__ void norm_out(const NormParams& p, int64_t row, int c
   else norm_store<T, MX_E4M3>(p, row, ch, y);
 }
 
+// h is kept in its own type (its rounded value is exact there): half the registers of fp32 for
+// 16-bit rows.
 template <typename T, int TPR, int CH>
-__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_kernel(const NormParams p) {
-  constexpr int kRows = TPR < 256 ? 256 / TPR : 1;  // rows of a workgroup
+__global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void rmsnorm_kernel(const NormParams p) {
+  constexpr int kRows = TPR == 64 ? 4 : 1;  // rows of a workgroup
   __shared__ float red[TPR > 64 ? TPR / 64 : 1];
   const int t = threadIdx.x % TPR;
   const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR;
   if (TPR == 64 && row >= p.rows) return;  // (a whole wave)
   const T* x = (const T*)p.x + row * p.ldx;
-  float h[CH][8];
+  Chunk<T> h[CH];
   float ss = 0.f;
 #pragma unroll
-  for (int j = 0; j < CH; ++j) load8_tail(x, (t + j * TPR) * 8, p.cols, h[j]);
+  for (int j = 0; j < CH; ++j) h[j] = load_chunk(x, (t + j * TPR) * 8, p.cols);
   if (p.r) {
     const T* r = (const T*)p.r + row * p.ldr;
-    float rv[CH][8];
+    Chunk<T> rc[CH];
 #pragma unroll
-    for (int j = 0; j < CH; ++j) load8_tail(r, (t + j * TPR) * 8, p.cols, rv[j]);
+    for (int j = 0; j < CH; ++j) rc[j] = load_chunk(r, (t + j * TPR) * 8, p.cols);
 #pragma unroll
-    for (int j = 0; j < CH; ++j)
+    for (int j = 0; j < CH; ++j) {
+      const int c = (t + j * TPR) * 8;
+      float a[8], b[8];
+      settle(h[j], c, p.cols);
+      settle(rc[j], c, p.cols);
+      unpack(h[j], a);
+      unpack(rc[j], b);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) h[j][e] = round_to<T>(h[j][e] + rv[j][e]);
-    if (p.h) {
+      for (int e = 0; e < 8; ++e) a[e] += b[e];
+      h[j] = pack<T>(a);
+      if (p.h) store_chunk((T*)p.h + row * p.ldh, c, p.cols, h[j]);
+      unpack(h[j], a);
 #pragma unroll
-      for (int j = 0; j < CH; ++j) store8_tail((T*)p.h + row * p.ldh, (t + j * TPR) * 8, p.cols, h[j]);
+      for (int e = 0; e < 8; ++e) ss = fmaf(a[e], a[e], ss);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < CH; ++j) {
+      float a[8];
+      settle(h[j], (t + j * TPR) * 8, p.cols);
+      unpack(h[j], a);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss = fmaf(a[e], a[e], ss);
     }
   }
-#pragma unroll
-  for (int j = 0; j < CH; ++j)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) ss = fmaf(h[j][e], h[j][e], ss);
   const float rstd = 1.f / sqrtf(row_sum<TPR>(ss, red) * p.inv_cols + p.eps);
   if (p.rstd && t == 0) p.rstd[row] = rstd;
-  if (!p.y && !p.codes) return;
 #pragma unroll
   for (int j = 0; j < CH; ++j) {
     const int ch = t + j * TPR;
-    float w[8], y[8];
-    load8_tail((const T*)p.w, ch * 8, p.cols, w);
+    float a[8], w[8];
+    forget(h[j]);
+    unpack(h[j], a);
+    load8((const T*)p.w, ch * 8, p.cols, w);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = h[j][e] * rstd * w[e];
-    norm_out<T>(p, row, ch, y);
+    for (int e = 0; e < 8; ++e) a[e] = a[e] * rstd * w[e];
+    norm_out<T>(p, row, ch, a);
   }
 }
 
@@ -116,12 +128,13 @@ __global__ __launch_bounds__(1024) void rmsnorm_long_kernel(const NormParams p) 
   const T* r = p.r ? (const T*)p.r + row * p.ldr : nullptr;
   const int n = p.nb * 4;
   auto load_h = [&](int ch, float v[8]) {
-    load8_tail(x, ch * 8, p.cols, v);
+    load8(x, ch * 8, p.cols, v);
     if (r) {
       float q[8];
-      load8_tail(r, ch * 8, p.cols, q);
+      load8(r, ch * 8, p.cols, q);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = round_to<T>(v[e] + q[e]);
+      for (int e = 0; e < 8; ++e) v[e] += q[e];
+      unpack(pack<T>(v), v);
     }
   };
   float ss = 0.f;
@@ -137,8 +150,8 @@ __global__ __launch_bounds__(1024) void rmsnorm_long_kernel(const NormParams p) 
     float v[8], w[8], y[8];
     load_h(ch, v);
     // (h may be x or the residual: every element is read again by the thread that replaces it)
-    if (r && p.h) store8_tail((T*)p.h + row * p.ldh, ch * 8, p.cols, v);
-    load8_tail((const T*)p.w, ch * 8, p.cols, w);
+    if (r && p.h) store_chunk((T*)p.h + row * p.ldh, ch * 8, p.cols, pack<T>(v));
+    load8((const T*)p.w, ch * 8, p.cols, w);
 #pragma unroll
     for (int e = 0; e < 8; ++e) y[e] = v[e] * rstd * w[e];
     norm_out<T>(p, row, ch, y);
@@ -162,50 +175,72 @@ template <typename T, int TPR, int CH>
 __global__ __launch_bounds__(TPR) void rmsnorm_grad_kernel(const NormGradParams p) {
   __shared__ float red[TPR > 64 ? TPR / 64 : 1];
   const int t = threadIdx.x;
-  float dw[CH][8], w[CH][8];
+  float dw[CH][8];
+  Chunk<T> w[CH];
 #pragma unroll
   for (int j = 0; j < CH; ++j) {
-    load8_tail((const T*)p.w, (t + j * TPR) * 8, p.cols, w[j]);
+    const int c = (t + j * TPR) * 8;
+    w[j] = load_chunk((const T*)p.w, c, p.cols);
+    settle(w[j], c, p.cols);
 #pragma unroll
     for (int e = 0; e < 8; ++e) dw[j][e] = 0.f;
   }
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
     const float rstd = p.rstd[row];
-    float n[CH][8], dy[CH][8];
+    Chunk<T> hc[CH], dyc[CH], gc[CH];
+#pragma unroll
+    for (int j = 0; j < CH; ++j) {
+      hc[j] = load_chunk((const T*)p.h + row * p.ldh, (t + j * TPR) * 8, p.cols);
+      dyc[j] = load_chunk((const T*)p.dy + row * p.lddy, (t + j * TPR) * 8, p.cols);
+    }
+    if (p.dres) {
+#pragma unroll
+      for (int j = 0; j < CH; ++j) gc[j] = load_chunk((const T*)p.dres + row * p.lddres, (t + j * TPR) * 8, p.cols);
+    }
     float dot = 0.f;
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
-      load8_tail((const T*)p.h + row * p.ldh, (t + j * TPR) * 8, p.cols, n[j]);
-      load8_tail((const T*)p.dy + row * p.lddy, (t + j * TPR) * 8, p.cols, dy[j]);
-    }
-#pragma unroll
-    for (int j = 0; j < CH; ++j)
+      const int c = (t + j * TPR) * 8;
+      float n[8], dy[8], ww[8];
+      settle(hc[j], c, p.cols);
+      settle(dyc[j], c, p.cols);
+      forget(w[j]);
+      unpack(hc[j], n);
+      unpack(dyc[j], dy);
+      unpack(w[j], ww);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        n[j][e] *= rstd;
-        const float dyn = dy[j][e] * n[j][e];
+        const float dyn = dy[e] * (n[e] * rstd);
         dw[j][e] += dyn;
-        dot = fmaf(dyn, w[j][e], dot);
+        dot = fmaf(dyn, ww[e], dot);
       }
+    }
     const float m = row_sum<TPR>(dot, red) * p.inv_cols;
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
       const int c = (t + j * TPR) * 8;
-      float g[8];
+      float n[8], dy[8], ww[8], g[8];
+      forget(hc[j]);
+      forget(dyc[j]);
+      forget(w[j]);
+      unpack(hc[j], n);
+      unpack(dyc[j], dy);
+      unpack(w[j], ww);
       if (p.dres) {
-        load8_tail((const T*)p.dres + row * p.lddres, c, p.cols, g);
+        settle(gc[j], c, p.cols);
+        unpack(gc[j], g);
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) g[e] = 0.f;
       }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) g[e] = fmaf(rstd, dy[j][e] * w[j][e] - n[j][e] * m, g[e]);
-      store8_tail((T*)p.dx + row * p.lddx, c, p.cols, g);
+      for (int e = 0; e < 8; ++e) g[e] = fmaf(rstd, dy[e] * ww[e] - n[e] * rstd * m, g[e]);
+      store_chunk((T*)p.dx + row * p.lddx, c, p.cols, pack<T>(g));
     }
   }
   float* part = p.part + (int64_t)blockIdx.x * p.cols;
 #pragma unroll
-  for (int j = 0; j < CH; ++j) store8_tail(part, (t + j * TPR) * 8, p.cols, dw[j]);
+  for (int j = 0; j < CH; ++j) store_chunk(part, (t + j * TPR) * 8, p.cols, pack<float>(dw[j]));
 }
 
 // Rows of any length: each row is read twice and the column sums live in the workgroup's row of
@@ -222,14 +257,14 @@ __global__ __launch_bounds__(1024) void rmsnorm_grad_long_kernel(const NormGradP
     float dot = 0.f;
     for (int ch = threadIdx.x; ch < n8; ch += 1024) {
       float n[8], dy[8], w[8], s[8];
-      load8_tail(h, ch * 8, p.cols, n);
-      load8_tail(dyp, ch * 8, p.cols, dy);
-      load8_tail((const T*)p.w, ch * 8, p.cols, w);
+      load8(h, ch * 8, p.cols, n);
+      load8(dyp, ch * 8, p.cols, dy);
+      load8((const T*)p.w, ch * 8, p.cols, w);
       if (row == blockIdx.x) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) s[e] = 0.f;
       } else {
-        load8_tail(part, ch * 8, p.cols, s);
+        load8(part, ch * 8, p.cols, s);
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -237,42 +272,42 @@ __global__ __launch_bounds__(1024) void rmsnorm_grad_long_kernel(const NormGradP
         s[e] += dyn;
         dot = fmaf(dyn, w[e], dot);
       }
-      store8_tail(part, ch * 8, p.cols, s);
+      store_chunk(part, ch * 8, p.cols, pack<float>(s));
     }
     const float m = row_sum<1024>(dot, red) * p.inv_cols;
     for (int ch = threadIdx.x; ch < n8; ch += 1024) {
       float n[8], dy[8], w[8], g[8];
-      load8_tail(h, ch * 8, p.cols, n);
-      load8_tail(dyp, ch * 8, p.cols, dy);
-      load8_tail((const T*)p.w, ch * 8, p.cols, w);
+      load8(h, ch * 8, p.cols, n);
+      load8(dyp, ch * 8, p.cols, dy);
+      load8((const T*)p.w, ch * 8, p.cols, w);
       if (p.dres) {
-        load8_tail((const T*)p.dres + row * p.lddres, ch * 8, p.cols, g);
+        load8((const T*)p.dres + row * p.lddres, ch * 8, p.cols, g);
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) g[e] = 0.f;
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) g[e] = fmaf(rstd, dy[e] * w[e] - n[e] * rstd * m, g[e]);
-      store8_tail((T*)p.dx + row * p.lddx, ch * 8, p.cols, g);
+      store_chunk((T*)p.dx + row * p.lddx, ch * 8, p.cols, pack<T>(g));
     }
   }
 }
 
-// dw = sum of `n` rows of partial sums: 64 columns a workgroup, 16 threads a row strip.
-constexpr int kSumCols = 64, kSumRows = 16;
+// dw = sum of `n` rows of partial sums: 16 columns a workgroup, 64 threads a column.
+constexpr int kSumCols = 16, kSumRows = 64;
 __global__ __launch_bounds__(kSumCols* kSumRows) void column_sum_kernel(const float* part, int n, int cols, float* dw) {
   __shared__ float s[kSumRows][kSumCols];
   const int c = blockIdx.x * kSumCols + threadIdx.x % kSumCols, g = threadIdx.x / kSumCols;
   float a = 0.f;
   if (c < cols) {
-#pragma unroll 4
+#pragma unroll 8
     for (int i = g; i < n; i += kSumRows) a += part[(int64_t)i * cols + c];
   }
   s[g][threadIdx.x % kSumCols] = a;
   __syncthreads();
   if (g == 0 && c < cols) {
     a = 0.f;
-#pragma unroll
+#pragma unroll 8
     for (int i = 0; i < kSumRows; ++i) a += s[i][threadIdx.x];
     dw[c] = a;
   }
@@ -280,51 +315,49 @@ __global__ __launch_bounds__(kSumCols* kSumRows) void column_sum_kernel(const fl
 
 int cdiv(int a, int b) { return (a + b - 1) / b; }
 
-template <typename T>
-void launch_norm(const NormParams& p, hipStream_t s) {
-  // Threads of a row: a wave up to 4096 columns when there are rows enough to fill the card
-  // with waves, else a workgroup.
-  const int ch = p.nb * 4;
-  auto go = [&](auto tpr, auto n) {
-    constexpr int TPR = decltype(tpr)::value, CH = decltype(n)::value;
-    constexpr int rows = TPR < 256 ? 256 / TPR : 1;
-    rmsnorm_kernel<T, TPR, CH><<<cdiv(p.rows, rows), TPR < 256 ? 256 : TPR, 0, s>>>(p);
-  };
-#define GO(TPR, CH) go(std::integral_constant<int, TPR>{}, std::integral_constant<int, CH>{})
-  if (ch <= 64) GO(64, 1);
-  else if (ch <= 128 && p.rows >= 1024) GO(64, 2);
-  else if (ch <= 256 && p.rows >= 1024) GO(64, 4);
-  else if (ch <= 512 && p.rows >= 1024) GO(64, 8);
-  else if (ch <= 256) GO(256, 1);
-  else if (ch <= 512) GO(256, 2);
-  else if (ch <= 1024) GO(256, 4);
-  else if (ch <= 2048) GO(1024, 2);
-  else if (ch <= 4096) GO(1024, 4);
-  else rmsnorm_long_kernel<T><<<p.rows, 1024, 0, s>>>(p);
+// Threads of a row and chunks of a thread. Two chunks a thread wherever a row has them: on
+// 16768 x 4096 bf16 (residual, e4m3 output) 256 threads x 2 chunks run at 5.3 TB/s, 512 x 1 at
+// 4.7, one wave x 8 (too many registers for enough waves) at 3.6.
+template <typename F>
+bool with_shape(int chunks, F&& f) {
+#define GO(TPR, CH) f(std::integral_constant<int, TPR>{}, std::integral_constant<int, CH>{})
+  if (chunks <= 64) GO(64, 1);
+  else if (chunks <= 128) GO(64, 2);
+  else if (chunks <= 256) GO(128, 2);
+  else if (chunks <= 512) GO(256, 2);
+  else if (chunks <= 1024) GO(512, 2);
+  else if (chunks <= 2048) GO(1024, 2);
+  else return false;
 #undef GO
+  return true;
 }
 
-// Rows of partial sums: enough workgroups to fill the card, at most 16 MB of sums up to 16384
-// columns.
+template <typename T>
+void launch_norm(const NormParams& p, hipStream_t s) {
+  const bool done = with_shape(p.nb * 4, [&](auto tpr, auto ch) {
+    constexpr int TPR = decltype(tpr)::value, rows = TPR == 64 ? 4 : 1;
+    rmsnorm_kernel<T, TPR, decltype(ch)::value><<<cdiv(p.rows, rows), TPR * rows, 0, s>>>(p);
+  });
+  if (!done) rmsnorm_long_kernel<T><<<p.rows, 1024, 0, s>>>(p);
+}
+
+// Rows of partial sums: the workgroups that the card holds at once (16 waves a compute unit;
+// 8192 x 8192 bf16: 512 workgroups of 8 waves 106 us, 768 129 us, 256 163 us), at most 16 MB of
+// sums up to 16384 columns.
 int grad_parts(int rows, int cols) {
-  int n = cols > 0 ? (1 << 22) / cols : 2048;
-  n = n < 256 ? 256 : (n > 2048 ? 2048 : n);
+  int n = 256;
+  with_shape(cdiv(cols, 8), [&](auto tpr, auto) { n = 256 * 1024 / decltype(tpr)::value; });
+  n = n < 2048 ? n : 2048;
   return rows < n ? rows : n;
 }
 
 template <typename T>
 void launch_grad(const NormGradParams& p, int parts, hipStream_t s) {
-  const int ch = cdiv(p.cols, 8);
-#define GO(TPR, CH) rmsnorm_grad_kernel<T, TPR, CH><<<parts, TPR, 0, s>>>(p)
-  if (ch <= 64) GO(64, 1);
-  else if (ch <= 128) GO(64, 2);
-  else if (ch <= 256) GO(256, 1);
-  else if (ch <= 512) GO(256, 2);
-  else if (ch <= 1024) GO(256, 4);
-  else if (ch <= 2048) GO(1024, 2);
-  else if (ch <= 4096) GO(1024, 4);
-  else rmsnorm_grad_long_kernel<T><<<parts, 1024, 0, s>>>(p);
-#undef GO
+  const bool done = with_shape(cdiv(p.cols, 8), [&](auto tpr, auto ch) {
+    constexpr int TPR = decltype(tpr)::value;
+    rmsnorm_grad_kernel<T, TPR, decltype(ch)::value><<<parts, TPR, 0, s>>>(p);
+  });
+  if (!done) rmsnorm_grad_long_kernel<T><<<parts, 1024, 0, s>>>(p);
 }
 
 int type_bytes(int32_t t) { return t == GEMM_DT_F32 ? 4 : ((t == GEMM_DT_F16 || t == GEMM_DT_BF16) ? 2 : 0); }

@@ -28,36 +28,46 @@ def _cdiv(a, b):
     return -(-a // b)
 
 
-def _launch(device, stream, call):
-    """call(stream pointer) with `device` current, on `stream` (default: the device's current
-    one); raises what it reports."""
-    if device.index is not None and device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            return _launch(device, stream, call)
-    s = torch.cuda.current_stream() if stream is None else stream
-    _abi.check(call(s.cuda_stream))
+# the current stream's pointer by device index (torch.cuda.current_stream builds an object for it,
+# which takes as long as a launch)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _launch(device, stream, function, *args):
+    """function(*args, stream pointer) with `device` current, on `stream` (default: the device's
+    current one); raises what it reports."""
+    index = device.index
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(index):
+            return _launch(device, stream, function, *args)
+    status = function(*args, _raw_stream(index) if stream is None else stream.cuda_stream)
+    if status:
+        _abi.check(status)
 
 
 def _matrix(name, t, dtypes, shape=None, device=None):
     """Checks of a matrix argument on the GPU whose rows are contiguous; its row stride."""
-    if t.dim() != 2 or not t.is_cuda:
+    have = t.shape
+    if len(have) != 2 or not t.is_cuda:
         raise ValueError(f"{name}: a matrix on the GPU expected")
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: unsupported dtype {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if shape is not None and have != shape:
+        raise ValueError(f"{name} has shape {tuple(have)}, expected {tuple(shape)}")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    rows, cols = t.shape
+    rows, cols = have
     if rows == 0 or cols == 0:
         return cols
-    if cols > 1 and t.stride(1) != 1:
+    ld, step = t.stride()
+    if cols > 1 and step != 1:
         raise ValueError(f"{name}: rows must be contiguous")
     if rows == 1:
         return cols
-    if t.stride(0) < cols:
+    if ld < cols:
         raise ValueError(f"{name}: rows overlap")
-    return t.stride(0)
+    return ld
 
 
 class MxTensor:
@@ -137,11 +147,13 @@ def mx_quantize(x, fmt, out=None, transpose=False, stream=None):
     """The matrix x (16- or 32-bit floats, rows or columns contiguous) as MX codes: of x with
     blocks along its rows, or (transpose) of x^T with blocks along x's columns. Returns `out`
     (allocated if None). A block that holds a NaN or an infinity becomes NaN (scale 255)."""
-    if x.dim() != 2 or not x.is_cuda:
+    shape = x.shape
+    if len(shape) != 2 or not x.is_cuda:
         raise ValueError("x: a matrix on the GPU expected")
-    rows, cols = x.shape
-    shape = (cols, rows) if transpose else (rows, cols)
-    if x.stride(-1) != 1 and x.stride(0) == 1 and cols > 1:  # columns contiguous: x^T has contiguous rows
+    rows, cols = shape
+    if transpose:
+        shape = (cols, rows)
+    if x.stride(1) != 1 and x.stride(0) == 1 and cols > 1:  # columns contiguous: x^T has contiguous rows
         x, rows, cols, transpose = x.t(), cols, rows, not transpose
     ld = _matrix("x", x, _FLOAT_DT)
     if out is None:
@@ -149,11 +161,9 @@ def mx_quantize(x, fmt, out=None, transpose=False, stream=None):
     else:
         _plain_mx("out", out, x.device)
         if out.fmt != fmt or out.rows != shape[0] or out.k != shape[1]:
-            raise ValueError(f"out is {out.fmt} {tuple(out.shape)}, expected {fmt} {shape}")
-    lib = _abi.load()
-    _launch(x.device, stream, lambda s: lib.mx_quantize(
-        rows, cols, x.data_ptr(), _FLOAT_DT[x.dtype], ld, 1 if transpose else 0, MX_FORMAT[fmt],
-        out.codes.data_ptr(), out.scales.data_ptr(), s))
+            raise ValueError(f"out is {out.fmt} {tuple(out.shape)}, expected {fmt} {tuple(shape)}")
+    _launch(x.device, stream, _abi.load().mx_quantize, rows, cols, x.data_ptr(), _FLOAT_DT[x.dtype], ld,
+            1 if transpose else 0, MX_FORMAT[fmt], out.codes.data_ptr(), out.scales.data_ptr())
     return out
 
 
@@ -163,10 +173,8 @@ def mx_dequantize(q, out=None, dtype=torch.bfloat16, stream=None):
     if out is None:
         out = torch.empty((q.rows, q.k), dtype=dtype, device=q.device)
     ld = _matrix("out", out, _FLOAT_DT, (q.rows, q.k), q.device)
-    lib = _abi.load()
-    _launch(q.device, stream, lambda s: lib.mx_dequantize(
-        q.rows, q.k, MX_FORMAT[q.fmt], q.codes.data_ptr(), q.scales.data_ptr(), out.data_ptr(),
-        _FLOAT_DT[out.dtype], ld, s))
+    _launch(q.device, stream, _abi.load().mx_dequantize, q.rows, q.k, MX_FORMAT[q.fmt], q.codes.data_ptr(),
+            q.scales.data_ptr(), out.data_ptr(), _FLOAT_DT[out.dtype], ld)
     return out
 
 
@@ -248,7 +256,7 @@ class MxPlan:
             raise ValueError("the operands are not laid out as those this plan was made for")
         args = _abi.MxGemmArgs(a.codes.data_ptr(), a.scales.data_ptr(), b.codes.data_ptr(), b.scales.data_ptr(),
                                *(None if t is None else t.data_ptr() for t in (C, D, PostAct, cu_seqlens_m)))
-        _launch(self.device, stream, lambda s: self._lib.mx_gemm_run(self.handle, ctypes.byref(args), s))
+        _launch(self.device, stream, self._lib.mx_gemm_run, self.handle, ctypes.byref(args))
 
     def tile(self, num_cus=None):
         """The kernel this plan runs on a device with num_cus compute units."""

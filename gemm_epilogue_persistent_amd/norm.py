@@ -14,7 +14,7 @@ from .mx import _FLOAT_DT, _launch, _matrix, _plain_mx
 
 
 def _vector(name, t, n, dtype, device):
-    if t.dim() != 1 or t.shape[0] != n or t.dtype != dtype or t.device != device or (n > 1 and t.stride(0) != 1):
+    if t.shape != (n,) or t.dtype != dtype or t.device != device or (n > 1 and t.stride(0) != 1):
         raise ValueError(f"{name}: contiguous {dtype} vector of {n} on {device} expected")
     return t.data_ptr()
 
@@ -34,7 +34,7 @@ def rmsnorm(x, weight, residual=None, eps=1e-5, h=None, y=None, q=None, rstd=Non
     if x.dtype not in _FLOAT_DT:
         raise TypeError(f"x: unsupported dtype {x.dtype}")
     ldx = _matrix("x", x, types)
-    dev, shape = x.device, tuple(x.shape)
+    dev, shape = x.device, x.shape
     rows, cols = shape
     if y is None and q is None:
         y = torch.empty(shape, dtype=x.dtype, device=dev)
@@ -42,8 +42,8 @@ def rmsnorm(x, weight, residual=None, eps=1e-5, h=None, y=None, q=None, rstd=Non
         raise ValueError("h without a residual (it would be x)")
     if q is not None:
         _plain_mx("q", q, dev)
-        if (q.rows, q.k) != shape:
-            raise ValueError(f"q has shape {tuple(q.shape)}, expected {shape}")
+        if q.rows != rows or q.k != cols:
+            raise ValueError(f"q has shape {tuple(q.shape)}, expected {tuple(shape)}")
     a = _abi.RmsnormArgs(
         rows, cols, _FLOAT_DT[x.dtype], MX_FORMAT[q.fmt] if q is not None else 0, eps,
         x.data_ptr(), _ptr(residual), _vector("weight", weight, cols, x.dtype, dev), _ptr(h), _ptr(y),
@@ -52,8 +52,7 @@ def rmsnorm(x, weight, residual=None, eps=1e-5, h=None, y=None, q=None, rstd=Non
         ldx, _matrix("residual", residual, types, shape, dev) if residual is not None else 0,
         _matrix("h", h, types, shape, dev) if h is not None else 0,
         _matrix("y", y, types, shape, dev) if y is not None else 0)
-    lib = _abi.load()
-    _launch(dev, stream, lambda s: lib.rmsnorm_forward(ctypes.byref(a), s))
+    _launch(dev, stream, _abi.load().rmsnorm_forward, ctypes.byref(a))
     return y if y is not None else q
 
 
@@ -74,7 +73,7 @@ def rmsnorm_backward(dy, h, weight, rstd, dx=None, dw=None, dres=None, workspace
         raise TypeError(f"h: unsupported dtype {h.dtype}")
     types = (h.dtype,)
     ldh = _matrix("h", h, types)
-    dev, shape = h.device, tuple(h.shape)
+    dev, shape = h.device, h.shape
     rows, cols = shape
     if dx is None:
         dx = torch.empty(shape, dtype=h.dtype, device=dev)
@@ -90,6 +89,5 @@ def rmsnorm_backward(dy, h, weight, rstd, dx=None, dw=None, dres=None, workspace
         _vector("dw", dw, cols, torch.float32, dev), workspace.data_ptr(), workspace.numel(),
         _matrix("dy", dy, types, shape, dev), ldh,
         _matrix("dres", dres, types, shape, dev) if dres is not None else 0, _matrix("dx", dx, types, shape, dev))
-    lib = _abi.load()
-    _launch(dev, stream, lambda s: lib.rmsnorm_backward(ctypes.byref(a), s))
+    _launch(dev, stream, _abi.load().rmsnorm_backward, ctypes.byref(a))
     return dx, dw
