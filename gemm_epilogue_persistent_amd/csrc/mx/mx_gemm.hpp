@@ -154,6 +154,13 @@ struct MxRing {
   static constexpr bool kDeep = FA == MX_E2M1 && FB == MX_E2M1;
   static constexpr int kRA = kDeep ? 4 : 2;
   static constexpr bool kDB = kDeep;
+  // Two E2M1 operands: lane group g takes the K blocks c = {0, 6, 2, 4}[g] and c + 1 of the eight
+  // of a pair of steps, one in each step (A and B alike, so the same products meet). Its two
+  // scales are then neighbours. A ds_read_b128 serves 16 lanes at a time: rows 0-3 and 12-15 of
+  // one lane group with rows 4-11 of its neighbour, and so on; under kswz their chunks lie in
+  // distinct banks when the neighbours' blocks differ by 1, 6 or 7 (by 4: every read twice as
+  // long, counted).
+  static constexpr bool kPairScales = kDeep;
   // the barrier's position: past the last read of the step's own fragments (and, without kDB,
   // where the next step's fragments find free registers)
   static constexpr int kBarP = !kDB ? kLastP : ((kMI - kRA) * kNI > kNI ? (kMI - kRA) * kNI : kNI);
@@ -213,12 +220,14 @@ struct MxRing {
   static __device__ __forceinline__ Lane lane_offsets(int lane, int wm0, int wn0) {
     Lane o;
     const int ra = wm0 + (lane & 15), rb = wn0 + (lane & 15), g = lane >> 4;
-    o.a0 = ra * kRowBytes + ((g ^ kswz(ra)) << 4);
-    o.b0 = kBOff + rb * kRowBytes + ((g ^ kswz(rb)) << 4);
-    o.a1 = o.a0 ^ 64;
-    o.b1 = o.b0 ^ 64;
-    o.sa = kSOff + ra * 16 + g;
-    o.sb = kSOff + (BM + rb) * 16 + g;
+    // first K block (E2M1) or chunk (E4M3) of lane group g, and how far the other one is
+    const int c = kPairScales ? (0x4260 >> (4 * g)) & 7 : g, far = kPairScales ? 16 : 64;
+    o.a0 = ra * kRowBytes + ((c ^ kswz(ra)) << 4);
+    o.b0 = kBOff + rb * kRowBytes + ((c ^ kswz(rb)) << 4);
+    o.a1 = o.a0 ^ far;
+    o.b1 = o.b0 ^ far;
+    o.sa = kSOff + ra * 16 + c;
+    o.sb = kSOff + (BM + rb) * 16 + c;
     return o;
   }
   // Stage of an operand in step T of a quad.
@@ -236,26 +245,32 @@ struct MxRing {
     }
     return f;
   }
+  // kPairScales: the lane's two scales of a pair of steps in one read, every other step.
   template <int T>
-  static __device__ __forceinline__ int read_scale(const GEP_LDS char* smem, int o, int r) {
-    return *(const GEP_LDS uint8_t*)(smem + o + r * 256 + T * 4);
+  static __device__ __forceinline__ void read_scale(int& v, const GEP_LDS char* smem, int o, int r) {
+    if constexpr (kPairScales) {
+      if constexpr (T % 2 == 0) v = *(const GEP_LDS uint16_t*)(smem + o + r * 256 + T * 4);
+    } else {
+      v = *(const GEP_LDS uint8_t*)(smem + o + r * 256 + T * 4);
+    }
   }
 
   struct Frags {
     MxFrag<FA> a[kRA];
     MxFrag<FB> b[kDB ? 2 : 1][kNI];
-    int sa[kRA], sb[kDB ? 2 : 1][kNI];
+    int sa[kPairScales ? kMI : kRA], sb[kDB ? 2 : 1][kNI];
   };
+  static constexpr int sset(int t) { return !kDB ? 0 : (kPairScales ? (t >> 1) & 1 : t & 1); }
   static constexpr int bset(int t) { return kDB ? t & 1 : 0; }
   template <int T>
   static __device__ __forceinline__ void read_a(Frags& f, const GEP_LDS char* smem, const Lane& o, int r, int so) {
     f.a[r % kRA] = read<FA, T>(smem, kABytes, r, o.a0, o.a1);
-    f.sa[r % kRA] = read_scale<T>(smem, o.sa + so, r);
+    read_scale<T>(f.sa[kPairScales ? r : r % kRA], smem, o.sa + so, r);
   }
   template <int T>
   static __device__ __forceinline__ void read_b(Frags& f, const GEP_LDS char* smem, const Lane& o, int c, int so) {
     f.b[bset(T)][c] = read<FB, T>(smem, kBBytes, c, o.b0, o.b1);
-    f.sb[bset(T)][c] = read_scale<T>(smem, o.sb + so, c);
+    read_scale<T>(f.sb[sset(T)][c], smem, o.sb + so, c);
   }
 
   static constexpr bool bar(int t) { return A::k8 || B::k8 || (t & 1); }
@@ -279,8 +294,10 @@ struct MxRing {
     return -1;
   }
   static_assert(kDB || kRA == 2, "a deeper ring reads the next step's rows before the last");
-  static constexpr int reads(int p) {  // LDS reads after position p
-    return (A::k8 ? 3 : 2) * ((a_after(p) >= 0) + (na_after(p) >= 0)) + (B::k8 ? 3 : 2) * (nb_after(p) >= 0);
+  static constexpr int reads(int t, int p) {  // LDS reads after position p of step t
+    const int own = !kPairScales || t % 2 == 0, next = !kPairScales || t % 2 == 1;  // with a scale?
+    return ((A::k8 ? 2 : 1) + own) * (a_after(p) >= 0) + ((A::k8 ? 2 : 1) + next) * (na_after(p) >= 0) +
+           ((B::k8 ? 2 : 1) + next) * (nb_after(p) >= 0);
   }
   // transfers after position p of step t: the second half of the next stage at the head (A at
   // 0, 2, B at 4, 6; the next quad's scales at 8), the first half of the one after it behind the
@@ -302,7 +319,7 @@ struct MxRing {
   static __device__ __forceinline__ void sched() {
     if constexpr (P < E) {
       __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      if constexpr (reads(P) > 0) __builtin_amdgcn_sched_group_barrier(0x100, reads(P), 0);
+      if constexpr (reads(T, P) > 0) __builtin_amdgcn_sched_group_barrier(0x100, reads(T, P), 0);
       if constexpr (transfers(T, P) > 0) __builtin_amdgcn_sched_group_barrier(0x020, transfers(T, P), 0);
       sched<T, P + 1, E>();
     }
@@ -316,7 +333,8 @@ struct MxRing {
       constexpr int NT = (T + 1) & 3;
       if constexpr (MM) {
         constexpr int r = P / kNI, c = P % kNI;
-        acc[r][c] = mx_mma<FA, FB>(f.b[bset(T)][c], f.a[r % kRA], acc[r][c], f.sb[bset(T)][c], f.sa[r % kRA]);
+        acc[r][c] = mx_mma<FA, FB, kPairScales ? T % 2 : 0>(f.b[bset(T)][c], f.a[r % kRA], acc[r][c], f.sb[sset(T)][c],
+                                                            f.sa[kPairScales ? r : r % kRA]);
         if constexpr (a_after(P) >= 0) read_a<T>(f, smem, o, a_after(P), so);
         if constexpr (na_after(P) >= 0) read_a<NT>(f, smem, o, na_after(P), so_next);
         if constexpr (nb_after(P) >= 0) read_b<NT>(f, smem, o, nb_after(P), so_next);
@@ -389,37 +407,107 @@ struct MxRing {
     }
   }
 
-  // ---- epilogue: passes of 64 rows of the wave's block through its share of the idle ring, as
-  // fp32 rows of 64 columns, and back 8 columns a lane, so that C, D and PostAct are accessed 16
-  // bytes (or more) at a time and 128 bytes a row. Half-row chunks are XOR-swizzled by the row
-  // as in gemm_kernel.hpp's 16x16 epilogue.
+  // ---- epilogue. It runs while the next tile's first transfers are under way (they fill stage 0),
+  // through 8 KB a wave of stage 1. One 16-bit output without C: the values are final in the
+  // accumulators, so they are converted there and pass through LDS as 16-bit rows (64 rows a
+  // pass). Otherwise fp32 rows (32 a pass). Either way a lane then holds 8 consecutive columns, and C,
+  // D and PostAct are accessed 16 bytes or more at a time, 128 bytes a row. Chunks are XOR-swizzled
+  // by the row as in gemm_kernel.hpp's 16x16 epilogues.
+  static constexpr int kRegion = 8192;
+  static_assert(kRegion * NW == kABytes + kBBytes, "the epilogue's buffers are the second stages");
+  static __device__ __forceinline__ int region(int wave) {
+    return wave < NW / 2 ? kABytes + wave * kRegion : kBOff + kBBytes + (wave - NW / 2) * kRegion;
+  }
   static __device__ __forceinline__ int ebuf(int r, int c8, int hf) {
     return r * 256 + hf * 128 + ((c8 ^ ((r & 3) | ((r >> 1) & 4))) << 4);
   }
-  static __device__ __forceinline__ void epilogue(const KParams& p, const MxTileInfo& ti, const f32x4 (&acc)[kMI][kNI],
-                                                  GEP_LDS char* region, int lane, int wm0, int wn0) {
-    asm volatile("" : "+v"(lane));
+  static __device__ __forceinline__ int ebuf16(int r, int c) { return r * 128 + ((c ^ ((r >> 1) & 7)) << 4); }
+
+  // Stores of the 16-bit path; the count lets the wait for the transfers issued before them leave
+  // the stores in flight. (So every one is issued: rows and columns past the output go to an
+  // offset that the range check drops.)
+  static constexpr int kStores16 = kWM / 8;
+  static constexpr int64_t kMaxLd16 = 1 << 22;  // its offsets inside a tile are 32-bit
+
+  template <int DT>
+  static __device__ __forceinline__ void epilogue16(const KParams& p, const MxTileInfo& ti, const f32x4 (&acc)[kMI][kNI],
+                                                    GEP_LDS char* buf, int lane, int wm0, int wn0) {
+    const bool post = p.p_dt != DT_NONE;
+    const int64_t ld = post ? p.ldp : p.ldd;
     const int row0 = ti.m0 + wm0, col0 = ti.n0 + wn0;
-    const int rl = lane >> 3, n = col0 + 8 * (lane & 7);
+    const __amdgpu_buffer_rsrc_t out =
+        make_rsrc((post ? (char*)p.Post : (char*)p.D) + ((int64_t)row0 * ld + col0) * 2, 0x7FFFFFFF);
+    const int q = lane >> 4, rl = lane >> 3, c = lane & 7;
+    const bool col_ok = col0 + 8 * c < p.N;
 #pragma unroll
     for (int pass = 0; pass < kMI / 4; ++pass) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 4; ++i) {
+        const int r = i * 16 + (lane & 15);
 #pragma unroll
-        for (int j = 0; j < kNI; ++j)
-          *(f32x4 GEP_LDS*)(region + ebuf(i * 16 + (lane & 15), 2 * j + (lane >> 5), (lane >> 4) & 1)) = acc[pass * 4 + i][j];
+        for (int j = 0; j < kNI; j += 2) {
+          const f32x4 &x = acc[pass * 4 + i][j], &y = acc[pass * 4 + i][j + 1];
+          float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+          if (post) mx_act8(p.act, v);
+          const uint2 lo = pack4_16(DT, v), hi = pack4_16(DT, v + 4);
+          *(GEP_LDS i32x2*)(buf + ebuf16(r, 2 * j + (q >> 1)) + 8 * (q & 1)) = i32x2{(int)lo.x, (int)lo.y};
+          *(GEP_LDS i32x2*)(buf + ebuf16(r, 2 * j + 2 + (q >> 1)) + 8 * (q & 1)) = i32x2{(int)hi.x, (int)hi.y};
+        }
+      }
       asm volatile("" ::: "memory");  // (LDS operations of a wave complete in order)
-#pragma unroll 1
+#pragma unroll
       for (int it = 0; it < 8; ++it) {
         const int r = it * 8 + rl;
-        const int64_t m = row0 + pass * 64 + r;
-        const f32x4 x0 = *(const f32x4 GEP_LDS*)(region + ebuf(r, lane & 7, 0));
-        const f32x4 x1 = *(const f32x4 GEP_LDS*)(region + ebuf(r, lane & 7, 1));
+        const i32x4 x = *(const GEP_LDS i32x4*)(buf + ebuf16(r, c));
+        const bool ok = col_ok && row0 + pass * 64 + r < ti.row_end;
+        __builtin_amdgcn_raw_buffer_store_b128(x, out, ok ? (uint32_t)((pass * 64 + r) * (int)ld * 2 + c * 16) : kOOB, 0, 0);
+      }
+      asm volatile("" ::: "memory");
+    }
+  }
+
+  // Returns whether exactly kStores16 stores are the last vector memory operations issued.
+  static __device__ __forceinline__ bool epilogue(const KParams& p, const MxTileInfo& ti, const f32x4 (&acc)[kMI][kNI],
+                                                  GEP_LDS char* buf, int lane, int wm0, int wn0) {
+    asm volatile("" : "+v"(lane));
+    if (p.c_dt == DT_NONE && (p.d_dt == DT_NONE) != (p.p_dt == DT_NONE)) {
+      const int dt = p.d_dt != DT_NONE ? p.d_dt : p.p_dt;
+      if ((p.d_dt != DT_NONE ? p.ldd : p.ldp) < kMaxLd16 && dt != DT_F32) {
+        if (dt == DT_BF16) epilogue16<DT_BF16>(p, ti, acc, buf, lane, wm0, wn0);
+        else epilogue16<DT_F16>(p, ti, acc, buf, lane, wm0, wn0);
+        return true;
+      }
+    }
+    const int row0 = ti.m0 + wm0, col0 = ti.n0 + wn0;
+    const int rl = lane >> 3, n = col0 + 8 * (lane & 7);
+#pragma unroll
+    for (int pass = 0; pass < kMI / 2; ++pass) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < kNI; ++j)
+          *(f32x4 GEP_LDS*)(buf + ebuf(i * 16 + (lane & 15), 2 * j + (lane >> 5), (lane >> 4) & 1)) = acc[pass * 2 + i][j];
+      asm volatile("" ::: "memory");
+#pragma unroll 2
+      for (int it = 0; it < 4; ++it) {
+        const int r = it * 8 + rl;
+        const int64_t m = row0 + pass * 32 + r;
+        const f32x4 x0 = *(const f32x4 GEP_LDS*)(buf + ebuf(r, lane & 7, 0));
+        const f32x4 x1 = *(const f32x4 GEP_LDS*)(buf + ebuf(r, lane & 7, 1));
         float v[8] = {x0[0], x0[1], x0[2], x0[3], x1[0], x1[1], x1[2], x1[3]};
         if (m < ti.row_end && n < p.N) mx_finish8(p, m, n, v);
       }
       asm volatile("" ::: "memory");
     }
+    return false;
+  }
+  // All transfers issued before the last kStores16 operations have landed; then the workgroup meets.
+  static __device__ __forceinline__ void dma_barrier_stores() {
+    __builtin_amdgcn_sched_barrier(0);
+    static_assert(kStores16 == 16 || kStores16 == 8, "the literal counts below");
+    if constexpr (kStores16 == 16) asm volatile("s_waitcnt vmcnt(16) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    else asm volatile("s_waitcnt vmcnt(8) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
   }
 
   static __device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
@@ -508,28 +596,35 @@ struct MxRing {
     const int bid = blockIdx.x;
     const int b0 = xq ? (bid & 7) * (P >> 3) + (bid >> 3) : bid;
 
-    for (int t = b0; t < T; t += P) {
-      const MxTileInfo ti = decode(mp, t, gstart);
+    MxTileInfo ti;
+    Src s;
+    // The tile's operands, and its first transfers: stage 0 and the first scales.
+    auto begin_tile = [&](int t) {
+      ti = decode(mp, t, gstart);
       int lane = lane_id;
       asm volatile("" : "+v"(lane));  // (lane offsets are not kept across the main loop)
-      Src s;
       init<kInstrA>(s.la, wave, lane, ti.row_end - ti.m0, (int)p.lda, (int)p.lda);
       init<kInstrB>(s.lb, wave, lane, p.N - ti.n0, (int)p.ldb, (int)p.ldb);
       const int64_t ao = (int64_t)ti.m0 * p.lda, bo = (int64_t)ti.n0 * p.ldb;
       s.a = make_rsrc((const char*)p.A + ao, p.a_bytes - ao);
       s.b = make_rsrc((const char*)p.B + (int64_t)ti.g * p.b_bytes + bo, p.b_bytes - bo);
       s.nsb = mp.nsb;
-      {
-        const bool is_a = wave < BM / 64;
-        const int first = is_a ? ti.m0 : ti.n0;  // row of the tile's first scale
-        const int i = (is_a ? wave : wave - BM / 64) * 64 + lane;  // row of the tile
-        const int64_t so = (int64_t)(first >> 6) * mp.nsb * 1024;
-        s.s = make_rsrc(is_a ? mp.sa + so : mp.sb + (int64_t)ti.g * mp.sb_bytes + so,
-                        (is_a ? mp.sa_bytes : mp.sb_bytes) - so);
-        const int rr = (first & 63) + i;
-        s.s_off = first + i < (is_a ? ti.row_end : p.N) ? (uint32_t)((rr >> 6) * mp.nsb * 1024 + (rr & 63) * 16) : kOOB;
-      }
-      const Lane o = lane_offsets(lane, wm0, wn0);
+      const bool is_a = wave < BM / 64;
+      const int first = is_a ? ti.m0 : ti.n0;  // row of the tile's first scale
+      const int i = (is_a ? wave : wave - BM / 64) * 64 + lane;  // row of the tile
+      const int64_t so = (int64_t)(first >> 6) * mp.nsb * 1024;
+      s.s = make_rsrc(is_a ? mp.sa + so : mp.sb + (int64_t)ti.g * mp.sb_bytes + so,
+                      (is_a ? mp.sa_bytes : mp.sb_bytes) - so);
+      const int rr = (first & 63) + i;
+      s.s_off = first + i < (is_a ? ti.row_end : p.N) ? (uint32_t)((rr >> 6) * mp.nsb * 1024 + (rr & 63) * 16) : kOOB;
+      dma<0, 4>(s.la, s.a, 0, smem, wave);
+      dma<0, 4>(s.lb, s.b, 0, smem + kBOff, wave);
+      dma_scales(s, 0, smem, 0, wave);
+    };
+
+    if (b0 < T) begin_tile(b0);
+    bool stores = false;  // the wave's last operations are the stores of epilogue16
+    for (int t = b0; t < T;) {
       f32x4 acc[kMI][kNI];
 #pragma unroll
       for (int i = 0; i < kMI; ++i)
@@ -537,28 +632,33 @@ struct MxRing {
         for (int j = 0; j < kNI; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
       // a wave whose rows all lie past the output only moves data
       const bool idle = ti.m0 + wm0 >= ti.row_end;
-      lds_barrier();  // the previous tile's epilogue buffers are free
-      if (mp.steps > 0) {
-        dma<0, 4>(s.la, s.a, 0, smem, wave);
-        dma<0, 4>(s.lb, s.b, 0, smem + kBOff, wave);
-        dma_scales(s, 0, smem, 0, wave);
-        dma<0, 2>(s.la, s.a, 128, smem + kABytes, wave);
-        dma<0, 2>(s.lb, s.b, 128, smem + kBOff + kBBytes, wave);
-        dma_barrier();
-        Frags f;
-        if (idle) {
-          __builtin_amdgcn_s_setprio(0);
-          mainloop<false>(acc, f, smem, o, s, mp.steps, wave);
-        } else {
+      // stage 0 has landed; the previous tile's epilogue buffers (stage 1) are free
+      if (stores) dma_barrier_stores();
+      else dma_barrier();
+      dma<0, 2>(s.la, s.a, 128, smem + kABytes, wave);
+      dma<0, 2>(s.lb, s.b, 128, smem + kBOff + kBBytes, wave);
+      int lane = lane_id;
+      asm volatile("" : "+v"(lane));
+      const Lane o = lane_offsets(lane, wm0, wn0);
+      Frags f;
+      if (idle) {
+        __builtin_amdgcn_s_setprio(0);
+        mainloop<false>(acc, f, smem, o, s, mp.steps, wave);
+      } else {
 #pragma unroll
-          for (int r = 0; r < kRA - 1; ++r) read_a<0>(f, smem, o, r, 0);
+        for (int r = 0; r < kRA - 1; ++r) read_a<0>(f, smem, o, r, 0);
 #pragma unroll
-          for (int c = 0; c < kNI; ++c) read_b<0>(f, smem, o, c, 0);
-          mainloop<true>(acc, f, smem, o, s, mp.steps, wave);
-        }
+        for (int c = 0; c < kNI; ++c) read_b<0>(f, smem, o, c, 0);
+        mainloop<true>(acc, f, smem, o, s, mp.steps, wave);
       }
       dma_barrier();  // transfers past K have landed and every wave has left the ring
-      if (!idle) epilogue(p, ti, acc, smem + wave * (kSOff / NW), lane, wm0, wn0);
+      const MxTileInfo done = ti;
+      t += P;
+      if (t < T) begin_tile(t);
+      asm volatile("" ::: "memory");  // (its transfers are issued before the epilogue's stores)
+      __builtin_amdgcn_sched_barrier(0);
+      stores = false;
+      if (!idle) stores = epilogue(p, done, acc, smem + region(wave), lane_id, wm0, wn0);
     }
   }
 };
