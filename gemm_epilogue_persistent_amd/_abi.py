@@ -11,7 +11,7 @@ DT = {"none": 0, "f16": 1, "bf16": 2, "f32": 3, "e4m3": 4, "e5m2": 5}
 ROW, COL = 0, 1
 ACT = {"none": 0, "relu": 1, "relu_sq": 2, "gelu_tanh": 3, "silu": 4}
 MX_FORMAT = {"e2m1": 0, "e4m3": 1}
-MX_TILE = {"auto": 0, "256": 1, "128": 2, "64": 3, "rows32": 4, "rows16": 5}
+MX_TILE = {"auto": 0, "256": 1, "128": 2, "64": 3, "rows32": 4, "rows16": 5, "256x128": 6}
 MX_HEADER = os.path.join(os.path.dirname(HERE), "include", "mx_mi355x.h")
 
 

@@ -81,23 +81,41 @@ extern "C" gemm_status mx_gemm_run(const mx_gemm_plan* plan, const mx_gemm_args*
   p.steps = (d.K + 127) / 128;
   const int64_t tm = mx_row_blocks(*plan, bm), tn = (d.N + bn - 1) / bn;
   dim3 grid;
-  if (tile == MX_TILE_256 || tile == MX_TILE_128) {
+  int32_t tail_grid = 0;  // workgroups of the split tail's launch
+  if (tile == MX_TILE_256 || tile == MX_TILE_256X128 || tile == MX_TILE_128) {
     k.tm = (int32_t)tm;
     k.tn = (int32_t)tn;
     k.T = (int32_t)(tm * tn);  // (grouped: the kernel counts its tiles itself)
-    const int32_t cap = tile == MX_TILE_256 ? cus : 2 * cus;
+    const int32_t cap = tile == MX_TILE_128 ? 2 * cus : cus;
     k.P = k.T < cap ? k.T : cap;
     k.log2G = 3;
     k.xcd_remap = 1;
     k.fd_Gtn = make_fastdiv((uint32_t)(kRasterG * tn));
     for (int w = 1; w < kRasterG; ++w) k.fd_tail[w] = make_fastdiv((uint32_t)w);
     grid = dim3((unsigned)k.P);
+    if (tile == MX_TILE_256 && k.T > k.P) {
+      // (a grouped plan's tile count is known on the device only; its second launch exits at
+      // once when there is no such tail)
+      const int32_t rem = k.T % k.P;
+      if (d.groups) tail_grid = 2 * cus;
+      else if (rem > 0 && 2 * rem <= k.P) tail_grid = 4 * rem < 2 * cus ? 4 * rem : 2 * cus;
+      if (tail_grid > 0) {
+        k.tail = 1;
+        k.P_big = k.P;
+      }
+    }
   } else {
     if (tm > 65535) return fail(GEMM_ERR_UNSUPPORTED, "mx_gemm_run: too many rows for the tile asked for");
     grid = dim3((unsigned)tn, (unsigned)tm);
   }
   hipStream_t s = (hipStream_t)stream;
-  const hipError_t e = d.groups ? launch<true>(d, tile, p, grid, s) : launch<false>(d, tile, p, grid, s);
+  auto run = [&](int32_t t, dim3 g) { return d.groups ? launch<true>(d, t, p, g, s) : launch<false>(d, t, p, g, s); };
+  hipError_t e = run(tile, grid);
+  if (e == hipSuccess && tail_grid > 0) {
+    k.tail = 2;
+    k.P = tail_grid;
+    e = run(MX_TILE_128, dim3((unsigned)tail_grid));
+  }
   if (e != hipSuccess) return fail(GEMM_ERR_HIP, "mx_gemm_run launch: %s", hipGetErrorString(e));
   clear_error();
   return GEMM_OK;

@@ -10,7 +10,7 @@
 // for both types; checked on the hardware element by element).
 //
 // Two kernels:
-//   MxRing   large problems. 256x256 outputs per workgroup of 8 waves, or 128x128 of 4: both
+//   MxRing   large problems. 256x256 or 256x128 outputs per workgroup of 8 waves, 128x128 of 4: both
 //            operands go through LDS (global -> LDS transfers, two stages), persistent tile loop.
 //   MxDirect few rows. 16x16 to 64x64 outputs per workgroup, whose waves share out K and read
 //            their fragments from global memory themselves; one join in LDS at the end.
@@ -30,7 +30,7 @@ struct MxParams {
   int32_t steps;           // MFMA steps of 128 along K
 };
 
-enum MxTile : int32_t { MX_T_AUTO = 0, MX_T_256 = 1, MX_T_128 = 2, MX_T_64 = 3, MX_T_R32 = 4, MX_T_R16 = 5 };
+enum MxTile : int32_t { MX_T_AUTO = 0, MX_T_256 = 1, MX_T_128 = 2, MX_T_64 = 3, MX_T_R32 = 4, MX_T_R16 = 5, MX_T_256X128 = 6 };
 
 template <int FMT>
 struct MxFmt {
@@ -148,8 +148,10 @@ struct MxRing {
   static constexpr int kLdsBytes = kSOff + 2 * kSBytes;
   static constexpr int kVarlenLds = VM ? (kMaxVarlenGroups + 1 + kThreads + 1) * 4 : 0;
   static constexpr int kInstrA = BM / 8 / NW, kInstrB = BN / 8 / NW;  // transfers (8 rows each) of a stage
-  static_assert((BM + BN) / 64 == NW, "one scale transfer (64 rows) a wave");
+  static_assert((BM + BN) / 64 <= NW, "at most one scale transfer (64 rows) a wave");
   static_assert(kMI >= 4 && kMI % 2 == 0 && kNI == 4, "the fragment schedule below");
+  static_assert(kInstrA % 2 == 0 && kInstrB % 2 == 0 && kInstrA <= 4 && kInstrB <= 4, "half a stage at a time");
+  static constexpr int kHalfA = kInstrA / 2, kHalf = kInstrA / 2 + kInstrB / 2;  // transfers of half a stage: A's, then B's
   static constexpr int kN = kMI * kNI, kLastP = kN - kNI;
   static constexpr bool kDeep = FA == MX_E2M1 && FB == MX_E2M1;
   static constexpr int kRA = kDeep ? 4 : 2;
@@ -165,7 +167,7 @@ struct MxRing {
   // where the next step's fragments find free registers)
   static constexpr int kBarP = !kDB ? kLastP : ((kMI - kRA) * kNI > kNI ? (kMI - kRA) * kNI : kNI);
   static constexpr int kPrioP = (kBarP / 2 + 3) / 4 * 4;
-  static constexpr int kTailStep = (kN - kBarP) / 4;  // between the transfers after the barrier
+  static constexpr int kTailStep = (kN - kBarP) / kHalf;  // between the transfers after the barrier
   using A = MxFmt<FA>;
   using B = MxFmt<FB>;
 
@@ -205,6 +207,8 @@ struct MxRing {
     int32_t nsb;
   };
   static __device__ __forceinline__ void dma_scales(const Src& s, int quad, GEP_LDS char* smem, int stage, int wave) {
+    if constexpr ((BM + BN) / 64 < NW)
+      if (wave >= (BM + BN) / 64) return;
 #if defined(__HIP_DEVICE_COMPILE__)
     __builtin_amdgcn_raw_ptr_buffer_load_lds(s.s, (GEP_LDS void*)(smem + kSOff + stage * kSBytes + wave * 1024), 16,
                                              quad < s.nsb ? s.s_off + quad * 1024 : kOOB, 0, 0, 0);
@@ -299,21 +303,35 @@ struct MxRing {
     return ((A::k8 ? 2 : 1) + own) * (a_after(p) >= 0) + ((A::k8 ? 2 : 1) + next) * (na_after(p) >= 0) +
            ((B::k8 ? 2 : 1) + next) * (nb_after(p) >= 0);
   }
-  // transfers after position p of step t: the second half of the next stage at the head (A at
-  // 0, 2, B at 4, 6; the next quad's scales at 8), the first half of the one after it behind the
-  // barrier
-  static constexpr bool head(bool k8, int t) { return k8 || !(t & 1); }
-  static constexpr bool tail(bool k8, int t) { return k8 || (t & 1); }
-  static constexpr int tail_at(int p) {  // which of the four tail transfers (A, A, B, B), or -1
-    return p >= kBarP && (p - kBarP) % kTailStep == 0 ? (p - kBarP) / kTailStep : -1;
+  // Transfers after position p of step t: the second half of the next stage at the head (every other
+  // position; behind them the next quad's scales), the first half of the one after it behind the
+  // barrier. head_at / tail_at: which transfer of its half goes out after position p (A's first), or -1.
+  static constexpr int head_at(int p) { return p % 2 == 0 && p / 2 < kHalf ? p / 2 : -1; }
+  static constexpr int tail_at(int p) {
+    return p >= kBarP && (p - kBarP) % kTailStep == 0 && (p - kBarP) / kTailStep < kHalf ? (p - kBarP) / kTailStep : -1;
   }
+  static constexpr bool in_step(bool is_a, bool tail, int t) {  // an E2M1 stage covers two steps
+    return (is_a ? A::k8 : B::k8) || (t & 1) == (tail ? 1 : 0);
+  }
+  static constexpr int kScaleP = 2 * kHalf;
   static constexpr int transfers(int t, int p) {
-    int n = 0;
-    if (p < 4 && p % 2 == 0) n += head(A::k8, t);
-    if (p >= 4 && p < 8 && p % 2 == 0) n += head(B::k8, t);
-    if (p == 8 && t == 0) n += 1;
-    if (tail_at(p) >= 0) n += tail_at(p) < 2 ? tail(A::k8, t) : tail(B::k8, t);
+    int n = p == kScaleP && t == 0;
+    if (head_at(p) >= 0) n += in_step(head_at(p) < kHalfA, false, t);
+    if (tail_at(p) >= 0) n += in_step(tail_at(p) < kHalfA, true, t);
     return n;
+  }
+  static_assert(kScaleP < kN, "the scales' transfer is issued inside the step");
+  // Transfer u of the first (SECOND = false) or second half of the stage `slot` (a step of an E4M3
+  // operand, a pair of an E2M1 one; 128 bytes of a row each) that is held in stage st.
+  template <int U, bool SECOND>
+  static __device__ __forceinline__ void transfer(const Src& s, int slot, GEP_LDS char* smem, int st, int wave) {
+    if constexpr (U < kHalfA) {
+      constexpr int q = U + (SECOND ? kInstrA / 2 : 0);
+      dma<q, q + 1>(s.la, s.a, slot * 128, smem + st * kABytes, wave);
+    } else {
+      constexpr int q = U - kHalfA + (SECOND ? kInstrB / 2 : 0);
+      dma<q, q + 1>(s.lb, s.b, slot * 128, smem + kBOff + st * kBBytes, wave);
+    }
   }
   template <int T, int P, int E>
   static __device__ __forceinline__ void sched() {
@@ -340,32 +358,19 @@ struct MxRing {
         if constexpr (nb_after(P) >= 0) read_b<NT>(f, smem, o, nb_after(P), so_next);
       }
       const int step = q * 4 + T;
-      // (slots: steps of an E4M3 operand, pairs of an E2M1 one, 128 bytes each)
-      if constexpr (P < 4 && P % 2 == 0 && head(A::k8, T)) {
-        constexpr int st = stage<FA>(A::k8 ? T : T + 1) ^ 1;
-        const int slot = (A::k8 ? step : step >> 1) + 1;
-        dma<kInstrA / 2 + P / 2 * (kInstrA / 4), kInstrA / 2 + (P / 2 + 1) * (kInstrA / 4)>(s.la, s.a, slot * 128, smem + st * kABytes, wave);
+      constexpr int h = head_at(P), u = tail_at(P);
+      if constexpr (h >= 0 && in_step(h < kHalfA, false, T)) {
+        constexpr bool k8 = h < kHalfA ? A::k8 : B::k8;
+        transfer<h, true>(s, (k8 ? step : step >> 1) + 1, smem, (h < kHalfA ? stage<FA>(T) : stage<FB>(T)) ^ 1, wave);
       }
-      if constexpr (P >= 4 && P < 8 && P % 2 == 0 && head(B::k8, T)) {
-        constexpr int st = stage<FB>(B::k8 ? T : T + 1) ^ 1, u = (P - 4) / 2;
-        const int slot = (B::k8 ? step : step >> 1) + 1;
-        dma<kInstrB / 2 + u * (kInstrB / 4), kInstrB / 2 + (u + 1) * (kInstrB / 4)>(s.lb, s.b, slot * 128, smem + kBOff + st * kBBytes, wave);
-      }
-      if constexpr (P == 8 && T == 0) dma_scales(s, q + 1, smem, (q + 1) & 1, wave);
-      constexpr int u = tail_at(P);
-      if constexpr (u >= 0 && u < 2 && tail(A::k8, T)) {
-        const int slot = (A::k8 ? step : step >> 1) + 2;
-        dma<u * (kInstrA / 4), (u + 1) * (kInstrA / 4)>(s.la, s.a, slot * 128, smem + stage<FA>(T) * kABytes, wave);
-      }
-      if constexpr (u >= 2 && tail(B::k8, T)) {
-        const int slot = (B::k8 ? step : step >> 1) + 2;
-        dma<(u - 2) * (kInstrB / 4), (u - 1) * (kInstrB / 4)>(s.lb, s.b, slot * 128, smem + kBOff + stage<FB>(T) * kBBytes, wave);
+      if constexpr (P == kScaleP && T == 0) dma_scales(s, q + 1, smem, (q + 1) & 1, wave);
+      if constexpr (u >= 0 && in_step(u < kHalfA, true, T)) {
+        constexpr bool k8 = u < kHalfA ? A::k8 : B::k8;
+        transfer<u, false>(s, (k8 ? step : step >> 1) + 2, smem, u < kHalfA ? stage<FA>(T) : stage<FB>(T), wave);
       }
       positions<MM, T, P + 1, E>(acc, f, smem, o, s, q, so, so_next, wave);
     }
   }
-  static_assert(kInstrA == 4 && kInstrB == 4, "two transfers in each half of a stage");
-
   template <bool MM, int T>
   static __device__ __forceinline__ void step(f32x4 (&acc)[kMI][kNI], Frags& f, GEP_LDS char* smem, const Lane& lo,
                                               const Src& s, int q, int wave) {
@@ -408,16 +413,13 @@ struct MxRing {
   }
 
   // ---- epilogue. It runs while the next tile's first transfers are under way (they fill stage 0),
-  // through 8 KB a wave of stage 1. One 16-bit output without C: the values are final in the
-  // accumulators, so they are converted there and pass through LDS as 16-bit rows (64 rows a
-  // pass). Otherwise fp32 rows (32 a pass). Either way a lane then holds 8 consecutive columns, and C,
+  // through 4 KB a wave of A's stage 1. One 16-bit output without C: the values are final in the
+  // accumulators, so they are converted there and pass through LDS as 16-bit rows (32 rows a
+  // pass). Otherwise fp32 rows (16 a pass). Either way a lane then holds 8 consecutive columns, and C,
   // D and PostAct are accessed 16 bytes or more at a time, 128 bytes a row. Chunks are XOR-swizzled
   // by the row as in gemm_kernel.hpp's 16x16 epilogues.
-  static constexpr int kRegion = 8192;
-  static_assert(kRegion * NW == kABytes + kBBytes, "the epilogue's buffers are the second stages");
-  static __device__ __forceinline__ int region(int wave) {
-    return wave < NW / 2 ? kABytes + wave * kRegion : kBOff + kBBytes + (wave - NW / 2) * kRegion;
-  }
+  static constexpr int kRegion = 4096;
+  static_assert(kRegion * NW <= kABytes, "the epilogue's buffers lie in a stage of A");
   static __device__ __forceinline__ int ebuf(int r, int c8, int hf) {
     return r * 256 + hf * 128 + ((c8 ^ ((r & 3) | ((r >> 1) & 4))) << 4);
   }
@@ -440,13 +442,13 @@ struct MxRing {
     const int q = lane >> 4, rl = lane >> 3, c = lane & 7;
     const bool col_ok = col0 + 8 * c < p.N;
 #pragma unroll
-    for (int pass = 0; pass < kMI / 4; ++pass) {
+    for (int pass = 0; pass < kMI / 2; ++pass) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 2; ++i) {
         const int r = i * 16 + (lane & 15);
 #pragma unroll
         for (int j = 0; j < kNI; j += 2) {
-          const f32x4 &x = acc[pass * 4 + i][j], &y = acc[pass * 4 + i][j + 1];
+          const f32x4 &x = acc[pass * 2 + i][j], &y = acc[pass * 2 + i][j + 1];
           float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
           if (post) mx_act8(p.act, v);
           const uint2 lo = pack4_16(DT, v), hi = pack4_16(DT, v + 4);
@@ -456,11 +458,11 @@ struct MxRing {
       }
       asm volatile("" ::: "memory");  // (LDS operations of a wave complete in order)
 #pragma unroll
-      for (int it = 0; it < 8; ++it) {
+      for (int it = 0; it < 4; ++it) {
         const int r = it * 8 + rl;
         const i32x4 x = *(const GEP_LDS i32x4*)(buf + ebuf16(r, c));
-        const bool ok = col_ok && row0 + pass * 64 + r < ti.row_end;
-        __builtin_amdgcn_raw_buffer_store_b128(x, out, ok ? (uint32_t)((pass * 64 + r) * (int)ld * 2 + c * 16) : kOOB, 0, 0);
+        const bool ok = col_ok && row0 + pass * 32 + r < ti.row_end;
+        __builtin_amdgcn_raw_buffer_store_b128(x, out, ok ? (uint32_t)((pass * 32 + r) * (int)ld * 2 + c * 16) : kOOB, 0, 0);
       }
       asm volatile("" ::: "memory");
     }
@@ -481,17 +483,15 @@ struct MxRing {
     const int row0 = ti.m0 + wm0, col0 = ti.n0 + wn0;
     const int rl = lane >> 3, n = col0 + 8 * (lane & 7);
 #pragma unroll
-    for (int pass = 0; pass < kMI / 2; ++pass) {
+    for (int pass = 0; pass < kMI; ++pass) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < kNI; ++j)
-          *(f32x4 GEP_LDS*)(buf + ebuf(i * 16 + (lane & 15), 2 * j + (lane >> 5), (lane >> 4) & 1)) = acc[pass * 2 + i][j];
+      for (int j = 0; j < kNI; ++j)
+        *(f32x4 GEP_LDS*)(buf + ebuf(lane & 15, 2 * j + (lane >> 5), (lane >> 4) & 1)) = acc[pass][j];
       asm volatile("" ::: "memory");
-#pragma unroll 2
-      for (int it = 0; it < 4; ++it) {
+#pragma unroll
+      for (int it = 0; it < 2; ++it) {
         const int r = it * 8 + rl;
-        const int64_t m = row0 + pass * 32 + r;
+        const int64_t m = row0 + pass * 16 + r;
         const f32x4 x0 = *(const f32x4 GEP_LDS*)(buf + ebuf(r, lane & 7, 0));
         const f32x4 x1 = *(const f32x4 GEP_LDS*)(buf + ebuf(r, lane & 7, 1));
         float v[8] = {x0[0], x0[1], x0[2], x0[3], x1[0], x1[1], x1[2], x1[3]};
@@ -512,8 +512,13 @@ struct MxRing {
 
   static __device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
-  static __device__ __forceinline__ MxTileInfo decode(const MxParams& mp, int t, const int32_t* gstart) {
+  // Item u of this launch -> output tile. The map has tiles of BM x BN; in a split tail's launch
+  // (p.tail == 2, the 128x128 kernels) of 256x256, and item u is quarter u & 3 of map tile t_lo + u / 4:
+  // its rows (u & 1) and columns (u >> 1 & 1), possibly wholly outside the output.
+  static __device__ __forceinline__ MxTileInfo decode(const MxParams& mp, int u, const int32_t* gstart, int t_lo) {
     const KParams& p = mp.k;
+    const bool quarter = BM == 128 && p.tail == 2;
+    const int MT = quarter ? 2 * BM : BM, NT = quarter ? 2 * BN : BN, t = quarter ? t_lo + (u >> 2) : u;
     MxTileInfo ti;
     uint32_t mb, nb;
     int row_base = 0;
@@ -526,15 +531,15 @@ struct MxRing {
       row_base = p.cu_seqlens[lo];
       ti.row_end = p.cu_seqlens[lo + 1];
       ti.g = lo;
-      raster(p, (uint32_t)(t - gstart[lo]), (uint32_t)((ti.row_end - row_base + BM - 1) / BM), (uint32_t)p.tn, p.fd_Gtn, mb, nb);
+      raster(p, (uint32_t)(t - gstart[lo]), (uint32_t)((ti.row_end - row_base + MT - 1) / MT), (uint32_t)p.tn, p.fd_Gtn, mb, nb);
     } else {
       ti.g = 0;
       ti.row_end = p.M;
       raster(p, (uint32_t)t, (uint32_t)p.tm, (uint32_t)p.tn, p.fd_Gtn, mb, nb);
     }
     ti.g = uni(ti.g);
-    ti.m0 = uni(row_base + (int)mb * BM);
-    ti.n0 = uni((int)nb * BN);
+    ti.m0 = uni(row_base + (int)mb * MT + (quarter ? (u & 1) * BM : 0));
+    ti.n0 = uni((int)nb * NT + (quarter ? ((u >> 1) & 1) * BN : 0));
     ti.row_end = uni(ti.row_end);
     return ti;
   }
@@ -550,6 +555,7 @@ struct MxRing {
 
     int T = p.T;
     [[maybe_unused]] int32_t* gstart = nullptr;
+    [[maybe_unused]] const int MT = BM == 128 && p.tail == 2 ? 2 * BM : BM;
     if constexpr (VM) {
       // tile offsets of the groups; an array that does not run 0 .. M without decreasing gives
       // no tiles (see gemm_kernel.hpp: the flag shares the one LDS array)
@@ -568,7 +574,7 @@ struct MxRing {
         if (g < p.L) {
           const int c0 = p.cu_seqlens[g], c1 = p.cu_seqlens[g + 1];
           bad |= c1 < c0 || (g == 0 && c0 != 0) || (g == p.L - 1 && c1 != p.M);
-          tiles = c1 > c0 ? (int)(((int64_t)c1 - c0 + BM - 1) / BM) * p.tn : 0;
+          tiles = c1 > c0 ? (int)(((int64_t)c1 - c0 + MT - 1) / MT) * p.tn : 0;
         }
         local[q] = sum;
         sum += tiles;
@@ -594,13 +600,28 @@ struct MxRing {
     const int P = p.P;
     const bool xq = p.xcd_remap && (P & 7) == 0;
     const int bid = blockIdx.x;
-    const int b0 = xq ? (bid & 7) * (P >> 3) + (bid >> 3) : bid;
+    const int qx = xq ? bid & 7 : 0, qj = xq ? bid >> 3 : bid, Q = xq ? P >> 3 : P;
+    int b0 = qx * Q + qj;
+    // Split tail: when the last round of map tiles is partial and at most half full, the first
+    // launch (tail 1) stops before it and a second one (tail 2) takes it in quarters. Both decide
+    // from T. The second one's XCDs take a run of quarters each.
+    int t_lo = 0, U = T;
+    if (p.tail != 0) {
+      const int rem = T % p.P_big;
+      const bool split = T > p.P_big && rem > 0 && 2 * rem <= p.P_big;
+      U = p.tail == 1 ? (split ? T - rem : T) : (split ? 4 * rem : 0);
+      t_lo = T - rem;
+      if (p.tail == 2 && xq && U <= P) {
+        const int run = (U + 7) >> 3;
+        b0 = qj < run ? qx * run + qj : U;
+      }
+    }
 
     MxTileInfo ti;
     Src s;
     // The tile's operands, and its first transfers: stage 0 and the first scales.
     auto begin_tile = [&](int t) {
-      ti = decode(mp, t, gstart);
+      ti = decode(mp, t, gstart, t_lo);
       int lane = lane_id;
       asm volatile("" : "+v"(lane));  // (lane offsets are not kept across the main loop)
       init<kInstrA>(s.la, wave, lane, ti.row_end - ti.m0, (int)p.lda, (int)p.lda);
@@ -609,7 +630,7 @@ struct MxRing {
       s.a = make_rsrc((const char*)p.A + ao, p.a_bytes - ao);
       s.b = make_rsrc((const char*)p.B + (int64_t)ti.g * p.b_bytes + bo, p.b_bytes - bo);
       s.nsb = mp.nsb;
-      const bool is_a = wave < BM / 64;
+      const bool is_a = wave < BM / 64;  // (waves past (BM + BN) / 64 move no scales)
       const int first = is_a ? ti.m0 : ti.n0;  // row of the tile's first scale
       const int i = (is_a ? wave : wave - BM / 64) * 64 + lane;  // row of the tile
       const int64_t so = (int64_t)(first >> 6) * mp.nsb * 1024;
@@ -617,26 +638,26 @@ struct MxRing {
                       (is_a ? mp.sa_bytes : mp.sb_bytes) - so);
       const int rr = (first & 63) + i;
       s.s_off = first + i < (is_a ? ti.row_end : p.N) ? (uint32_t)((rr >> 6) * mp.nsb * 1024 + (rr & 63) * 16) : kOOB;
-      dma<0, 4>(s.la, s.a, 0, smem, wave);
-      dma<0, 4>(s.lb, s.b, 0, smem + kBOff, wave);
+      dma<0, kInstrA>(s.la, s.a, 0, smem, wave);
+      dma<0, kInstrB>(s.lb, s.b, 0, smem + kBOff, wave);
       dma_scales(s, 0, smem, 0, wave);
     };
 
-    if (b0 < T) begin_tile(b0);
+    if (b0 < U) begin_tile(b0);
     bool stores = false;  // the wave's last operations are the stores of epilogue16
-    for (int t = b0; t < T;) {
+    for (int t = b0; t < U;) {
       f32x4 acc[kMI][kNI];
 #pragma unroll
       for (int i = 0; i < kMI; ++i)
 #pragma unroll
         for (int j = 0; j < kNI; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-      // a wave whose rows all lie past the output only moves data
-      const bool idle = ti.m0 + wm0 >= ti.row_end;
+      // a wave whose rows or columns all lie past the output only moves data
+      const bool idle = ti.m0 + wm0 >= ti.row_end || ti.n0 + wn0 >= p.N;
       // stage 0 has landed; the previous tile's epilogue buffers (stage 1) are free
       if (stores) dma_barrier_stores();
       else dma_barrier();
-      dma<0, 2>(s.la, s.a, 128, smem + kABytes, wave);
-      dma<0, 2>(s.lb, s.b, 128, smem + kBOff + kBBytes, wave);
+      dma<0, kInstrA / 2>(s.la, s.a, 128, smem + kABytes, wave);
+      dma<0, kInstrB / 2>(s.lb, s.b, 128, smem + kBOff + kBBytes, wave);
       int lane = lane_id;
       asm volatile("" : "+v"(lane));
       const Lane o = lane_offsets(lane, wm0, wn0);
@@ -654,11 +675,11 @@ struct MxRing {
       dma_barrier();  // transfers past K have landed and every wave has left the ring
       const MxTileInfo done = ti;
       t += P;
-      if (t < T) begin_tile(t);
+      if (t < U) begin_tile(t);
       asm volatile("" ::: "memory");  // (its transfers are issued before the epilogue's stores)
       __builtin_amdgcn_sched_barrier(0);
       stores = false;
-      if (!idle) stores = epilogue(p, done, acc, smem + region(wave), lane_id, wm0, wn0);
+      if (!idle) stores = epilogue(p, done, acc, smem + kABytes + wave * kRegion, lane_id, wm0, wn0);
     }
   }
 };
@@ -843,9 +864,9 @@ struct MxDirect {
   }
 };
 
-template <int BM, int NW, int FA, int FB, bool VM>
-__global__ __launch_bounds__(NW * 64, (BM == 256 ? 1 : 2)) void mx_ring_kernel(const MxParams p) {
-  MxRing<BM, BM, NW, FA, FB, VM>::run(p);
+template <int BM, int BN, int NW, int FA, int FB, bool VM>
+__global__ __launch_bounds__(NW * 64, (NW == 8 ? 1 : 2)) void mx_ring_kernel(const MxParams p) {
+  MxRing<BM, BN, NW, FA, FB, VM>::run(p);
 }
 template <int MB, int NB, int NW, int D, int FA, int FB, bool VM>
 __global__ __launch_bounds__(NW * 64) void mx_direct_kernel(const MxParams p) {
@@ -861,8 +882,9 @@ hipError_t mx_launch(int32_t tile, const MxParams& p, dim3 grid, hipStream_t s);
   template <>                                                                                        \
   hipError_t mx_launch<FA, FB, VM>(int32_t tile, const MxParams& p, dim3 grid, hipStream_t s) {      \
     switch (tile) {                                                                                  \
-      case MX_T_256: mx_ring_kernel<256, 8, FA, FB, VM><<<grid, 512, 0, s>>>(p); break;              \
-      case MX_T_128: mx_ring_kernel<128, 4, FA, FB, VM><<<grid, 256, 0, s>>>(p); break;              \
+      case MX_T_256: mx_ring_kernel<256, 256, 8, FA, FB, VM><<<grid, 512, 0, s>>>(p); break;         \
+      case MX_T_256X128: mx_ring_kernel<256, 128, 8, FA, FB, VM><<<grid, 512, 0, s>>>(p); break;     \
+      case MX_T_128: mx_ring_kernel<128, 128, 4, FA, FB, VM><<<grid, 256, 0, s>>>(p); break;         \
       case MX_T_64: mx_direct_kernel<4, 4, 4, 2, FA, FB, VM><<<grid, 256, 0, s>>>(p); break;         \
       case MX_T_R32: mx_direct_kernel<2, 2, 8, 2, FA, FB, VM><<<grid, 512, 0, s>>>(p); break;        \
       case MX_T_R16: mx_direct_kernel<1, 1, 8, 4, FA, FB, VM><<<grid, 512, 0, s>>>(p); break;        \

@@ -34,8 +34,14 @@ gemm_status check_out(const char* name, int32_t dt, int64_t ld, int32_t M, int32
 }  // namespace
 
 void mx_tile_extent(int32_t tile, int32_t* bm, int32_t* bn) {
-  const int32_t e = tile == MX_TILE_256 ? 256 : tile == MX_TILE_128 ? 128 : tile == MX_TILE_64 ? 64 : tile == MX_TILE_ROWS_32 ? 32 : 16;
-  *bm = *bn = e;
+  switch (tile) {
+    case MX_TILE_256: *bm = *bn = 256; break;
+    case MX_TILE_256X128: *bm = 256; *bn = 128; break;
+    case MX_TILE_128: *bm = *bn = 128; break;
+    case MX_TILE_64: *bm = *bn = 64; break;
+    case MX_TILE_ROWS_32: *bm = *bn = 32; break;
+    default: *bm = *bn = 16; break;
+  }
 }
 
 int64_t mx_row_blocks(const mx_gemm_plan& p, int32_t bm) {
@@ -86,7 +92,7 @@ gemm_status mx_gemm_create(const mx_gemm_desc* d, mx_gemm_plan** out) {
   if (d->d == GEMM_DT_NONE && d->post == GEMM_DT_NONE) return fail(GEMM_ERR_INVALID_ARG, "mx_gemm_create: neither D nor PostAct");
   if (d->act < GEMM_ACT_NONE || d->act > GEMM_ACT_SILU) return fail(GEMM_ERR_INVALID_ARG, "mx_gemm_create: unknown activation %d", d->act);
   if (d->act != GEMM_ACT_NONE && d->post == GEMM_DT_NONE) return fail(GEMM_ERR_INVALID_ARG, "mx_gemm_create: an activation without PostAct");
-  if (d->tile < MX_TILE_AUTO || d->tile > MX_TILE_ROWS_16) return fail(GEMM_ERR_INVALID_ARG, "mx_gemm_create: unknown tile %d", d->tile);
+  if (d->tile < MX_TILE_AUTO || d->tile > MX_TILE_256X128) return fail(GEMM_ERR_INVALID_ARG, "mx_gemm_create: unknown tile %d", d->tile);
   if (d->N % 8) return fail(GEMM_ERR_ALIGNMENT, "mx_gemm_create: N = %d is not a multiple of 8", d->N);
   // (256 rows of codes stay below 2^31 bytes: the kernels' offsets inside a tile are 32-bit)
   if (d->K > (1 << 22)) return fail(GEMM_ERR_UNSUPPORTED, "mx_gemm_create: K above 2^22");

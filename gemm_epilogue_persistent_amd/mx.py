@@ -193,8 +193,8 @@ class MxPlan:
     memory; reusable, from several streams too). a (m, k); b (n, k), or (G, n, k) with
     cu_seqlens_m: int32 of G + 1 row offsets on the GPU, whose values are read by each run. n is a
     multiple of 8. C, D, PostAct: 16- or 32-bit floats, rows contiguous, row strides of whole 16
-    bytes; at least one of D, PostAct. tile: "auto", or the kernel to use ("256", "128", "64",
-    "rows32", "rows16")."""
+    bytes; at least one of D, PostAct. tile: "auto", or the kernel to use ("256", "256x128", "128",
+    "64", "rows32", "rows16")."""
 
     def __init__(self, a, b, C=None, D=None, PostAct=None, act="none", cu_seqlens_m=None, tile="auto"):
         self.handle = None

@@ -122,7 +122,8 @@ typedef enum {
   MX_TILE_128 = 2,    /* 128x128 outputs, operands staged through LDS               */
   MX_TILE_64 = 3,     /* 64x64 outputs, K split over the waves of a workgroup       */
   MX_TILE_ROWS_32 = 4,/* 32 rows x 32 columns, K split over the waves               */
-  MX_TILE_ROWS_16 = 5 /* 16 rows x 16 columns, K split over the waves               */
+  MX_TILE_ROWS_16 = 5,/* 16 rows x 16 columns, K split over the waves               */
+  MX_TILE_256X128 = 6 /* 256x128 outputs, operands staged through LDS               */
 } mx_tile;
 typedef struct {
   int32_t M, N, K;

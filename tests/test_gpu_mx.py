@@ -246,7 +246,7 @@ def run_product(M, N, K, fa, fb, tile, c=None, d="f32", post=None, act="none", s
         check_product(P, R.act(x, act), bound, post, act, x)
 
 
-TILES = ["256", "128", "64", "rows32", "rows16"]
+TILES = ["256", "256x128", "128", "64", "rows32", "rows16"]
 
 
 @pytest.mark.parametrize("tile", TILES)
@@ -265,6 +265,14 @@ def test_product_depths(K, tile):
     announce(f"product depth {K} tile {tile}")
     run_product(40, 72, K, "e4m3", "e2m1", tile, seed=K)
     run_product(24, 72, K, "e2m1", "e2m1", tile, seed=K + 1)
+
+
+@pytest.mark.parametrize("fa", FORMATS)
+@pytest.mark.parametrize("sizes", [None, [1000, 0, 3097, 253]])
+def test_product_split_tail(sizes, fa):
+    """More 256x256 tiles than one round of the card, the last round a small one."""
+    announce(f"product split tail {fa} {sizes}")
+    run_product(4350, 4104, 96, fa, "e2m1", "256", sizes=sizes, seed=21, d="bf16")
 
 
 @pytest.mark.parametrize("tile", TILES)

@@ -136,7 +136,7 @@ def gemm_desc(**kw):
 @pytest.mark.parametrize("kw,status", [
     (dict(), 0), (dict(K=0), 0), (dict(M=0), 0), (dict(c=0), 0), (dict(d=3), 0), (dict(groups=1024), 0),
     (dict(M=-1), 1), (dict(groups=-1), 1), (dict(groups=1025), 2), (dict(a_format=2), 1), (dict(b_format=-1), 1),
-    (dict(d=9), 1), (dict(d=0, post=0, act=0), 1), (dict(act=5), 1), (dict(post=0), 1), (dict(tile=6), 1),
+    (dict(d=9), 1), (dict(d=0, post=0, act=0), 1), (dict(act=5), 1), (dict(post=0), 1), (dict(tile=7), 1), (dict(tile=-1), 1),
     (dict(N=60), 3), (dict(K=(1 << 22) + 1), 2), (dict(d=4), 2), (dict(c=5), 2), (dict(ldd=56), 1), (dict(ldd=-8), 1),
     (dict(ldp=68), 3), (dict(ldc=1 << 49), 2), (dict(M=2 ** 31 - 1, N=1 << 20, ldc=1 << 20, ldd=1 << 20, ldp=1 << 20), 2),
 ])
@@ -187,7 +187,7 @@ def test_plan_tile(lib):
         lib.mx_gemm_destroy(h)
         return t.value
     wide = dict(ldc=8192, ldd=8192, ldp=8192)
-    for want in range(1, 6):
+    for want in range(1, 7):
         assert tile(tile=want) == want
     assert tile(M=8192, N=8192, **wide) == _abi.MX_TILE["256"]
     assert tile(M=1, N=8192, **wide) == _abi.MX_TILE["rows16"]
