@@ -11,7 +11,7 @@ DT = {"none": 0, "f16": 1, "bf16": 2, "f32": 3, "e4m3": 4, "e5m2": 5}
 ROW, COL = 0, 1
 ACT = {"none": 0, "relu": 1, "relu_sq": 2, "gelu_tanh": 3, "silu": 4}
 MX_FORMAT = {"e2m1": 0, "e4m3": 1}
-MX_TILE = {"auto": 0, "256": 1, "128": 2, "64": 3, "rows32": 4, "rows16": 5, "256x128": 6}
+MX_TILE = {"auto": 0, "256": 1, "128": 2, "32x64": 3, "32": 4, "16x32": 5, "16": 6}
 MX_HEADER = os.path.join(os.path.dirname(HERE), "include", "mx_mi355x.h")
 
 
@@ -42,13 +42,14 @@ class GemmArgs(ctypes.Structure):
 
 class MxGemmDesc(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("M", "N", "K", "groups", "a_format", "b_format", "c", "d", "post",
-                                              "act", "tile")] + [
+                                              "act", "tile", "split")] + [
         (n, ctypes.c_int64) for n in ("ldc", "ldd", "ldp")]
 
 
 class MxGemmArgs(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("a_codes", "a_scales", "b_codes", "b_scales", "C", "D", "PostAct",
-                                               "cu_seqlens_m")]
+                                               "cu_seqlens_m", "workspace")] + [
+        ("workspace_bytes", ctypes.c_int64)]
 
 
 class RmsnormArgs(ctypes.Structure):
@@ -127,7 +128,9 @@ def load():
         lib.mx_gemm_destroy.restype = ctypes.c_int
         lib.mx_gemm_destroy.argtypes = [vp]
         lib.mx_gemm_plan_tile.restype = ctypes.c_int
-        lib.mx_gemm_plan_tile.argtypes = [vp, i32, ctypes.POINTER(i32)]
+        lib.mx_gemm_plan_tile.argtypes = [vp, i32, ctypes.POINTER(i32), ctypes.POINTER(i32)]
+        lib.mx_gemm_workspace.restype = ctypes.c_int
+        lib.mx_gemm_workspace.argtypes = [vp, i32, ctypes.POINTER(i64)]
         lib.gemm_status_string.restype = ctypes.c_char_p
         lib.gemm_status_string.argtypes = [ctypes.c_int]
         lib.gemm_last_error.restype = ctypes.c_char_p

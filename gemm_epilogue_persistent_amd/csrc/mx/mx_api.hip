@@ -25,6 +25,26 @@ static hipError_t launch(const mx_gemm_desc& d, int32_t tile, const MxParams& p,
 
 constexpr int32_t kRasterG = 8;
 
+// Adds up the slices of K, in order, and finishes 8 columns a thread.
+__global__ __launch_bounds__(256) void mx_join_kernel(const MxParams p, uint32_t n, FastDiv fd_cols8) {
+  const uint32_t i = blockIdx.x * 256 + threadIdx.x;
+  if (i >= n) return;
+  uint32_t m, c;
+  fd_divmod(fd_cols8, i, m, c);
+  const float* q = p.sums + (int64_t)m * p.k.N + c * 8;
+  const int64_t plane = (int64_t)p.k.M * p.k.N;
+  float v[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = 0.f;
+#pragma unroll 4
+  for (int s = 0; s < p.split; ++s) {
+    const f32x4 a = *(const f32x4*)(q + s * plane), b = *(const f32x4*)(q + s * plane + 4);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] += a[e], v[4 + e] += b[e];
+  }
+  mx_finish8(p.k, m, (int)c * 8, v);
+}
+
 // Compute units of the current device, looked up once per device.
 static gemm_status compute_units(int32_t* cus) {
   static std::atomic<int32_t> cache[64];
@@ -64,7 +84,14 @@ extern "C" gemm_status mx_gemm_run(const mx_gemm_plan* plan, const mx_gemm_args*
   const gemm_status st = compute_units(&cus);
   if (st != GEMM_OK) return st;
 
-  const int32_t tile = mx_choose_tile(*plan, cus);
+  MxChoice choice = mx_choose(*plan, cus, true);
+  if (choice.split > 1) {
+    const int64_t need = mx_workspace_bytes(*plan, choice);
+    if (!a->workspace) choice = mx_choose(*plan, cus, false);
+    else if (a->workspace_bytes < need) return fail(GEMM_ERR_INVALID_ARG, "mx_gemm_run: workspace of %lld bytes expected", (long long)need);
+    else if ((uintptr_t)a->workspace & 15) return fail(GEMM_ERR_ALIGNMENT, "mx_gemm_run: workspace not 16-byte aligned");
+  }
+  const int32_t tile = choice.tile;
   int32_t bm, bn;
   mx_tile_extent(tile, &bm, &bn);
   MxParams p{};
@@ -79,15 +106,18 @@ extern "C" gemm_status mx_gemm_run(const mx_gemm_plan* plan, const mx_gemm_args*
   p.sa_bytes = plan->sa_bytes; p.sb_bytes = plan->sb_bytes;
   p.nsb = (d.K + 511) / 512;
   p.steps = (d.K + 127) / 128;
+  p.split = choice.split;
+  p.per = choice.per;
+  p.sums = (float*)a->workspace;
   const int64_t tm = mx_row_blocks(*plan, bm), tn = (d.N + bn - 1) / bn;
   dim3 grid;
   int32_t tail_grid = 0;  // workgroups of the split tail's launch
-  if (tile == MX_TILE_256 || tile == MX_TILE_256X128 || tile == MX_TILE_128) {
+  if (tile == MX_TILE_256 || tile == MX_TILE_128) {
     k.tm = (int32_t)tm;
     k.tn = (int32_t)tn;
     k.T = (int32_t)(tm * tn);  // (grouped: the kernel counts its tiles itself)
     const int32_t cap = tile == MX_TILE_128 ? 2 * cus : cus;
-    k.P = k.T < cap ? k.T : cap;
+    k.P = k.T * p.split < cap ? k.T * p.split : cap;
     k.log2G = 3;
     k.xcd_remap = 1;
     k.fd_Gtn = make_fastdiv((uint32_t)(kRasterG * tn));
@@ -106,7 +136,7 @@ extern "C" gemm_status mx_gemm_run(const mx_gemm_plan* plan, const mx_gemm_args*
     }
   } else {
     if (tm > 65535) return fail(GEMM_ERR_UNSUPPORTED, "mx_gemm_run: too many rows for the tile asked for");
-    grid = dim3((unsigned)tn, (unsigned)tm);
+    grid = dim3((unsigned)tn, (unsigned)tm, (unsigned)p.split);
   }
   hipStream_t s = (hipStream_t)stream;
   auto run = [&](int32_t t, dim3 g) { return d.groups ? launch<true>(d, t, p, g, s) : launch<false>(d, t, p, g, s); };
@@ -115,6 +145,11 @@ extern "C" gemm_status mx_gemm_run(const mx_gemm_plan* plan, const mx_gemm_args*
     k.tail = 2;
     k.P = tail_grid;
     e = run(MX_TILE_128, dim3((unsigned)tail_grid));
+  }
+  if (e == hipSuccess && p.split > 1) {
+    const uint32_t n = (uint32_t)((int64_t)d.M * (d.N / 8));
+    mx_join_kernel<<<(n + 255) / 256, 256, 0, s>>>(p, n, make_fastdiv((uint32_t)d.N / 8));
+    e = hipGetLastError();
   }
   if (e != hipSuccess) return fail(GEMM_ERR_HIP, "mx_gemm_run launch: %s", hipGetErrorString(e));
   clear_error();

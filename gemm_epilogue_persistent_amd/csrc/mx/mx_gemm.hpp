@@ -28,9 +28,11 @@ struct MxParams {
   int64_t sa_bytes, sb_bytes;  // their extents (sb: of one group)
   int32_t nsb;             // scale tiles along K (512 values each)
   int32_t steps;           // MFMA steps of 128 along K
+  // K shared out over `split` workgroups a tile (dense; 1: not), `per` scale tiles each: slice s
+  // writes its fp32 sums as matrix s of `sums`, (split, M, N), and mx_join_kernel adds them up
+  int32_t split, per;
+  float* sums;
 };
-
-enum MxTile : int32_t { MX_T_AUTO = 0, MX_T_256 = 1, MX_T_128 = 2, MX_T_64 = 3, MX_T_R32 = 4, MX_T_R16 = 5, MX_T_256X128 = 6 };
 
 template <int FMT>
 struct MxFmt {
@@ -119,9 +121,14 @@ __device__ __forceinline__ void mx_finish8(const KParams& p, int64_t m, int n, f
   }
 }
 
+// The same for a slice of K: its sums, to be added up later.
+__device__ __forceinline__ void mx_slice8(const MxParams& p, int slice, int64_t m, int n, const float v[8]) {
+  mx_store8(DT_F32, (char*)(p.sums + ((int64_t)slice * p.k.M + m) * p.k.N + n), v);
+}
+
 // One output tile of a grouped or dense problem.
 struct MxTileInfo {
-  int g, m0, n0, row_end;
+  int g, m0, n0, row_end, slice;
 };
 
 // ------------------------------------------------------------------------------------
@@ -141,6 +148,7 @@ struct MxTileInfo {
 template <int BM, int BN, int NW, int FA, int FB, bool VM>
 struct MxRing {
   static constexpr int kThreads = NW * 64;
+  static constexpr bool kSplit = BM == 128 && !VM;  // may run slices of K
   static constexpr int kWN = 64, kWavesN = BN / kWN, kWavesM = NW / kWavesN, kWM = BM / kWavesM;
   static constexpr int kMI = kWM / 16, kNI = kWN / 16;
   static constexpr int kABytes = BM * kRowBytes, kBBytes = BN * kRowBytes;
@@ -469,10 +477,12 @@ struct MxRing {
   }
 
   // Returns whether exactly kStores16 stores are the last vector memory operations issued.
-  static __device__ __forceinline__ bool epilogue(const KParams& p, const MxTileInfo& ti, const f32x4 (&acc)[kMI][kNI],
+  static __device__ __forceinline__ bool epilogue(const MxParams& mp, const MxTileInfo& ti, const f32x4 (&acc)[kMI][kNI],
                                                   GEP_LDS char* buf, int lane, int wm0, int wn0) {
+    const KParams& p = mp.k;
+    const bool slice = kSplit && mp.split > 1;
     asm volatile("" : "+v"(lane));
-    if (p.c_dt == DT_NONE && (p.d_dt == DT_NONE) != (p.p_dt == DT_NONE)) {
+    if (!slice && p.c_dt == DT_NONE && (p.d_dt == DT_NONE) != (p.p_dt == DT_NONE)) {
       const int dt = p.d_dt != DT_NONE ? p.d_dt : p.p_dt;
       if ((p.d_dt != DT_NONE ? p.ldd : p.ldp) < kMaxLd16 && dt != DT_F32) {
         if (dt == DT_BF16) epilogue16<DT_BF16>(p, ti, acc, buf, lane, wm0, wn0);
@@ -495,7 +505,10 @@ struct MxRing {
         const f32x4 x0 = *(const f32x4 GEP_LDS*)(buf + ebuf(r, lane & 7, 0));
         const f32x4 x1 = *(const f32x4 GEP_LDS*)(buf + ebuf(r, lane & 7, 1));
         float v[8] = {x0[0], x0[1], x0[2], x0[3], x1[0], x1[1], x1[2], x1[3]};
-        if (m < ti.row_end && n < p.N) mx_finish8(p, m, n, v);
+        if (m < ti.row_end && n < p.N) {
+          if (slice) mx_slice8(mp, ti.slice, m, n, v);
+          else mx_finish8(p, m, n, v);
+        }
       }
       asm volatile("" ::: "memory");
     }
@@ -518,8 +531,10 @@ struct MxRing {
   static __device__ __forceinline__ MxTileInfo decode(const MxParams& mp, int u, const int32_t* gstart, int t_lo) {
     const KParams& p = mp.k;
     const bool quarter = BM == 128 && p.tail == 2;
-    const int MT = quarter ? 2 * BM : BM, NT = quarter ? 2 * BN : BN, t = quarter ? t_lo + (u >> 2) : u;
+    const int MT = quarter ? 2 * BM : BM, NT = quarter ? 2 * BN : BN;
     MxTileInfo ti;
+    ti.slice = kSplit && mp.split > 1 ? u / p.T : 0;  // slices of K: all tiles of the first, then the second, ...
+    const int t = quarter ? t_lo + (u >> 2) : u - ti.slice * p.T;
     uint32_t mb, nb;
     int row_base = 0;
     if constexpr (VM) {
@@ -538,6 +553,7 @@ struct MxRing {
       raster(p, (uint32_t)t, (uint32_t)p.tm, (uint32_t)p.tn, p.fd_Gtn, mb, nb);
     }
     ti.g = uni(ti.g);
+    ti.slice = uni(ti.slice);
     ti.m0 = uni(row_base + (int)mb * MT + (quarter ? (u & 1) * BM : 0));
     ti.n0 = uni((int)nb * NT + (quarter ? ((u >> 1) & 1) * BN : 0));
     ti.row_end = uni(ti.row_end);
@@ -605,7 +621,7 @@ struct MxRing {
     // Split tail: when the last round of map tiles is partial and at most half full, the first
     // launch (tail 1) stops before it and a second one (tail 2) takes it in quarters. Both decide
     // from T. The second one's XCDs take a run of quarters each.
-    int t_lo = 0, U = T;
+    int t_lo = 0, U = kSplit && mp.split > 1 ? T * mp.split : T;
     if (p.tail != 0) {
       const int rem = T % p.P_big;
       const bool split = T > p.P_big && rem > 0 && 2 * rem <= p.P_big;
@@ -619,21 +635,25 @@ struct MxRing {
 
     MxTileInfo ti;
     Src s;
+    int steps;
     // The tile's operands, and its first transfers: stage 0 and the first scales.
     auto begin_tile = [&](int t) {
       ti = decode(mp, t, gstart, t_lo);
       int lane = lane_id;
       asm volatile("" : "+v"(lane));  // (lane offsets are not kept across the main loop)
-      init<kInstrA>(s.la, wave, lane, ti.row_end - ti.m0, (int)p.lda, (int)p.lda);
-      init<kInstrB>(s.lb, wave, lane, p.N - ti.n0, (int)p.ldb, (int)p.ldb);
-      const int64_t ao = (int64_t)ti.m0 * p.lda, bo = (int64_t)ti.n0 * p.ldb;
+      const int q0 = kSplit ? ti.slice * mp.per : 0;  // the slice's first scale tile, four steps each
+      const int ka = q0 * 4 * A::kStepBytes, kb = q0 * 4 * B::kStepBytes;
+      steps = kSplit && mp.split > 1 ? min(mp.per * 4, mp.steps - q0 * 4) : mp.steps;
+      init<kInstrA>(s.la, wave, lane, ti.row_end - ti.m0, (int)p.lda, (int)p.lda - ka);
+      init<kInstrB>(s.lb, wave, lane, p.N - ti.n0, (int)p.ldb, (int)p.ldb - kb);
+      const int64_t ao = (int64_t)ti.m0 * p.lda + ka, bo = (int64_t)ti.n0 * p.ldb + kb;
       s.a = make_rsrc((const char*)p.A + ao, p.a_bytes - ao);
       s.b = make_rsrc((const char*)p.B + (int64_t)ti.g * p.b_bytes + bo, p.b_bytes - bo);
-      s.nsb = mp.nsb;
+      s.nsb = mp.nsb - q0;
       const bool is_a = wave < BM / 64;  // (waves past (BM + BN) / 64 move no scales)
       const int first = is_a ? ti.m0 : ti.n0;  // row of the tile's first scale
       const int i = (is_a ? wave : wave - BM / 64) * 64 + lane;  // row of the tile
-      const int64_t so = (int64_t)(first >> 6) * mp.nsb * 1024;
+      const int64_t so = ((int64_t)(first >> 6) * mp.nsb + q0) * 1024;
       s.s = make_rsrc(is_a ? mp.sa + so : mp.sb + (int64_t)ti.g * mp.sb_bytes + so,
                       (is_a ? mp.sa_bytes : mp.sb_bytes) - so);
       const int rr = (first & 63) + i;
@@ -664,13 +684,13 @@ struct MxRing {
       Frags f;
       if (idle) {
         __builtin_amdgcn_s_setprio(0);
-        mainloop<false>(acc, f, smem, o, s, mp.steps, wave);
+        mainloop<false>(acc, f, smem, o, s, steps, wave);
       } else {
 #pragma unroll
         for (int r = 0; r < kRA - 1; ++r) read_a<0>(f, smem, o, r, 0);
 #pragma unroll
         for (int c = 0; c < kNI; ++c) read_b<0>(f, smem, o, c, 0);
-        mainloop<true>(acc, f, smem, o, s, mp.steps, wave);
+        mainloop<true>(acc, f, smem, o, s, steps, wave);
       }
       dma_barrier();  // transfers past K have landed and every wave has left the ring
       const MxTileInfo done = ti;
@@ -679,7 +699,7 @@ struct MxRing {
       asm volatile("" ::: "memory");  // (its transfers are issued before the epilogue's stores)
       __builtin_amdgcn_sched_barrier(0);
       stores = false;
-      if (!idle) stores = epilogue(p, done, acc, smem + kABytes + wave * kRegion, lane_id, wm0, wn0);
+      if (!idle) stores = epilogue(mp, done, acc, smem + kABytes + wave * kRegion, lane_id, wm0, wn0);
     }
   }
 };
@@ -754,6 +774,8 @@ struct MxDirect {
     __shared__ __attribute__((aligned(16))) float sums[NW * kPlane];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     int g = 0, m0 = blockIdx.y * kBM, row_end = p.M;
+    // this workgroup's scale tiles [t0, t1)
+    const int slice = VM ? 0 : blockIdx.z, t0 = VM ? 0 : slice * mp.per, t1 = VM ? mp.nsb : min(mp.nsb, t0 + mp.per);
     const int n0 = blockIdx.x * kBN;
     if constexpr (VM) {
       // the group of row block blockIdx.y: 64 groups a pass, one a lane; the whole array is
@@ -799,9 +821,9 @@ struct MxDirect {
     const int64_t sao = (int64_t)(m0 >> 6) * mp.nsb * 1024, sbo = (int64_t)(n0 >> 6) * mp.nsb * 1024;
     s.sa = make_rsrc(mp.sa + sao, mp.sa_bytes - sao);
     s.sb = make_rsrc(mp.sb + (int64_t)g * mp.sb_bytes + sbo, mp.sb_bytes - sbo);
-    s.nsb = mp.nsb;
-    s.ka = (int)p.lda - kg * 16;
-    s.kb = (int)p.ldb - kg * 16;
+    s.nsb = t1;
+    s.ka = min((int)p.lda, t1 * 4 * MxFmt<FA>::kStepBytes) - kg * 16;
+    s.kb = min((int)p.ldb, t1 * 4 * MxFmt<FB>::kStepBytes) - kg * 16;
 #pragma unroll
     for (int i = 0; i < MB; ++i) {
       const int row = i * 16 + r, q = (m0 & 63) + row;
@@ -820,14 +842,14 @@ struct MxDirect {
 #pragma unroll
       for (int j = 0; j < NB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    if (wave < mp.nsb) {
+    if (t0 + wave < t1) {
       const uint32_t sel = (uint32_t)kg | ((uint32_t)(4 + kg) << 8) | 0x0C0C0000u;  // (0x0C: a zero byte)
       Scales sc;
-      fetch_scales(sc, s, wave);
+      fetch_scales(sc, s, t0 + wave);
       Buf buf[D];
 #pragma unroll
-      for (int t = 0; t < D; ++t) fetch(buf[t], s, wave * 4 + t);
-      for (int tile = wave; tile < mp.nsb; tile += NW) {
+      for (int t = 0; t < D; ++t) fetch(buf[t], s, (t0 + wave) * 4 + t);
+      for (int tile = t0 + wave; tile < t1; tile += NW) {
         int sa[MB], sb[NB];
 #pragma unroll
         for (int i = 0; i < MB; ++i) sa[i] = gather_scale(sc.a[i], sel);
@@ -859,7 +881,10 @@ struct MxDirect {
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] += x[e], v[4 + e] += y[e];
       }
-      if (m0 + row < row_end && n0 + col < p.N) mx_finish8(p, m0 + row, n0 + col, v);
+      if (m0 + row < row_end && n0 + col < p.N) {
+        if (!VM && mp.split > 1) mx_slice8(mp, slice, m0 + row, n0 + col, v);
+        else mx_finish8(p, m0 + row, n0 + col, v);
+      }
     }
   }
 };
@@ -873,8 +898,7 @@ __global__ __launch_bounds__(NW * 64) void mx_direct_kernel(const MxParams p) {
   MxDirect<MB, NB, NW, D, FA, FB, VM>::run(p);
 }
 
-// Launch tile kind `tile` (an MxTile) of one pair of formats; grid: workgroups of a ring kernel, or
-// x (columns) by y (rows) of a direct one.
+// The kernels (launch configuration by mx_plan.cpp).
 template <int FA, int FB, bool VM>
 hipError_t mx_launch(int32_t tile, const MxParams& p, dim3 grid, hipStream_t s);
 
@@ -882,12 +906,12 @@ hipError_t mx_launch(int32_t tile, const MxParams& p, dim3 grid, hipStream_t s);
   template <>                                                                                        \
   hipError_t mx_launch<FA, FB, VM>(int32_t tile, const MxParams& p, dim3 grid, hipStream_t s) {      \
     switch (tile) {                                                                                  \
-      case MX_T_256: mx_ring_kernel<256, 256, 8, FA, FB, VM><<<grid, 512, 0, s>>>(p); break;         \
-      case MX_T_256X128: mx_ring_kernel<256, 128, 8, FA, FB, VM><<<grid, 512, 0, s>>>(p); break;     \
-      case MX_T_128: mx_ring_kernel<128, 128, 4, FA, FB, VM><<<grid, 256, 0, s>>>(p); break;         \
-      case MX_T_64: mx_direct_kernel<4, 4, 4, 2, FA, FB, VM><<<grid, 256, 0, s>>>(p); break;         \
-      case MX_T_R32: mx_direct_kernel<2, 2, 8, 2, FA, FB, VM><<<grid, 512, 0, s>>>(p); break;        \
-      case MX_T_R16: mx_direct_kernel<1, 1, 8, 4, FA, FB, VM><<<grid, 512, 0, s>>>(p); break;        \
+      case MX_TILE_256: mx_ring_kernel<256, 256, 8, FA, FB, VM><<<grid, 512, 0, s>>>(p); break;      \
+      case MX_TILE_128: mx_ring_kernel<128, 128, 4, FA, FB, VM><<<grid, 256, 0, s>>>(p); break;      \
+      case MX_TILE_32X64: mx_direct_kernel<2, 4, 4, 2, FA, FB, VM><<<grid, 256, 0, s>>>(p); break;   \
+      case MX_TILE_32: mx_direct_kernel<2, 2, 4, 2, FA, FB, VM><<<grid, 256, 0, s>>>(p); break;      \
+      case MX_TILE_16X32: mx_direct_kernel<1, 2, 8, 2, FA, FB, VM><<<grid, 512, 0, s>>>(p); break;   \
+      case MX_TILE_16: mx_direct_kernel<1, 1, 8, 2, FA, FB, VM><<<grid, 512, 0, s>>>(p); break;      \
       default: return hipErrorInvalidValue;                                                          \
     }                                                                                                \
     return hipGetLastError();                                                                        \

@@ -36,10 +36,10 @@ gemm_status check_out(const char* name, int32_t dt, int64_t ld, int32_t M, int32
 void mx_tile_extent(int32_t tile, int32_t* bm, int32_t* bn) {
   switch (tile) {
     case MX_TILE_256: *bm = *bn = 256; break;
-    case MX_TILE_256X128: *bm = 256; *bn = 128; break;
     case MX_TILE_128: *bm = *bn = 128; break;
-    case MX_TILE_64: *bm = *bn = 64; break;
-    case MX_TILE_ROWS_32: *bm = *bn = 32; break;
+    case MX_TILE_32X64: *bm = 32; *bn = 64; break;
+    case MX_TILE_32: *bm = *bn = 32; break;
+    case MX_TILE_16X32: *bm = 16; *bn = 32; break;
     default: *bm = *bn = 16; break;
   }
 }
@@ -51,14 +51,27 @@ int64_t mx_row_blocks(const mx_gemm_plan& p, int32_t bm) {
   return m / bm + (m < p.d.groups ? m : p.d.groups);
 }
 
-int32_t mx_choose_tile(const mx_gemm_plan& p, int32_t cus) {
-  if (p.d.tile != MX_TILE_AUTO) return p.d.tile;
+MxChoice mx_choose(const mx_gemm_plan& p, int32_t cus, bool workspace) {
+  MxChoice c{p.d.tile, 1, 0};
+  const int32_t nsb = (int32_t)cdiv(p.d.K, 512);
   const int64_t rows = p.d.groups ? cdiv(p.d.M, p.d.groups) : p.d.M;
-  if (rows <= 16) return MX_TILE_ROWS_16;
-  if (rows <= 32) return MX_TILE_ROWS_32;
-  if (mx_row_blocks(p, 256) * cdiv(p.d.N, 256) >= cus) return MX_TILE_256;
-  if (mx_row_blocks(p, 128) * cdiv(p.d.N, 128) >= cus / 2) return MX_TILE_128;
-  return MX_TILE_64;
+  if (c.tile == MX_TILE_AUTO) {
+    if (rows <= 16) c.tile = MX_TILE_16;
+    else if (rows <= 32) c.tile = MX_TILE_16X32;
+    else if (rows <= 64) c.tile = MX_TILE_32;
+    else if (mx_row_blocks(p, 256) * cdiv(p.d.N, 256) >= cus) c.tile = MX_TILE_256;
+    else if (mx_row_blocks(p, 128) * cdiv(p.d.N, 128) >= cus / 2) c.tile = MX_TILE_128;
+    else c.tile = MX_TILE_32X64;
+  }
+  if (!p.d.groups && workspace && c.tile != MX_TILE_256 && p.d.split > 1) c.split = p.d.split;
+  if (c.split > nsb) c.split = nsb > 1 ? nsb : 1;
+  c.per = nsb > 0 ? (int32_t)cdiv(nsb, c.split) : 1;
+  c.split = nsb > 0 ? (int32_t)cdiv(nsb, c.per) : 1;
+  return c;
+}
+
+int64_t mx_workspace_bytes(const mx_gemm_plan& p, const MxChoice& c) {
+  return c.split > 1 ? (int64_t)c.split * p.d.M * p.d.N * 4 : 0;
 }
 
 }  // namespace gep
@@ -92,7 +105,10 @@ gemm_status mx_gemm_create(const mx_gemm_desc* d, mx_gemm_plan** out) {
   if (d->d == GEMM_DT_NONE && d->post == GEMM_DT_NONE) return fail(GEMM_ERR_INVALID_ARG, "mx_gemm_create: neither D nor PostAct");
   if (d->act < GEMM_ACT_NONE || d->act > GEMM_ACT_SILU) return fail(GEMM_ERR_INVALID_ARG, "mx_gemm_create: unknown activation %d", d->act);
   if (d->act != GEMM_ACT_NONE && d->post == GEMM_DT_NONE) return fail(GEMM_ERR_INVALID_ARG, "mx_gemm_create: an activation without PostAct");
-  if (d->tile < MX_TILE_AUTO || d->tile > MX_TILE_256X128) return fail(GEMM_ERR_INVALID_ARG, "mx_gemm_create: unknown tile %d", d->tile);
+  if (d->tile < MX_TILE_AUTO || d->tile > MX_TILE_16) return fail(GEMM_ERR_INVALID_ARG, "mx_gemm_create: unknown tile %d", d->tile);
+  if (d->split < 0 || d->split > 64) return fail(GEMM_ERR_INVALID_ARG, "mx_gemm_create: split must lie in [0, 64]");
+  if (d->split > 1 && (d->groups || d->tile == MX_TILE_256))
+    return fail(GEMM_ERR_UNSUPPORTED, "mx_gemm_create: a grouped plan and MX_TILE_256 do not split K");
   if (d->N % 8) return fail(GEMM_ERR_ALIGNMENT, "mx_gemm_create: N = %d is not a multiple of 8", d->N);
   // (256 rows of codes stay below 2^31 bytes: the kernels' offsets inside a tile are 32-bit)
   if (d->K > (1 << 22)) return fail(GEMM_ERR_UNSUPPORTED, "mx_gemm_create: K above 2^22");
@@ -111,7 +127,7 @@ gemm_status mx_gemm_create(const mx_gemm_desc* d, mx_gemm_plan** out) {
   p->sb_bytes = mx_scale_bytes(d->N, d->K);
   int32_t bm, bn;
   mx_tile_extent(MX_TILE_128, &bm, &bn);
-  if (mx_row_blocks(*p, bm) * cdiv(d->N, bn) > 0x3FFFFFFF) {
+  if (mx_row_blocks(*p, bm) * cdiv(d->N, bn) > 0xFFFFFF) {
     delete p;
     return fail(GEMM_ERR_UNSUPPORTED, "mx_gemm_create: too many output tiles");
   }
@@ -126,9 +142,18 @@ gemm_status mx_gemm_destroy(mx_gemm_plan* plan) {
   return GEMM_OK;
 }
 
-gemm_status mx_gemm_plan_tile(const mx_gemm_plan* plan, int32_t num_cus, int32_t* tile) {
-  if (!plan || !tile || num_cus < 1) return fail(GEMM_ERR_INVALID_ARG, "mx_gemm_plan_tile: NULL argument or no compute units");
-  *tile = mx_choose_tile(*plan, num_cus);
+gemm_status mx_gemm_plan_tile(const mx_gemm_plan* plan, int32_t num_cus, int32_t* tile, int32_t* split) {
+  if (!plan || num_cus < 1) return fail(GEMM_ERR_INVALID_ARG, "mx_gemm_plan_tile: NULL plan or no compute units");
+  const MxChoice c = mx_choose(*plan, num_cus, true);
+  if (tile) *tile = c.tile;
+  if (split) *split = c.split;
+  clear_error();
+  return GEMM_OK;
+}
+
+gemm_status mx_gemm_workspace(const mx_gemm_plan* plan, int32_t num_cus, int64_t* bytes) {
+  if (!plan || !bytes || num_cus < 1) return fail(GEMM_ERR_INVALID_ARG, "mx_gemm_workspace: NULL argument or no compute units");
+  *bytes = mx_workspace_bytes(*plan, mx_choose(*plan, num_cus, true));
   clear_error();
   return GEMM_OK;
 }

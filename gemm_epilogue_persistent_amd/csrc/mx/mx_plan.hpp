@@ -13,9 +13,14 @@ struct mx_gemm_plan {
 };
 
 namespace gep {
-// The tile a plan runs with `cus` compute units (an mx_tile, never AUTO), and its rows and columns.
-int32_t mx_choose_tile(const mx_gemm_plan& p, int32_t cus);
+// How a plan runs on `cus` compute units: the tile (an mx_tile, never AUTO), over how many
+// workgroups a tile's K is shared out, and the scale tiles (512 values of K) of each.
+struct MxChoice {
+  int32_t tile, split, per;
+};
+MxChoice mx_choose(const mx_gemm_plan& p, int32_t cus, bool workspace);
 void mx_tile_extent(int32_t tile, int32_t* bm, int32_t* bn);
 // Upper bound of the row blocks of a tile of bm rows over all groups (exact for a dense plan).
 int64_t mx_row_blocks(const mx_gemm_plan& p, int32_t bm);
+int64_t mx_workspace_bytes(const mx_gemm_plan& p, const MxChoice& c);
 }  // namespace gep

@@ -193,10 +193,15 @@ class MxPlan:
     memory; reusable, from several streams too). a (m, k); b (n, k), or (G, n, k) with
     cu_seqlens_m: int32 of G + 1 row offsets on the GPU, whose values are read by each run. n is a
     multiple of 8. C, D, PostAct: 16- or 32-bit floats, rows contiguous, row strides of whole 16
-    bytes; at least one of D, PostAct. tile: "auto", or the kernel to use ("256", "256x128", "128",
-    "64", "rows32", "rows16")."""
+    bytes; at least one of D, PostAct. tile, split: "auto" and 0, or the kernel to use ("256", "128",
+    "32x64", "32", "16x32", "16") and over how many workgroups it shares out a tile's K.
 
-    def __init__(self, a, b, C=None, D=None, PostAct=None, act="none", cu_seqlens_m=None, tile="auto"):
+    Where K is shared out, the plan keeps the workspace for the partial sums: runs of one plan on
+    several streams that may overlap need a workspace each (a uint8 tensor of
+    plan.workspace_bytes)."""
+
+    def __init__(self, a, b, C=None, D=None, PostAct=None, act="none", cu_seqlens_m=None, tile="auto",
+                 split=0):
         self.handle = None
         self._sig = self._signature(a, b, C, D, PostAct, cu_seqlens_m)
         _plain_mx("a", a)
@@ -224,18 +229,25 @@ class MxPlan:
         d.c, d.ldc = _out("C", C, shape, a.device)
         d.d, d.ldd = _out("D", D, shape, a.device)
         d.post, d.ldp = _out("PostAct", PostAct, shape, a.device)
-        d.act, d.tile = ACT[act], MX_TILE[tile]
+        d.act, d.tile, d.split = ACT[act], MX_TILE[tile], int(split)
         self.desc, self.device = d, a.device
         self._lib = _abi.load()
         h = ctypes.c_void_p()
         _abi.check(self._lib.mx_gemm_create(ctypes.byref(d), ctypes.byref(h)))
         self.handle = h
+        n = ctypes.c_int64()
+        _abi.check(self._lib.mx_gemm_workspace(h, self._cus(), ctypes.byref(n)))
+        self.workspace_bytes = n.value
+        self._workspace = torch.empty(n.value, dtype=torch.uint8, device=a.device) if n.value else None
 
     def __del__(self):
         h = getattr(self, "handle", None)
         if h is not None and h.value:
             self._lib.mx_gemm_destroy(h)
             self.handle = None
+
+    def _cus(self):
+        return torch.cuda.get_device_properties(self.device).multi_processor_count
 
     @staticmethod
     def _check_cu(cu, b, device):
@@ -249,28 +261,32 @@ class MxPlan:
         return (a.fmt, a.codes.shape, a.k, a.device, b.fmt, b.codes.shape, b.device) + tuple(
             None if t is None else (t.dtype, t.shape, t.stride(), t.device) for t in (C, D, PostAct, cu))
 
-    def run(self, a, b, C=None, D=None, PostAct=None, cu_seqlens_m=None, stream=None):
+    def run(self, a, b, C=None, D=None, PostAct=None, cu_seqlens_m=None, stream=None, workspace=None):
         """Enqueue on `stream` (default: torch's current stream of the operands' device). The
-        tensors are laid out as those the plan was made for."""
+        tensors are laid out as those the plan was made for. workspace: instead of the plan's own."""
         if self._signature(a, b, C, D, PostAct, cu_seqlens_m) != self._sig:
             raise ValueError("the operands are not laid out as those this plan was made for")
+        if workspace is None:
+            workspace = self._workspace
+        elif workspace.device != self.device or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+            raise ValueError("workspace: contiguous uint8 tensor on the operands' GPU expected")
         args = _abi.MxGemmArgs(a.codes.data_ptr(), a.scales.data_ptr(), b.codes.data_ptr(), b.scales.data_ptr(),
-                               *(None if t is None else t.data_ptr() for t in (C, D, PostAct, cu_seqlens_m)))
+                               *(None if t is None else t.data_ptr() for t in (C, D, PostAct, cu_seqlens_m, workspace)),
+                               0 if workspace is None else workspace.numel())
         _launch(self.device, stream, self._lib.mx_gemm_run, self.handle, ctypes.byref(args))
 
     def tile(self, num_cus=None):
-        """The kernel this plan runs on a device with num_cus compute units."""
-        if num_cus is None:
-            num_cus = torch.cuda.get_device_properties(self.device).multi_processor_count
-        t = ctypes.c_int32()
-        _abi.check(self._lib.mx_gemm_plan_tile(self.handle, int(num_cus), ctypes.byref(t)))
-        return next(k for k, v in MX_TILE.items() if v == t.value)
+        """(kernel, split) this plan runs with on a device with num_cus compute units."""
+        t, n = ctypes.c_int32(), ctypes.c_int32()
+        _abi.check(self._lib.mx_gemm_plan_tile(self.handle, int(num_cus or self._cus()), ctypes.byref(t), ctypes.byref(n)))
+        return next(k for k, v in MX_TILE.items() if v == t.value), n.value
 
 
-def mx_gemm(a, b, D=None, C=None, PostAct=None, act="none", cu_seqlens_m=None, stream=None, tile="auto"):
+def mx_gemm(a, b, D=None, C=None, PostAct=None, act="none", cu_seqlens_m=None, stream=None, tile="auto",
+            split=0):
     """One-shot product: plan and enqueue. Without D and PostAct, D is allocated in bf16. Returns
     D, or PostAct without D."""
     if D is None and PostAct is None:
         D = torch.empty((a.rows, b.rows), dtype=torch.bfloat16, device=a.device)
-    MxPlan(a, b, C, D, PostAct, act, cu_seqlens_m, tile).run(a, b, C, D, PostAct, cu_seqlens_m, stream)
+    MxPlan(a, b, C, D, PostAct, act, cu_seqlens_m, tile, split).run(a, b, C, D, PostAct, cu_seqlens_m, stream)
     return D if D is not None else PostAct

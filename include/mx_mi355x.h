@@ -118,13 +118,15 @@ int64_t rmsnorm_backward_workspace(int32_t rows, int32_t cols);
  * D or PostAct itself. tile: 0 lets the library choose; otherwise one of the MX_TILE values. */
 typedef enum {
   MX_TILE_AUTO = 0,
-  MX_TILE_256 = 1,    /* 256x256 outputs, operands staged through LDS               */
-  MX_TILE_128 = 2,    /* 128x128 outputs, operands staged through LDS               */
-  MX_TILE_64 = 3,     /* 64x64 outputs, K split over the waves of a workgroup       */
-  MX_TILE_ROWS_32 = 4,/* 32 rows x 32 columns, K split over the waves               */
-  MX_TILE_ROWS_16 = 5,/* 16 rows x 16 columns, K split over the waves               */
-  MX_TILE_256X128 = 6 /* 256x128 outputs, operands staged through LDS               */
+  MX_TILE_256 = 1,   /* 256x256 outputs a workgroup, operands staged through LDS         */
+  MX_TILE_128 = 2,   /* 128x128, the same                                                */
+  MX_TILE_32X64 = 3, /* 32 rows x 64 columns, the waves of a workgroup share out K       */
+  MX_TILE_32 = 4,    /* 32x32, the same                                                  */
+  MX_TILE_16X32 = 5, /* 16 rows x 32 columns, the same                                   */
+  MX_TILE_16 = 6     /* 16x16, the same                                                  */
 } mx_tile;
+/* split: how many workgroups share out the K of a tile: 0 lets the library choose, 1 one. More
+ * than one needs a dense plan, a tile other than MX_TILE_256 and the workspace at run time. */
 typedef struct {
   int32_t M, N, K;
   int32_t groups; /* 0: dense */
@@ -132,6 +134,7 @@ typedef struct {
   int32_t c, d, post;         /* gemm_dtype (NONE: absent) */
   int32_t act;                /* gemm_act; NONE without post */
   int32_t tile;               /* mx_tile */
+  int32_t split;
   int64_t ldc, ldd, ldp;
 } mx_gemm_desc;
 typedef struct {
@@ -143,16 +146,22 @@ typedef struct {
   void* D;
   void* PostAct;
   const int32_t* cu_seqlens_m; /* grouped plans */
+  void* workspace;             /* mx_gemm_workspace bytes, 16-byte aligned, or NULL: K is not split */
+  int64_t workspace_bytes;
 } mx_gemm_args;
 typedef struct mx_gemm_plan mx_gemm_plan;
 
 /* Validate and build a plan (host memory only, no HIP call; may be used from several threads and
- * streams at once). Errors as gemm_create. */
+ * streams at once, by runs that overlap with a workspace each). Errors as gemm_create. */
 gemm_status mx_gemm_create(const mx_gemm_desc* desc, mx_gemm_plan** out);
 gemm_status mx_gemm_run(const mx_gemm_plan* plan, const mx_gemm_args* args, void* stream);
 gemm_status mx_gemm_destroy(mx_gemm_plan* plan);
-/* The tile (mx_tile) the plan runs on a device with num_cus compute units. */
-gemm_status mx_gemm_plan_tile(const mx_gemm_plan* plan, int32_t num_cus, int32_t* tile);
+/* The tile (mx_tile) and the split the plan runs with on a device with num_cus compute units, given
+ * its workspace. Either pointer may be NULL. */
+gemm_status mx_gemm_plan_tile(const mx_gemm_plan* plan, int32_t num_cus, int32_t* tile, int32_t* split);
+/* Bytes of workspace a run takes on such a device (0 for most shapes). Its contents need no
+ * preparation, and runs that follow each other on a stream may share it. */
+gemm_status mx_gemm_workspace(const mx_gemm_plan* plan, int32_t num_cus, int64_t* bytes);
 
 #ifdef __cplusplus
 }

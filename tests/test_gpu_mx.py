@@ -202,7 +202,7 @@ def largest(v):
     return np.abs(R.blocks(v)).max(-1)
 
 
-def run_product(M, N, K, fa, fb, tile, c=None, d="f32", post=None, act="none", sizes=None, seed=0, scale=1.0):
+def run_product(M, N, K, fa, fb, tile, c=None, d="f32", post=None, act="none", sizes=None, seed=0, scale=1.0, split=1):
     ca, sa = operand(seed + 1, M, K, fa)
     va = R.values(ca, sa, fa, K)
     G = len(sizes) if sizes is not None else None
@@ -232,7 +232,8 @@ def run_product(M, N, K, fa, fb, tile, c=None, d="f32", post=None, act="none", s
         mag = mag + np.abs(C.double().cpu().numpy())
     D, dbuf = guarded(M, N, d) if d else (None, None)
     P, pbuf = guarded(M, N, post) if post else (None, None)
-    plan = gep.MxPlan(a, b, C, D, P, act=act, cu_seqlens_m=cu, tile=tile)
+    plan = gep.MxPlan(a, b, C, D, P, act=act, cu_seqlens_m=cu, tile=tile, split=split)
+    assert split == 1 or (plan.tile()[1] > 1) == (K > 512)
     plan.run(a, b, C, D, P, cu_seqlens_m=cu)
     torch.cuda.synchronize()
     bound = (K + 1) * 2.0 ** -24 * mag
@@ -246,7 +247,7 @@ def run_product(M, N, K, fa, fb, tile, c=None, d="f32", post=None, act="none", s
         check_product(P, R.act(x, act), bound, post, act, x)
 
 
-TILES = ["256", "256x128", "128", "64", "rows32", "rows16"]
+TILES = ["256", "128", "32x64", "32", "16x32", "16"]
 
 
 @pytest.mark.parametrize("tile", TILES)
@@ -265,6 +266,14 @@ def test_product_depths(K, tile):
     announce(f"product depth {K} tile {tile}")
     run_product(40, 72, K, "e4m3", "e2m1", tile, seed=K)
     run_product(24, 72, K, "e2m1", "e2m1", tile, seed=K + 1)
+
+
+@pytest.mark.parametrize("tile", TILES[1:])
+@pytest.mark.parametrize("fa,fb", [("e4m3", "e2m1"), ("e2m1", "e2m1"), ("e4m3", "e4m3")])
+@pytest.mark.parametrize("M,N,K,split", [(1, 8, 520, 2), (70, 136, 1000, 2), (150, 264, 2100, 5), (33, 72, 4128, 9), (40, 40, 500, 4)])
+def test_product_split_k(M, N, K, split, fa, fb, tile):
+    announce(f"product split K {M}x{N}x{K} / {split} {fa} x {fb} tile {tile}")
+    run_product(M, N, K, fa, fb, tile, c="bf16", d="f32", post="bf16", act="silu", split=split, seed=31)
 
 
 @pytest.mark.parametrize("fa", FORMATS)
@@ -363,10 +372,43 @@ def test_product_in_place_and_stream():
     plan.run(a, b, D, D, stream=s)
     s.synchronize()
     assert torch.equal(D, want)
+    split = gep.MxPlan(a, gep.mx_empty(64, 500, "e4m3"), None, D, split=2)
+    assert split.tile()[1] == 1 and split.workspace_bytes == 0  # one scale tile cannot be shared out
     with pytest.raises(ValueError):
         plan.run(a, b, D, D.t())
     with pytest.raises(ValueError):
         plan.run(a, b, None, D)
+
+
+def test_workspace():
+    """A given workspace is used; one that is too small is refused; without one in the C ABI K is
+    not split; runs repeat bit for bit."""
+    announce("product workspace")
+    import ctypes
+    from gemm_epilogue_persistent_amd import _abi
+    a = gep.mx_quantize(torch.randn(40, 2048, device="cuda"), "e4m3")
+    b = gep.mx_quantize(torch.randn(64, 2048, device="cuda"), "e4m3")
+    D, E = torch.empty(40, 64, device="cuda"), torch.empty(40, 64, device="cuda")
+    plan = gep.MxPlan(a, b, None, D, tile="32", split=4)
+    assert plan.workspace_bytes == 4 * 40 * 64 * 4
+    plan.run(a, b, None, D)
+    ws = torch.full((plan.workspace_bytes,), 255, dtype=torch.uint8, device="cuda")
+    plan.run(a, b, None, E, workspace=ws)
+    assert torch.equal(D, E)
+    assert torch.equal(ws.view(torch.float32).view(4, 40, 64).double().sum(0).float(), E) or (
+        (ws.view(torch.float32).view(4, 40, 64).sum(0) - E).abs().max() <= 1e-5 * E.abs().max())
+    with pytest.raises(gep.GemmError):
+        plan.run(a, b, None, E, workspace=ws[:-16])
+    with pytest.raises(gep.GemmError):
+        plan.run(a, b, None, E, workspace=torch.empty(plan.workspace_bytes + 16, dtype=torch.uint8, device="cuda")[8:])
+    with pytest.raises(ValueError):
+        plan.run(a, b, None, E, workspace=ws.float())
+    args = _abi.MxGemmArgs(a.codes.data_ptr(), a.scales.data_ptr(), b.codes.data_ptr(), b.scales.data_ptr(), None,
+                           E.data_ptr(), None, None, None, 0)
+    E.zero_()
+    _abi.check(_abi.load().mx_gemm_run(plan.handle, ctypes.byref(args), torch.cuda.current_stream().cuda_stream))
+    want = gep.mx_gemm(a, b, torch.empty_like(E), tile="32", split=1)
+    assert torch.equal(E, want)
 
 
 def test_python_refusals():

@@ -126,7 +126,7 @@ def test_backward_workspace():
 
 
 def gemm_desc(**kw):
-    d = _abi.MxGemmDesc(M=64, N=64, K=100, groups=0, a_format=1, b_format=0, c=2, d=2, post=2, act=4, tile=0, ldc=64,
+    d = _abi.MxGemmDesc(M=64, N=64, K=100, groups=0, a_format=1, b_format=0, c=2, d=2, post=2, act=4, tile=0, split=0, ldc=64,
                         ldd=64, ldp=64)
     for k, v in kw.items():
         setattr(d, k, v)
@@ -136,7 +136,8 @@ def gemm_desc(**kw):
 @pytest.mark.parametrize("kw,status", [
     (dict(), 0), (dict(K=0), 0), (dict(M=0), 0), (dict(c=0), 0), (dict(d=3), 0), (dict(groups=1024), 0),
     (dict(M=-1), 1), (dict(groups=-1), 1), (dict(groups=1025), 2), (dict(a_format=2), 1), (dict(b_format=-1), 1),
-    (dict(d=9), 1), (dict(d=0, post=0, act=0), 1), (dict(act=5), 1), (dict(post=0), 1), (dict(tile=7), 1), (dict(tile=-1), 1),
+    (dict(d=9), 1), (dict(d=0, post=0, act=0), 1), (dict(act=5), 1), (dict(post=0), 1), (dict(tile=7), 1), (dict(tile=-1), 1), (dict(split=-1), 1), (dict(split=65), 1),
+    (dict(split=2, groups=2), 2), (dict(split=2, tile=1), 2),
     (dict(N=60), 3), (dict(K=(1 << 22) + 1), 2), (dict(d=4), 2), (dict(c=5), 2), (dict(ldd=56), 1), (dict(ldd=-8), 1),
     (dict(ldp=68), 3), (dict(ldc=1 << 49), 2), (dict(M=2 ** 31 - 1, N=1 << 20, ldc=1 << 20, ldd=1 << 20, ldp=1 << 20), 2),
 ])
@@ -158,7 +159,7 @@ def test_gemm_create_refusals(lib, kw, status):
 def test_gemm_run_refusals(lib, kw, status):
     h = ctypes.c_void_p()
     assert lib.mx_gemm_create(ctypes.byref(gemm_desc()), ctypes.byref(h)) == 0
-    a = _abi.MxGemmArgs(P, P, P, P, P, P, P, None)
+    a = _abi.MxGemmArgs(P, P, P, P, P, P, P, None, None, 0)
     for k, v in kw.items():
         setattr(a, k, v)
     assert lib.mx_gemm_run(h, ctypes.byref(a), None) == status and lib.gemm_last_error()
@@ -167,7 +168,7 @@ def test_gemm_run_refusals(lib, kw, status):
     lib.mx_gemm_destroy(h)
     # a grouped plan wants its offsets; an empty problem wants nothing
     assert lib.mx_gemm_create(ctypes.byref(gemm_desc(groups=2)), ctypes.byref(h)) == 0
-    a = _abi.MxGemmArgs(P, P, P, P, P, P, P, None)
+    a = _abi.MxGemmArgs(P, P, P, P, P, P, P, None, None, 0)
     assert lib.mx_gemm_run(h, ctypes.byref(a), None) == _abi.INVALID_ARG
     a.cu_seqlens_m = P + 2
     assert lib.mx_gemm_run(h, ctypes.byref(a), None) == _abi.ALIGNMENT
@@ -179,18 +180,27 @@ def test_gemm_run_refusals(lib, kw, status):
 
 
 def test_plan_tile(lib):
-    def tile(cus=256, **kw):
-        h, t = ctypes.c_void_p(), ctypes.c_int32()
+    def choice(cus=256, **kw):
+        h, t, n, b = ctypes.c_void_p(), ctypes.c_int32(), ctypes.c_int32(), ctypes.c_int64()
         assert lib.mx_gemm_create(ctypes.byref(gemm_desc(**kw)), ctypes.byref(h)) == 0
-        assert lib.mx_gemm_plan_tile(h, cus, ctypes.byref(t)) == 0
-        assert lib.mx_gemm_plan_tile(h, 0, ctypes.byref(t)) == _abi.INVALID_ARG
+        assert lib.mx_gemm_plan_tile(h, cus, ctypes.byref(t), ctypes.byref(n)) == 0
+        assert lib.mx_gemm_workspace(h, cus, ctypes.byref(b)) == 0
+        assert lib.mx_gemm_plan_tile(h, 0, ctypes.byref(t), None) == _abi.INVALID_ARG
+        assert lib.mx_gemm_workspace(h, 0, ctypes.byref(b)) == _abi.INVALID_ARG
+        assert lib.mx_gemm_workspace(h, cus, None) == _abi.INVALID_ARG
         lib.mx_gemm_destroy(h)
-        return t.value
+        d = gemm_desc(**kw)
+        assert b.value == (n.value * d.M * d.N * 4 if n.value > 1 else 0)
+        return t.value, n.value
     wide = dict(ldc=8192, ldd=8192, ldp=8192)
     for want in range(1, 7):
-        assert tile(tile=want) == want
-    assert tile(M=8192, N=8192, **wide) == _abi.MX_TILE["256"]
-    assert tile(M=1, N=8192, **wide) == _abi.MX_TILE["rows16"]
+        assert choice(tile=want, split=1) == (want, 1)
+    assert choice(tile=2, split=3, K=4096) == (2, 3)
+    assert choice(tile=3, split=7, K=4096) == (3, 4)  # 8 scale tiles, two a slice
+    assert choice(tile=3, split=9, K=1000) == (3, 2)
+    assert choice(tile=3, split=9, K=0) == (3, 1)
+    assert choice(M=8192, N=8192, K=8192, **wide) == (_abi.MX_TILE["256"], 1)
+    assert choice(M=1, N=8192, K=8192, **wide) == (_abi.MX_TILE["16"], 1)
 
 
 def test_mx_tensor_refusals():
