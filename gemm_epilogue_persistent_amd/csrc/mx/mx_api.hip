@@ -106,6 +106,7 @@ extern "C" gemm_status mx_gemm_run(const mx_gemm_plan* plan, const mx_gemm_args*
   p.sa_bytes = plan->sa_bytes; p.sb_bytes = plan->sb_bytes;
   p.nsb = (d.K + 511) / 512;
   p.steps = (d.K + 127) / 128;
+  p.cus = cus;
   p.split = choice.split;
   p.per = choice.per;
   p.sums = (float*)a->workspace;

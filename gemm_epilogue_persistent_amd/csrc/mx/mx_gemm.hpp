@@ -32,6 +32,7 @@ struct MxParams {
   // writes its fp32 sums as matrix s of `sums`, (split, M, N), and mx_join_kernel adds them up
   int32_t split, per;
   float* sums;
+  int32_t cus;  // compute units of the device
 };
 
 template <int FMT>
@@ -131,73 +132,135 @@ struct MxTileInfo {
   int g, m0, n0, row_end, slice;
 };
 
+// The group that holds tile `want` when every group has ceil(rows / bm) * per tiles: its index, rows
+// [begin, end) and first tile. 64 groups a pass, one a lane; every lane gets the result. The whole
+// offset array is checked (0 .. M, never decreasing): if it is not such, or `want` is in no group, index
+// is -1 and first the number of tiles (0 for a bad array).
+struct MxGroup {
+  int index, begin, end, first;
+};
+__device__ __forceinline__ MxGroup mx_find_group(const KParams& p, int want, int bm, int per, int lane) {
+  MxGroup r{-1, 0, 0, 0};
+  int base = 0, bad = 0, first_hit = 0;
+  for (int g0 = 0; g0 < p.L; g0 += 64) {
+    const int gi = g0 + lane;
+    int c0 = 0, c1 = 0;
+    if (gi < p.L) {
+      c0 = p.cu_seqlens[gi];
+      c1 = p.cu_seqlens[gi + 1];
+      bad |= c1 < c0 || (gi == 0 && c0 != 0) || (gi == p.L - 1 && c1 != p.M);
+    }
+    const int tiles = c1 > c0 ? (int)(((int64_t)c1 - c0 + bm - 1) / bm) * per : 0;
+    int incl = tiles;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int u = __shfl_up(incl, off);
+      if (lane >= off) incl += u;
+    }
+    const int first = base + incl - tiles;
+    const uint64_t hit = __ballot(want >= first && want < first + tiles);
+    if (hit) {
+      const int src = __ffsll((unsigned long long)hit) - 1;
+      r.index = g0 + src;
+      r.begin = __shfl(c0, src);
+      r.end = __shfl(c1, src);
+      first_hit = __shfl(first, src);
+    }
+    base += __shfl(incl, 63);
+  }
+  if (__ballot(bad)) return MxGroup{-1, 0, 0, 0};
+  r.first = r.index >= 0 ? first_hit : base;
+  r.index = __builtin_amdgcn_readfirstlane(r.index);
+  r.begin = __builtin_amdgcn_readfirstlane(r.begin);
+  r.end = __builtin_amdgcn_readfirstlane(r.end);
+  r.first = __builtin_amdgcn_readfirstlane(r.first);
+  return r;
+}
+
 // ------------------------------------------------------------------------------------
 // MxRing
 // ------------------------------------------------------------------------------------
-// A stage holds 128 bytes of K per row: one step (128 values) of an E4M3 operand, a pair of
-// steps (256 values) of an E2M1 one; each operand has two stages. The scales of four steps (16
-// bytes a row, in storage order) go through a two-stage ring of their own. The loop runs quads of
-// four steps; steps past K read zero codes.
+// A stage holds kSPS steps (of 128 values of K) of both operands: two steps of two E2M1 operands
+// (128 bytes a row), else one (128 bytes a row of E4M3, 64 of E2M1). NS stages lie in LDS: one is
+// being multiplied, the next has landed or is landing, the others are on their way. The scales of
+// four steps (a quad; 16 bytes a row, in storage order) go through a two-stage ring of their own.
+// Steps past K read zero codes.
 //
 // A step is kMI x kNI MFMAs, row by row. kRA A fragments are held in a ring (block row r in r %
 // kRA; r is read after row r - kRA's last MFMA) and the kNI B fragments of the step, with kDB
 // those of the next step too. The barrier comes when every wave has read its last fragment of
-// the stage; after it the next step's first fragments are read and the first half of the
-// transfers into the freed stage goes out; the second half follows at the head of the next step.
-// (No barrier in the middle of a pair when both operands are E2M1: neither stage changes.)
-template <int BM, int BN, int NW, int FA, int FB, bool VM>
+// the stage; it also waits for the transfers of the next stage (those of later stages, issued
+// after them, may be outstanding). After it the next step's first fragments are read and the first
+// half of the transfers into the freed stage goes out; the second half follows at the head of the
+// next step.
+template <int BM, int BN, int NW, int NS, int FA, int FB, bool VM>
 struct MxRing {
   static constexpr int kThreads = NW * 64;
   static constexpr bool kSplit = BM == 128 && !VM;  // may run slices of K
   static constexpr int kWN = 64, kWavesN = BN / kWN, kWavesM = NW / kWavesN, kWM = BM / kWavesM;
   static constexpr int kMI = kWM / 16, kNI = kWN / 16;
-  static constexpr int kABytes = BM * kRowBytes, kBBytes = BN * kRowBytes;
-  static constexpr int kBOff = 2 * kABytes, kSOff = kBOff + 2 * kBBytes, kSBytes = (BM + BN) * 16;
+  using A = MxFmt<FA>;
+  using B = MxFmt<FB>;
+  static constexpr bool kDeep = FA == MX_E2M1 && FB == MX_E2M1;
+  static constexpr int kSPS = kDeep ? 2 : 1;
+  static constexpr int kRowA = A::kStepBytes * kSPS, kRowB = B::kStepBytes * kSPS;  // bytes of a row in a stage
+  static constexpr int kABytes = BM * kRowA, kBBytes = BN * kRowB, kStage = kABytes + kBBytes;
+  static constexpr int kSOff = NS * kStage, kSBytes = (BM + BN) * 16;
   static constexpr int kLdsBytes = kSOff + 2 * kSBytes;
-  static constexpr int kVarlenLds = VM ? (kMaxVarlenGroups + 1 + kThreads + 1) * 4 : 0;
-  static constexpr int kInstrA = BM / 8 / NW, kInstrB = BN / 8 / NW;  // transfers (8 rows each) of a stage
+  static constexpr int kInstrA = kABytes / 1024 / NW, kInstrB = kBBytes / 1024 / NW;  // a wave's transfers of a stage
+  static constexpr int kPer = kInstrA + kInstrB;
+  static constexpr int kHalfA = kInstrA / 2, kHalf = kHalfA + kInstrB / 2;  // half a stage: A's transfers, then B's
   static_assert((BM + BN) / 64 <= NW, "at most one scale transfer (64 rows) a wave");
   static_assert(kMI >= 4 && kMI % 2 == 0 && kNI == 4, "the fragment schedule below");
   static_assert(kInstrA % 2 == 0 && kInstrB % 2 == 0 && kInstrA <= 4 && kInstrB <= 4, "half a stage at a time");
-  static constexpr int kHalfA = kInstrA / 2, kHalf = kInstrA / 2 + kInstrB / 2;  // transfers of half a stage: A's, then B's
+  static_assert(NS >= 2 && NS <= (kSPS == 2 ? 3 : 4), "a quad's scales must have landed by its predecessor's last barrier");
+  static constexpr int kStores16 = kWM / 8;  // stores of the 16-bit epilogue (see there)
+  static constexpr int kAhead = (NS - 2) * kPer;  // transfers that may be outstanding at a barrier
   static constexpr int kN = kMI * kNI, kLastP = kN - kNI;
-  static constexpr bool kDeep = FA == MX_E2M1 && FB == MX_E2M1;
-  static constexpr int kRA = kDeep ? 4 : 2;
-  static constexpr bool kDB = kDeep;
+  // (What the registers hold next to the accumulators. With two stages an earlier barrier leaves the
+  // transfers less time: E4M3 x E4M3, 128x128 tiles, 8192^3: 521 us instead of 490.)
+  static constexpr int kRA = kDeep || (BM == 128 && NS > 2) ? 4 : 2;
+  static constexpr bool kDB = FB == MX_E2M1 || (BM == 128 && NS > 2);
+  // The barrier's position: past the last read of the step's own fragments, and past the head's
+  // transfers if they belong to the same stage; without kDB, where the next step's fragments find
+  // free registers.
+  static constexpr int kFreeP = (kMI - kRA) * kNI, kHeadEnd = kSPS == 1 ? 2 * kHalf : kNI;
+  static constexpr int kBarP = !kDB ? kLastP : (kFreeP > kHeadEnd ? kFreeP : kHeadEnd);
   // Two E2M1 operands: lane group g takes the K blocks c = {0, 6, 2, 4}[g] and c + 1 of the eight
   // of a pair of steps, one in each step (A and B alike, so the same products meet). Its two
-  // scales are then neighbours. A ds_read_b128 serves 16 lanes at a time: rows 0-3 and 12-15 of
-  // one lane group with rows 4-11 of its neighbour, and so on; under kswz their chunks lie in
-  // distinct banks when the neighbours' blocks differ by 1, 6 or 7 (by 4: every read twice as
-  // long, counted).
+  // scales are then neighbours and read as one.
   static constexpr bool kPairScales = kDeep;
-  // the barrier's position: past the last read of the step's own fragments (and, without kDB,
-  // where the next step's fragments find free registers)
-  static constexpr int kBarP = !kDB ? kLastP : ((kMI - kRA) * kNI > kNI ? (kMI - kRA) * kNI : kNI);
   static constexpr int kPrioP = (kBarP / 2 + 3) / 4 * 4;
   static constexpr int kTailStep = (kN - kBarP) / kHalf;  // between the transfers after the barrier
-  using A = MxFmt<FA>;
-  using B = MxFmt<FB>;
 
+  // 16-byte chunk c of row r of a stage lies at chunk c ^ key(r). A ds_read_b128 serves 16 lanes
+  // at a time, rows 0-3 and 12-15 of one lane group with rows 4-11 of its neighbour, and so on.
+  // Under these keys their chunks lie in distinct banks when those of neighbouring groups differ
+  // by 1, 6 or 7 (rows of 128 bytes; by 4: every read twice as long, counted), or by 1 (64 bytes).
+  template <int ROW>
+  static __device__ __forceinline__ int key(int r) { return ROW == 128 ? kswz(r) : ((r >> 3) & 1) * 2; }
+
+  template <int N>
   struct Loader {  // this lane's share of one operand's transfers
-    uint32_t off[4];
+    uint32_t off[N];
     int32_t klim;  // bytes of a row past this lane's chunk
   };
-  template <int N>
-  static __device__ __forceinline__ void init(Loader& l, int wave, int lane, int rows_valid, int ld, int row_bytes) {
-    const int c = (lane & 7) ^ kswz(wave * 8 + (lane >> 3));  // (the key repeats every 16 rows)
+  template <int ROW, int N>
+  static __device__ __forceinline__ void init(Loader<N>& l, int wave, int lane, int rows_valid, int ld, int row_bytes) {
+    constexpr int cpr = ROW / 16, rpi = 64 / cpr;  // chunks of a row, rows of a transfer
+    const int c = (lane % cpr) ^ key<ROW>(wave * rpi + lane / cpr);  // (the key repeats every 16 rows)
 #pragma unroll
     for (int q = 0; q < N; ++q) {
-      const int row = (q * NW + wave) * 8 + (lane >> 3);
+      const int row = (q * NW + wave) * rpi + lane / cpr;
       l.off[q] = row < rows_valid ? (uint32_t)(row * ld + c * 16) : kOOB;
     }
     l.klim = row_bytes - c * 16;
   }
-  // Transfers [Q0, Q1) of the stage at `lds`: bytes [kb, kb + 128) of the rows. (kb is added to
-  // the lane's offset: the range check, which turns kOOB into zeros, is stated for that sum. An
-  // offset is below 2^31, so kOOB + kb does not wrap.)
-  template <int Q0, int Q1>
-  static __device__ __forceinline__ void dma(const Loader& l, __amdgpu_buffer_rsrc_t rs, int kb, GEP_LDS char* lds,
+  // Transfers [Q0, Q1) of one operand's part (at `lds`) of a stage: the rows' bytes from kb on. (kb is
+  // added to the lane's offset: the range check, which turns kOOB into zeros, is stated for that
+  // sum. An offset is below 2^31, so kOOB + kb does not wrap.)
+  template <int Q0, int Q1, int N>
+  static __device__ __forceinline__ void dma(const Loader<N>& l, __amdgpu_buffer_rsrc_t rs, int kb, GEP_LDS char* lds,
                                              int wave) {
     if constexpr (Q0 < Q1) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -210,7 +273,8 @@ struct MxRing {
 
   struct Src {
     __amdgpu_buffer_rsrc_t a, b, s;
-    Loader la, lb;
+    Loader<kInstrA> la;
+    Loader<kInstrB> lb;
     uint32_t s_off;  // this lane's row in the wave's scale transfer
     int32_t nsb;
   };
@@ -222,49 +286,58 @@ struct MxRing {
                                              quad < s.nsb ? s.s_off + quad * 1024 : kOOB, 0, 0, 0);
 #endif
   }
+  // Transfer U of the first (SECOND = false) or second half of the K range's stage number `n`, to `lds`.
+  template <int U, bool SECOND>
+  static __device__ __forceinline__ void transfer(const Src& s, int n, GEP_LDS char* lds, int wave) {
+    if constexpr (U < kHalfA) {
+      constexpr int q = U + (SECOND ? kInstrA / 2 : 0);
+      dma<q, q + 1>(s.la, s.a, n * kRowA, lds, wave);
+    } else {
+      constexpr int q = U - kHalfA + (SECOND ? kInstrB / 2 : 0);
+      dma<q, q + 1>(s.lb, s.b, n * kRowB, lds + kABytes, wave);
+    }
+  }
 
-  // Lane offsets (A: from the start of the ring; B and scales likewise).
+  // Wait until at most kAhead of this wave's vector memory operations are outstanding (kAhead +
+  // kStores16 with `more`, the same in every lane) and its LDS operations are done; then the
+  // workgroup meets. (The branch is inside the asm: as one of the compiler's it would cut the step
+  // into blocks and the accumulators would move between them.)
+  static __device__ __forceinline__ void ring_barrier() {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kAhead) : "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  static __device__ __forceinline__ void ring_barrier(int more) {
+    static_assert(kAhead + kStores16 < 64, "a six-bit counter");
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile(
+        "s_cmp_eq_u32 %2, 0\n\ts_cbranch_scc0 1f\n\ts_waitcnt vmcnt(%0)\n1:\n\ts_waitcnt vmcnt(%1) lgkmcnt(0)\n\ts_barrier" ::"n"(kAhead),
+        "n"(kAhead + kStores16), "s"(more)
+        : "memory", "scc");
+    __builtin_amdgcn_sched_barrier(0);
+  }
+
+  // Lane offsets of the fragments in a stage, and of the scale bytes from kSOff on.
   struct Lane {
-    int a0, a1;  // E4M3: the two chunks; E2M1: steps 0 and 1 of a pair
-    int b0, b1;
-    int sa, sb;  // scale bytes, of the current scale stage
+    int a, b, sa, sb;
   };
   static __device__ __forceinline__ Lane lane_offsets(int lane, int wm0, int wn0) {
     Lane o;
     const int ra = wm0 + (lane & 15), rb = wn0 + (lane & 15), g = lane >> 4;
-    // first K block (E2M1) or chunk (E4M3) of lane group g, and how far the other one is
-    const int c = kPairScales ? (0x4260 >> (4 * g)) & 7 : g, far = kPairScales ? 16 : 64;
-    o.a0 = ra * kRowBytes + ((c ^ kswz(ra)) << 4);
-    o.b0 = kBOff + rb * kRowBytes + ((c ^ kswz(rb)) << 4);
-    o.a1 = o.a0 ^ far;
-    o.b1 = o.b0 ^ far;
+    const int c = kPairScales ? (0x4260 >> (4 * g)) & 7 : g;  // the lane group's first chunk and K block
+    o.a = ra * kRowA + ((c ^ key<kRowA>(ra)) << 4);
+    o.b = kABytes + rb * kRowB + ((c ^ key<kRowB>(rb)) << 4);
     o.sa = kSOff + ra * 16 + c;
     o.sb = kSOff + (BM + rb) * 16 + c;
     return o;
   }
-  // Stage of an operand in step T of a quad.
-  template <int F>
-  static constexpr int stage(int t) { return F == MX_E4M3 ? (t & 1) : ((t >> 1) & 1); }
-  template <int F, int T>
-  static __device__ __forceinline__ MxFrag<F> read(const GEP_LDS char* smem, int stage_bytes, int r, int o0, int o1) {
-    const GEP_LDS char* p = smem + stage<F>(T) * stage_bytes + r * 16 * kRowBytes;
+  // The fragment of block row r whose first chunk of row block 0 is at p (E4M3: p2 the second one).
+  template <int F, int ROW>
+  static __device__ __forceinline__ MxFrag<F> read(const GEP_LDS char* smem, int p, int p2, int r) {
     MxFrag<F> f;
-    if constexpr (F == MX_E4M3) {
-      f.lo = *(const GEP_LDS i32x4*)(p + o0);
-      f.hi = *(const GEP_LDS i32x4*)(p + o1);
-    } else {
-      f.lo = *(const GEP_LDS i32x4*)(p + ((T & 1) ? o1 : o0));
-    }
+    f.lo = *(const GEP_LDS i32x4*)(smem + p + r * 16 * ROW);
+    if constexpr (F == MX_E4M3) f.hi = *(const GEP_LDS i32x4*)(smem + p2 + r * 16 * ROW);
     return f;
-  }
-  // kPairScales: the lane's two scales of a pair of steps in one read, every other step.
-  template <int T>
-  static __device__ __forceinline__ void read_scale(int& v, const GEP_LDS char* smem, int o, int r) {
-    if constexpr (kPairScales) {
-      if constexpr (T % 2 == 0) v = *(const GEP_LDS uint16_t*)(smem + o + r * 256 + T * 4);
-    } else {
-      v = *(const GEP_LDS uint8_t*)(smem + o + r * 256 + T * 4);
-    }
   }
 
   struct Frags {
@@ -272,20 +345,38 @@ struct MxRing {
     MxFrag<FB> b[kDB ? 2 : 1][kNI];
     int sa[kPairScales ? kMI : kRA], sb[kDB ? 2 : 1][kNI];
   };
-  static constexpr int sset(int t) { return !kDB ? 0 : (kPairScales ? (t >> 1) & 1 : t & 1); }
   static constexpr int bset(int t) { return kDB ? t & 1 : 0; }
+  static constexpr int sset(int t) { return !kDB ? 0 : (kPairScales ? (t >> 1) & 1 : t & 1); }
+  static constexpr int sa_at(int r) { return kPairScales ? r : r % kRA; }
+  struct At {  // addresses of one step's fragments and scales
+    int a, a2, b, b2, sa, sb;
+  };
   template <int T>
-  static __device__ __forceinline__ void read_a(Frags& f, const GEP_LDS char* smem, const Lane& o, int r, int so) {
-    f.a[r % kRA] = read<FA, T>(smem, kABytes, r, o.a0, o.a1);
-    read_scale<T>(f.sa[kPairScales ? r : r % kRA], smem, o.sa + so, r);
+  static __device__ __forceinline__ At at(const Lane& o, int stage, int scale_stage) {
+    constexpr int flip = kSPS == 2 && (T & 1) ? 16 : 0;  // the second step's chunk
+    At x{(o.a ^ flip) + stage, (o.a ^ 64) + stage, (o.b ^ flip) + stage, (o.b ^ 64) + stage, o.sa + scale_stage, o.sb + scale_stage};
+    // opaque: block-row offsets then fold into the reads' immediates
+    asm volatile("" : "+v"(x.a), "+v"(x.b), "+v"(x.sa), "+v"(x.sb));
+    if constexpr (A::k8) asm volatile("" : "+v"(x.a2));
+    if constexpr (B::k8) asm volatile("" : "+v"(x.b2));
+    return x;
   }
   template <int T>
-  static __device__ __forceinline__ void read_b(Frags& f, const GEP_LDS char* smem, const Lane& o, int c, int so) {
-    f.b[bset(T)][c] = read<FB, T>(smem, kBBytes, c, o.b0, o.b1);
-    read_scale<T>(f.sb[sset(T)][c], smem, o.sb + so, c);
+  static __device__ __forceinline__ void read_scale(int& v, const GEP_LDS char* p) {
+    if constexpr (!kPairScales) v = *(const GEP_LDS uint8_t*)(p + T * 4);
+    else if constexpr (T % 2 == 0) v = *(const GEP_LDS uint16_t*)(p + T * 4);
+  }
+  template <int T>
+  static __device__ __forceinline__ void read_a(Frags& f, const GEP_LDS char* smem, const At& x, int r) {
+    f.a[r % kRA] = read<FA, kRowA>(smem, x.a, x.a2, r);
+    read_scale<T>(f.sa[sa_at(r)], smem + x.sa + r * 256);
+  }
+  template <int T>
+  static __device__ __forceinline__ void read_b(Frags& f, const GEP_LDS char* smem, const At& x, int c) {
+    f.b[bset(T)][c] = read<FB, kRowB>(smem, x.b, x.b2, c);
+    read_scale<T>(f.sb[sset(T)][c], smem + x.sb + c * 256);
   }
 
-  static constexpr bool bar(int t) { return A::k8 || B::k8 || (t & 1); }
   // What is read after position p: the A fragment of this step's row a_after (the rows past the ring's
   // first kRA - 1), of the next step's row na_after, the next step's B fragment nb_after (-1: none).
   static constexpr int a_after(int p) {
@@ -295,8 +386,8 @@ struct MxRing {
   }
   static constexpr int na_after(int p) {
     for (int r = 0; r < kRA - 1; ++r) {
-      const int free = (kMI - kRA + r + 1) * kNI - 1;
-      if ((free > kBarP ? free : kBarP) == p) return r;
+      const int free = (kMI - kRA + r + 1) * kNI - 1, first = kBarP + (kDB ? 2 * r + 1 : 0);
+      if ((free > first ? free : first) == p) return r;
     }
     return -1;
   }
@@ -311,36 +402,20 @@ struct MxRing {
     return ((A::k8 ? 2 : 1) + own) * (a_after(p) >= 0) + ((A::k8 ? 2 : 1) + next) * (na_after(p) >= 0) +
            ((B::k8 ? 2 : 1) + next) * (nb_after(p) >= 0);
   }
-  // Transfers after position p of step t: the second half of the next stage at the head (every other
-  // position; behind them the next quad's scales), the first half of the one after it behind the
-  // barrier. head_at / tail_at: which transfer of its half goes out after position p (A's first), or -1.
-  static constexpr int head_at(int p) { return p % 2 == 0 && p / 2 < kHalf ? p / 2 : -1; }
-  static constexpr int tail_at(int p) {
-    return p >= kBarP && (p - kBarP) % kTailStep == 0 && (p - kBarP) / kTailStep < kHalf ? (p - kBarP) / kTailStep : -1;
-  }
-  static constexpr bool in_step(bool is_a, bool tail, int t) {  // an E2M1 stage covers two steps
-    return (is_a ? A::k8 : B::k8) || (t & 1) == (tail ? 1 : 0);
+  // Transfers after position p of step t: the second half of the stage NS - 1 ahead at the head of a
+  // stage's first step (every other position; behind them the next quad's scales), the first half of
+  // the one NS ahead behind the barrier, in its last. head_at / tail_at: which transfer of its half
+  // goes out after position p (A's first), or -1.
+  static constexpr bool first_step(int t) { return t % kSPS == 0; }
+  static constexpr bool last_step(int t) { return t % kSPS == kSPS - 1; }
+  static constexpr int head_at(int t, int p) { return first_step(t) && p % 2 == 0 && p / 2 < kHalf ? p / 2 : -1; }
+  static constexpr int tail_at(int t, int p) {
+    return last_step(t) && p >= kBarP && (p - kBarP) % kTailStep == 0 && (p - kBarP) / kTailStep < kHalf ? (p - kBarP) / kTailStep : -1;
   }
   static constexpr int kScaleP = 2 * kHalf;
-  static constexpr int transfers(int t, int p) {
-    int n = p == kScaleP && t == 0;
-    if (head_at(p) >= 0) n += in_step(head_at(p) < kHalfA, false, t);
-    if (tail_at(p) >= 0) n += in_step(tail_at(p) < kHalfA, true, t);
-    return n;
-  }
-  static_assert(kScaleP < kN, "the scales' transfer is issued inside the step");
-  // Transfer u of the first (SECOND = false) or second half of the stage `slot` (a step of an E4M3
-  // operand, a pair of an E2M1 one; 128 bytes of a row each) that is held in stage st.
-  template <int U, bool SECOND>
-  static __device__ __forceinline__ void transfer(const Src& s, int slot, GEP_LDS char* smem, int st, int wave) {
-    if constexpr (U < kHalfA) {
-      constexpr int q = U + (SECOND ? kInstrA / 2 : 0);
-      dma<q, q + 1>(s.la, s.a, slot * 128, smem + st * kABytes, wave);
-    } else {
-      constexpr int q = U - kHalfA + (SECOND ? kInstrB / 2 : 0);
-      dma<q, q + 1>(s.lb, s.b, slot * 128, smem + kBOff + st * kBBytes, wave);
-    }
-  }
+  static_assert((kSPS == 2 || 2 * (kHalf - 1) < kBarP) && kScaleP < kN, "the head's transfers come before the stage's barrier");
+  static constexpr int transfers(int t, int p) { return (p == kScaleP && t == 0) + (head_at(t, p) >= 0) + (tail_at(t, p) >= 0); }
+
   template <int T, int P, int E>
   static __device__ __forceinline__ void sched() {
     if constexpr (P < E) {
@@ -351,83 +426,95 @@ struct MxRing {
     }
   }
 
-  // Positions [P, E) of step T of quad q (so: its scale stage's offset; so_next: the next step's).
+  // The offsets of the previous, this and the next stage.
+  struct Stages {
+    int prev, cur, next;
+    __device__ __forceinline__ void advance() {
+      prev = cur;
+      cur = next;
+      next = next + kStage == kSOff ? 0 : next + kStage;
+      asm volatile("" : "+s"(next));  // (known, the compiler would keep addresses of all stages)
+    }
+  };
+
+  // Positions [P, E) of step T of quad q (x: this step's addresses, y: the next one's).
   template <bool MM, int T, int P, int E>
-  static __device__ __forceinline__ void positions(f32x4 (&acc)[kMI][kNI], Frags& f, GEP_LDS char* smem, const Lane& o,
-                                                   const Src& s, int q, int so, int so_next, int wave) {
+  static __device__ __forceinline__ void positions(f32x4 (&acc)[kMI][kNI], Frags& f, GEP_LDS char* smem, const At& x,
+                                                   const At& y, const Src& s, int q, const Stages& st, int wave) {
     if constexpr (P < E) {
       constexpr int NT = (T + 1) & 3;
       if constexpr (MM) {
         constexpr int r = P / kNI, c = P % kNI;
-        acc[r][c] = mx_mma<FA, FB, kPairScales ? T % 2 : 0>(f.b[bset(T)][c], f.a[r % kRA], acc[r][c], f.sb[sset(T)][c],
-                                                            f.sa[kPairScales ? r : r % kRA]);
-        if constexpr (a_after(P) >= 0) read_a<T>(f, smem, o, a_after(P), so);
-        if constexpr (na_after(P) >= 0) read_a<NT>(f, smem, o, na_after(P), so_next);
-        if constexpr (nb_after(P) >= 0) read_b<NT>(f, smem, o, nb_after(P), so_next);
+        acc[r][c] = mx_mma<FA, FB, kPairScales ? T % 2 : 0>(f.b[bset(T)][c], f.a[r % kRA], acc[r][c], f.sb[sset(T)][c], f.sa[sa_at(r)]);
+        if constexpr (a_after(P) >= 0) read_a<T>(f, smem, x, a_after(P));
+        if constexpr (na_after(P) >= 0) read_a<NT>(f, smem, y, na_after(P));
+        if constexpr (nb_after(P) >= 0) read_b<NT>(f, smem, y, nb_after(P));
       }
-      const int step = q * 4 + T;
-      constexpr int h = head_at(P), u = tail_at(P);
-      if constexpr (h >= 0 && in_step(h < kHalfA, false, T)) {
-        constexpr bool k8 = h < kHalfA ? A::k8 : B::k8;
-        transfer<h, true>(s, (k8 ? step : step >> 1) + 1, smem, (h < kHalfA ? stage<FA>(T) : stage<FB>(T)) ^ 1, wave);
-      }
+      constexpr int h = head_at(T, P), u = tail_at(T, P);
+      const int n = (q * 4 + T) / kSPS;  // this stage's number
+      if constexpr (h >= 0) transfer<h, true>(s, n + NS - 1, smem + st.prev, wave);
       if constexpr (P == kScaleP && T == 0) dma_scales(s, q + 1, smem, (q + 1) & 1, wave);
-      if constexpr (u >= 0 && in_step(u < kHalfA, true, T)) {
-        constexpr bool k8 = u < kHalfA ? A::k8 : B::k8;
-        transfer<u, false>(s, (k8 ? step : step >> 1) + 2, smem, u < kHalfA ? stage<FA>(T) : stage<FB>(T), wave);
-      }
-      positions<MM, T, P + 1, E>(acc, f, smem, o, s, q, so, so_next, wave);
+      if constexpr (u >= 0) transfer<u, false>(s, n + NS, smem + st.cur, wave);
+      positions<MM, T, P + 1, E>(acc, f, smem, x, y, s, q, st, wave);
     }
   }
+
+  // stores: the kStores16 stores of the previous tile's epilogue lie between this tile's transfers of
+  // stage NS - 2 and NS - 1, and need not be waited for before those.
   template <bool MM, int T>
   static __device__ __forceinline__ void step(f32x4 (&acc)[kMI][kNI], Frags& f, GEP_LDS char* smem, const Lane& lo,
-                                              const Src& s, int q, int wave) {
+                                              const Src& s, int q, Stages& st, int stores, int wave) {
     const int so = (q & 1) * kSBytes, so_next = T == 3 ? ((q + 1) & 1) * kSBytes : so;
-    // opaque offsets: stage and block-row offsets then fold into the reads' immediates
-    Lane o = lo;
-    asm volatile("" : "+v"(o.a0), "+v"(o.a1), "+v"(o.b0), "+v"(o.b1), "+v"(o.sa), "+v"(o.sb));
+    const At x = at<T>(lo, st.cur, so), y = at<(T + 1) & 3>(lo, last_step(T) ? st.next : st.cur, so_next);
     if constexpr (MM) {
       __builtin_amdgcn_sched_barrier(0);
       __builtin_amdgcn_s_setprio(1);
       __builtin_amdgcn_sched_barrier(0);
-      positions<true, T, 0, kPrioP>(acc, f, smem, o, s, q, so, so_next, wave);
+      positions<true, T, 0, kPrioP>(acc, f, smem, x, y, s, q, st, wave);
       sched<T, 0, kPrioP>();
       __builtin_amdgcn_sched_barrier(0);
       __builtin_amdgcn_s_setprio(0);
       __builtin_amdgcn_sched_barrier(0);
-      positions<true, T, kPrioP, kBarP>(acc, f, smem, o, s, q, so, so_next, wave);
-      sched<T, kPrioP, kBarP>();
-      if constexpr (bar(T)) dma_barrier();
-      positions<true, T, kBarP, kN>(acc, f, smem, o, s, q, so, so_next, wave);
+    }
+    positions<MM, T, MM ? kPrioP : 0, kBarP>(acc, f, smem, x, y, s, q, st, wave);
+    if constexpr (MM) sched<T, kPrioP, kBarP>();
+    if constexpr (last_step(T)) {
+      if constexpr (T / kSPS <= NS - 3) ring_barrier(stores);
+      else ring_barrier();
+    }
+    positions<MM, T, kBarP, kN>(acc, f, smem, x, y, s, q, st, wave);
+    if constexpr (MM) {
       sched<T, kBarP, kN>();
       __builtin_amdgcn_sched_barrier(0);
-    } else {
-      positions<false, T, 0, kBarP>(acc, f, smem, o, s, q, so, so_next, wave);
-      if constexpr (bar(T)) dma_barrier();
-      positions<false, T, kBarP, kN>(acc, f, smem, o, s, q, so, so_next, wave);
     }
+    if constexpr (last_step(T)) st.advance();
   }
   template <bool MM>
   static __device__ __forceinline__ void mainloop(f32x4 (&acc)[kMI][kNI], Frags& f, GEP_LDS char* smem, const Lane& o,
-                                                  const Src& s, int steps, int wave) {
-    for (int q = 0; q * 4 < steps; ++q) {
-      step<MM, 0>(acc, f, smem, o, s, q, wave);
-      step<MM, 1>(acc, f, smem, o, s, q, wave);
-      if (q * 4 + 2 < steps) {
-        step<MM, 2>(acc, f, smem, o, s, q, wave);
-        step<MM, 3>(acc, f, smem, o, s, q, wave);
-      }
+                                                  const Src& s, int steps, int stores, int wave) {
+    Stages st{(NS - 1) * kStage, 0, kStage};
+    int q = 0;
+    for (; q * 4 + 2 < steps; ++q) {
+      step<MM, 0>(acc, f, smem, o, s, q, st, stores, wave);
+      step<MM, 1>(acc, f, smem, o, s, q, st, stores, wave);
+      step<MM, 2>(acc, f, smem, o, s, q, st, stores, wave);
+      step<MM, 3>(acc, f, smem, o, s, q, st, stores, wave);
+      stores = 0;
+    }
+    if (q * 4 < steps) {
+      step<MM, 0>(acc, f, smem, o, s, q, st, stores, wave);
+      step<MM, 1>(acc, f, smem, o, s, q, st, stores, wave);
     }
   }
 
-  // ---- epilogue. It runs while the next tile's first transfers are under way (they fill stage 0),
-  // through 4 KB a wave of A's stage 1. One 16-bit output without C: the values are final in the
+  // ---- epilogue. It runs while the next tile's first transfers are under way (all stages but the
+  // last), through 4 KB a wave of the last stage. One 16-bit output without C: the values are final in the
   // accumulators, so they are converted there and pass through LDS as 16-bit rows (32 rows a
   // pass). Otherwise fp32 rows (16 a pass). Either way a lane then holds 8 consecutive columns, and C,
   // D and PostAct are accessed 16 bytes or more at a time, 128 bytes a row. Chunks are XOR-swizzled
   // by the row as in gemm_kernel.hpp's 16x16 epilogues.
   static constexpr int kRegion = 4096;
-  static_assert(kRegion * NW <= kABytes, "the epilogue's buffers lie in a stage of A");
+  static_assert(kRegion * NW <= kStage, "the epilogue's buffers lie in one stage");
   static __device__ __forceinline__ int ebuf(int r, int c8, int hf) {
     return r * 256 + hf * 128 + ((c8 ^ ((r & 3) | ((r >> 1) & 4))) << 4);
   }
@@ -436,7 +523,6 @@ struct MxRing {
   // Stores of the 16-bit path; the count lets the wait for the transfers issued before them leave
   // the stores in flight. (So every one is issued: rows and columns past the output go to an
   // offset that the range check drops.)
-  static constexpr int kStores16 = kWM / 8;
   static constexpr int64_t kMaxLd16 = 1 << 22;  // its offsets inside a tile are 32-bit
 
   template <int DT>
@@ -514,21 +600,12 @@ struct MxRing {
     }
     return false;
   }
-  // All transfers issued before the last kStores16 operations have landed; then the workgroup meets.
-  static __device__ __forceinline__ void dma_barrier_stores() {
-    __builtin_amdgcn_sched_barrier(0);
-    static_assert(kStores16 == 16 || kStores16 == 8, "the literal counts below");
-    if constexpr (kStores16 == 16) asm volatile("s_waitcnt vmcnt(16) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    else asm volatile("s_waitcnt vmcnt(8) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    __builtin_amdgcn_sched_barrier(0);
-  }
-
   static __device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
   // Item u of this launch -> output tile. The map has tiles of BM x BN; in a split tail's launch
   // (p.tail == 2, the 128x128 kernels) of 256x256, and item u is quarter u & 3 of map tile t_lo + u / 4:
   // its rows (u & 1) and columns (u >> 1 & 1), possibly wholly outside the output.
-  static __device__ __forceinline__ MxTileInfo decode(const MxParams& mp, int u, const int32_t* gstart, int t_lo) {
+  static __device__ __forceinline__ MxTileInfo decode(const MxParams& mp, int u, int t_lo, int lane) {
     const KParams& p = mp.k;
     const bool quarter = BM == 128 && p.tail == 2;
     const int MT = quarter ? 2 * BM : BM, NT = quarter ? 2 * BN : BN;
@@ -538,15 +615,11 @@ struct MxRing {
     uint32_t mb, nb;
     int row_base = 0;
     if constexpr (VM) {
-      int lo = 0, hi = p.L - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (gstart[mid] <= t) lo = mid; else hi = mid - 1;
-      }
-      row_base = p.cu_seqlens[lo];
-      ti.row_end = p.cu_seqlens[lo + 1];
-      ti.g = lo;
-      raster(p, (uint32_t)(t - gstart[lo]), (uint32_t)((ti.row_end - row_base + MT - 1) / MT), (uint32_t)p.tn, p.fd_Gtn, mb, nb);
+      const MxGroup g = mx_find_group(p, t, MT, p.tn, lane);
+      row_base = g.begin;
+      ti.row_end = g.end;
+      ti.g = g.index;
+      raster(p, (uint32_t)(t - g.first), (uint32_t)((ti.row_end - row_base + MT - 1) / MT), (uint32_t)p.tn, p.fd_Gtn, mb, nb);
     } else {
       ti.g = 0;
       ti.row_end = p.M;
@@ -562,7 +635,7 @@ struct MxRing {
 
   static __device__ __forceinline__ void run(const MxParams& mp) {
     const KParams& p = mp.k;
-    __shared__ __attribute__((aligned(1024))) char smem_raw[kLdsBytes + kVarlenLds];
+    __shared__ __attribute__((aligned(1024))) char smem_raw[kLdsBytes];
     GEP_LDS char* smem = (GEP_LDS char*)smem_raw;
     const int tid = threadIdx.x, lane_id = tid & 63;
     const int wave = uni(tid >> 6);
@@ -570,49 +643,8 @@ struct MxRing {
     const int wm0 = (wave / kWavesN) * kWM, wn0 = (wave % kWavesN) * kWN;
 
     int T = p.T;
-    [[maybe_unused]] int32_t* gstart = nullptr;
-    [[maybe_unused]] const int MT = BM == 128 && p.tail == 2 ? 2 * BM : BM;
-    if constexpr (VM) {
-      // tile offsets of the groups; an array that does not run 0 .. M without decreasing gives
-      // no tiles (see gemm_kernel.hpp: the flag shares the one LDS array)
-      gstart = (int32_t*)(smem_raw + kLdsBytes);
-      int32_t* part = gstart + kMaxVarlenGroups + 1;
-      volatile int32_t* s_bad = part + kThreads;
-      if (tid == 0) *s_bad = 0;
-      __syncthreads();
-      constexpr int kPer = kMaxVarlenGroups / kThreads;
-      int32_t local[kPer], sum = 0;
-      int bad = 0;
-#pragma unroll
-      for (int q = 0; q < kPer; ++q) {
-        const int g = tid * kPer + q;
-        int32_t tiles = 0;
-        if (g < p.L) {
-          const int c0 = p.cu_seqlens[g], c1 = p.cu_seqlens[g + 1];
-          bad |= c1 < c0 || (g == 0 && c0 != 0) || (g == p.L - 1 && c1 != p.M);
-          tiles = c1 > c0 ? (int)(((int64_t)c1 - c0 + MT - 1) / MT) * p.tn : 0;
-        }
-        local[q] = sum;
-        sum += tiles;
-      }
-      if (bad) *s_bad = 1;
-      part[tid] = sum;
-      __syncthreads();
-      bad = uni(*s_bad);
-      for (int off = 1; off < kThreads; off <<= 1) {
-        const int32_t add = tid >= off ? part[tid - off] : 0;
-        __syncthreads();
-        part[tid] += add;
-        __syncthreads();
-      }
-#pragma unroll
-      for (int q = 0; q < kPer; ++q) {
-        const int g = tid * kPer + q;
-        if (g < p.L) gstart[g] = part[tid] - sum + local[q];
-      }
-      T = uni(bad ? 0 : part[kThreads - 1]);
-      __syncthreads();
-    }
+    // (an array that does not run 0 .. M without decreasing gives no tiles)
+    if constexpr (VM) T = mx_find_group(p, -1, BM == 128 && p.tail == 2 ? 2 * BM : BM, p.tn, lane_id).first;
     const int P = p.P;
     const bool xq = p.xcd_remap && (P & 7) == 0;
     const int bid = blockIdx.x;
@@ -636,16 +668,16 @@ struct MxRing {
     MxTileInfo ti;
     Src s;
     int steps;
-    // The tile's operands, and its first transfers: stage 0 and the first scales.
+    // The tile's operands, and its first transfers: the first scales and all stages but the last.
     auto begin_tile = [&](int t) {
-      ti = decode(mp, t, gstart, t_lo);
       int lane = lane_id;
       asm volatile("" : "+v"(lane));  // (lane offsets are not kept across the main loop)
+      ti = decode(mp, t, t_lo, lane);
       const int q0 = kSplit ? ti.slice * mp.per : 0;  // the slice's first scale tile, four steps each
       const int ka = q0 * 4 * A::kStepBytes, kb = q0 * 4 * B::kStepBytes;
       steps = kSplit && mp.split > 1 ? min(mp.per * 4, mp.steps - q0 * 4) : mp.steps;
-      init<kInstrA>(s.la, wave, lane, ti.row_end - ti.m0, (int)p.lda, (int)p.lda - ka);
-      init<kInstrB>(s.lb, wave, lane, p.N - ti.n0, (int)p.ldb, (int)p.ldb - kb);
+      init<kRowA>(s.la, wave, lane, ti.row_end - ti.m0, (int)p.lda, (int)p.lda - ka);
+      init<kRowB>(s.lb, wave, lane, p.N - ti.n0, (int)p.ldb, (int)p.ldb - kb);
       const int64_t ao = (int64_t)ti.m0 * p.lda + ka, bo = (int64_t)ti.n0 * p.ldb + kb;
       s.a = make_rsrc((const char*)p.A + ao, p.a_bytes - ao);
       s.b = make_rsrc((const char*)p.B + (int64_t)ti.g * p.b_bytes + bo, p.b_bytes - bo);
@@ -658,13 +690,16 @@ struct MxRing {
                       (is_a ? mp.sa_bytes : mp.sb_bytes) - so);
       const int rr = (first & 63) + i;
       s.s_off = first + i < (is_a ? ti.row_end : p.N) ? (uint32_t)((rr >> 6) * mp.nsb * 1024 + (rr & 63) * 16) : kOOB;
-      dma<0, kInstrA>(s.la, s.a, 0, smem, wave);
-      dma<0, kInstrB>(s.lb, s.b, 0, smem + kBOff, wave);
       dma_scales(s, 0, smem, 0, wave);
+#pragma unroll
+      for (int i = 0; i < NS - 1; ++i) {
+        dma<0, kInstrA>(s.la, s.a, i * kRowA, smem + i * kStage, wave);
+        dma<0, kInstrB>(s.lb, s.b, i * kRowB, smem + i * kStage + kABytes, wave);
+      }
     };
 
     if (b0 < U) begin_tile(b0);
-    bool stores = false;  // the wave's last operations are the stores of epilogue16
+    int stores = 0;  // 1: the wave's last operations are the stores of epilogue16
     for (int t = b0; t < U;) {
       f32x4 acc[kMI][kNI];
 #pragma unroll
@@ -673,24 +708,24 @@ struct MxRing {
         for (int j = 0; j < kNI; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
       // a wave whose rows or columns all lie past the output only moves data
       const bool idle = ti.m0 + wm0 >= ti.row_end || ti.n0 + wn0 >= p.N;
-      // stage 0 has landed; the previous tile's epilogue buffers (stage 1) are free
-      if (stores) dma_barrier_stores();
-      else dma_barrier();
-      dma<0, kInstrA / 2>(s.la, s.a, 128, smem + kABytes, wave);
-      dma<0, kInstrB / 2>(s.lb, s.b, 128, smem + kBOff + kBBytes, wave);
+      // the first step has landed; the previous tile's epilogue buffers (the last stage) are free
+      ring_barrier(stores);
+      dma<0, kInstrA / 2>(s.la, s.a, (NS - 1) * kRowA, smem + (NS - 1) * kStage, wave);
+      dma<0, kInstrB / 2>(s.lb, s.b, (NS - 1) * kRowB, smem + (NS - 1) * kStage + kABytes, wave);
       int lane = lane_id;
       asm volatile("" : "+v"(lane));
       const Lane o = lane_offsets(lane, wm0, wn0);
       Frags f;
       if (idle) {
         __builtin_amdgcn_s_setprio(0);
-        mainloop<false>(acc, f, smem, o, s, steps, wave);
+        mainloop<false>(acc, f, smem, o, s, steps, stores, wave);
       } else {
+        const At x = at<0>(o, 0, 0);
 #pragma unroll
-        for (int r = 0; r < kRA - 1; ++r) read_a<0>(f, smem, o, r, 0);
+        for (int r = 0; r < kRA - 1; ++r) read_a<0>(f, smem, x, r);
 #pragma unroll
-        for (int c = 0; c < kNI; ++c) read_b<0>(f, smem, o, c, 0);
-        mainloop<true>(acc, f, smem, o, s, steps, wave);
+        for (int c = 0; c < kNI; ++c) read_b<0>(f, smem, x, c);
+        mainloop<true>(acc, f, smem, o, s, steps, stores, wave);
       }
       dma_barrier();  // transfers past K have landed and every wave has left the ring
       const MxTileInfo done = ti;
@@ -698,8 +733,8 @@ struct MxRing {
       if (t < U) begin_tile(t);
       asm volatile("" ::: "memory");  // (its transfers are issued before the epilogue's stores)
       __builtin_amdgcn_sched_barrier(0);
-      stores = false;
-      if (!idle) stores = epilogue(mp, done, acc, smem + kABytes + wave * kRegion, lane_id, wm0, wn0);
+      stores = 0;
+      if (!idle) stores = uni(epilogue(mp, done, acc, smem + (NS - 1) * kStage + wave * kRegion, lane_id, wm0, wn0) ? 1 : 0);
     }
   }
 };
@@ -778,40 +813,11 @@ struct MxDirect {
     const int slice = VM ? 0 : blockIdx.z, t0 = VM ? 0 : slice * mp.per, t1 = VM ? mp.nsb : min(mp.nsb, t0 + mp.per);
     const int n0 = blockIdx.x * kBN;
     if constexpr (VM) {
-      // the group of row block blockIdx.y: 64 groups a pass, one a lane; the whole array is
-      // checked (0 .. M, never decreasing)
-      int base = 0, found = 0, bad = 0;
-      const int want = blockIdx.y;
-      for (int g0 = 0; g0 < p.L; g0 += 64) {
-        const int gi = g0 + lane;
-        int c0 = 0, c1 = 0;
-        if (gi < p.L) {
-          c0 = p.cu_seqlens[gi];
-          c1 = p.cu_seqlens[gi + 1];
-          bad |= c1 < c0 || (gi == 0 && c0 != 0) || (gi == p.L - 1 && c1 != p.M);
-        }
-        const int tiles = c1 > c0 ? (int)(((int64_t)c1 - c0 + kBM - 1) / kBM) : 0;
-        int incl = tiles;
-#pragma unroll
-        for (int off = 1; off < 64; off <<= 1) {
-          const int u = __shfl_up(incl, off);
-          if (lane >= off) incl += u;
-        }
-        const int first = base + incl - tiles;
-        const uint64_t hit = __ballot(want >= first && want < first + tiles);
-        if (hit) {
-          const int src = __ffsll((unsigned long long)hit) - 1;
-          g = g0 + src;
-          m0 = __shfl(c0, src) + (want - __shfl(first, src)) * kBM;
-          row_end = __shfl(c1, src);
-          found = 1;
-        }
-        base += __shfl(incl, 63);
-      }
-      if (__ballot(bad) || !found) return;  // (the same in every wave)
-      g = __builtin_amdgcn_readfirstlane(g);
-      m0 = __builtin_amdgcn_readfirstlane(m0);
-      row_end = __builtin_amdgcn_readfirstlane(row_end);
+      const MxGroup found = mx_find_group(p, (int)blockIdx.y, kBM, 1, lane);
+      if (found.index < 0) return;  // (the same in every wave)
+      g = found.index;
+      m0 = found.begin + ((int)blockIdx.y - found.first) * kBM;
+      row_end = found.end;
     }
     const int r = lane & 15, kg = lane >> 4;
     Src s;
@@ -889,9 +895,20 @@ struct MxDirect {
   }
 };
 
-template <int BM, int BN, int NW, int FA, int FB, bool VM>
-__global__ __launch_bounds__(NW * 64, (NW == 8 ? 1 : 2)) void mx_ring_kernel(const MxParams p) {
-  MxRing<BM, BN, NW, FA, FB, VM>::run(p);
+// Stages in LDS: as many as fit, at most four (two E2M1 operands: three). WG: workgroups a compute unit.
+template <int BM, int FA, int FB, int WG>
+constexpr int mx_stages() {
+  constexpr bool deep = FA == MX_E2M1 && FB == MX_E2M1;
+  const int stage = BM * (MxFmt<FA>::kStepBytes + MxFmt<FB>::kStepBytes) * (deep ? 2 : 1);
+  const int n = (163840 / WG - 2 * 2 * BM * 16) / stage, most = deep ? 3 : 4;
+  return n > most ? most : n;
+}
+// 128x128 tiles run two workgroups a compute unit, or with no more workgroups than compute units
+// one with all of LDS: 512 x 4096 x 16384 (128 tiles) e4m3 x e4m3 56 us with four stages, 78 with
+// two; 8192^3 (many tiles) 564 and 490.
+template <int BM, int NW, int WG, int FA, int FB, bool VM>
+__global__ __launch_bounds__(NW * 64, WG) void mx_ring_kernel(const MxParams p) {
+  MxRing<BM, BM, NW, mx_stages<BM, FA, FB, WG>(), FA, FB, VM>::run(p);
 }
 template <int MB, int NB, int NW, int D, int FA, int FB, bool VM>
 __global__ __launch_bounds__(NW * 64) void mx_direct_kernel(const MxParams p) {
@@ -906,8 +923,11 @@ hipError_t mx_launch(int32_t tile, const MxParams& p, dim3 grid, hipStream_t s);
   template <>                                                                                        \
   hipError_t mx_launch<FA, FB, VM>(int32_t tile, const MxParams& p, dim3 grid, hipStream_t s) {      \
     switch (tile) {                                                                                  \
-      case MX_TILE_256: mx_ring_kernel<256, 256, 8, FA, FB, VM><<<grid, 512, 0, s>>>(p); break;      \
-      case MX_TILE_128: mx_ring_kernel<128, 128, 4, FA, FB, VM><<<grid, 256, 0, s>>>(p); break;      \
+      case MX_TILE_256: mx_ring_kernel<256, 8, 1, FA, FB, VM><<<grid, 512, 0, s>>>(p); break;        \
+      case MX_TILE_128:                                                                              \
+        if (p.k.P <= p.cus) mx_ring_kernel<128, 4, 1, FA, FB, VM><<<grid, 256, 0, s>>>(p);           \
+        else mx_ring_kernel<128, 4, 2, FA, FB, VM><<<grid, 256, 0, s>>>(p);                          \
+        break;                                                                                       \
       case MX_TILE_32X64: mx_direct_kernel<2, 4, 4, 2, FA, FB, VM><<<grid, 256, 0, s>>>(p); break;   \
       case MX_TILE_32: mx_direct_kernel<2, 2, 4, 2, FA, FB, VM><<<grid, 256, 0, s>>>(p); break;      \
       case MX_TILE_16X32: mx_direct_kernel<1, 2, 8, 2, FA, FB, VM><<<grid, 512, 0, s>>>(p); break;   \
