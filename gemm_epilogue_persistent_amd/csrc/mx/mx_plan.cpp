@@ -51,19 +51,76 @@ int64_t mx_row_blocks(const mx_gemm_plan& p, int32_t bm) {
   return m / bm + (m < p.d.groups ? m : p.d.groups);
 }
 
-MxChoice mx_choose(const mx_gemm_plan& p, int32_t cus, bool workspace) {
-  MxChoice c{p.d.tile, 1, 0};
-  const int32_t nsb = (int32_t)cdiv(p.d.K, 512);
-  const int64_t rows = p.d.groups ? cdiv(p.d.M, p.d.groups) : p.d.M;
-  if (c.tile == MX_TILE_AUTO) {
-    if (rows <= 16) c.tile = MX_TILE_16;
-    else if (rows <= 32) c.tile = MX_TILE_16X32;
-    else if (rows <= 64) c.tile = MX_TILE_32;
-    else if (mx_row_blocks(p, 256) * cdiv(p.d.N, 256) >= cus) c.tile = MX_TILE_256;
-    else if (mx_row_blocks(p, 128) * cdiv(p.d.N, 128) >= cus / 2) c.tile = MX_TILE_128;
-    else c.tile = MX_TILE_32X64;
+// Which kernel: the one with the least estimated time, over the tiles and, for a dense plan with a
+// workspace, over 1 to 16 workgroups a tile's K. The estimates (microseconds) are fits to
+// measurements of all of them at 30 shapes from 1x1024x1024 to 8192x512x4096 in the three usual
+// pairs of formats:
+//   direct kernels: 2.7 to 3.4 us, and a step of 128 along K moves the tile's rows of both operands at 33
+//     KB a microsecond and compute unit, whether one workgroup runs there or several, each for 1.6
+//     us at least (32x64: 2.2) (128x4096x4096 e4m3 x e2m1 in 32x64 tiles 12.0 measured, 11.2 estimated)
+//   128x128: 7 us, and 74 KB a microsecond alone on a compute unit, 56 for two workgroups
+//     (512x4096x4096 19.0, 17.4; 16384x4096x4096 226, 234)
+//   256x256: 6 us, a round 5 us and 1.36 a step with an e4m3 operand, 0.85 without (4096^3 51.6, 54.5;
+//     16384x4096x4096 197, 200), the quarters of a last round 4 us and 1.3 times their share of one
+//   a split adds 3 us and the sums' way to memory and back at 4.2 MB a microsecond
+//     (1024x1024x8192 in 128x128 tiles over four workgroups 23.7, 23.2; over one 30.1)
+// so 16-row tiles serve few rows (1x8192x8192 10.5; in 32x64 tiles 13.5), 32x64 up to 128 or 256 rows,
+// 128x128 up to one round of 256x256 tiles, and deep products with few tiles are split
+// (128x512x8192: 9.9 in 32x32 tiles over four workgroups, 14.9 over one).
+static double estimate(const mx_gemm_plan& p, int32_t cus, int32_t tile, int32_t split) {
+  int32_t bm, bn;
+  mx_tile_extent(tile, &bm, &bn);
+  // (grouped: half a partial row block for each group)
+  const double blocks = p.d.groups ? (double)p.d.M / bm + 0.5 * (p.d.M < p.d.groups ? p.d.M : p.d.groups) : (double)mx_row_blocks(p, bm);
+  const double wgs = blocks * (double)cdiv(p.d.N, bn) * split;
+  const int64_t nsb = cdiv(p.d.K, 512);
+  const double steps = split > 1 ? 4.0 * (double)cdiv(nsb, split) : (double)cdiv(p.d.K, 128);
+  const double rows_a = p.d.M < bm ? p.d.M : bm, rows_b = p.d.N < bn ? p.d.N : bn;
+  const double kb = (rows_a * (p.d.a_format == MX_E4M3 ? 128 : 64) + rows_b * (p.d.b_format == MX_E4M3 ? 128 : 64)) / 1024;
+  double t;
+  if (tile == MX_TILE_256) {
+    // (a last round of at most half the card runs in 128x128 quarters)
+    const double step = p.d.a_format == MX_E2M1 && p.d.b_format == MX_E2M1 ? 0.85 : 1.36;
+    const double full = (double)((int64_t)wgs / cus), rest = wgs / cus - full;
+    const bool quarters = full > 0 && rest > 0 && rest <= 0.5;
+    t = 6 + (full + (quarters ? rest * 1.3 : rest > 0)) * (steps * step + 5) + (quarters ? 4 : 0);
+  } else if (tile == MX_TILE_128) {
+    t = 7 + (wgs <= cus ? steps * kb / 74 : (double)cdiv((int64_t)wgs, 2 * (int64_t)cus) * (steps * 2 * kb / 56 + 1) - 1);
+  } else {
+    const double load = wgs / cus, one = steps * kb / 33;
+    const double start = tile == MX_TILE_16 ? 2.7 : tile == MX_TILE_16X32 ? 2.8 : tile == MX_TILE_32 ? 3.0 : 3.4;
+    const double least = tile == MX_TILE_32X64 ? 2.2 : 1.6;
+    t = start + (one > least ? one : least) * (load > 1 ? load : 1);
   }
-  if (!p.d.groups && workspace && c.tile != MX_TILE_256 && p.d.split > 1) c.split = p.d.split;
+  if (split > 1) t += 3 + (double)split * p.d.M * p.d.N * 8 / 4.2e6;
+  return t;
+}
+
+MxChoice mx_choose(const mx_gemm_plan& p, int32_t cus, bool workspace) {
+  const int32_t nsb = (int32_t)cdiv(p.d.K, 512);
+  const bool may_split = !p.d.groups && workspace;
+  int32_t best_tile = p.d.tile, best_split = 1;
+  double best = 1e300;
+  for (int32_t tile = MX_TILE_256; tile <= MX_TILE_16; ++tile) {
+    if (p.d.tile != MX_TILE_AUTO && p.d.tile != tile) continue;
+    int32_t bm, bn;
+    mx_tile_extent(tile, &bm, &bn);
+    // (the direct kernels' grid counts row blocks in 16 bits)
+    if (p.d.tile == MX_TILE_AUTO && tile > MX_TILE_128 && mx_row_blocks(p, bm) > 65535) continue;
+    for (int32_t split = 1; split <= 64; ++split) {
+      const bool wanted = p.d.split > 0 ? split == p.d.split : (split & (split - 1)) == 0 && split <= 16;
+      if (!wanted && split > 1) continue;
+      if (split > 1 && (!may_split || tile == MX_TILE_256 || split > nsb)) continue;
+      if (p.d.split == 1 && split > 1) continue;
+      const double t = estimate(p, cus, tile, split) - (p.d.split > 1 && split == p.d.split ? 1e9 : 0);
+      if (t < best) {
+        best = t;
+        best_tile = tile;
+        best_split = split;
+      }
+    }
+  }
+  MxChoice c{best_tile, p.d.split > 1 && may_split && best_tile != MX_TILE_256 ? p.d.split : best_split, 0};
   if (c.split > nsb) c.split = nsb > 1 ? nsb : 1;
   c.per = nsb > 0 ? (int32_t)cdiv(nsb, c.split) : 1;
   c.split = nsb > 0 ? (int32_t)cdiv(nsb, c.per) : 1;

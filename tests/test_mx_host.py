@@ -200,7 +200,8 @@ def test_plan_tile(lib):
     assert choice(tile=3, split=9, K=1000) == (3, 2)
     assert choice(tile=3, split=9, K=0) == (3, 1)
     assert choice(M=8192, N=8192, K=8192, **wide) == (_abi.MX_TILE["256"], 1)
-    assert choice(M=1, N=8192, K=8192, **wide) == (_abi.MX_TILE["16"], 1)
+    assert choice(M=1, N=8192, K=8192, **wide)[0] in (_abi.MX_TILE["16"], _abi.MX_TILE["16x32"])
+    assert choice(M=128, N=512, K=8192, d=2, ldd=512, c=0, post=0, act=0, tile=4)[1] > 1  # few tiles, a deep product
 
 
 def test_mx_tensor_refusals():
