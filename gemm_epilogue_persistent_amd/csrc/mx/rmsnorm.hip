@@ -7,7 +7,7 @@
 // Both are bound by memory. A row is held in registers from its single read to its last use:
 // TPR threads x CH chunks of 8 elements, chunk j of thread t at column (t + j TPR) 8. Four
 // adjacent lanes hold an MX block. Rows too long for registers take a kernel that reads them
-// twice. All sums are fp32, in a fixed order.
+// twice. All sums run in a fixed order.
 #include <type_traits>
 
 #include "mx_common.hpp"
@@ -25,27 +25,94 @@ struct NormParams {
   float* rstd;
   int64_t ldx, ldr, ldh, ldy;
   int32_t rows, cols, nb, nsb, fmt;
-  float eps, inv_cols;
+  float eps;
+  double inv_cols;
 };
 
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int m = 32; m > 0; m >>= 1) v += __shfl_xor(v, m);
+// v of another lane of the 16-lane row, by a DPP pattern.
+template <int PATTERN>
+__device__ __forceinline__ float dpp(float v) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), PATTERN, 0xF, 0xF, true));
+}
+template <int PATTERN>
+__device__ __forceinline__ double dpp(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, PATTERN, 0xF, 0xF, true);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), PATTERN, 0xF, 0xF, true);
+  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+template <typename V>
+__device__ __forceinline__ V wave_sum(V v) {
+  v += dpp<0xB1>(v);   // lanes 1 0 3 2 of a quad
+  v += dpp<0x4E>(v);   // lanes 2 3 0 1
+  v += dpp<0x141>(v);  // mirrored half rows
+  v += dpp<0x140>(v);  // mirrored rows
+  v += __shfl_xor(v, 16);
+  v += __shfl_xor(v, 32);
   return v;
 }
-// Sum over the TPR threads that share a row, in each of them (red: one float per wave).
-template <int TPR>
-__device__ __forceinline__ float row_sum(float v, float* red) {
+// Sum over the TPR threads that share a row, in each of them (red: one value per wave).
+template <int TPR, typename V>
+__device__ __forceinline__ V row_sum(V v, V* red) {
   v = wave_sum(v);
   if constexpr (TPR > 64) {
     __syncthreads();  // the last use of red is over
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
     __syncthreads();
-    v = 0.f;
+    v = 0;
 #pragma unroll
     for (int i = 0; i < TPR / 64; ++i) v += red[i];
   }
   return v;
+}
+
+// ---- y = h rstd w. A quantised value flips to its neighbour where an error carries y over the
+// border between them, so y is the rounding of the exact product: squares are summed in 64 bits,
+// rstd is held as hi + lo, h w is exact for 16-bit h and w (22 bits) or held as hi + lo too, and a y
+// that falls on a border of the element type is moved to the side of it that the product lies on.
+// (With fp32 sums and two fp32 products 56 of 69 million values flipped, and now none.)
+struct Rstd {
+  float hi, lo;
+};
+__device__ __forceinline__ Rstd reciprocal_root(double mean_eps) {
+  const double r0 = (double)__builtin_amdgcn_rsqf((float)mean_eps);
+  // One Newton step squares the relative error of about 2^-22. (The fp32 root is infinite for 0 and
+  // below the fp32 range, and 0 or NaN for an infinite or NaN sum; those need no step.)
+  const double r = __builtin_isfinite(r0) && r0 > 0 ? r0 + 0.5 * r0 * (1.0 - mean_eps * r0 * r0) : r0;
+  Rstd s;
+  s.hi = (float)r;
+  s.lo = __builtin_isfinite(s.hi) ? (float)(r - (double)s.hi) : 0.f;
+  return s;
+}
+template <typename T>
+__device__ __forceinline__ void scale8(const float h[8], const float w[8], const Rstd& r, float y[8]) {
+  float hw[8], c[8];
+  uint32_t low = ~0u;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    hw[e] = h[e] * w[e];
+    c[e] = hw[e] * r.lo;
+    if constexpr (sizeof(T) == 4) c[e] = fmaf(fmaf(h[e], w[e], -hw[e]), r.hi, c[e]);
+    y[e] = fmaf(hw[e], r.hi, c[e]);
+    low = min(low, __float_as_uint(y[e]) << 13);
+  }
+  // Borders between values of at most four significant bits: the last 19 bits of y are zero there.
+  if (low == 0) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float rest = fmaf(hw[e], r.hi, -y[e]) + c[e];  // product - y
+      const uint32_t b = __float_as_uint(y[e]);
+      if ((b << 13) == 0 && (b << 1) != 0 && rest != 0.f && __builtin_isfinite(rest))
+        y[e] = __uint_as_float((rest > 0.f) == (y[e] > 0.f) ? b + 1 : b - 1);
+    }
+  }
+}
+// Sum of squares of a chunk.
+__device__ __forceinline__ double squares(const float v[8]) {
+  double s = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) s = fma((double)v[e], (double)v[e], s);
+  return s;
 }
 
 template <typename T, int FMT>
@@ -64,13 +131,13 @@ __device__ __forceinline__ void norm_out(const NormParams& p, int64_t row, int c
 template <typename T, int TPR, int CH>
 __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void rmsnorm_kernel(const NormParams p) {
   constexpr int kRows = TPR == 64 ? 4 : 1;  // rows of a workgroup
-  __shared__ float red[TPR > 64 ? TPR / 64 : 1];
+  __shared__ double red[TPR > 64 ? TPR / 64 : 1];
   const int t = threadIdx.x % TPR;
   const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR;
   if (TPR == 64 && row >= p.rows) return;  // (a whole wave)
   const T* x = (const T*)p.x + row * p.ldx;
   Chunk<T> h[CH];
-  float ss = 0.f;
+  double ss = 0;
 #pragma unroll
   for (int j = 0; j < CH; ++j) h[j] = load_chunk(x, (t + j * TPR) * 8, p.cols);
   if (p.r) {
@@ -91,8 +158,7 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void rmsnorm_kernel(const No
       h[j] = pack<T>(a);
       if (p.h) store_chunk((T*)p.h + row * p.ldh, c, p.cols, h[j]);
       unpack(h[j], a);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(a[e], a[e], ss);
+      ss += squares(a);
     }
   } else {
 #pragma unroll
@@ -100,12 +166,11 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void rmsnorm_kernel(const No
       float a[8];
       settle(h[j], (t + j * TPR) * 8, p.cols);
       unpack(h[j], a);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(a[e], a[e], ss);
+      ss += squares(a);
     }
   }
-  const float rstd = 1.f / sqrtf(row_sum<TPR>(ss, red) * p.inv_cols + p.eps);
-  if (p.rstd && t == 0) p.rstd[row] = rstd;
+  const Rstd rstd = reciprocal_root(row_sum<TPR>(ss, red) * p.inv_cols + (double)p.eps);
+  if (p.rstd && t == 0) p.rstd[row] = rstd.hi;
 #pragma unroll
   for (int j = 0; j < CH; ++j) {
     const int ch = t + j * TPR;
@@ -113,8 +178,7 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void rmsnorm_kernel(const No
     forget(h[j]);
     unpack(h[j], a);
     load8((const T*)p.w, ch * 8, p.cols, w);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) a[e] = a[e] * rstd * w[e];
+    scale8<T>(a, w, rstd, a);
     norm_out<T>(p, row, ch, a);
   }
 }
@@ -122,7 +186,7 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void rmsnorm_kernel(const No
 // Rows of any length: one workgroup a row, read twice (the second time from the caches).
 template <typename T>
 __global__ __launch_bounds__(1024) void rmsnorm_long_kernel(const NormParams p) {
-  __shared__ float red[16];
+  __shared__ double red[16];
   const int64_t row = blockIdx.x;
   const T* x = (const T*)p.x + row * p.ldx;
   const T* r = p.r ? (const T*)p.r + row * p.ldr : nullptr;
@@ -137,23 +201,21 @@ __global__ __launch_bounds__(1024) void rmsnorm_long_kernel(const NormParams p) 
       unpack(pack<T>(v), v);
     }
   };
-  float ss = 0.f;
+  double ss = 0;
   for (int ch = threadIdx.x; ch < n; ch += 1024) {
     float v[8];
     load_h(ch, v);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) ss = fmaf(v[e], v[e], ss);
+    ss += squares(v);
   }
-  const float rstd = 1.f / sqrtf(row_sum<1024>(ss, red) * p.inv_cols + p.eps);
-  if (p.rstd && threadIdx.x == 0) p.rstd[row] = rstd;
+  const Rstd rstd = reciprocal_root(row_sum<1024>(ss, red) * p.inv_cols + (double)p.eps);
+  if (p.rstd && threadIdx.x == 0) p.rstd[row] = rstd.hi;
   for (int ch = threadIdx.x; ch < n; ch += 1024) {
     float v[8], w[8], y[8];
     load_h(ch, v);
     // (h may be x or the residual: every element is read again by the thread that replaces it)
     if (r && p.h) store_chunk((T*)p.h + row * p.ldh, ch * 8, p.cols, pack<T>(v));
     load8((const T*)p.w, ch * 8, p.cols, w);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = v[e] * rstd * w[e];
+    scale8<T>(v, w, rstd, y);
     norm_out<T>(p, row, ch, y);
   }
 }
@@ -424,7 +486,7 @@ gemm_status rmsnorm_forward(const rmsnorm_args* a, void* stream) {
   p.nsb = cdiv(p.nb, kMxScaleBlocks);
   p.fmt = a->q_codes ? a->q_format : MX_E4M3;
   p.eps = a->eps;
-  p.inv_cols = 1.f / (float)a->cols;
+  p.inv_cols = 1.0 / a->cols;
   with_type(a->type, [&](auto* t) { launch_norm<std::remove_pointer_t<decltype(t)>>(p, (hipStream_t)stream); });
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return fail(GEMM_ERR_HIP, "%s launch: %s", fn, hipGetErrorString(e));
