@@ -18,12 +18,6 @@ namespace gep {
 constexpr int kMxBlock = 32;
 constexpr int kMxScaleRows = 64, kMxScaleBlocks = 16;  // one scale tile, 1 KB
 
-// Byte offset of the scale of block b of row r; nsb = ceil(blocks per row / 16).
-__host__ __device__ __forceinline__ int64_t mx_scale_at(int64_t r, int b, int nsb) {
-  return ((r / kMxScaleRows * nsb + b / kMxScaleBlocks) * kMxScaleRows + r % kMxScaleRows) * kMxScaleBlocks +
-         b % kMxScaleBlocks;
-}
-
 // ---- chunks of 8 elements of a row of n elements of T (_Float16, __bf16 or float), at the
 // alignment of the element: rows of an odd length start anywhere, and gfx950 takes 16-byte
 // accesses at such addresses.
@@ -38,12 +32,12 @@ struct Chunk {
 };
 
 // Load elements [c, c + 8) of a row. The load itself has no branch, so that a thread's loads go out
-// together: a chunk that reaches past the end loads the row's last 8 elements instead, and unpack
-// moves them into place.
-template <typename T>
+// together: a chunk that reaches past the end loads the row's last 8 elements instead, and settle
+// moves them into place. WHOLE: n is a multiple of 8 and not 0.
+template <bool WHOLE, typename T>
 __device__ __forceinline__ Chunk<T> load_chunk(const T* row, int c, int n) {
   Chunk<T> k;
-  if (n >= 8) {  // (the same in every thread)
+  if (WHOLE || n >= 8) {  // (the same in every thread)
     const T* p = row + (c + 8 <= n ? c : n - 8);
     if constexpr (sizeof(T) == 4) {
       const Packed32 x = *(const Packed32*)p;
@@ -74,9 +68,12 @@ __device__ __forceinline__ void unpack(const Chunk<T>& k, float v[8]) {
 }
 // After load_chunk(row, c, n): a chunk that reaches past the end gets its elements into place, zeros
 // behind them. To be called once per loaded chunk, before unpack.
-template <typename T>
+template <bool WHOLE, typename T>
 __device__ __forceinline__ void settle(Chunk<T>& k, int c, int n) {
-  if (c + 8 > n && n >= 8) {
+  if constexpr (WHOLE) {
+#pragma unroll
+    for (int i = 0; i < Chunk<T>::kW; ++i) k.w[i] = c < n ? k.w[i] : 0u;
+  } else if (c + 8 > n && n >= 8) {
     const int s = c + 8 - n;  // places to move down
     T v[8];
     __builtin_memcpy(v, k.w, sizeof(v));
@@ -96,10 +93,10 @@ __device__ __forceinline__ void forget(Chunk<T>& k) {
 #pragma unroll
   for (int i = 0; i < Chunk<T>::kW; ++i) asm volatile("" : "+v"(k.w[i]));
 }
-template <typename T>
+template <bool WHOLE, typename T>
 __device__ __forceinline__ void load8(const T* row, int c, int n, float v[8]) {
-  Chunk<T> k = load_chunk(row, c, n);
-  settle(k, c, n);
+  Chunk<T> k = load_chunk<WHOLE>(row, c, n);
+  settle<WHOLE>(k, c, n);
   unpack(k, v);
 }
 // Eight values rounded to T.
@@ -113,7 +110,7 @@ __device__ __forceinline__ Chunk<T> pack(const float v[8]) {
   return k;
 }
 // Store a chunk of unshifted elements; those past the end of the row are not written.
-template <typename T>
+template <bool WHOLE, typename T>
 __device__ __forceinline__ void store_chunk(T* row, int c, int n, const Chunk<T>& k) {
   if (c + 8 <= n) {
     if constexpr (sizeof(T) == 4) {
@@ -127,7 +124,7 @@ __device__ __forceinline__ void store_chunk(T* row, int c, int n, const Chunk<T>
       for (int i = 0; i < 4; ++i) x.w[i] = k.w[i];
       *(Packed16*)(row + c) = x;
     }
-  } else if (c < n) {
+  } else if (!WHOLE && c < n) {
     T e[8];
     __builtin_memcpy(e, k.w, sizeof(e));
 #pragma unroll
@@ -193,23 +190,35 @@ __device__ __forceinline__ uint2 mx_codes8(const float v[8], float inv, bool bad
   return w;
 }
 
-// Quantise and store chunk `ch` (8 values, in the lanes of one quad the 32 of a block) of row r:
-// its codes, the block's scale (by the quad's first lane) and, after the row's last block, zero
-// scales up to a whole tile. nb blocks per row, nsb = ceil(nb / 16).
+// The codes of row r, and the scale of its block 0 (block b: (b / 16) * 1024 + b % 16 bytes further).
 template <int FMT>
-__device__ __forceinline__ void mx_store_chunk(const float v[8], int64_t r, int ch, int nb, int nsb, uint8_t* codes,
-                                               uint8_t* scales) {
+__device__ __forceinline__ uint8_t* mx_code_row(uint8_t* codes, int64_t r, int nb) {
+  return codes + r * nb * (FMT == MX_E4M3 ? 32 : 16);
+}
+__device__ __forceinline__ uint8_t* mx_scale_row(uint8_t* scales, int64_t r, int nsb) {
+  return scales + ((r / kMxScaleRows) * nsb * kMxScaleRows + r % kMxScaleRows) * kMxScaleBlocks;
+}
+__device__ __forceinline__ int mx_scale_offset(int b) {
+  return (b / kMxScaleBlocks) * (kMxScaleRows * kMxScaleBlocks) + b % kMxScaleBlocks;
+}
+
+// Quantise and store chunk `ch` of a row (8 values, in the lanes of one quad the 32 of a block): its
+// codes, the block's scale (by the quad's first lane) and, after the row's last block, zero scales up
+// to a whole tile. nb blocks a row, nsb = ceil(nb / 16).
+template <int FMT>
+__device__ __forceinline__ void mx_store_chunk(const float v[8], int ch, int nb, int nsb, uint8_t* code_row,
+                                               uint8_t* scale_row) {
   const uint32_t am = quad_max(amax_bits(v));
   float inv;
   const uint32_t s = mx_scale<FMT>(am, inv);
   const uint2 w = mx_codes8<FMT>(v, inv, s == 255u);
-  if constexpr (FMT == MX_E4M3) *(uint2*)(codes + (r * nb * 4 + ch) * 8) = w;
-  else *(uint32_t*)(codes + (r * nb * 4 + ch) * 4) = w.x;
+  if constexpr (FMT == MX_E4M3) *(uint2*)(code_row + ch * 8) = w;
+  else *(uint32_t*)(code_row + ch * 4) = w.x;
   const int b = ch >> 2;
   if ((ch & 3) == 0) {
-    scales[mx_scale_at(r, b, nsb)] = (uint8_t)s;
+    scale_row[mx_scale_offset(b)] = (uint8_t)s;
     if (b == nb - 1)
-      for (int q = nb; q < nsb * kMxScaleBlocks; ++q) scales[mx_scale_at(r, q, nsb)] = 0;
+      for (int q = nb; q < nsb * kMxScaleBlocks; ++q) scale_row[mx_scale_offset(q)] = 0;
   }
 }
 

@@ -2,6 +2,8 @@
 //
 // Both are bound by memory: the input is read once, codes and scales (8.25 or 4.25 bits a value)
 // are written once, and a value costs about ten vector instructions.
+#include <type_traits>
+
 #include "mx_common.hpp"
 
 namespace gep {
@@ -15,7 +17,7 @@ constexpr int kThreads = 256;
 // ---- blocks along a row. A thread takes a chunk of 8 values (16 or 32 bytes), the four lanes of
 // a quad a block: the maximum crosses lanes by DPP, loads and stores are contiguous over the
 // wave. Chunks are numbered row by row over rows [r0, r0 + rows) (below 2^31 in one launch).
-template <typename T, int FMT>
+template <typename T, int FMT, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(const T* x, int64_t ldx, int64_t r0, int cols, int nb,
                                                                  int nsb, uint32_t n, FastDiv fd_cpr, uint8_t* codes,
                                                                  uint8_t* scales) {
@@ -25,8 +27,8 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(const T* x, int
   fd_divmod(fd_cpr, i, rr, ch);
   const int64_t r = r0 + rr;
   float v[8];
-  load8(x + r * ldx, (int)ch * 8, cols, v);
-  mx_store_chunk<FMT>(v, r, (int)ch, nb, nsb, codes, scales);
+  load8<WHOLE>(x + r * ldx, (int)ch * 8, cols, v);
+  mx_store_chunk<FMT>(v, (int)ch, nb, nsb, mx_code_row<FMT>(codes, r, nb), mx_scale_row(scales, r, nsb));
 }
 
 // ---- blocks along a column. A workgroup takes 128 rows (four blocks) by 256 bytes of columns:
@@ -124,9 +126,10 @@ __global__ __launch_bounds__(kTB* kRowDw) void quantize_cols_kernel(const T* x, 
     } else {
       *(uint4*)(codes + ((int64_t)c * nb + b) * 16) = uint4{o[0], o[1], o[2], o[3]};
     }
-    scales[mx_scale_at(c, b, nsb)] = (uint8_t)s;
+    uint8_t* scale_row = mx_scale_row(scales, c, nsb);
+    scale_row[mx_scale_offset(b)] = (uint8_t)s;
     if (b == nb - 1)
-      for (int q = nb; q < nsb * kMxScaleBlocks; ++q) scales[mx_scale_at(c, q, nsb)] = 0;
+      for (int q = nb; q < nsb * kMxScaleBlocks; ++q) scale_row[mx_scale_offset(q)] = 0;
   }
 }
 
@@ -140,7 +143,7 @@ __global__ __launch_bounds__(kThreads) void dequantize_kernel(const uint8_t* cod
   uint32_t rr, ch;
   fd_divmod(fd_cpr, i, rr, ch);
   const int64_t r = r0 + rr;
-  const int s = scales[mx_scale_at(r, (int)ch >> 2, nsb)];
+  const int s = mx_scale_row(const_cast<uint8_t*>(scales), r, nsb)[mx_scale_offset((int)ch >> 2)];
   float v[8];
   typedef float f32x2 __attribute__((ext_vector_type(2)));
   f32x2 p[4];
@@ -162,7 +165,7 @@ __global__ __launch_bounds__(kThreads) void dequantize_kernel(const uint8_t* cod
 #pragma unroll
   for (int e = 0; e < 8; ++e)
     v[e] = s == 255 ? __uint_as_float(0x7FC00000u) : __builtin_ldexpf(p[e >> 1][e & 1], s - 127);
-  store_chunk(out + r * ldo, (int)ch * 8, k, pack<T>(v));
+  store_chunk<false>(out + r * ldo, (int)ch * 8, k, pack<T>(v));
 }
 
 // Launch `f(r0, n)` over ranges of rows whose chunks number below 2^31.
@@ -229,8 +232,14 @@ gemm_status mx_quantize(int32_t rows, int32_t cols, const void* x, int32_t x_typ
       const uint32_t cpr = (uint32_t)nb * 4;
       row_ranges(rows, cpr, [&](int64_t r0, uint32_t n) {
         const unsigned g = (n + kThreads - 1) / kThreads;
-        if (format == MX_E2M1) quantize_rows_kernel<T, MX_E2M1><<<g, kThreads, 0, s>>>((const T*)x, ldx, r0, cols, nb, nsb, n, make_fastdiv(cpr), qc, qs);
-        else quantize_rows_kernel<T, MX_E4M3><<<g, kThreads, 0, s>>>((const T*)x, ldx, r0, cols, nb, nsb, n, make_fastdiv(cpr), qc, qs);
+        auto go = [&](auto fmt, auto whole) {
+          quantize_rows_kernel<T, decltype(fmt)::value, decltype(whole)::value><<<g, kThreads, 0, s>>>(
+              (const T*)x, ldx, r0, cols, nb, nsb, n, make_fastdiv(cpr), qc, qs);
+        };
+        using E2M1 = std::integral_constant<int, MX_E2M1>;
+        using E4M3 = std::integral_constant<int, MX_E4M3>;
+        if (cols % 8 == 0) format == MX_E2M1 ? go(E2M1{}, std::true_type{}) : go(E4M3{}, std::true_type{});
+        else format == MX_E2M1 ? go(E2M1{}, std::false_type{}) : go(E4M3{}, std::false_type{});
       });
     }
   });

@@ -24,7 +24,7 @@ struct NormParams {
   uint8_t *codes, *scales;
   float* rstd;
   int64_t ldx, ldr, ldh, ldy;
-  int32_t rows, cols, nb, nsb, fmt;
+  int32_t rows, cols, nb, nsb;
   float eps;
   double inv_cols;
 };
@@ -115,20 +115,20 @@ __device__ __forceinline__ double squares(const float v[8]) {
   return s;
 }
 
-template <typename T, int FMT>
-__device__ __forceinline__ void norm_store(const NormParams& p, int64_t row, int ch, const float y[8]) {
-  if (p.y) store_chunk((T*)p.y + row * p.ldy, ch * 8, p.cols, pack<T>(y));
-  if (p.codes && ch < p.nb * 4) mx_store_chunk<FMT>(y, row, ch, p.nb, p.nsb, p.codes, p.scales);
-}
-template <typename T>
-__device__ __forceinline__ void norm_out(const NormParams& p, int64_t row, int ch, const float y[8]) {
-  if (p.fmt == MX_E2M1) norm_store<T, MX_E2M1>(p, row, ch, y);
-  else norm_store<T, MX_E4M3>(p, row, ch, y);
+// Output chunk `ch` of a row: y in its type and / or (FMT an mx_format, or kNoMx) quantised.
+constexpr int kNoMx = -1;
+template <typename T, int FMT, bool WHOLE>
+__device__ __forceinline__ void norm_out(const NormParams& p, T* y_row, uint8_t* code_row, uint8_t* scale_row, int ch,
+                                         const float y[8]) {
+  if (p.y) store_chunk<WHOLE>(y_row, ch * 8, p.cols, pack<T>(y));
+  if constexpr (FMT != kNoMx) {
+    if (ch < p.nb * 4) mx_store_chunk<FMT>(y, ch, p.nb, p.nsb, code_row, scale_row);
+  }
 }
 
 // h is kept in its own type (its rounded value is exact there): half the registers of fp32 for
 // 16-bit rows.
-template <typename T, int TPR, int CH>
+template <typename T, int TPR, int CH, int FMT, bool WHOLE>
 __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void rmsnorm_kernel(const NormParams p) {
   constexpr int kRows = TPR == 64 ? 4 : 1;  // rows of a workgroup
   __shared__ double red[TPR > 64 ? TPR / 64 : 1];
@@ -139,24 +139,24 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void rmsnorm_kernel(const No
   Chunk<T> h[CH];
   double ss = 0;
 #pragma unroll
-  for (int j = 0; j < CH; ++j) h[j] = load_chunk(x, (t + j * TPR) * 8, p.cols);
+  for (int j = 0; j < CH; ++j) h[j] = load_chunk<WHOLE>(x, (t + j * TPR) * 8, p.cols);
   if (p.r) {
     const T* r = (const T*)p.r + row * p.ldr;
     Chunk<T> rc[CH];
 #pragma unroll
-    for (int j = 0; j < CH; ++j) rc[j] = load_chunk(r, (t + j * TPR) * 8, p.cols);
+    for (int j = 0; j < CH; ++j) rc[j] = load_chunk<WHOLE>(r, (t + j * TPR) * 8, p.cols);
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
       const int c = (t + j * TPR) * 8;
       float a[8], b[8];
-      settle(h[j], c, p.cols);
-      settle(rc[j], c, p.cols);
+      settle<WHOLE>(h[j], c, p.cols);
+      settle<WHOLE>(rc[j], c, p.cols);
       unpack(h[j], a);
       unpack(rc[j], b);
 #pragma unroll
       for (int e = 0; e < 8; ++e) a[e] += b[e];
       h[j] = pack<T>(a);
-      if (p.h) store_chunk((T*)p.h + row * p.ldh, c, p.cols, h[j]);
+      if (p.h) store_chunk<WHOLE>((T*)p.h + row * p.ldh, c, p.cols, h[j]);
       unpack(h[j], a);
       ss += squares(a);
     }
@@ -164,27 +164,29 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void rmsnorm_kernel(const No
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
       float a[8];
-      settle(h[j], (t + j * TPR) * 8, p.cols);
+      settle<WHOLE>(h[j], (t + j * TPR) * 8, p.cols);
       unpack(h[j], a);
       ss += squares(a);
     }
   }
   const Rstd rstd = reciprocal_root(row_sum<TPR>(ss, red) * p.inv_cols + (double)p.eps);
   if (p.rstd && t == 0) p.rstd[row] = rstd.hi;
+  T* y_row = (T*)p.y + row * p.ldy;
+  uint8_t *code_row = mx_code_row<FMT>(p.codes, row, p.nb), *scale_row = mx_scale_row(p.scales, row, p.nsb);
 #pragma unroll
   for (int j = 0; j < CH; ++j) {
     const int ch = t + j * TPR;
     float a[8], w[8];
     forget(h[j]);
     unpack(h[j], a);
-    load8((const T*)p.w, ch * 8, p.cols, w);
+    load8<WHOLE>((const T*)p.w, ch * 8, p.cols, w);
     scale8<T>(a, w, rstd, a);
-    norm_out<T>(p, row, ch, a);
+    norm_out<T, FMT, WHOLE>(p, y_row, code_row, scale_row, ch, a);
   }
 }
 
 // Rows of any length: one workgroup a row, read twice (the second time from the caches).
-template <typename T>
+template <typename T, int FMT>
 __global__ __launch_bounds__(1024) void rmsnorm_long_kernel(const NormParams p) {
   __shared__ double red[16];
   const int64_t row = blockIdx.x;
@@ -192,10 +194,10 @@ __global__ __launch_bounds__(1024) void rmsnorm_long_kernel(const NormParams p) 
   const T* r = p.r ? (const T*)p.r + row * p.ldr : nullptr;
   const int n = p.nb * 4;
   auto load_h = [&](int ch, float v[8]) {
-    load8(x, ch * 8, p.cols, v);
+    load8<false>(x, ch * 8, p.cols, v);
     if (r) {
       float q[8];
-      load8(r, ch * 8, p.cols, q);
+      load8<false>(r, ch * 8, p.cols, q);
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] += q[e];
       unpack(pack<T>(v), v);
@@ -213,10 +215,10 @@ __global__ __launch_bounds__(1024) void rmsnorm_long_kernel(const NormParams p) 
     float v[8], w[8], y[8];
     load_h(ch, v);
     // (h may be x or the residual: every element is read again by the thread that replaces it)
-    if (r && p.h) store_chunk((T*)p.h + row * p.ldh, ch * 8, p.cols, pack<T>(v));
-    load8((const T*)p.w, ch * 8, p.cols, w);
+    if (r && p.h) store_chunk<false>((T*)p.h + row * p.ldh, ch * 8, p.cols, pack<T>(v));
+    load8<false>((const T*)p.w, ch * 8, p.cols, w);
     scale8<T>(v, w, rstd, y);
-    norm_out<T>(p, row, ch, y);
+    norm_out<T, FMT, false>(p, (T*)p.y + row * p.ldy, mx_code_row<FMT>(p.codes, row, p.nb), mx_scale_row(p.scales, row, p.nsb), ch, y);
   }
 }
 
@@ -233,7 +235,7 @@ struct NormGradParams {
   float inv_cols;
 };
 
-template <typename T, int TPR, int CH>
+template <typename T, int TPR, int CH, bool WHOLE>
 __global__ __launch_bounds__(TPR) void rmsnorm_grad_kernel(const NormGradParams p) {
   __shared__ float red[TPR > 64 ? TPR / 64 : 1];
   const int t = threadIdx.x;
@@ -242,8 +244,8 @@ __global__ __launch_bounds__(TPR) void rmsnorm_grad_kernel(const NormGradParams 
 #pragma unroll
   for (int j = 0; j < CH; ++j) {
     const int c = (t + j * TPR) * 8;
-    w[j] = load_chunk((const T*)p.w, c, p.cols);
-    settle(w[j], c, p.cols);
+    w[j] = load_chunk<WHOLE>((const T*)p.w, c, p.cols);
+    settle<WHOLE>(w[j], c, p.cols);
 #pragma unroll
     for (int e = 0; e < 8; ++e) dw[j][e] = 0.f;
   }
@@ -252,20 +254,20 @@ __global__ __launch_bounds__(TPR) void rmsnorm_grad_kernel(const NormGradParams 
     Chunk<T> hc[CH], dyc[CH], gc[CH];
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
-      hc[j] = load_chunk((const T*)p.h + row * p.ldh, (t + j * TPR) * 8, p.cols);
-      dyc[j] = load_chunk((const T*)p.dy + row * p.lddy, (t + j * TPR) * 8, p.cols);
+      hc[j] = load_chunk<WHOLE>((const T*)p.h + row * p.ldh, (t + j * TPR) * 8, p.cols);
+      dyc[j] = load_chunk<WHOLE>((const T*)p.dy + row * p.lddy, (t + j * TPR) * 8, p.cols);
     }
     if (p.dres) {
 #pragma unroll
-      for (int j = 0; j < CH; ++j) gc[j] = load_chunk((const T*)p.dres + row * p.lddres, (t + j * TPR) * 8, p.cols);
+      for (int j = 0; j < CH; ++j) gc[j] = load_chunk<WHOLE>((const T*)p.dres + row * p.lddres, (t + j * TPR) * 8, p.cols);
     }
     float dot = 0.f;
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
       const int c = (t + j * TPR) * 8;
       float n[8], dy[8], ww[8];
-      settle(hc[j], c, p.cols);
-      settle(dyc[j], c, p.cols);
+      settle<WHOLE>(hc[j], c, p.cols);
+      settle<WHOLE>(dyc[j], c, p.cols);
       forget(w[j]);
       unpack(hc[j], n);
       unpack(dyc[j], dy);
@@ -289,7 +291,7 @@ __global__ __launch_bounds__(TPR) void rmsnorm_grad_kernel(const NormGradParams 
       unpack(dyc[j], dy);
       unpack(w[j], ww);
       if (p.dres) {
-        settle(gc[j], c, p.cols);
+        settle<WHOLE>(gc[j], c, p.cols);
         unpack(gc[j], g);
       } else {
 #pragma unroll
@@ -297,12 +299,12 @@ __global__ __launch_bounds__(TPR) void rmsnorm_grad_kernel(const NormGradParams 
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) g[e] = fmaf(rstd, dy[e] * ww[e] - n[e] * rstd * m, g[e]);
-      store_chunk((T*)p.dx + row * p.lddx, c, p.cols, pack<T>(g));
+      store_chunk<WHOLE>((T*)p.dx + row * p.lddx, c, p.cols, pack<T>(g));
     }
   }
   float* part = p.part + (int64_t)blockIdx.x * p.cols;
 #pragma unroll
-  for (int j = 0; j < CH; ++j) store_chunk(part, (t + j * TPR) * 8, p.cols, pack<float>(dw[j]));
+  for (int j = 0; j < CH; ++j) store_chunk<WHOLE>(part, (t + j * TPR) * 8, p.cols, pack<float>(dw[j]));
 }
 
 // Rows of any length: each row is read twice and the column sums live in the workgroup's row of
@@ -319,14 +321,14 @@ __global__ __launch_bounds__(1024) void rmsnorm_grad_long_kernel(const NormGradP
     float dot = 0.f;
     for (int ch = threadIdx.x; ch < n8; ch += 1024) {
       float n[8], dy[8], w[8], s[8];
-      load8(h, ch * 8, p.cols, n);
-      load8(dyp, ch * 8, p.cols, dy);
-      load8((const T*)p.w, ch * 8, p.cols, w);
+      load8<false>(h, ch * 8, p.cols, n);
+      load8<false>(dyp, ch * 8, p.cols, dy);
+      load8<false>((const T*)p.w, ch * 8, p.cols, w);
       if (row == blockIdx.x) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) s[e] = 0.f;
       } else {
-        load8(part, ch * 8, p.cols, s);
+        load8<false>(part, ch * 8, p.cols, s);
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -334,23 +336,23 @@ __global__ __launch_bounds__(1024) void rmsnorm_grad_long_kernel(const NormGradP
         s[e] += dyn;
         dot = fmaf(dyn, w[e], dot);
       }
-      store_chunk(part, ch * 8, p.cols, pack<float>(s));
+      store_chunk<false>(part, ch * 8, p.cols, pack<float>(s));
     }
     const float m = row_sum<1024>(dot, red) * p.inv_cols;
     for (int ch = threadIdx.x; ch < n8; ch += 1024) {
       float n[8], dy[8], w[8], g[8];
-      load8(h, ch * 8, p.cols, n);
-      load8(dyp, ch * 8, p.cols, dy);
-      load8((const T*)p.w, ch * 8, p.cols, w);
+      load8<false>(h, ch * 8, p.cols, n);
+      load8<false>(dyp, ch * 8, p.cols, dy);
+      load8<false>((const T*)p.w, ch * 8, p.cols, w);
       if (p.dres) {
-        load8((const T*)p.dres + row * p.lddres, ch * 8, p.cols, g);
+        load8<false>((const T*)p.dres + row * p.lddres, ch * 8, p.cols, g);
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) g[e] = 0.f;
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) g[e] = fmaf(rstd, dy[e] * w[e] - n[e] * rstd * m, g[e]);
-      store_chunk((T*)p.dx + row * p.lddx, ch * 8, p.cols, pack<T>(g));
+      store_chunk<false>((T*)p.dx + row * p.lddx, ch * 8, p.cols, pack<T>(g));
     }
   }
 }
@@ -394,13 +396,15 @@ bool with_shape(int chunks, F&& f) {
   return true;
 }
 
-template <typename T>
+template <typename T, int FMT>
 void launch_norm(const NormParams& p, hipStream_t s) {
   const bool done = with_shape(p.nb * 4, [&](auto tpr, auto ch) {
-    constexpr int TPR = decltype(tpr)::value, rows = TPR == 64 ? 4 : 1;
-    rmsnorm_kernel<T, TPR, decltype(ch)::value><<<cdiv(p.rows, rows), TPR * rows, 0, s>>>(p);
+    constexpr int TPR = decltype(tpr)::value, CH = decltype(ch)::value, rows = TPR == 64 ? 4 : 1;
+    const unsigned g = (unsigned)cdiv(p.rows, rows);
+    if (p.cols % 8 == 0) rmsnorm_kernel<T, TPR, CH, FMT, true><<<g, TPR * rows, 0, s>>>(p);
+    else rmsnorm_kernel<T, TPR, CH, FMT, false><<<g, TPR * rows, 0, s>>>(p);
   });
-  if (!done) rmsnorm_long_kernel<T><<<p.rows, 1024, 0, s>>>(p);
+  if (!done) rmsnorm_long_kernel<T, FMT><<<p.rows, 1024, 0, s>>>(p);
 }
 
 // Rows of partial sums: the workgroups that the card holds at once (16 waves a compute unit;
@@ -416,8 +420,9 @@ int grad_parts(int rows, int cols) {
 template <typename T>
 void launch_grad(const NormGradParams& p, int parts, hipStream_t s) {
   const bool done = with_shape(cdiv(p.cols, 8), [&](auto tpr, auto ch) {
-    constexpr int TPR = decltype(tpr)::value;
-    rmsnorm_grad_kernel<T, TPR, decltype(ch)::value><<<parts, TPR, 0, s>>>(p);
+    constexpr int TPR = decltype(tpr)::value, CH = decltype(ch)::value;
+    if (p.cols % 8 == 0) rmsnorm_grad_kernel<T, TPR, CH, true><<<parts, TPR, 0, s>>>(p);
+    else rmsnorm_grad_kernel<T, TPR, CH, false><<<parts, TPR, 0, s>>>(p);
   });
   if (!done) rmsnorm_grad_long_kernel<T><<<parts, 1024, 0, s>>>(p);
 }
@@ -484,10 +489,14 @@ gemm_status rmsnorm_forward(const rmsnorm_args* a, void* stream) {
   p.rows = a->rows; p.cols = a->cols;
   p.nb = cdiv(a->cols, kMxBlock);
   p.nsb = cdiv(p.nb, kMxScaleBlocks);
-  p.fmt = a->q_codes ? a->q_format : MX_E4M3;
   p.eps = a->eps;
   p.inv_cols = 1.0 / a->cols;
-  with_type(a->type, [&](auto* t) { launch_norm<std::remove_pointer_t<decltype(t)>>(p, (hipStream_t)stream); });
+  with_type(a->type, [&](auto* t) {
+    using T = std::remove_pointer_t<decltype(t)>;
+    if (!a->q_codes) launch_norm<T, kNoMx>(p, (hipStream_t)stream);
+    else if (a->q_format == MX_E2M1) launch_norm<T, MX_E2M1>(p, (hipStream_t)stream);
+    else launch_norm<T, MX_E4M3>(p, (hipStream_t)stream);
+  });
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return fail(GEMM_ERR_HIP, "%s launch: %s", fn, hipGetErrorString(e));
   return GEMM_OK;
