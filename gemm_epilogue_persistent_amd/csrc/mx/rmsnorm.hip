@@ -5,7 +5,7 @@
 //   dx = rstd (p - n mean(p n)) + dres,  dw = sum_rows dy n,   n = h rstd, p = dy w
 //
 // Both are bound by memory. A row is held in registers from its single read to its last use:
-// TPR threads x CH chunks of 8 elements, chunk j of thread t at column (t + j TPR) 8. Four
+// threads x CH chunks of 8 elements, chunk j of thread t at column (t + j threads) 8. Four
 // adjacent lanes hold an MX block. Rows too long for registers take a kernel that reads them
 // twice. All sums run in a fixed order.
 #include <type_traits>
@@ -51,17 +51,17 @@ __device__ __forceinline__ V wave_sum(V v) {
   v += __shfl_xor(v, 32);
   return v;
 }
-// Sum over the TPR threads that share a row, in each of them (red: one value per wave).
-template <int TPR, typename V>
+// Sum over the threads of a row, in each of them. WAVE: a wave a row; else the workgroup (red: one
+// value per wave).
+template <bool WAVE, typename V>
 __device__ __forceinline__ V row_sum(V v, V* red) {
   v = wave_sum(v);
-  if constexpr (TPR > 64) {
+  if constexpr (!WAVE) {
     __syncthreads();  // the last use of red is over
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
     __syncthreads();
     v = 0;
-#pragma unroll
-    for (int i = 0; i < TPR / 64; ++i) v += red[i];
+    for (int i = 0; i < (int)blockDim.x / 64; ++i) v += red[i];
   }
   return v;
 }
@@ -128,26 +128,26 @@ __device__ __forceinline__ void norm_out(const NormParams& p, T* y_row, uint8_t*
 
 // h is kept in its own type (its rounded value is exact there): half the registers of fp32 for
 // 16-bit rows.
-template <typename T, int TPR, int CH, int FMT, bool WHOLE>
-__global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void rmsnorm_kernel(const NormParams p) {
-  constexpr int kRows = TPR == 64 ? 4 : 1;  // rows of a workgroup
-  __shared__ double red[TPR > 64 ? TPR / 64 : 1];
-  const int t = threadIdx.x % TPR;
-  const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR;
-  if (TPR == 64 && row >= p.rows) return;  // (a whole wave)
+template <typename T, bool WAVE, int CH, int FMT, bool WHOLE>
+__global__ __launch_bounds__(WAVE ? 256 : 1024) void rmsnorm_kernel(const NormParams p) {
+  __shared__ double red[WAVE ? 1 : 16];
+  const int threads = WAVE ? 64 : blockDim.x;
+  const int t = WAVE ? threadIdx.x & 63 : threadIdx.x;
+  const int64_t row = WAVE ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
+  if (WAVE && row >= p.rows) return;  // (a whole wave)
   const T* x = (const T*)p.x + row * p.ldx;
   Chunk<T> h[CH];
   double ss = 0;
 #pragma unroll
-  for (int j = 0; j < CH; ++j) h[j] = load_chunk<WHOLE>(x, (t + j * TPR) * 8, p.cols);
+  for (int j = 0; j < CH; ++j) h[j] = load_chunk<WHOLE>(x, (t + j * threads) * 8, p.cols);
   if (p.r) {
     const T* r = (const T*)p.r + row * p.ldr;
     Chunk<T> rc[CH];
 #pragma unroll
-    for (int j = 0; j < CH; ++j) rc[j] = load_chunk<WHOLE>(r, (t + j * TPR) * 8, p.cols);
+    for (int j = 0; j < CH; ++j) rc[j] = load_chunk<WHOLE>(r, (t + j * threads) * 8, p.cols);
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
-      const int c = (t + j * TPR) * 8;
+      const int c = (t + j * threads) * 8;
       float a[8], b[8];
       settle<WHOLE>(h[j], c, p.cols);
       settle<WHOLE>(rc[j], c, p.cols);
@@ -164,18 +164,18 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void rmsnorm_kernel(const No
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
       float a[8];
-      settle<WHOLE>(h[j], (t + j * TPR) * 8, p.cols);
+      settle<WHOLE>(h[j], (t + j * threads) * 8, p.cols);
       unpack(h[j], a);
       ss += squares(a);
     }
   }
-  const Rstd rstd = reciprocal_root(row_sum<TPR>(ss, red) * p.inv_cols + (double)p.eps);
+  const Rstd rstd = reciprocal_root(row_sum<WAVE>(ss, red) * p.inv_cols + (double)p.eps);
   if (p.rstd && t == 0) p.rstd[row] = rstd.hi;
   T* y_row = (T*)p.y + row * p.ldy;
   uint8_t *code_row = mx_code_row<FMT>(p.codes, row, p.nb), *scale_row = mx_scale_row(p.scales, row, p.nsb);
 #pragma unroll
   for (int j = 0; j < CH; ++j) {
-    const int ch = t + j * TPR;
+    const int ch = t + j * threads;
     float a[8], w[8];
     forget(h[j]);
     unpack(h[j], a);
@@ -209,7 +209,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_long_kernel(const NormParams p) 
     load_h(ch, v);
     ss += squares(v);
   }
-  const Rstd rstd = reciprocal_root(row_sum<1024>(ss, red) * p.inv_cols + (double)p.eps);
+  const Rstd rstd = reciprocal_root(row_sum<false>(ss, red) * p.inv_cols + (double)p.eps);
   if (p.rstd && threadIdx.x == 0) p.rstd[row] = rstd.hi;
   for (int ch = threadIdx.x; ch < n; ch += 1024) {
     float v[8], w[8], y[8];
@@ -235,15 +235,15 @@ struct NormGradParams {
   float inv_cols;
 };
 
-template <typename T, int TPR, int CH, bool WHOLE>
-__global__ __launch_bounds__(TPR) void rmsnorm_grad_kernel(const NormGradParams p) {
-  __shared__ float red[TPR > 64 ? TPR / 64 : 1];
-  const int t = threadIdx.x;
+template <typename T, bool WAVE, int CH, bool WHOLE>
+__global__ __launch_bounds__(WAVE ? 64 : 1024) void rmsnorm_grad_kernel(const NormGradParams p) {
+  __shared__ float red[WAVE ? 1 : 16];
+  const int t = threadIdx.x, threads = blockDim.x;
   float dw[CH][8];
   Chunk<T> w[CH];
 #pragma unroll
   for (int j = 0; j < CH; ++j) {
-    const int c = (t + j * TPR) * 8;
+    const int c = (t + j * threads) * 8;
     w[j] = load_chunk<WHOLE>((const T*)p.w, c, p.cols);
     settle<WHOLE>(w[j], c, p.cols);
 #pragma unroll
@@ -254,17 +254,17 @@ __global__ __launch_bounds__(TPR) void rmsnorm_grad_kernel(const NormGradParams 
     Chunk<T> hc[CH], dyc[CH], gc[CH];
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
-      hc[j] = load_chunk<WHOLE>((const T*)p.h + row * p.ldh, (t + j * TPR) * 8, p.cols);
-      dyc[j] = load_chunk<WHOLE>((const T*)p.dy + row * p.lddy, (t + j * TPR) * 8, p.cols);
+      hc[j] = load_chunk<WHOLE>((const T*)p.h + row * p.ldh, (t + j * threads) * 8, p.cols);
+      dyc[j] = load_chunk<WHOLE>((const T*)p.dy + row * p.lddy, (t + j * threads) * 8, p.cols);
     }
     if (p.dres) {
 #pragma unroll
-      for (int j = 0; j < CH; ++j) gc[j] = load_chunk<WHOLE>((const T*)p.dres + row * p.lddres, (t + j * TPR) * 8, p.cols);
+      for (int j = 0; j < CH; ++j) gc[j] = load_chunk<WHOLE>((const T*)p.dres + row * p.lddres, (t + j * threads) * 8, p.cols);
     }
     float dot = 0.f;
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
-      const int c = (t + j * TPR) * 8;
+      const int c = (t + j * threads) * 8;
       float n[8], dy[8], ww[8];
       settle<WHOLE>(hc[j], c, p.cols);
       settle<WHOLE>(dyc[j], c, p.cols);
@@ -279,10 +279,10 @@ __global__ __launch_bounds__(TPR) void rmsnorm_grad_kernel(const NormGradParams 
         dot = fmaf(dyn, ww[e], dot);
       }
     }
-    const float m = row_sum<TPR>(dot, red) * p.inv_cols;
+    const float m = row_sum<WAVE>(dot, red) * p.inv_cols;
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
-      const int c = (t + j * TPR) * 8;
+      const int c = (t + j * threads) * 8;
       float n[8], dy[8], ww[8], g[8];
       forget(hc[j]);
       forget(dyc[j]);
@@ -304,7 +304,7 @@ __global__ __launch_bounds__(TPR) void rmsnorm_grad_kernel(const NormGradParams 
   }
   float* part = p.part + (int64_t)blockIdx.x * p.cols;
 #pragma unroll
-  for (int j = 0; j < CH; ++j) store_chunk<WHOLE>(part, (t + j * TPR) * 8, p.cols, pack<float>(dw[j]));
+  for (int j = 0; j < CH; ++j) store_chunk<WHOLE>(part, (t + j * threads) * 8, p.cols, pack<float>(dw[j]));
 }
 
 // Rows of any length: each row is read twice and the column sums live in the workgroup's row of
@@ -338,7 +338,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_grad_long_kernel(const NormGradP
       }
       store_chunk<false>(part, ch * 8, p.cols, pack<float>(s));
     }
-    const float m = row_sum<1024>(dot, red) * p.inv_cols;
+    const float m = row_sum<false>(dot, red) * p.inv_cols;
     for (int ch = threadIdx.x; ch < n8; ch += 1024) {
       float n[8], dy[8], w[8], g[8];
       load8<false>(h, ch * 8, p.cols, n);
@@ -379,50 +379,48 @@ __global__ __launch_bounds__(kSumCols* kSumRows) void column_sum_kernel(const fl
 
 int cdiv(int a, int b) { return (a + b - 1) / b; }
 
-// Threads of a row and chunks of a thread. Two chunks a thread wherever a row has them: on
-// 16768 x 4096 bf16 (residual, e4m3 output) 256 threads x 2 chunks run at 5.3 TB/s, 512 x 1 at
-// 4.7, one wave x 8 (too many registers for enough waves) at 3.6.
+// Threads of a row and chunks of a thread: a wave up to 128 chunks (1024 columns), else two chunks
+// a thread and as many waves as that takes, up to 16384 columns. (16768 x 4096 bf16 with residual
+// and e4m3 output: 256 threads x 2 chunks 95 us, 512 x 1 103; one wave x 8 too many registers for
+// enough waves, 138.)
 template <typename F>
 bool with_shape(int chunks, F&& f) {
-#define GO(TPR, CH) f(std::integral_constant<int, TPR>{}, std::integral_constant<int, CH>{})
-  if (chunks <= 64) GO(64, 1);
-  else if (chunks <= 128) GO(64, 2);
-  else if (chunks <= 256) GO(128, 2);
-  else if (chunks <= 512) GO(256, 2);
-  else if (chunks <= 1024) GO(512, 2);
-  else if (chunks <= 2048) GO(1024, 2);
+  if (chunks <= 64) f(std::true_type{}, std::integral_constant<int, 1>{}, 64);
+  else if (chunks <= 128) f(std::true_type{}, std::integral_constant<int, 2>{}, 64);
+  else if (chunks <= 2048) f(std::false_type{}, std::integral_constant<int, 2>{}, cdiv(chunks, 128) * 64);
   else return false;
-#undef GO
   return true;
 }
 
 template <typename T, int FMT>
 void launch_norm(const NormParams& p, hipStream_t s) {
-  const bool done = with_shape(p.nb * 4, [&](auto tpr, auto ch) {
-    constexpr int TPR = decltype(tpr)::value, CH = decltype(ch)::value, rows = TPR == 64 ? 4 : 1;
-    const unsigned g = (unsigned)cdiv(p.rows, rows);
-    if (p.cols % 8 == 0) rmsnorm_kernel<T, TPR, CH, FMT, true><<<g, TPR * rows, 0, s>>>(p);
-    else rmsnorm_kernel<T, TPR, CH, FMT, false><<<g, TPR * rows, 0, s>>>(p);
+  const bool done = with_shape(p.nb * 4, [&](auto wave, auto ch, int threads) {
+    constexpr bool WAVE = decltype(wave)::value;
+    constexpr int CH = decltype(ch)::value;
+    const unsigned g = (unsigned)(WAVE ? cdiv(p.rows, 4) : p.rows), n = WAVE ? 256 : threads;
+    if (p.cols % 8 == 0) rmsnorm_kernel<T, WAVE, CH, FMT, true><<<g, n, 0, s>>>(p);
+    else rmsnorm_kernel<T, WAVE, CH, FMT, false><<<g, n, 0, s>>>(p);
   });
   if (!done) rmsnorm_long_kernel<T, FMT><<<p.rows, 1024, 0, s>>>(p);
 }
 
 // Rows of partial sums: the workgroups that the card holds at once (16 waves a compute unit;
-// 8192 x 8192 bf16: 512 workgroups of 8 waves 106 us, 768 129 us, 256 163 us), at most 16 MB of
-// sums up to 16384 columns.
+// 8192 x 8192 bf16, before the loads lost their branches: 512 workgroups of 8 waves 106 us, 768 129
+// us, 256 163 us), at most 16 MB of sums up to 16384 columns.
 int grad_parts(int rows, int cols) {
   int n = 256;
-  with_shape(cdiv(cols, 8), [&](auto tpr, auto) { n = 256 * 1024 / decltype(tpr)::value; });
+  with_shape(cdiv(cols, 8), [&](auto, auto, int threads) { n = 256 * (1024 / threads); });
   n = n < 2048 ? n : 2048;
   return rows < n ? rows : n;
 }
 
 template <typename T>
 void launch_grad(const NormGradParams& p, int parts, hipStream_t s) {
-  const bool done = with_shape(cdiv(p.cols, 8), [&](auto tpr, auto ch) {
-    constexpr int TPR = decltype(tpr)::value, CH = decltype(ch)::value;
-    if (p.cols % 8 == 0) rmsnorm_grad_kernel<T, TPR, CH, true><<<parts, TPR, 0, s>>>(p);
-    else rmsnorm_grad_kernel<T, TPR, CH, false><<<parts, TPR, 0, s>>>(p);
+  const bool done = with_shape(cdiv(p.cols, 8), [&](auto wave, auto ch, int threads) {
+    constexpr bool WAVE = decltype(wave)::value;
+    constexpr int CH = decltype(ch)::value;
+    if (p.cols % 8 == 0) rmsnorm_grad_kernel<T, WAVE, CH, true><<<parts, threads, 0, s>>>(p);
+    else rmsnorm_grad_kernel<T, WAVE, CH, false><<<parts, threads, 0, s>>>(p);
   });
   if (!done) rmsnorm_grad_long_kernel<T><<<parts, 1024, 0, s>>>(p);
 }
