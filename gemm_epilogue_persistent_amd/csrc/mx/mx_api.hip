@@ -110,6 +110,7 @@ extern "C" gemm_status mx_gemm_run(const mx_gemm_plan* plan, const mx_gemm_args*
   p.split = choice.split;
   p.per = choice.per;
   p.sums = (float*)a->workspace;
+  if (p.split > 1 && (int64_t)d.M * (d.N / 8) > 0x7FFFFF00) return fail(GEMM_ERR_UNSUPPORTED, "mx_gemm_run: too many outputs to share out K");
   const int64_t tm = mx_row_blocks(*plan, bm), tn = (d.N + bn - 1) / bn;
   dim3 grid;
   int32_t tail_grid = 0;  // workgroups of the split tail's launch
@@ -136,7 +137,7 @@ extern "C" gemm_status mx_gemm_run(const mx_gemm_plan* plan, const mx_gemm_args*
       }
     }
   } else {
-    if (tm > 65535) return fail(GEMM_ERR_UNSUPPORTED, "mx_gemm_run: too many rows for the tile asked for");
+    if (!mx_direct_fits(*plan, tile)) return fail(GEMM_ERR_UNSUPPORTED, "mx_gemm_run: too many rows or columns for the tile asked for");
     grid = dim3((unsigned)tn, (unsigned)tm, (unsigned)p.split);
   }
   hipStream_t s = (hipStream_t)stream;

@@ -105,8 +105,7 @@ MxChoice mx_choose(const mx_gemm_plan& p, int32_t cus, bool workspace) {
     if (p.d.tile != MX_TILE_AUTO && p.d.tile != tile) continue;
     int32_t bm, bn;
     mx_tile_extent(tile, &bm, &bn);
-    // (the direct kernels' grid counts row blocks in 16 bits)
-    if (p.d.tile == MX_TILE_AUTO && tile > MX_TILE_128 && mx_row_blocks(p, bm) > 65535) continue;
+    if (p.d.tile == MX_TILE_AUTO && !mx_direct_fits(p, tile)) continue;
     for (int32_t split = 1; split <= 64; ++split) {
       const bool wanted = p.d.split > 0 ? split == p.d.split : (split & (split - 1)) == 0 && split <= 16;
       if (!wanted && split > 1) continue;
@@ -125,6 +124,13 @@ MxChoice mx_choose(const mx_gemm_plan& p, int32_t cus, bool workspace) {
   c.per = nsb > 0 ? (int32_t)cdiv(nsb, c.split) : 1;
   c.split = nsb > 0 ? (int32_t)cdiv(nsb, c.per) : 1;
   return c;
+}
+
+bool mx_direct_fits(const mx_gemm_plan& p, int32_t tile) {
+  if (tile == MX_TILE_256 || tile == MX_TILE_128) return true;
+  int32_t bm, bn;
+  mx_tile_extent(tile, &bm, &bn);
+  return mx_row_blocks(p, bm) <= 65535 && cdiv(p.d.N, bn) < (1 << 23);
 }
 
 int64_t mx_workspace_bytes(const mx_gemm_plan& p, const MxChoice& c) {

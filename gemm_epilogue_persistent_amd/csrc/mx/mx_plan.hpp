@@ -22,5 +22,8 @@ MxChoice mx_choose(const mx_gemm_plan& p, int32_t cus, bool workspace);
 void mx_tile_extent(int32_t tile, int32_t* bm, int32_t* bn);
 // Upper bound of the row blocks of a tile of bm rows over all groups (exact for a dense plan).
 int64_t mx_row_blocks(const mx_gemm_plan& p, int32_t bm);
+// Whether the grid of a direct kernel (tiles of at most 32 rows) can be launched: row blocks in 16 bits,
+// columns of up to 512 threads in 32. True for the other tiles.
+bool mx_direct_fits(const mx_gemm_plan& p, int32_t tile);
 int64_t mx_workspace_bytes(const mx_gemm_plan& p, const MxChoice& c);
 }  // namespace gep

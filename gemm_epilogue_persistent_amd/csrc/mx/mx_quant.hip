@@ -39,8 +39,8 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(const T* x, int
 // columns x 4 blocks that a wave reads lie in 64 distinct banks.
 template <typename T, int FMT, int kTB, int kRowDw>
 __global__ __launch_bounds__(kTB* kRowDw) void quantize_cols_kernel(const T* x, int64_t ldx, int rows, int cols, int nb,
-                                                                 int nsb, uint32_t tiles, FastDiv fd_ty, uint8_t* codes,
-                                                                 uint8_t* scales) {
+                                                                 int nsb, uint32_t first, uint32_t tiles, FastDiv fd_ty,
+                                                                 uint8_t* codes, uint8_t* scales) {
   constexpr int kVec = 16 / (int)sizeof(T);     // elements of a 16-byte load
   constexpr int kCols = kRowDw * 4 / (int)sizeof(T);   // columns of a tile
   constexpr int kTR = kTB * kMxBlock, kSkewDw = 64 / kTB;
@@ -51,11 +51,12 @@ __global__ __launch_bounds__(kTB* kRowDw) void quantize_cols_kernel(const T* x, 
   __shared__ __attribute__((aligned(16))) uint32_t tile[kTileDw];
   const int tid = threadIdx.x;
   // Workgroups go to the eight XCDs in turn; each XCD takes a run of tiles down the rows, so that
-  // the lines of the output that two tiles share are put together in one L2.
-  const uint32_t per = (tiles + 7) >> 3, tile_id = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-  if (tile_id >= tiles) return;
+  // the lines of the output that two tiles share are put together in one L2. This launch has tiles
+  // first, ..., first + tiles - 1.
+  const uint32_t per = (tiles + 7) >> 3, i = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+  if (i >= tiles) return;
   uint32_t bx, by;
-  fd_divmod(fd_ty, tile_id, bx, by);
+  fd_divmod(fd_ty, first + i, bx, by);
   const int r0 = (int)by * kTR, c0 = (int)bx * kCols;
   uint4 in[kTR / kRP];
   const int lc = c0 + (tid % kLR) * kVec;
@@ -175,6 +176,9 @@ void row_ranges(int32_t rows, uint32_t cpr, F&& f) {
   for (int64_t r0 = 0; r0 < rows; r0 += per) f(r0, (uint32_t)(min((int64_t)rows - r0, per) * cpr));
 }
 
+using E2M1 = std::integral_constant<int, MX_E2M1>;
+using E4M3 = std::integral_constant<int, MX_E4M3>;
+
 constexpr int32_t kMaxExtent = 1 << 30;
 
 gemm_status check_matrix(const char* fn, int32_t rows, int32_t cols, int32_t type, int64_t ld, const char* name,
@@ -224,10 +228,16 @@ gemm_status mx_quantize(int32_t rows, int32_t cols, const void* x, int32_t x_typ
       constexpr int kTB = 4, kRowDw = 64, tc = kRowDw * 4 / (int)sizeof(T);
       const int64_t ty = (nb + kTB - 1) / kTB, tx = ((int64_t)cols + tc - 1) / tc;
       if (ty * tx > 0x7FFFFF00) { st = fail(GEMM_ERR_UNSUPPORTED, "mx_quantize: more than 2^31 tiles"); return; }
-      const uint32_t tiles = (uint32_t)(ty * tx), grid = (tiles + 7) / 8 * 8;
       const FastDiv fd = make_fastdiv((uint32_t)ty);
-      if (format == MX_E2M1) quantize_cols_kernel<T, MX_E2M1, kTB, kRowDw><<<grid, kTB * kRowDw, 0, s>>>((const T*)x, ldx, rows, cols, nb, nsb, tiles, fd, qc, qs);
-      else quantize_cols_kernel<T, MX_E4M3, kTB, kRowDw><<<grid, kTB * kRowDw, 0, s>>>((const T*)x, ldx, rows, cols, nb, nsb, tiles, fd, qc, qs);
+      constexpr int64_t most = 1 << 23;  // tiles of a launch (a grid has below 2^32 threads)
+      for (int64_t first = 0; first < ty * tx; first += most) {
+        const uint32_t tiles = (uint32_t)min(ty * tx - first, most), grid = (tiles + 7) / 8 * 8;
+        auto go = [&](auto fmt) {
+          quantize_cols_kernel<T, decltype(fmt)::value, kTB, kRowDw><<<grid, kTB * kRowDw, 0, s>>>(
+              (const T*)x, ldx, rows, cols, nb, nsb, (uint32_t)first, tiles, fd, qc, qs);
+        };
+        format == MX_E2M1 ? go(E2M1{}) : go(E4M3{});
+      }
     } else {
       const uint32_t cpr = (uint32_t)nb * 4;
       row_ranges(rows, cpr, [&](int64_t r0, uint32_t n) {
@@ -236,8 +246,6 @@ gemm_status mx_quantize(int32_t rows, int32_t cols, const void* x, int32_t x_typ
           quantize_rows_kernel<T, decltype(fmt)::value, decltype(whole)::value><<<g, kThreads, 0, s>>>(
               (const T*)x, ldx, r0, cols, nb, nsb, n, make_fastdiv(cpr), qc, qs);
         };
-        using E2M1 = std::integral_constant<int, MX_E2M1>;
-        using E4M3 = std::integral_constant<int, MX_E4M3>;
         if (cols % 8 == 0) format == MX_E2M1 ? go(E2M1{}, std::true_type{}) : go(E4M3{}, std::true_type{});
         else format == MX_E2M1 ? go(E2M1{}, std::false_type{}) : go(E4M3{}, std::false_type{});
       });

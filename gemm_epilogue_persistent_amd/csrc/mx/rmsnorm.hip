@@ -25,6 +25,7 @@ struct NormParams {
   float* rstd;
   int64_t ldx, ldr, ldh, ldy;
   int32_t rows, cols, nb, nsb;
+  int32_t row0;  // this launch's first row
   float eps;
   double inv_cols;
 };
@@ -75,9 +76,10 @@ struct Rstd {
   float hi, lo;
 };
 __device__ __forceinline__ Rstd reciprocal_root(double mean_eps) {
-  const double r0 = (double)__builtin_amdgcn_rsqf((float)mean_eps);
-  // One Newton step squares the relative error of about 2^-22. (The fp32 root is infinite for 0 and
-  // below the fp32 range, and 0 or NaN for an infinite or NaN sum; those need no step.)
+  // (in 64 bits: squares of fp32 and bf16 values leave the fp32 range)
+  const double r0 = __builtin_amdgcn_rsq(mean_eps);
+  // One Newton step squares the relative error of the approximate root. (That is infinite for 0, and 0
+  // or NaN for an infinite or NaN sum; those need no step.)
   const double r = __builtin_isfinite(r0) && r0 > 0 ? r0 + 0.5 * r0 * (1.0 - mean_eps * r0 * r0) : r0;
   Rstd s;
   s.hi = (float)r;
@@ -133,7 +135,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void rmsnorm_kernel(const NormPa
   __shared__ double red[WAVE ? 1 : 16];
   const int threads = WAVE ? 64 : blockDim.x;
   const int t = WAVE ? threadIdx.x & 63 : threadIdx.x;
-  const int64_t row = WAVE ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
+  const int64_t row = p.row0 + (WAVE ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : (int64_t)blockIdx.x);
   if (WAVE && row >= p.rows) return;  // (a whole wave)
   const T* x = (const T*)p.x + row * p.ldx;
   Chunk<T> h[CH];
@@ -189,7 +191,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void rmsnorm_kernel(const NormPa
 template <typename T, int FMT>
 __global__ __launch_bounds__(1024) void rmsnorm_long_kernel(const NormParams p) {
   __shared__ double red[16];
-  const int64_t row = blockIdx.x;
+  const int64_t row = p.row0 + (int64_t)blockIdx.x;
   const T* x = (const T*)p.x + row * p.ldx;
   const T* r = p.r ? (const T*)p.r + row * p.ldr : nullptr;
   const int n = p.nb * 4;
@@ -393,15 +395,26 @@ bool with_shape(int chunks, F&& f) {
 }
 
 template <typename T, int FMT>
-void launch_norm(const NormParams& p, hipStream_t s) {
+void launch_norm(NormParams p, hipStream_t s) {
+  // (ranges of rows, a multiple of the four of a workgroup: a grid has below 2^32 threads)
+  constexpr int kMostThreads = 1 << 30;
+  auto ranges = [&](int threads, auto&& launch) {
+    const int per = kMostThreads / threads;
+    for (p.row0 = 0;; p.row0 += per) {
+      launch(p.rows - p.row0 < per ? p.rows - p.row0 : per);
+      if (p.rows - p.row0 <= per) break;
+    }
+  };
   const bool done = with_shape(p.nb * 4, [&](auto wave, auto ch, int threads) {
     constexpr bool WAVE = decltype(wave)::value;
     constexpr int CH = decltype(ch)::value;
-    const unsigned g = (unsigned)(WAVE ? cdiv(p.rows, 4) : p.rows), n = WAVE ? 256 : threads;
-    if (p.cols % 8 == 0) rmsnorm_kernel<T, WAVE, CH, FMT, true><<<g, n, 0, s>>>(p);
-    else rmsnorm_kernel<T, WAVE, CH, FMT, false><<<g, n, 0, s>>>(p);
+    ranges(WAVE ? 64 : 1024, [&](int rows) {
+      const unsigned g = (unsigned)(WAVE ? cdiv(rows, 4) : rows), n = WAVE ? 256 : threads;
+      if (p.cols % 8 == 0) rmsnorm_kernel<T, WAVE, CH, FMT, true><<<g, n, 0, s>>>(p);
+      else rmsnorm_kernel<T, WAVE, CH, FMT, false><<<g, n, 0, s>>>(p);
+    });
   });
-  if (!done) rmsnorm_long_kernel<T, FMT><<<p.rows, 1024, 0, s>>>(p);
+  if (!done) ranges(1024, [&](int rows) { rmsnorm_long_kernel<T, FMT><<<rows, 1024, 0, s>>>(p); });
 }
 
 // Rows of partial sums: the workgroups that the card holds at once (16 waves a compute unit;
@@ -427,11 +440,11 @@ void launch_grad(const NormGradParams& p, int parts, hipStream_t s) {
 
 int type_bytes(int32_t t) { return t == GEMM_DT_F32 ? 4 : ((t == GEMM_DT_F16 || t == GEMM_DT_BF16) ? 2 : 0); }
 
-constexpr int32_t kMaxExtent = 1 << 30;
+constexpr int32_t kMaxExtent = 1 << 30, kMaxCols = 1 << 24;
 
 gemm_status check_sizes(const char* fn, int32_t rows, int32_t cols, int32_t type) {
   if (rows < 0 || cols < 1) return fail(GEMM_ERR_INVALID_ARG, "%s: rows >= 0 and cols >= 1 expected", fn);
-  if (rows > kMaxExtent || cols > kMaxExtent) return fail(GEMM_ERR_UNSUPPORTED, "%s: more than 2^30 rows or columns", fn);
+  if (rows > kMaxExtent || cols > kMaxCols) return fail(GEMM_ERR_UNSUPPORTED, "%s: more than 2^30 rows or 2^24 columns", fn);
   if (!type_bytes(type)) return fail(GEMM_ERR_INVALID_ARG, "%s: the type must be F16, BF16 or F32", fn);
   return GEMM_OK;
 }
@@ -477,6 +490,7 @@ gemm_status rmsnorm_forward(const rmsnorm_args* a, void* stream) {
     if ((uintptr_t)a->rstd & 3) return fail(GEMM_ERR_ALIGNMENT, "%s: rstd not 4-byte aligned", fn);
     if (a->h_out == a->x && a->h_out && a->ldh != a->ldx) return fail(GEMM_ERR_INVALID_ARG, "%s: h_out in the place of x needs its leading dimension", fn);
     if (a->h_out == a->residual && a->h_out && a->ldh != a->ldr) return fail(GEMM_ERR_INVALID_ARG, "%s: h_out in the place of residual needs its leading dimension", fn);
+    if (a->y && (a->y == a->x || a->y == a->residual || a->y == a->h_out)) return fail(GEMM_ERR_INVALID_ARG, "%s: y in the place of x, residual or h_out", fn);
   }
   clear_error();
   if (a->rows == 0) return GEMM_OK;

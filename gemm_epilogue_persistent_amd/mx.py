@@ -12,6 +12,7 @@ consecutive values of a row (OCP Microscaling v1.0):
 
 Grouped: b holds one matrix per expert, (G, n, k), and cu_seqlens_m gives the experts' rows.
 """
+import contextlib
 import ctypes
 
 import torch
@@ -32,6 +33,12 @@ def _cdiv(a, b):
 # which takes as long as a launch)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _allocating(stream):
+    """Where a call on `stream` allocates: memory of that stream, so that its first fill and its reuse
+    after a free are ordered with the call."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 def _launch(device, stream, function, *args):
@@ -157,7 +164,8 @@ def mx_quantize(x, fmt, out=None, transpose=False, stream=None):
         x, rows, cols, transpose = x.t(), cols, rows, not transpose
     ld = _matrix("x", x, _FLOAT_DT)
     if out is None:
-        out = mx_empty(*shape, fmt, device=x.device)
+        with _allocating(stream):
+            out = mx_empty(*shape, fmt, device=x.device)
     else:
         _plain_mx("out", out, x.device)
         if out.fmt != fmt or out.rows != shape[0] or out.k != shape[1]:
@@ -171,7 +179,8 @@ def mx_dequantize(q, out=None, dtype=torch.bfloat16, stream=None):
     """The values of an MX matrix in `out` (allocated in `dtype` if None), rounded to nearest."""
     _plain_mx("q", q)
     if out is None:
-        out = torch.empty((q.rows, q.k), dtype=dtype, device=q.device)
+        with _allocating(stream):
+            out = torch.empty((q.rows, q.k), dtype=dtype, device=q.device)
     ld = _matrix("out", out, _FLOAT_DT, (q.rows, q.k), q.device)
     _launch(q.device, stream, _abi.load().mx_dequantize, q.rows, q.k, MX_FORMAT[q.fmt], q.codes.data_ptr(),
             q.scales.data_ptr(), out.data_ptr(), _FLOAT_DT[out.dtype], ld)
@@ -198,7 +207,7 @@ class MxPlan:
 
     Where K is shared out, the plan keeps the workspace for the partial sums: runs of one plan on
     several streams that may overlap need a workspace each (a uint8 tensor of
-    plan.workspace_bytes)."""
+    plan.workspace_bytes), and the plan has to outlive a graph that captured its run."""
 
     def __init__(self, a, b, C=None, D=None, PostAct=None, act="none", cu_seqlens_m=None, tile="auto",
                  split=0):
@@ -239,6 +248,7 @@ class MxPlan:
         _abi.check(self._lib.mx_gemm_workspace(h, self._cus(), ctypes.byref(n)))
         self.workspace_bytes = n.value
         self._workspace = torch.empty(n.value, dtype=torch.uint8, device=a.device) if n.value else None
+        self._streams = {_raw_stream(a.device.index)}  # those the workspace is known to be used on
 
     def __del__(self):
         h = getattr(self, "handle", None)
@@ -268,12 +278,21 @@ class MxPlan:
             raise ValueError("the operands are not laid out as those this plan was made for")
         if workspace is None:
             workspace = self._workspace
+            if workspace is not None:
+                self._hold(stream)
         elif workspace.device != self.device or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
             raise ValueError("workspace: contiguous uint8 tensor on the operands' GPU expected")
         args = _abi.MxGemmArgs(a.codes.data_ptr(), a.scales.data_ptr(), b.codes.data_ptr(), b.scales.data_ptr(),
                                *(None if t is None else t.data_ptr() for t in (C, D, PostAct, cu_seqlens_m, workspace)),
                                0 if workspace is None else workspace.numel())
         _launch(self.device, stream, self._lib.mx_gemm_run, self.handle, ctypes.byref(args))
+
+    def _hold(self, stream):
+        """The allocator is told of another stream that the workspace is used on, once."""
+        raw = _raw_stream(self.device.index) if stream is None else stream.cuda_stream
+        if raw not in self._streams:
+            self._workspace.record_stream(torch.cuda.current_stream(self.device) if stream is None else stream)
+            self._streams.add(raw)
 
     def tile(self, num_cus=None):
         """(kernel, split) this plan runs with on a device with num_cus compute units."""
@@ -286,7 +305,9 @@ def mx_gemm(a, b, D=None, C=None, PostAct=None, act="none", cu_seqlens_m=None, s
             split=0):
     """One-shot product: plan and enqueue. Without D and PostAct, D is allocated in bf16. Returns
     D, or PostAct without D."""
-    if D is None and PostAct is None:
-        D = torch.empty((a.rows, b.rows), dtype=torch.bfloat16, device=a.device)
-    MxPlan(a, b, C, D, PostAct, act, cu_seqlens_m, tile, split).run(a, b, C, D, PostAct, cu_seqlens_m, stream)
+    with _allocating(stream):  # (the plan's workspace too)
+        if D is None and PostAct is None:
+            D = torch.empty((a.rows, b.rows), dtype=torch.bfloat16, device=a.device)
+        plan = MxPlan(a, b, C, D, PostAct, act, cu_seqlens_m, tile, split)
+    plan.run(a, b, C, D, PostAct, cu_seqlens_m, stream)
     return D if D is not None else PostAct

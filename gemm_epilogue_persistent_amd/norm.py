@@ -10,7 +10,7 @@ import torch
 
 from . import _abi
 from ._abi import MX_FORMAT
-from .mx import _FLOAT_DT, _launch, _matrix, _plain_mx
+from .mx import _FLOAT_DT, _allocating, _launch, _matrix, _plain_mx
 
 
 def _vector(name, t, n, dtype, device):
@@ -37,7 +37,8 @@ def rmsnorm(x, weight, residual=None, eps=1e-5, h=None, y=None, q=None, rstd=Non
     dev, shape = x.device, x.shape
     rows, cols = shape
     if y is None and q is None:
-        y = torch.empty(shape, dtype=x.dtype, device=dev)
+        with _allocating(stream):
+            y = torch.empty(shape, dtype=x.dtype, device=dev)
     if h is not None and residual is None:
         raise ValueError("h without a residual (it would be x)")
     if q is not None:
@@ -75,13 +76,15 @@ def rmsnorm_backward(dy, h, weight, rstd, dx=None, dw=None, dres=None, workspace
     ldh = _matrix("h", h, types)
     dev, shape = h.device, h.shape
     rows, cols = shape
-    if dx is None:
-        dx = torch.empty(shape, dtype=h.dtype, device=dev)
-    if dw is None:
-        dw = torch.empty(cols, dtype=torch.float32, device=dev)
-    if workspace is None:
-        workspace = torch.empty(rmsnorm_backward_workspace(rows, cols), dtype=torch.uint8, device=dev)
-    elif workspace.device != dev or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+    if dx is None or dw is None or workspace is None:
+        with _allocating(stream):
+            if dx is None:
+                dx = torch.empty(shape, dtype=h.dtype, device=dev)
+            if dw is None:
+                dw = torch.empty(cols, dtype=torch.float32, device=dev)
+            if workspace is None:
+                workspace = torch.empty(rmsnorm_backward_workspace(rows, cols), dtype=torch.uint8, device=dev)
+    if workspace.device != dev or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise ValueError("workspace: contiguous uint8 tensor on the operands' GPU expected")
     a = _abi.RmsnormBackwardArgs(
         rows, cols, _FLOAT_DT[h.dtype], dy.data_ptr(), h.data_ptr(), _vector("weight", weight, cols, h.dtype, dev),

@@ -247,3 +247,24 @@ def test_cpu_tensors_are_refused():
         gep.rmsnorm_backward(x, x, torch.ones(32), torch.ones(4))
     with pytest.raises(ValueError):
         gep.MxPlan(q, q, D=x)
+
+
+def test_plan_tile_of_very_many_columns(lib):
+    """A grid is launched only where its threads number below 2^32: one row and 2^27 columns go to a
+    kernel of a persistent grid, and a tile asked for that cannot be launched is refused."""
+    d = dict(M=1, N=1 << 27, K=32, c=0, post=0, act=0, ldd=1 << 27)
+    h, t = ctypes.c_void_p(), ctypes.c_int32()
+    assert lib.mx_gemm_create(ctypes.byref(gemm_desc(**d)), ctypes.byref(h)) == 0
+    assert lib.mx_gemm_plan_tile(h, 256, ctypes.byref(t), None) == 0
+    bn = {1: 256, 2: 128, 3: 64, 4: 32, 5: 32, 6: 16}[t.value]
+    assert t.value <= 2 or (1 << 27) // bn * 512 < 1 << 32
+    lib.mx_gemm_destroy(h)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(), 1), (dict(x=P + 4096, h_out=P + 8192), 1), (dict(x=P + 4096, residual=P + 8192), 1),
+    (dict(cols=(1 << 24) + 1), 2),
+])
+def test_norm_output_overlap_refusals(lib, kw, status):
+    """y in the place of x, of the residual or of h."""
+    assert lib.rmsnorm_forward(ctypes.byref(norm_args(**kw)), None) == status and lib.gemm_last_error()
