@@ -1,6 +1,7 @@
 """ctypes view of include/gemm_mi355x.h (argument marshalling only)."""
 import ctypes
 import os
+import struct
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libgemm_mi355x.so")
@@ -64,6 +65,13 @@ class RmsnormBackwardArgs(ctypes.Structure):
         (n, ctypes.c_int64) for n in ("workspace_bytes", "lddy", "ldh", "lddres", "lddx")]
 
 
+# The same structures as bytes, filled in a quarter of a ctypes structure's time (0.4 instead of 1.3
+# us, of 5 to 10 that a call takes); NULL is 0.
+MX_GEMM_ARGS = struct.Struct("@9Pq")
+RMSNORM_ARGS = struct.Struct("@4if8P4q")
+RMSNORM_BACKWARD_ARGS = struct.Struct("@3i8P5q")
+
+
 class GemmError(RuntimeError):
     def __init__(self, status, message):
         super().__init__(f"{message} (status {status})")
@@ -116,15 +124,15 @@ def load():
         lib.mx_dequantize.restype = ctypes.c_int
         lib.mx_dequantize.argtypes = [i32, i32, i32, vp, vp, vp, i32, i64, vp]
         lib.rmsnorm_forward.restype = ctypes.c_int
-        lib.rmsnorm_forward.argtypes = [ctypes.POINTER(RmsnormArgs), vp]
+        lib.rmsnorm_forward.argtypes = [vp, vp]
         lib.rmsnorm_backward.restype = ctypes.c_int
-        lib.rmsnorm_backward.argtypes = [ctypes.POINTER(RmsnormBackwardArgs), vp]
+        lib.rmsnorm_backward.argtypes = [vp, vp]
         lib.rmsnorm_backward_workspace.restype = i64
         lib.rmsnorm_backward_workspace.argtypes = [i32, i32]
         lib.mx_gemm_create.restype = ctypes.c_int
         lib.mx_gemm_create.argtypes = [ctypes.POINTER(MxGemmDesc), ctypes.POINTER(vp)]
         lib.mx_gemm_run.restype = ctypes.c_int
-        lib.mx_gemm_run.argtypes = [vp, ctypes.POINTER(MxGemmArgs), vp]
+        lib.mx_gemm_run.argtypes = [vp, vp, vp]
         lib.mx_gemm_destroy.restype = ctypes.c_int
         lib.mx_gemm_destroy.argtypes = [vp]
         lib.mx_gemm_plan_tile.restype = ctypes.c_int

@@ -282,10 +282,10 @@ class MxPlan:
                 self._hold(stream)
         elif workspace.device != self.device or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
             raise ValueError("workspace: contiguous uint8 tensor on the operands' GPU expected")
-        args = _abi.MxGemmArgs(a.codes.data_ptr(), a.scales.data_ptr(), b.codes.data_ptr(), b.scales.data_ptr(),
-                               *(None if t is None else t.data_ptr() for t in (C, D, PostAct, cu_seqlens_m, workspace)),
-                               0 if workspace is None else workspace.numel())
-        _launch(self.device, stream, self._lib.mx_gemm_run, self.handle, ctypes.byref(args))
+        args = _abi.MX_GEMM_ARGS.pack(a.codes.data_ptr(), a.scales.data_ptr(), b.codes.data_ptr(), b.scales.data_ptr(),
+                                      *[0 if t is None else t.data_ptr() for t in (C, D, PostAct, cu_seqlens_m, workspace)],
+                                      0 if workspace is None else workspace.numel())
+        _launch(self.device, stream, self._lib.mx_gemm_run, self.handle, args)
 
     def _hold(self, stream):
         """The allocator is told of another stream that the workspace is used on, once."""

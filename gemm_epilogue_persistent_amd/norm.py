@@ -4,8 +4,6 @@ include/mx_mi355x.h; argument checks and marshalling only).
     h = x + residual (rounded to x's type)    rstd = 1 / sqrt(mean(h^2) + eps)
     y = h * rstd * weight, in x's type and / or as an MX matrix
 """
-import ctypes
-
 import torch
 
 from . import _abi
@@ -20,7 +18,7 @@ def _vector(name, t, n, dtype, device):
 
 
 def _ptr(t):
-    return None if t is None else t.data_ptr()
+    return 0 if t is None else t.data_ptr()
 
 
 def rmsnorm(x, weight, residual=None, eps=1e-5, h=None, y=None, q=None, rstd=None, stream=None):
@@ -45,15 +43,15 @@ def rmsnorm(x, weight, residual=None, eps=1e-5, h=None, y=None, q=None, rstd=Non
         _plain_mx("q", q, dev)
         if q.rows != rows or q.k != cols:
             raise ValueError(f"q has shape {tuple(q.shape)}, expected {tuple(shape)}")
-    a = _abi.RmsnormArgs(
+    a = _abi.RMSNORM_ARGS.pack(
         rows, cols, _FLOAT_DT[x.dtype], MX_FORMAT[q.fmt] if q is not None else 0, eps,
         x.data_ptr(), _ptr(residual), _vector("weight", weight, cols, x.dtype, dev), _ptr(h), _ptr(y),
-        q.codes.data_ptr() if q is not None else None, q.scales.data_ptr() if q is not None else None,
-        _vector("rstd", rstd, rows, torch.float32, dev) if rstd is not None else None,
+        q.codes.data_ptr() if q is not None else 0, q.scales.data_ptr() if q is not None else 0,
+        _vector("rstd", rstd, rows, torch.float32, dev) if rstd is not None else 0,
         ldx, _matrix("residual", residual, types, shape, dev) if residual is not None else 0,
         _matrix("h", h, types, shape, dev) if h is not None else 0,
         _matrix("y", y, types, shape, dev) if y is not None else 0)
-    _launch(dev, stream, _abi.load().rmsnorm_forward, ctypes.byref(a))
+    _launch(dev, stream, _abi.load().rmsnorm_forward, a)
     return y if y is not None else q
 
 
@@ -86,11 +84,11 @@ def rmsnorm_backward(dy, h, weight, rstd, dx=None, dw=None, dres=None, workspace
                 workspace = torch.empty(rmsnorm_backward_workspace(rows, cols), dtype=torch.uint8, device=dev)
     if workspace.device != dev or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise ValueError("workspace: contiguous uint8 tensor on the operands' GPU expected")
-    a = _abi.RmsnormBackwardArgs(
+    a = _abi.RMSNORM_BACKWARD_ARGS.pack(
         rows, cols, _FLOAT_DT[h.dtype], dy.data_ptr(), h.data_ptr(), _vector("weight", weight, cols, h.dtype, dev),
         _vector("rstd", rstd, rows, torch.float32, dev), _ptr(dres), dx.data_ptr(),
         _vector("dw", dw, cols, torch.float32, dev), workspace.data_ptr(), workspace.numel(),
         _matrix("dy", dy, types, shape, dev), ldh,
         _matrix("dres", dres, types, shape, dev) if dres is not None else 0, _matrix("dx", dx, types, shape, dev))
-    _launch(dev, stream, _abi.load().rmsnorm_backward, ctypes.byref(a))
+    _launch(dev, stream, _abi.load().rmsnorm_backward, a)
     return dx, dw

@@ -268,3 +268,14 @@ def test_plan_tile_of_very_many_columns(lib):
 def test_norm_output_overlap_refusals(lib, kw, status):
     """y in the place of x, of the residual or of h."""
     assert lib.rmsnorm_forward(ctypes.byref(norm_args(**kw)), None) == status and lib.gemm_last_error()
+
+
+@pytest.mark.parametrize("packed,structure", [
+    (_abi.MX_GEMM_ARGS, _abi.MxGemmArgs), (_abi.RMSNORM_ARGS, _abi.RmsnormArgs),
+    (_abi.RMSNORM_BACKWARD_ARGS, _abi.RmsnormBackwardArgs)])
+def test_packed_arguments(packed, structure):
+    """The bytes that the binding passes are the structure's, field by field."""
+    assert packed.size == ctypes.sizeof(structure)
+    names = [f for f, _ in structure._fields_]
+    got = structure.from_buffer_copy(packed.pack(*range(1, len(names) + 1)))
+    assert [getattr(got, f) for f in names] == list(range(1, len(names) + 1))
