@@ -10,9 +10,9 @@
 // for both types; checked on the hardware element by element).
 //
 // Two kernels:
-//   MxRing   large problems. 256x256 or 256x128 outputs per workgroup of 8 waves, 128x128 of 4: both
-//            operands go through LDS (global -> LDS transfers, two stages), persistent tile loop.
-//   MxDirect few rows. 16x16 to 64x64 outputs per workgroup, whose waves share out K and read
+//   MxRing   large problems. 256x256 outputs per workgroup of 8 waves, 128x128 of 4: both operands go
+//            through LDS (global -> LDS transfers, two to four stages), persistent tile loop.
+//   MxDirect few rows. 16x16 to 32x64 outputs per workgroup, whose waves share out K and read
 //            their fragments from global memory themselves; one join in LDS at the end.
 #pragma once
 #include "../gemm_kernel.hpp"
@@ -910,6 +910,9 @@ template <int BM, int NW, int WG, int FA, int FB, bool VM>
 __global__ __launch_bounds__(NW * 64, WG) void mx_ring_kernel(const MxParams p) {
   MxRing<BM, BM, NW, mx_stages<BM, FA, FB, WG>(), FA, FB, VM>::run(p);
 }
+// Direct kernels: fragments two steps ahead. (Four steps, or twice the waves, are slower everywhere:
+// 1 x 8192 x 8192 e4m3 x e2m1 in 16x32 tiles 7.8 us, with four steps 8.6, with 16 waves 8.9; in 16x16
+// tiles 8.7 on four waves, 9.4 on eight, 11.2 on 16.)
 template <int MB, int NB, int NW, int D, int FA, int FB, bool VM>
 __global__ __launch_bounds__(NW * 64) void mx_direct_kernel(const MxParams p) {
   MxDirect<MB, NB, NW, D, FA, FB, VM>::run(p);
@@ -931,7 +934,7 @@ hipError_t mx_launch(int32_t tile, const MxParams& p, dim3 grid, hipStream_t s);
       case MX_TILE_32X64: mx_direct_kernel<2, 4, 4, 2, FA, FB, VM><<<grid, 256, 0, s>>>(p); break;   \
       case MX_TILE_32: mx_direct_kernel<2, 2, 4, 2, FA, FB, VM><<<grid, 256, 0, s>>>(p); break;      \
       case MX_TILE_16X32: mx_direct_kernel<1, 2, 8, 2, FA, FB, VM><<<grid, 512, 0, s>>>(p); break;   \
-      case MX_TILE_16: mx_direct_kernel<1, 1, 8, 2, FA, FB, VM><<<grid, 512, 0, s>>>(p); break;      \
+      case MX_TILE_16: mx_direct_kernel<1, 1, 4, 2, FA, FB, VM><<<grid, 256, 0, s>>>(p); break;      \
       default: return hipErrorInvalidValue;                                                          \
     }                                                                                                \
     return hipGetLastError();                                                                        \

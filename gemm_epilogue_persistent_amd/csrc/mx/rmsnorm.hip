@@ -119,10 +119,10 @@ __device__ __forceinline__ double squares(const float v[8]) {
 
 // Output chunk `ch` of a row: y in its type and / or (FMT an mx_format, or kNoMx) quantised.
 constexpr int kNoMx = -1;
-template <typename T, int FMT, bool WHOLE>
+template <typename T, int FMT, bool WHOLE, int STREAM = 0>
 __device__ __forceinline__ void norm_out(const NormParams& p, T* y_row, uint8_t* code_row, uint8_t* scale_row, int ch,
                                          const float y[8]) {
-  if (p.y) store_chunk<WHOLE>(y_row, ch * 8, p.cols, pack<T>(y));
+  if (p.y) store_chunk<WHOLE, STREAM != 0>(y_row, ch * 8, p.cols, pack<T>(y));
   if constexpr (FMT != kNoMx) {
     if (ch < p.nb * 4) mx_store_chunk<FMT>(y, ch, p.nb, p.nsb, code_row, scale_row);
   }
@@ -130,7 +130,7 @@ __device__ __forceinline__ void norm_out(const NormParams& p, T* y_row, uint8_t*
 
 // h is kept in its own type (its rounded value is exact there): half the registers of fp32 for
 // 16-bit rows.
-template <typename T, bool WAVE, int CH, int FMT, bool WHOLE>
+template <typename T, bool WAVE, int CH, int FMT, bool WHOLE, int STREAM>
 __global__ __launch_bounds__(WAVE ? 256 : 1024) void rmsnorm_kernel(const NormParams p) {
   __shared__ double red[WAVE ? 1 : 16];
   const int threads = WAVE ? 64 : blockDim.x;
@@ -141,12 +141,12 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void rmsnorm_kernel(const NormPa
   Chunk<T> h[CH];
   double ss = 0;
 #pragma unroll
-  for (int j = 0; j < CH; ++j) h[j] = load_chunk<WHOLE>(x, (t + j * threads) * 8, p.cols);
+  for (int j = 0; j < CH; ++j) h[j] = load_chunk<WHOLE, STREAM == 2>(x, (t + j * threads) * 8, p.cols);
   if (p.r) {
     const T* r = (const T*)p.r + row * p.ldr;
     Chunk<T> rc[CH];
 #pragma unroll
-    for (int j = 0; j < CH; ++j) rc[j] = load_chunk<WHOLE>(r, (t + j * threads) * 8, p.cols);
+    for (int j = 0; j < CH; ++j) rc[j] = load_chunk<WHOLE, STREAM == 2>(r, (t + j * threads) * 8, p.cols);
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
       const int c = (t + j * threads) * 8;
@@ -158,7 +158,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void rmsnorm_kernel(const NormPa
 #pragma unroll
       for (int e = 0; e < 8; ++e) a[e] += b[e];
       h[j] = pack<T>(a);
-      if (p.h) store_chunk<WHOLE>((T*)p.h + row * p.ldh, c, p.cols, h[j]);
+      if (p.h) store_chunk<WHOLE, STREAM != 0>((T*)p.h + row * p.ldh, c, p.cols, h[j]);
       unpack(h[j], a);
       ss += squares(a);
     }
@@ -183,7 +183,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void rmsnorm_kernel(const NormPa
     unpack(h[j], a);
     load8<WHOLE>((const T*)p.w, ch * 8, p.cols, w);
     scale8<T>(a, w, rstd, a);
-    norm_out<T, FMT, WHOLE>(p, y_row, code_row, scale_row, ch, a);
+    norm_out<T, FMT, WHOLE, STREAM>(p, y_row, code_row, scale_row, ch, a);
   }
 }
 
@@ -237,9 +237,16 @@ struct NormGradParams {
   float inv_cols;
 };
 
-template <typename T, bool WAVE, int CH, bool WHOLE>
+template <typename T, bool WHOLE>
+constexpr bool rows_ahead() {
+  return WHOLE && sizeof(T) == 2;
+}
+template <typename T, bool WAVE, int CH, bool WHOLE, int STREAM>
 __global__ __launch_bounds__(WAVE ? 64 : 1024) void rmsnorm_grad_kernel(const NormGradParams p) {
   __shared__ float red[WAVE ? 1 : 16];
+  // The next row is on its way while this one meets at the barriers and is stored, where its registers
+  // fit (fp32 rows, or chunks to be moved into place: 333 x 2050 fp32 8.9 us, ahead 15.0).
+  constexpr bool kAhead = rows_ahead<T, WHOLE>();
   const int t = threadIdx.x, threads = blockDim.x;
   float dw[CH][8];
   Chunk<T> w[CH];
@@ -251,18 +258,31 @@ __global__ __launch_bounds__(WAVE ? 64 : 1024) void rmsnorm_grad_kernel(const No
 #pragma unroll
     for (int e = 0; e < 8; ++e) dw[j][e] = 0.f;
   }
-  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
-    const float rstd = p.rstd[row];
-    Chunk<T> hc[CH], dyc[CH], gc[CH];
+  struct Row {
+    Chunk<T> h[CH], dy[CH], g[CH];
+    float rstd;
+  };
+  auto load = [&](Row& r, int64_t row) {
+    r.rstd = p.rstd[row];
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
-      hc[j] = load_chunk<WHOLE>((const T*)p.h + row * p.ldh, (t + j * threads) * 8, p.cols);
-      dyc[j] = load_chunk<WHOLE>((const T*)p.dy + row * p.lddy, (t + j * threads) * 8, p.cols);
+      r.h[j] = load_chunk<WHOLE, STREAM == 2>((const T*)p.h + row * p.ldh, (t + j * threads) * 8, p.cols);
+      r.dy[j] = load_chunk<WHOLE, STREAM == 2>((const T*)p.dy + row * p.lddy, (t + j * threads) * 8, p.cols);
     }
     if (p.dres) {
 #pragma unroll
-      for (int j = 0; j < CH; ++j) gc[j] = load_chunk<WHOLE>((const T*)p.dres + row * p.lddres, (t + j * threads) * 8, p.cols);
+      for (int j = 0; j < CH; ++j)
+        r.g[j] = load_chunk<WHOLE, STREAM == 2>((const T*)p.dres + row * p.lddres, (t + j * threads) * 8, p.cols);
     }
+  };
+  Row next;
+  if (kAhead && blockIdx.x < p.rows) load(next, blockIdx.x);
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    if (!kAhead) load(next, row);
+    Chunk<T> hc[CH], dyc[CH], gc[CH];
+#pragma unroll
+    for (int j = 0; j < CH; ++j) hc[j] = next.h[j], dyc[j] = next.dy[j], gc[j] = next.g[j];
+    const float rstd = next.rstd;
     float dot = 0.f;
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
@@ -281,6 +301,7 @@ __global__ __launch_bounds__(WAVE ? 64 : 1024) void rmsnorm_grad_kernel(const No
         dot = fmaf(dyn, ww[e], dot);
       }
     }
+    if (kAhead && row + gridDim.x < p.rows) load(next, row + gridDim.x);
     const float m = row_sum<WAVE>(dot, red) * p.inv_cols;
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
@@ -301,7 +322,7 @@ __global__ __launch_bounds__(WAVE ? 64 : 1024) void rmsnorm_grad_kernel(const No
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) g[e] = fmaf(rstd, dy[e] * ww[e] - n[e] * rstd * m, g[e]);
-      store_chunk<WHOLE>((T*)p.dx + row * p.lddx, c, p.cols, pack<T>(g));
+      store_chunk<WHOLE, STREAM != 0>((T*)p.dx + row * p.lddx, c, p.cols, pack<T>(g));
     }
   }
   float* part = p.part + (int64_t)blockIdx.x * p.cols;
@@ -359,8 +380,10 @@ __global__ __launch_bounds__(1024) void rmsnorm_grad_long_kernel(const NormGradP
   }
 }
 
-// dw = sum of `n` rows of partial sums: 16 columns a workgroup, 64 threads a column.
-constexpr int kSumCols = 16, kSumRows = 64;
+// dw = sum of `n` rows of partial sums: 32 columns (whole lines) a workgroup, 32 threads a column.
+// (8192 x 8192 bf16, 512 rows of sums: both kernels 107.0 us; 16 columns 109.5, and with fewer
+// rows 64 columns are slower than 32: 8192 x 512 15.8 and 13.6.)
+constexpr int kSumCols = 32, kSumRows = 32;
 __global__ __launch_bounds__(kSumCols* kSumRows) void column_sum_kernel(const float* part, int n, int cols, float* dw) {
   __shared__ float s[kSumRows][kSumCols];
   const int c = blockIdx.x * kSumCols + threadIdx.x % kSumCols, g = threadIdx.x / kSumCols;
@@ -385,17 +408,40 @@ int cdiv(int a, int b) { return (a + b - 1) / b; }
 // a thread and as many waves as that takes, up to 16384 columns. (16768 x 4096 bf16 with residual
 // and e4m3 output: 256 threads x 2 chunks 95 us, 512 x 1 103; one wave x 8 too many registers for
 // enough waves, 138.)
+// With few rows one chunk a thread: the row's time is its latency (1 x 4096: 3.1 us, with two 3.9).
+constexpr int kFewRows = 256;
 template <typename F>
-bool with_shape(int chunks, F&& f) {
+bool with_shape(int rows, int chunks, F&& f) {
   if (chunks <= 64) f(std::true_type{}, std::integral_constant<int, 1>{}, 64);
   else if (chunks <= 128) f(std::true_type{}, std::integral_constant<int, 2>{}, 64);
+  else if (rows <= kFewRows && chunks <= 1024) f(std::false_type{}, std::integral_constant<int, 1>{}, cdiv(chunks, 64) * 64);
   else if (chunks <= 2048) f(std::false_type{}, std::integral_constant<int, 2>{}, cdiv(chunks, 128) * 64);
   else return false;
   return true;
 }
 
+// How a call's rows pass the caches (STREAM): 0 through them; past them, where it moves more bytes than
+// they hold, 2 both ways or 1 only what it writes. 2 needs rows of whole lines: past the caches a line
+// that two waves share is fetched twice (norm gradients 8192 x 5000 f16: 69 us with 1, 82 with 2, 81
+// with 0; 16768 x 4096 bf16: 103, 100, 107; norm 16768 x 4096 bf16 84, 78, 87). An fp32 chunk is two
+// 16-byte accesses to one line: 0 (norm 16384 x 4096: 199 us, with 2 204).
+int stream_mode(int64_t elements, int bytes, int64_t strides) {
+  if (bytes != 2 || elements * bytes <= kCacheBytes) return 0;
+  return strides % 64 ? 1 : 2;
+}
+// Call f with whether rows are whole chunks, and STREAM.
+template <typename T, typename F>
+void by_rows(int cols, int stream, F&& f) {
+  using One = std::integral_constant<int, 1>;
+  using Two = std::integral_constant<int, 2>;
+  using Zero = std::integral_constant<int, 0>;
+  if (cols % 8) f(std::false_type{}, Zero{});
+  else if (sizeof(T) == 4 || stream == 0) f(std::true_type{}, Zero{});
+  else if constexpr (sizeof(T) == 2) stream == 1 ? f(std::true_type{}, One{}) : f(std::true_type{}, Two{});
+}
+
 template <typename T, int FMT>
-void launch_norm(NormParams p, hipStream_t s) {
+void launch_norm(NormParams p, int stream, hipStream_t s) {
   // (ranges of rows, a multiple of the four of a workgroup: a grid has below 2^32 threads)
   constexpr int kMostThreads = 1 << 30;
   auto ranges = [&](int threads, auto&& launch) {
@@ -405,35 +451,37 @@ void launch_norm(NormParams p, hipStream_t s) {
       if (p.rows - p.row0 <= per) break;
     }
   };
-  const bool done = with_shape(p.nb * 4, [&](auto wave, auto ch, int threads) {
+  const bool done = with_shape(p.rows, p.nb * 4, [&](auto wave, auto ch, int threads) {
     constexpr bool WAVE = decltype(wave)::value;
     constexpr int CH = decltype(ch)::value;
     ranges(WAVE ? 64 : 1024, [&](int rows) {
       const unsigned g = (unsigned)(WAVE ? cdiv(rows, 4) : rows), n = WAVE ? 256 : threads;
-      if (p.cols % 8 == 0) rmsnorm_kernel<T, WAVE, CH, FMT, true><<<g, n, 0, s>>>(p);
-      else rmsnorm_kernel<T, WAVE, CH, FMT, false><<<g, n, 0, s>>>(p);
+      by_rows<T>(p.cols, stream, [&](auto whole, auto past) {
+        rmsnorm_kernel<T, WAVE, CH, FMT, decltype(whole)::value, decltype(past)::value><<<g, n, 0, s>>>(p);
+      });
     });
   });
   if (!done) ranges(1024, [&](int rows) { rmsnorm_long_kernel<T, FMT><<<rows, 1024, 0, s>>>(p); });
 }
 
-// Rows of partial sums: the workgroups that the card holds at once (16 waves a compute unit;
-// 8192 x 8192 bf16, before the loads lost their branches: 512 workgroups of 8 waves 106 us, 768 129
-// us, 256 163 us), at most 16 MB of sums up to 16384 columns.
-int grad_parts(int rows, int cols) {
+// Rows of partial sums: the workgroups that run at once, with `waves` waves a compute unit, at most 16
+// MB of sums up to 16384 columns. 16 waves, or 8 where the next row is loaded ahead
+// (16768 x 4096 bf16: 8 waves 103 us, 16 waves 112; 8192 x 8192: 104, 107).
+int grad_parts(int rows, int cols, int waves) {
   int n = 256;
-  with_shape(cdiv(cols, 8), [&](auto, auto, int threads) { n = 256 * (1024 / threads); });
+  with_shape(rows, cdiv(cols, 8), [&](auto, auto, int threads) { n = 256 * (waves * 64 > threads ? waves * 64 / threads : 1); });
   n = n < 2048 ? n : 2048;
   return rows < n ? rows : n;
 }
 
 template <typename T>
-void launch_grad(const NormGradParams& p, int parts, hipStream_t s) {
-  const bool done = with_shape(cdiv(p.cols, 8), [&](auto wave, auto ch, int threads) {
+void launch_grad(const NormGradParams& p, int stream, int parts, hipStream_t s) {
+  const bool done = with_shape(p.rows, cdiv(p.cols, 8), [&](auto wave, auto ch, int threads) {
     constexpr bool WAVE = decltype(wave)::value;
     constexpr int CH = decltype(ch)::value;
-    if (p.cols % 8 == 0) rmsnorm_grad_kernel<T, WAVE, CH, true><<<parts, threads, 0, s>>>(p);
-    else rmsnorm_grad_kernel<T, WAVE, CH, false><<<parts, threads, 0, s>>>(p);
+    by_rows<T>(p.cols, stream, [&](auto whole, auto past) {
+      rmsnorm_grad_kernel<T, WAVE, CH, decltype(whole)::value, decltype(past)::value><<<parts, threads, 0, s>>>(p);
+    });
   });
   if (!done) rmsnorm_grad_long_kernel<T><<<parts, 1024, 0, s>>>(p);
 }
@@ -503,11 +551,13 @@ gemm_status rmsnorm_forward(const rmsnorm_args* a, void* stream) {
   p.nsb = cdiv(p.nb, kMxScaleBlocks);
   p.eps = a->eps;
   p.inv_cols = 1.0 / a->cols;
+  const int tensors = 1 + (a->residual ? 1 : 0) + (a->h_out ? 1 : 0) + (a->y ? 1 : 0);
+  const int stream_past = stream_mode((int64_t)a->rows * a->cols * tensors, es, a->cols | a->ldx | (a->residual ? a->ldr : 0));
   with_type(a->type, [&](auto* t) {
     using T = std::remove_pointer_t<decltype(t)>;
-    if (!a->q_codes) launch_norm<T, kNoMx>(p, (hipStream_t)stream);
-    else if (a->q_format == MX_E2M1) launch_norm<T, MX_E2M1>(p, (hipStream_t)stream);
-    else launch_norm<T, MX_E4M3>(p, (hipStream_t)stream);
+    if (!a->q_codes) launch_norm<T, kNoMx>(p, stream_past, (hipStream_t)stream);
+    else if (a->q_format == MX_E2M1) launch_norm<T, MX_E2M1>(p, stream_past, (hipStream_t)stream);
+    else launch_norm<T, MX_E4M3>(p, stream_past, (hipStream_t)stream);
   });
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return fail(GEMM_ERR_HIP, "%s launch: %s", fn, hipGetErrorString(e));
@@ -516,7 +566,7 @@ gemm_status rmsnorm_forward(const rmsnorm_args* a, void* stream) {
 
 int64_t rmsnorm_backward_workspace(int32_t rows, int32_t cols) {
   if (rows < 0 || cols < 0) return -1;
-  return (int64_t)grad_parts(rows, cols) * cols * 4;
+  return (int64_t)grad_parts(rows, cols, 16) * cols * 4;
 }
 
 gemm_status rmsnorm_backward(const rmsnorm_backward_args* a, void* stream) {
@@ -541,7 +591,9 @@ gemm_status rmsnorm_backward(const rmsnorm_backward_args* a, void* stream) {
     if (a->dx == a->dres && a->lddx != a->lddres) return fail(GEMM_ERR_INVALID_ARG, "%s: dx in the place of dres needs its leading dimension", fn);
   }
   clear_error();
-  const int parts = grad_parts(a->rows, a->cols);
+  const int stream_past = stream_mode((int64_t)a->rows * a->cols * (a->dres ? 4 : 3), es,
+                                      a->cols | a->lddy | a->ldh | (a->dres ? a->lddres : 0));
+  const int parts = grad_parts(a->rows, a->cols, es == 2 && a->cols % 8 == 0 && stream_past != 2 ? 8 : 16);
   hipStream_t s = (hipStream_t)stream;
   NormGradParams p;
   p.dy = a->dy; p.h = a->h; p.w = a->weight; p.dres = a->dres; p.rstd = a->rstd; p.dx = a->dx;
@@ -549,7 +601,7 @@ gemm_status rmsnorm_backward(const rmsnorm_backward_args* a, void* stream) {
   p.lddy = a->lddy; p.ldh = a->ldh; p.lddres = a->lddres; p.lddx = a->lddx;
   p.rows = a->rows; p.cols = a->cols;
   p.inv_cols = 1.f / (float)a->cols;
-  if (parts > 0) with_type(a->type, [&](auto* t) { launch_grad<std::remove_pointer_t<decltype(t)>>(p, parts, s); });
+  if (parts > 0) with_type(a->type, [&](auto* t) { launch_grad<std::remove_pointer_t<decltype(t)>>(p, stream_past, parts, s); });
   column_sum_kernel<<<cdiv(a->cols, kSumCols), kSumCols * kSumRows, 0, s>>>(p.part, parts, a->cols, a->dw);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return fail(GEMM_ERR_HIP, "%s launch: %s", fn, hipGetErrorString(e));
