@@ -14,6 +14,12 @@
 //            through LDS (global -> LDS transfers, two to four stages), persistent tile loop.
 //   MxDirect few rows. 16x16 to 32x64 outputs per workgroup, whose waves share out K and read
 //            their fragments from global memory themselves; one join in LDS at the end.
+// MxRing 8192^3 e2m1 x e2m1: 245 us, 4.49 PFLOP/s; the matrix pipes are busy 61% of the cycles, and the
+// chip holds 1.75 GHz of its 2.4 under that load (power). 16768 x 4096 x 4096 e4m3 x e2m1 over 8 experts: 237
+// us, 2.37 PFLOP/s, 60% busy at 2.0 GHz; a library product of e4m3 8192^3 reaches 2.66 here.
+// MxDirect 1 x 8192 x 8192 e4m3 x e2m1: 7.8 us for 35.7 MB, of which 2.5 are the launch. 256x128 tiles
+// were measured and are not kept: 4096 x 2048 x 4096 e4m3 34 us as with 128x128, one round either way,
+// 2048 x 2048 x 4096 28 us and 22.
 #pragma once
 #include "../gemm_kernel.hpp"
 #include "mx_common.hpp"

@@ -7,7 +7,10 @@
 // Both are bound by memory. A row is held in registers from its single read to its last use:
 // threads x CH chunks of 8 elements, chunk j of thread t at column (t + j threads) 8. Four
 // adjacent lanes hold an MX block. Rows too long for registers take a kernel that reads them
-// twice. All sums run in a fixed order.
+// twice. All sums run in a fixed order. 16768 x 4096 bf16 with residual, h and e4m3 output: 78.5 us (483
+// MB, 6.2 TB/s); gradients 8192 x 8192 bf16 with dres: 94.9 us (537 MB and 17 MB of column sums written and
+// read, 6.0 TB/s; 90 and 5 us of it in the two kernels); one row of 4096: 3 us, the launch and two
+// rounds of memory latency.
 #include <type_traits>
 
 #include "mx_common.hpp"

@@ -236,3 +236,49 @@ def test_python_refusals():
         gep.rmsnorm_backward(x, x, w, rstd, workspace=torch.empty(4, device="cuda"))
     with pytest.raises(ValueError):
         gep.rmsnorm_backward(x[:3], x, w, rstd)
+
+
+@pytest.mark.parametrize("rows,cols", [(16768, 4096), (16385, 5000)])
+def test_large_calls_equal_their_parts(rows, cols):
+    """A call that moves more than the last-level cache holds gives, row by row, what calls on a few of
+    its rows give (bit for bit), whichever kernel each of them takes."""
+    announce(f"rmsnorm large {rows}x{cols}")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x, r = (torch.randn(rows, cols, generator=g, device="cuda").bfloat16() for _ in range(2))
+    w = (1 + 0.2 * torch.randn(cols, generator=g, device="cuda")).bfloat16()
+    h, y, rstd = torch.empty_like(x), torch.empty_like(x), torch.empty(rows, device="cuda")
+    q = gep.mx_empty(rows, cols, "e4m3")
+    gep.rmsnorm(x, w, residual=r, h=h, y=y, q=q, rstd=rstd)
+    assert torch.equal(h, (x.float() + r.float()).bfloat16())
+    values = gep.mx_dequantize(q)
+    ph, py, pr = torch.empty_like(x), torch.empty_like(x), torch.empty(rows, device="cuda")
+    for a in range(0, rows, 1000):
+        s = slice(a, min(a + 1000, rows))
+        pq = gep.mx_empty(s.stop - a, cols, "e4m3")
+        gep.rmsnorm(x[s], w, residual=r[s], h=ph[s], y=py[s], q=pq, rstd=pr[s])
+        assert torch.equal(pq.codes, q.codes[s])
+        assert torch.equal(gep.mx_dequantize(pq), values[s])
+    assert torch.equal(ph, h) and torch.equal(py, y) and torch.equal(pr, rstd)
+
+
+@pytest.mark.parametrize("rows,cols", [(16768, 4096), (16385, 5000)])
+def test_large_gradients_equal_their_parts(rows, cols):
+    """dx as above; dw: every row's term carries 3 u (rstd's product, dy's, the sum's), the sum (rows + 6) u
+    of sum |dy n| as in test_backward."""
+    announce(f"rmsnorm backward large {rows}x{cols}")
+    g = torch.Generator(device="cuda").manual_seed(2)
+    dy, h, dres = (torch.randn(rows, cols, generator=g, device="cuda").bfloat16() for _ in range(3))
+    w = (1 + 0.2 * torch.randn(cols, generator=g, device="cuda")).bfloat16()
+    rstd = torch.rsqrt(h.float().square().mean(1) + 1e-5)
+    dx, dw = gep.rmsnorm_backward(dy, h, w, rstd, dres=dres)
+    for a in range(0, rows, 1000):
+        s = slice(a, min(a + 1000, rows))
+        part, _ = gep.rmsnorm_backward(dy[s], h[s], w, rstd[s], dres=dres[s])
+        assert torch.equal(part, dx[s])
+    want, mag = torch.zeros(cols, dtype=torch.float64, device="cuda"), torch.zeros(cols, dtype=torch.float64, device="cuda")
+    for a in range(0, rows, 1000):
+        s = slice(a, min(a + 1000, rows))
+        t = dy[s].double() * h[s].double() * rstd[s].double()[:, None]
+        want += t.sum(0)
+        mag += t.abs().sum(0)
+    assert ((dw.double() - want).abs() <= (rows + 6) * U * mag).all()
