@@ -84,10 +84,10 @@ extern "C" gemm_status mx_gemm_run(const mx_gemm_plan* plan, const mx_gemm_args*
   const gemm_status st = compute_units(&cus);
   if (st != GEMM_OK) return st;
 
-  MxChoice choice = mx_choose(*plan, cus, true);
+  MxChoice choice = mx_choice(*plan, cus, true);
   if (choice.split > 1) {
     const int64_t need = mx_workspace_bytes(*plan, choice);
-    if (!a->workspace) choice = mx_choose(*plan, cus, false);
+    if (!a->workspace) choice = mx_choice(*plan, cus, false);
     else if (a->workspace_bytes < need) return fail(GEMM_ERR_INVALID_ARG, "mx_gemm_run: workspace of %lld bytes expected", (long long)need);
     else if ((uintptr_t)a->workspace & 15) return fail(GEMM_ERR_ALIGNMENT, "mx_gemm_run: workspace not 16-byte aligned");
   }

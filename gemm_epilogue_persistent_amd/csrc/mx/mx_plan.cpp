@@ -126,6 +126,16 @@ MxChoice mx_choose(const mx_gemm_plan& p, int32_t cus, bool workspace) {
   return c;
 }
 
+MxChoice mx_choice(const mx_gemm_plan& p, int32_t cus, bool workspace) {
+  if (cus > 0xFFFF) return mx_choose(p, cus, workspace);
+  std::atomic<uint64_t>& slot = p.chosen[workspace];
+  const uint64_t v = slot.load(std::memory_order_relaxed);
+  if (v >> 48 == (uint64_t)cus) return MxChoice{(int32_t)(v >> 40 & 0xFF), (int32_t)(v >> 32 & 0xFF), (int32_t)(uint32_t)v};
+  const MxChoice c = mx_choose(p, cus, workspace);
+  slot.store((uint64_t)cus << 48 | (uint64_t)c.tile << 40 | (uint64_t)c.split << 32 | (uint32_t)c.per, std::memory_order_relaxed);
+  return c;
+}
+
 bool mx_direct_fits(const mx_gemm_plan& p, int32_t tile) {
   if (tile == MX_TILE_256 || tile == MX_TILE_128) return true;
   int32_t bm, bn;
@@ -207,7 +217,7 @@ gemm_status mx_gemm_destroy(mx_gemm_plan* plan) {
 
 gemm_status mx_gemm_plan_tile(const mx_gemm_plan* plan, int32_t num_cus, int32_t* tile, int32_t* split) {
   if (!plan || num_cus < 1) return fail(GEMM_ERR_INVALID_ARG, "mx_gemm_plan_tile: NULL plan or no compute units");
-  const MxChoice c = mx_choose(*plan, num_cus, true);
+  const MxChoice c = mx_choice(*plan, num_cus, true);
   if (tile) *tile = c.tile;
   if (split) *split = c.split;
   clear_error();
@@ -216,7 +226,7 @@ gemm_status mx_gemm_plan_tile(const mx_gemm_plan* plan, int32_t num_cus, int32_t
 
 gemm_status mx_gemm_workspace(const mx_gemm_plan* plan, int32_t num_cus, int64_t* bytes) {
   if (!plan || !bytes || num_cus < 1) return fail(GEMM_ERR_INVALID_ARG, "mx_gemm_workspace: NULL argument or no compute units");
-  *bytes = mx_workspace_bytes(*plan, mx_choose(*plan, num_cus, true));
+  *bytes = mx_workspace_bytes(*plan, mx_choice(*plan, num_cus, true));
   clear_error();
   return GEMM_OK;
 }

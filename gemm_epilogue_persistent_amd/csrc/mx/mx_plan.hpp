@@ -2,6 +2,8 @@
 #pragma once
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../../include/mx_mi355x.h"
 #include "../params.hpp"
 
@@ -10,6 +12,9 @@ struct mx_gemm_plan {
   int64_t a_bytes, b_bytes;    // codes (B: of one group)
   int64_t sa_bytes, sb_bytes;  // scales
   int32_t lda, ldb;            // bytes of a row of codes
+  // The choice made last, with and without a workspace: compute units, tile, split and per in 16, 8, 8
+  // and 32 bits (0: none yet). Choosing takes 1.2 us, a fifth of a short run.
+  mutable std::atomic<uint64_t> chosen[2] = {{0}, {0}};
 };
 
 namespace gep {
@@ -19,6 +24,8 @@ struct MxChoice {
   int32_t tile, split, per;
 };
 MxChoice mx_choose(const mx_gemm_plan& p, int32_t cus, bool workspace);
+// The same, kept in the plan for the next run.
+MxChoice mx_choice(const mx_gemm_plan& p, int32_t cus, bool workspace);
 void mx_tile_extent(int32_t tile, int32_t* bm, int32_t* bn);
 // Upper bound of the row blocks of a tile of bm rows over all groups (exact for a dense plan).
 int64_t mx_row_blocks(const mx_gemm_plan& p, int32_t bm);

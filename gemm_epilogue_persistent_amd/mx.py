@@ -33,6 +33,7 @@ def _cdiv(a, b):
 # which takes as long as a launch)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _allocating(stream):
@@ -45,7 +46,7 @@ def _launch(device, stream, function, *args):
     """function(*args, stream pointer) with `device` current, on `stream` (default: the device's
     current one); raises what it reports."""
     index = device.index
-    if index != torch.cuda.current_device():
+    if index != _current_device():
         with torch.cuda.device(index):
             return _launch(device, stream, function, *args)
     status = function(*args, _raw_stream(index) if stream is None else stream.cuda_stream)
@@ -160,7 +161,7 @@ def mx_quantize(x, fmt, out=None, transpose=False, stream=None):
     rows, cols = shape
     if transpose:
         shape = (cols, rows)
-    if x.stride(1) != 1 and x.stride(0) == 1 and cols > 1:  # columns contiguous: x^T has contiguous rows
+    if cols > 1 and x.stride(1) != 1 and x.stride(0) == 1:  # columns contiguous: x^T has contiguous rows
         x, rows, cols, transpose = x.t(), cols, rows, not transpose
     ld = _matrix("x", x, _FLOAT_DT)
     if out is None:

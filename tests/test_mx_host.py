@@ -279,3 +279,28 @@ def test_packed_arguments(packed, structure):
     names = [f for f, _ in structure._fields_]
     got = structure.from_buffer_copy(packed.pack(*range(1, len(names) + 1)))
     assert [getattr(got, f) for f in names] == list(range(1, len(names) + 1))
+
+
+def test_plan_choice_is_that_of_the_device_asked_for(lib):
+    """The choice that a plan keeps is used for the same number of compute units only, whatever the order
+    of the questions."""
+    kw = dict(M=512, N=4096, K=8192, c=0, d=2, post=0, act=0, ldd=4096)
+    counts = (8, 32, 256, 304, 100000)
+
+    def ask(h, cus):
+        t, n = ctypes.c_int32(), ctypes.c_int32()
+        assert lib.mx_gemm_plan_tile(h, cus, ctypes.byref(t), ctypes.byref(n)) == 0
+        return t.value, n.value
+    fresh = []
+    for cus in counts:
+        h = ctypes.c_void_p()
+        assert lib.mx_gemm_create(ctypes.byref(gemm_desc(**kw)), ctypes.byref(h)) == 0
+        fresh.append(ask(h, cus))
+        lib.mx_gemm_destroy(h)
+    assert len(set(fresh)) > 1
+    h = ctypes.c_void_p()
+    assert lib.mx_gemm_create(ctypes.byref(gemm_desc(**kw)), ctypes.byref(h)) == 0
+    for _ in range(2):
+        for cus, want in zip(counts, fresh):
+            assert ask(h, cus) == want and ask(h, cus) == want
+    lib.mx_gemm_destroy(h)
