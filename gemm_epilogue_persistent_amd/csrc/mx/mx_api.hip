@@ -1,5 +1,6 @@
 // mx_gemm_run (C ABI): the launch of an MX product.
 #include <atomic>
+#include <utility>
 
 #include "mx_gemm.hpp"
 #include "mx_plan.hpp"
@@ -80,6 +81,10 @@ extern "C" gemm_status mx_gemm_run(const mx_gemm_plan* plan, const mx_gemm_args*
   for (const void* p : {a->a_codes, a->a_scales, a->b_codes, a->b_scales, a->C, (const void*)a->D, (const void*)a->PostAct})
     if ((uintptr_t)p & 15) return fail(GEMM_ERR_ALIGNMENT, "mx_gemm_run: pointers must be 16-byte aligned");
   if ((uintptr_t)a->cu_seqlens_m & 3) return fail(GEMM_ERR_ALIGNMENT, "mx_gemm_run: cu_seqlens_m not 4-byte aligned");
+  for (const auto& o : {std::pair<const void*, std::pair<int32_t, int64_t>>{a->D, {d.d, d.ldd}}, {a->PostAct, {d.post, d.ldp}}})
+    if (a->C && a->C == o.first && (d.c != o.second.first || (d.M > 1 && d.ldc != o.second.second)))
+      return fail(GEMM_ERR_INVALID_ARG, "mx_gemm_run: C in the place of an output needs its type and leading dimension");
+  if (a->D && a->D == a->PostAct) return fail(GEMM_ERR_INVALID_ARG, "mx_gemm_run: D and PostAct are one matrix");
   int32_t cus = 0;
   const gemm_status st = compute_units(&cus);
   if (st != GEMM_OK) return st;

@@ -16,7 +16,7 @@
 //            their fragments from global memory themselves; one join in LDS at the end.
 // MxRing 8192^3 e2m1 x e2m1: 245 us, 4.49 PFLOP/s; the matrix pipes are busy 61% of the cycles, and the
 // chip holds 1.75 GHz of its 2.4 under that load (power). 16768 x 4096 x 4096 e4m3 x e2m1 over 8 experts: 237
-// us, 2.37 PFLOP/s, 60% busy at 2.0 GHz; a library product of e4m3 8192^3 reaches 2.66 here.
+// to 241 us, 2.35 PFLOP/s, 60% busy at 2.0 GHz; a library product of e4m3 8192^3 reaches 2.66 here.
 // MxDirect 1 x 8192 x 8192 e4m3 x e2m1: 7.8 us for 35.7 MB, of which 2.5 are the launch. 256x128 tiles
 // were measured and are not kept: 4096 x 2048 x 4096 e4m3 34 us as with 128x128, one round either way,
 // 2048 x 2048 x 4096 28 us and 22.
@@ -183,6 +183,18 @@ __device__ __forceinline__ MxGroup mx_find_group(const KParams& p, int want, int
   return r;
 }
 
+// Which epilogue of MxRing: 0 any types, and slices of K; 1 one 16-bit output without C; else 16-bit rows,
+// 2 + (C) + 2 (both outputs). (16-bit offsets inside a tile are 32-bit: 256 rows of less than 2^22.)
+constexpr int64_t kMaxLd16 = 1 << 22;
+__host__ __device__ __forceinline__ int mx_epilogue_kind(const MxParams& mp) {
+  const KParams& p = mp.k;
+  if (mp.split > 1) return 0;
+  auto fits = [](int dt, int64_t ld) { return dt == DT_NONE || (dt != DT_F32 && ld < kMaxLd16); };
+  if (!fits(p.c_dt, p.ldc) || !fits(p.d_dt, p.ldd) || !fits(p.p_dt, p.ldp)) return 0;
+  const int c = p.c_dt != DT_NONE, both = p.d_dt != DT_NONE && p.p_dt != DT_NONE;
+  return !c && !both ? 1 : 2 + c + 2 * both;
+}
+
 // ------------------------------------------------------------------------------------
 // MxRing
 // ------------------------------------------------------------------------------------
@@ -199,10 +211,15 @@ __device__ __forceinline__ MxGroup mx_find_group(const KParams& p, int want, int
 // after them, may be outstanding). After it the next step's first fragments are read and the first
 // half of the transfers into the freed stage goes out; the second half follows at the head of the
 // next step.
-template <int BM, int BN, int NW, int NS, int FA, int FB, bool VM>
+//
+// EPI: the epilogues of the kernel, all kinds (0), kind 1 (1) or the others (2). Kind 1 has a kernel of
+// its own where the larger code costs it something: in 128x128 tiles (4096 x 2048 x 4096 e4m3 36.9 us
+// instead of 35.6) and in 256x256 tiles of two E2M1 operands (8192^3 230.4 and 227.8), but not in
+// those with an E4M3 operand (16384 x 4096 x 4096 192.8 in one kernel, 194.3 in two).
+template <int BM, int BN, int NW, int NS, int FA, int FB, bool VM, int EPI>
 struct MxRing {
   static constexpr int kThreads = NW * 64;
-  static constexpr bool kSplit = BM == 128 && !VM;  // may run slices of K
+  static constexpr bool kSplit = BM == 128 && !VM && EPI != 1;  // may run slices of K
   static constexpr int kWN = 64, kWavesN = BN / kWN, kWavesM = NW / kWavesN, kWM = BM / kWavesM;
   static constexpr int kMI = kWM / 16, kNI = kWN / 16;
   using A = MxFmt<FA>;
@@ -304,9 +321,9 @@ struct MxRing {
     }
   }
 
-  // Wait until at most kAhead of this wave's vector memory operations are outstanding (kAhead +
-  // kStores16 with `more`, the same in every lane) and its LDS operations are done; then the
-  // workgroup meets. (The branch is inside the asm: as one of the compiler's it would cut the step
+  // Wait until at most kAhead of this wave's vector memory operations are outstanding (and `more` x
+  // kStores16 besides; 0, 1 or 2, the same in every lane) and its LDS operations are done; then the
+  // workgroup meets. (The branches are inside the asm: as one of the compiler's it would cut the step
   // into blocks and the accumulators would move between them.)
   static __device__ __forceinline__ void ring_barrier() {
     __builtin_amdgcn_sched_barrier(0);
@@ -314,11 +331,13 @@ struct MxRing {
     __builtin_amdgcn_sched_barrier(0);
   }
   static __device__ __forceinline__ void ring_barrier(int more) {
-    static_assert(kAhead + kStores16 < 64, "a six-bit counter");
+    static_assert(kAhead + 2 * kStores16 < 64, "a six-bit counter");
     __builtin_amdgcn_sched_barrier(0);
     asm volatile(
-        "s_cmp_eq_u32 %2, 0\n\ts_cbranch_scc0 1f\n\ts_waitcnt vmcnt(%0)\n1:\n\ts_waitcnt vmcnt(%1) lgkmcnt(0)\n\ts_barrier" ::"n"(kAhead),
-        "n"(kAhead + kStores16), "s"(more)
+        "s_cmp_lt_u32 %3, 1\n\ts_cbranch_scc0 1f\n\ts_waitcnt vmcnt(%0)\n1:\n\t"
+        "s_cmp_lt_u32 %3, 2\n\ts_cbranch_scc0 2f\n\ts_waitcnt vmcnt(%1)\n2:\n\t"
+        "s_waitcnt vmcnt(%2) lgkmcnt(0)\n\ts_barrier" ::"n"(kAhead),
+        "n"(kAhead + kStores16), "n"(kAhead + 2 * kStores16), "s"(more)
         : "memory", "scc");
     __builtin_amdgcn_sched_barrier(0);
   }
@@ -465,8 +484,8 @@ struct MxRing {
     }
   }
 
-  // stores: the kStores16 stores of the previous tile's epilogue lie between this tile's transfers of
-  // stage NS - 2 and NS - 1, and need not be waited for before those.
+  // stores: the stores x kStores16 stores of the previous tile's epilogue lie between this tile's transfers
+  // of stage NS - 2 and NS - 1, and need not be waited for before those.
   template <bool MM, int T>
   static __device__ __forceinline__ void step(f32x4 (&acc)[kMI][kNI], Frags& f, GEP_LDS char* smem, const Lane& lo,
                                               const Src& s, int q, Stages& st, int stores, int wave) {
@@ -516,9 +535,11 @@ struct MxRing {
   // ---- epilogue. It runs while the next tile's first transfers are under way (all stages but the
   // last), through 4 KB a wave of the last stage. One 16-bit output without C: the values are final in the
   // accumulators, so they are converted there and pass through LDS as 16-bit rows (32 rows a
-  // pass). Otherwise fp32 rows (16 a pass). Either way a lane then holds 8 consecutive columns, and C,
-  // D and PostAct are accessed 16 bytes or more at a time, 128 bytes a row. Chunks are XOR-swizzled
-  // by the row as in gemm_kernel.hpp's 16x16 epilogues.
+  // pass); a 16-bit C is then loaded four or eight rows a lane ahead, the first of them before the next
+  // tile's transfers (16384 x 4096 x 4096 e4m3 x e2m1 with C 217 us, each row's load waited for in its
+  // turn 237, without C 193; 8192 x 8192 x 2048 e2m1 with C 99 and 124). Either way a lane then holds 8
+  // consecutive columns, and C, D and PostAct are accessed 16 bytes or more at a time, 128 bytes a
+  // row. Chunks are XOR-swizzled by the row as in gemm_kernel.hpp's 16x16 epilogues.
   static constexpr int kRegion = 4096;
   static_assert(kRegion * NW <= kStage, "the epilogue's buffers lie in one stage");
   static __device__ __forceinline__ int ebuf(int r, int c8, int hf) {
@@ -529,8 +550,6 @@ struct MxRing {
   // Stores of the 16-bit path; the count lets the wait for the transfers issued before them leave
   // the stores in flight. (So every one is issued: rows and columns past the output go to an
   // offset that the range check drops.)
-  static constexpr int64_t kMaxLd16 = 1 << 22;  // its offsets inside a tile are 32-bit
-
   template <int DT>
   static __device__ __forceinline__ void epilogue16(const KParams& p, const MxTileInfo& ti, const f32x4 (&acc)[kMI][kNI],
                                                     GEP_LDS char* buf, int lane, int wm0, int wn0) {
@@ -568,19 +587,94 @@ struct MxRing {
     }
   }
 
-  // Returns whether exactly kStores16 stores are the last vector memory operations issued.
-  static __device__ __forceinline__ bool epilogue(const MxParams& mp, const MxTileInfo& ti, const f32x4 (&acc)[kMI][kNI],
-                                                  GEP_LDS char* buf, int lane, int wm0, int wn0) {
+  // 16-bit rows of C, D and PostAct with C or both outputs. Row i * 8 + lane / 8 of the wave's is item i of
+  // a lane; kRing items of C are under way (256x256: what the registers hold; eight spill 24 to 40).
+  static constexpr int kItems = 2 * kMI, kRing = BM == 256 ? 4 : 8;
+  struct CRing {
+    i32x4 v[kRing];
+  };
+  struct Rows16 {  // one of the matrices, at the wave's first row and column
+    __amdgpu_buffer_rsrc_t rs;
+    int ld;
+  };
+  static __device__ __forceinline__ Rows16 rows16(const void* base, int64_t ld, const MxTileInfo& ti, int wm0, int wn0) {
+    return Rows16{make_rsrc((const char*)base + ((int64_t)(ti.m0 + wm0) * ld + ti.n0 + wn0) * 2, 0x7FFFFFFF), (int)ld};
+  }
+  // Byte offset of item i, or past the range where the output has no such row or column.
+  static __device__ __forceinline__ uint32_t item_offset(const Rows16& m, const KParams& p, const MxTileInfo& ti, int i,
+                                                         int lane, int wm0, int wn0) {
+    const int r = i * 8 + (lane >> 3), c = 8 * (lane & 7);
+    return ti.m0 + wm0 + r < ti.row_end && ti.n0 + wn0 + c < p.N ? (uint32_t)((r * m.ld + c) * 2) : kOOB;
+  }
+  static __device__ __forceinline__ void load_c(CRing& ring, const KParams& p, const MxTileInfo& ti, int lane, int wm0, int wn0) {
+    const Rows16 c = rows16(p.C, p.ldc, ti, wm0, wn0);
+#pragma unroll
+    for (int i = 0; i < kRing; ++i)
+      ring.v[i] = __builtin_amdgcn_raw_buffer_load_b128(c.rs, item_offset(c, p, ti, i, lane, wm0, wn0), 0, 0);
+  }
+  template <bool HASC, bool BOTH>
+  static __device__ __forceinline__ void epilogue_rows(const KParams& p, const MxTileInfo& ti, const f32x4 (&acc)[kMI][kNI],
+                                                       CRing& ring, GEP_LDS char* buf, int lane, int wm0, int wn0) {
+    const bool post = p.p_dt != DT_NONE;
+    const Rows16 cm = rows16(p.C, p.ldc, ti, wm0, wn0);
+    const Rows16 d = BOTH || !post ? rows16(p.D, p.ldd, ti, wm0, wn0) : rows16(p.Post, p.ldp, ti, wm0, wn0);
+    const Rows16 q = BOTH ? rows16(p.Post, p.ldp, ti, wm0, wn0) : d;
+    const int d_dt = BOTH || !post ? p.d_dt : p.p_dt;
+    auto store = [&](const Rows16& m, int dt, int i, const float (&v)[8]) {
+      const uint2 lo = pack4_16(dt, v), hi = pack4_16(dt, v + 4);
+      __builtin_amdgcn_raw_buffer_store_b128(i32x4{(int)lo.x, (int)lo.y, (int)hi.x, (int)hi.y}, m.rs,
+                                             item_offset(m, p, ti, i, lane, wm0, wn0), 0, 0);
+    };
+#pragma unroll
+    for (int pass = 0; pass < kMI; ++pass) {
+#pragma unroll
+      for (int j = 0; j < kNI; ++j)
+        *(f32x4 GEP_LDS*)(buf + ebuf(lane & 15, 2 * j + (lane >> 5), (lane >> 4) & 1)) = acc[pass][j];
+      asm volatile("" ::: "memory");
+#pragma unroll
+      for (int it = 0; it < 2; ++it) {
+        const int i = pass * 2 + it, r = it * 8 + (lane >> 3);
+        const f32x4 x0 = *(const f32x4 GEP_LDS*)(buf + ebuf(r, lane & 7, 0));
+        const f32x4 x1 = *(const f32x4 GEP_LDS*)(buf + ebuf(r, lane & 7, 1));
+        float v[8] = {x0[0], x0[1], x0[2], x0[3], x1[0], x1[1], x1[2], x1[3]};
+        if constexpr (HASC) {
+          const i32x4 x = ring.v[i % kRing];
+          float c[8];
+          unpack4_16(p.c_dt, uint2{(uint32_t)x[0], (uint32_t)x[1]}, c);
+          unpack4_16(p.c_dt, uint2{(uint32_t)x[2], (uint32_t)x[3]}, c + 4);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] += c[e];
+          if (i + kRing < kItems)
+            ring.v[i % kRing] = __builtin_amdgcn_raw_buffer_load_b128(cm.rs, item_offset(cm, p, ti, i + kRing, lane, wm0, wn0), 0, 0);
+        }
+        if constexpr (BOTH) store(d, d_dt, i, v);
+        if (post) mx_act8(p.act, v);
+        if constexpr (BOTH) store(q, p.p_dt, i, v);
+        else store(d, d_dt, i, v);
+      }
+      asm volatile("" ::: "memory");
+    }
+  }
+
+  // Returns how often kStores16 stores are the last vector memory operations issued.
+  static __device__ __forceinline__ int epilogue(const MxParams& mp, int kind, const MxTileInfo& ti, const f32x4 (&acc)[kMI][kNI],
+                                                 CRing& ring, GEP_LDS char* buf, int lane, int wm0, int wn0) {
     const KParams& p = mp.k;
     const bool slice = kSplit && mp.split > 1;
     asm volatile("" : "+v"(lane));
-    if (!slice && p.c_dt == DT_NONE && (p.d_dt == DT_NONE) != (p.p_dt == DT_NONE)) {
-      const int dt = p.d_dt != DT_NONE ? p.d_dt : p.p_dt;
-      if ((p.d_dt != DT_NONE ? p.ldd : p.ldp) < kMaxLd16 && dt != DT_F32) {
-        if (dt == DT_BF16) epilogue16<DT_BF16>(p, ti, acc, buf, lane, wm0, wn0);
+    if constexpr (EPI != 2) {
+      if (kind == 1) {
+        if ((p.d_dt != DT_NONE ? p.d_dt : p.p_dt) == DT_BF16) epilogue16<DT_BF16>(p, ti, acc, buf, lane, wm0, wn0);
         else epilogue16<DT_F16>(p, ti, acc, buf, lane, wm0, wn0);
-        return true;
+        return 1;
       }
+    }
+    if constexpr (EPI == 1) return 0;
+    switch (kind) {
+      case 3: epilogue_rows<true, false>(p, ti, acc, ring, buf, lane, wm0, wn0); return 1;
+      case 4: epilogue_rows<false, true>(p, ti, acc, ring, buf, lane, wm0, wn0); return 2;
+      case 5: epilogue_rows<true, true>(p, ti, acc, ring, buf, lane, wm0, wn0); return 2;
+      default: break;
     }
     const int row0 = ti.m0 + wm0, col0 = ti.n0 + wn0;
     const int rl = lane >> 3, n = col0 + 8 * (lane & 7);
@@ -604,7 +698,7 @@ struct MxRing {
       }
       asm volatile("" ::: "memory");
     }
-    return false;
+    return 0;
   }
   static __device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
@@ -705,7 +799,8 @@ struct MxRing {
     };
 
     if (b0 < U) begin_tile(b0);
-    int stores = 0;  // 1: the wave's last operations are the stores of epilogue16
+    int stores = 0;  // how often kStores16 stores are the wave's last operations
+    const int kind = EPI == 1 ? 1 : uni(mx_epilogue_kind(mp));
     for (int t = b0; t < U;) {
       f32x4 acc[kMI][kNI];
 #pragma unroll
@@ -735,12 +830,14 @@ struct MxRing {
       }
       dma_barrier();  // transfers past K have landed and every wave has left the ring
       const MxTileInfo done = ti;
+      CRing ring;
+      if ((kind == 3 || kind == 5) && !idle) load_c(ring, p, done, lane, wm0, wn0);
       t += P;
       if (t < U) begin_tile(t);
       asm volatile("" ::: "memory");  // (its transfers are issued before the epilogue's stores)
       __builtin_amdgcn_sched_barrier(0);
       stores = 0;
-      if (!idle) stores = uni(epilogue(mp, done, acc, smem + (NS - 1) * kStage + wave * kRegion, lane_id, wm0, wn0) ? 1 : 0);
+      if (!idle) stores = uni(epilogue(mp, kind, done, acc, ring, smem + (NS - 1) * kStage + wave * kRegion, lane_id, wm0, wn0));
     }
   }
 };
@@ -912,9 +1009,15 @@ constexpr int mx_stages() {
 // 128x128 tiles run two workgroups a compute unit, or with no more workgroups than compute units
 // one with all of LDS: 512 x 4096 x 16384 (128 tiles) e4m3 x e4m3 56 us with four stages, 78 with
 // two; 8192^3 (many tiles) 564 and 490.
-template <int BM, int NW, int WG, int FA, int FB, bool VM>
+template <int BM, int NW, int WG, int FA, int FB, bool VM, int EPI>
 __global__ __launch_bounds__(NW * 64, WG) void mx_ring_kernel(const MxParams p) {
-  MxRing<BM, BM, NW, mx_stages<BM, FA, FB, WG>(), FA, FB, VM>::run(p);
+  MxRing<BM, BM, NW, mx_stages<BM, FA, FB, WG>(), FA, FB, VM, EPI>::run(p);
+}
+template <int BM, int NW, int WG, int FA, int FB, bool VM>
+void mx_launch_ring(const MxParams& p, dim3 grid, hipStream_t s) {
+  if constexpr (BM == 256 && (FA == MX_E4M3 || FB == MX_E4M3)) mx_ring_kernel<BM, NW, WG, FA, FB, VM, 0><<<grid, NW * 64, 0, s>>>(p);
+  else if (mx_epilogue_kind(p) == 1) mx_ring_kernel<BM, NW, WG, FA, FB, VM, 1><<<grid, NW * 64, 0, s>>>(p);
+  else mx_ring_kernel<BM, NW, WG, FA, FB, VM, 2><<<grid, NW * 64, 0, s>>>(p);
 }
 // Direct kernels: fragments two steps ahead. (Four steps, or twice the waves, are slower everywhere:
 // 1 x 8192 x 8192 e4m3 x e2m1 in 16x32 tiles 7.8 us, with four steps 8.6, with 16 waves 8.9; in 16x16
@@ -932,10 +1035,10 @@ hipError_t mx_launch(int32_t tile, const MxParams& p, dim3 grid, hipStream_t s);
   template <>                                                                                        \
   hipError_t mx_launch<FA, FB, VM>(int32_t tile, const MxParams& p, dim3 grid, hipStream_t s) {      \
     switch (tile) {                                                                                  \
-      case MX_TILE_256: mx_ring_kernel<256, 8, 1, FA, FB, VM><<<grid, 512, 0, s>>>(p); break;        \
+      case MX_TILE_256: mx_launch_ring<256, 8, 1, FA, FB, VM>(p, grid, s); break;                    \
       case MX_TILE_128:                                                                              \
-        if (p.k.P <= p.cus) mx_ring_kernel<128, 4, 1, FA, FB, VM><<<grid, 256, 0, s>>>(p);           \
-        else mx_ring_kernel<128, 4, 2, FA, FB, VM><<<grid, 256, 0, s>>>(p);                          \
+        if (p.k.P <= p.cus) mx_launch_ring<128, 4, 1, FA, FB, VM>(p, grid, s);                       \
+        else mx_launch_ring<128, 4, 2, FA, FB, VM>(p, grid, s);                                      \
         break;                                                                                       \
       case MX_TILE_32X64: mx_direct_kernel<2, 4, 4, 2, FA, FB, VM><<<grid, 256, 0, s>>>(p); break;   \
       case MX_TILE_32: mx_direct_kernel<2, 2, 4, 2, FA, FB, VM><<<grid, 256, 0, s>>>(p); break;      \

@@ -115,7 +115,7 @@ int64_t rmsnorm_backward_workspace(int32_t rows, int32_t cols);
  * an array that breaks this runs nothing and writes nothing).
  * At least one of d, post is present. N is a multiple of 8, every leading dimension one of 16
  * bytes, K at most 2^22, and every pointer is 16-byte aligned. K = 0 gives D = C (or 0). C may be
- * D or PostAct itself. tile: 0 lets the library choose; otherwise one of the MX_TILE values. */
+ * D or PostAct itself (of its type and leading dimension); D and PostAct are two matrices. tile: 0 lets the library choose; otherwise one of the MX_TILE values. */
 typedef enum {
   MX_TILE_AUTO = 0,
   MX_TILE_256 = 1,   /* 256x256 outputs a workgroup, operands staged through LDS         */

@@ -445,3 +445,46 @@ def test_python_refusals():
         gep.mx_dequantize(a, out=torch.empty(16, 63, device="cuda"))
     with pytest.raises(ValueError):
         gep.mx_dequantize(g)
+
+
+@pytest.mark.parametrize("tile", ["256", "128"])
+@pytest.mark.parametrize("fa,fb", [("e4m3", "e2m1"), ("e2m1", "e2m1"), ("e4m3", "e4m3")])
+@pytest.mark.parametrize("c,d,post,act", [
+    ("bf16", "bf16", None, "none"), ("f16", None, "bf16", "silu"), (None, "bf16", "f16", "gelu_tanh"),
+    ("bf16", "f16", "bf16", "silu"), ("f32", "bf16", "bf16", "relu")])
+def test_product_epilogue_over_tiles(c, d, post, act, fa, fb, tile):
+    """Several tiles a workgroup and edges in both directions: the stores of one tile under the first
+    transfers of the next, with each kind of epilogue."""
+    announce(f"product epilogue over tiles c={c} d={d} post={post} {act} {fa} x {fb} tile {tile}")
+    if "e4m3" in (fa, fb):  # (products of these operands pass f16's largest value, the first here with 67016)
+        d, post = ("bf16" if t == "f16" else t for t in (d, post))
+    n = 4104 if tile == "256" else 2312
+    run_product(4400 if tile == "256" else 4000, n, 160, fa, fb, tile, c, d, post, act, seed=41)
+
+
+@pytest.mark.parametrize("tile", ["256", "128", "32"])
+def test_product_c_in_place(tile):
+    """C in the place of D, and of PostAct."""
+    announce(f"product C in place tile {tile}")
+    a = gep.mx_quantize(torch.randn(700, 200, device="cuda"), "e4m3")
+    b = gep.mx_quantize(torch.randn(520, 200, device="cuda"), "e2m1")
+    C = torch.randn(700, 520, device="cuda").bfloat16()
+    D, P = torch.empty_like(C), torch.empty_like(C)
+    gep.mx_gemm(a, b, D, C, P, act="silu", tile=tile)
+    x = C.clone()
+    gep.mx_gemm(a, b, x, x, None, tile=tile)
+    assert torch.equal(x, D)
+    x, y = C.clone(), C.clone()
+    gep.mx_gemm(a, b, None, x, x, act="silu", tile=tile)
+    assert torch.equal(x, P)
+    gep.mx_gemm(a, b, y, y, x, act="silu", tile=tile)
+    assert torch.equal(y, D) and torch.equal(x, P)
+
+
+def test_product_aliases_refused():
+    a, b = gep.mx_empty(16, 64, "e4m3"), gep.mx_empty(24, 64, "e2m1")
+    buf = torch.zeros(16, 64, device="cuda")
+    for C, D, P in ((buf[:, :24], buf.view(32, 32)[:16, :24], None), (buf[:, :24], torch.empty(16, 24, device="cuda"), buf.view(32, 32)[:16, :24]),
+                    (None, buf[:, :24], buf[:, :24]), (buf.bfloat16()[:, :24], buf[:, :24], buf[:, :24])):
+        with pytest.raises(gep.GemmError):
+            gep.mx_gemm(a, b, D, C, P, act="silu" if P is not None else "none")
