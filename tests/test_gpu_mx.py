@@ -458,8 +458,21 @@ def test_product_epilogue_over_tiles(c, d, post, act, fa, fb, tile):
     announce(f"product epilogue over tiles c={c} d={d} post={post} {act} {fa} x {fb} tile {tile}")
     if "e4m3" in (fa, fb):  # (products of these operands pass f16's largest value, the first here with 67016)
         d, post = ("bf16" if t == "f16" else t for t in (d, post))
-    n = 4104 if tile == "256" else 2312
+    n = 5640 if tile == "256" else 2312  # (414 and 608 tiles; a last round of more than half the card is not split)
     run_product(4400 if tile == "256" else 4000, n, 160, fa, fb, tile, c, d, post, act, seed=41)
+
+
+@pytest.mark.parametrize("fa,fb", [("e4m3", "e2m1"), ("e2m1", "e2m1"), ("e4m3", "e4m3")])
+def test_product_epilogue_over_deep_tiles(fa, fb):
+    announce(f"product epilogue over deep tiles {fa} x {fb}")
+    run_product(4400, 5640, 1000, fa, fb, "256", "bf16", "bf16", "bf16", "silu", seed=45)
+
+
+@pytest.mark.parametrize("fa", FORMATS)
+@pytest.mark.parametrize("c,d,post", [("bf16", "bf16", None), (None, "bf16", "bf16"), ("bf16", "bf16", "bf16")])
+def test_product_epilogue_over_grouped_tiles(c, d, post, fa):
+    announce(f"product epilogue over grouped tiles c={c} d={d} post={post} {fa}")
+    run_product(4400, 5640, 96, fa, "e2m1", "256", c, d, post, "silu" if post else "none", sizes=[1000, 0, 3147, 253], seed=43)
 
 
 @pytest.mark.parametrize("tile", ["256", "128", "32"])
