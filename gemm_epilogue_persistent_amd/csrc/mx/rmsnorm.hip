@@ -74,9 +74,13 @@ __device__ __forceinline__ V row_sum(V v, V* red) {
 // border between them, so y is the rounding of the exact product: squares are summed in 64 bits,
 // rstd is held as hi + lo, h w is exact for 16-bit h and w (22 bits) or held as hi + lo too, and a y
 // that falls on a border of the element type is moved to the side of it that the product lies on.
-// (With fp32 sums and two fp32 products 56 of 69 million values flipped, and now none.)
+// (With fp32 sums and two fp32 products 56 of 69 million values flipped, and now none.) h w may leave
+// fp32's range where h rstd w does not: chunks with a y that is not finite and rows of a very large or
+// small rstd are computed again in 64 bits, as are those with a y on a border.
 struct Rstd {
   float hi, lo;
+  double r;
+  bool far;  // outside [2^-32, 2^20] (inside, an h w below the normal range costs y 2^-130 at most)
 };
 __device__ __forceinline__ Rstd reciprocal_root(double mean_eps) {
   // (in 64 bits: squares of fp32 and bf16 values leave the fp32 range)
@@ -85,30 +89,49 @@ __device__ __forceinline__ Rstd reciprocal_root(double mean_eps) {
   // or NaN for an infinite or NaN sum; those need no step.)
   const double r = __builtin_isfinite(r0) && r0 > 0 ? r0 + 0.5 * r0 * (1.0 - mean_eps * r0 * r0) : r0;
   Rstd s;
+  s.r = r;
   s.hi = (float)r;
   s.lo = __builtin_isfinite(s.hi) ? (float)(r - (double)s.hi) : 0.f;
+  s.far = !(s.hi >= 0x1p-32f && s.hi <= 0x1p20f);
   return s;
 }
 template <typename T>
 __device__ __forceinline__ void scale8(const float h[8], const float w[8], const Rstd& r, float y[8]) {
-  float hw[8], c[8];
   uint32_t low = ~0u;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    hw[e] = h[e] * w[e];
-    c[e] = hw[e] * r.lo;
-    if constexpr (sizeof(T) == 4) c[e] = fmaf(fmaf(h[e], w[e], -hw[e]), r.hi, c[e]);
-    y[e] = fmaf(hw[e], r.hi, c[e]);
+    const float hw = h[e] * w[e];
+    float c = hw * r.lo;
+    if constexpr (sizeof(T) == 4) c = fmaf(fmaf(h[e], w[e], -hw), r.hi, c);
+    y[e] = fmaf(hw, r.hi, c);
     low = min(low, __float_as_uint(y[e]) << 13);
   }
-  // Borders between values of at most four significant bits: the last 19 bits of y are zero there.
-  if (low == 0) {
+  // Borders between values of at most four significant bits: the last 19 bits of y are zero there. So
+  // they are in an infinity, and in the NaN that inf * hi + inf * lo gives.
+  // (Branches of the whole wave, and a loop: rare code lies past the end of the common one and is short.
+  // One row of 4096 bf16: 3.1 us; with eight copies of it in line 3.6.)
+  if (__builtin_expect(__ballot((low == 0) | r.far) != 0, 0)) {
+    bool again = r.far;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float rest = fmaf(hw[e], r.hi, -y[e]) + c[e];  // product - y
+    for (int e = 0; e < 8; ++e) {  // (zeros, as those past the row's end, are right as they are)
       const uint32_t b = __float_as_uint(y[e]);
-      if ((b << 13) == 0 && (b << 1) != 0 && rest != 0.f && __builtin_isfinite(rest))
-        y[e] = __uint_as_float((rest > 0.f) == (y[e] > 0.f) ? b + 1 : b - 1);
+      again |= (b << 13) == 0 && (b << 1) != 0;
+    }
+    if (__ballot(again) == 0) return;
+    float hr[8], wr[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) hr[e] = h[e], wr[e] = w[e];
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i) {  // element i is at place 0, and its result goes to place 7
+      const double p = (double)hr[0] * (double)wr[0] * r.r;
+      float v = (float)p;
+      const double rest = p - (double)v;
+      const uint32_t b = __float_as_uint(v);
+      if ((b << 13) == 0 && (b << 1) != 0 && rest != 0 && __builtin_isfinite(rest))
+        v = __uint_as_float((rest > 0) == (v > 0.f) ? b + 1 : b - 1);
+#pragma unroll
+      for (int e = 0; e < 7; ++e) hr[e] = hr[e + 1], wr[e] = wr[e + 1], y[e] = y[e + 1];
+      y[7] = v;
     }
   }
 }
@@ -181,12 +204,12 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void rmsnorm_kernel(const NormPa
 #pragma unroll
   for (int j = 0; j < CH; ++j) {
     const int ch = t + j * threads;
-    float a[8], w[8];
+    float a[8], w[8], y[8];
     forget(h[j]);
     unpack(h[j], a);
     load8<WHOLE>((const T*)p.w, ch * 8, p.cols, w);
-    scale8<T>(a, w, rstd, a);
-    norm_out<T, FMT, WHOLE, STREAM>(p, y_row, code_row, scale_row, ch, a);
+    scale8<T>(a, w, rstd, y);
+    norm_out<T, FMT, WHOLE, STREAM>(p, y_row, code_row, scale_row, ch, y);
   }
 }
 

@@ -282,3 +282,32 @@ def test_large_gradients_equal_their_parts(rows, cols):
         want += t.sum(0)
         mag += t.abs().sum(0)
     assert ((dw.double() - want).abs() <= (rows + 6) * U * mag).all()
+
+
+# (rstd is held to 2^-48 or so of itself and each product is rounded once: a y of 64 bits that lies this
+# close to a border between two results may fall on either side)
+EXACT = 2.0 ** -40
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("cols", [300, 1000, 5000, 17000])
+def test_products_past_the_range(cols, kind):
+    """h w leaves fp32's range, on either side, where h rstd w does not: y is the rounding of the
+    exact product (half an fp32 step, then half a step of the type), and its codes are those of it."""
+    announce(f"rmsnorm products past the range {cols} {kind}")
+    g = torch.Generator().manual_seed(cols)
+    scale = torch.tensor([1e37, 1e30, 1e19, 1e9, 1e5, 1.0, 1e-12, 1e-22, 1e-30, 1e-35], dtype=torch.float64)
+    x = torch.randn(11, cols, generator=g, dtype=torch.float64)
+    x[:10] *= scale[:, None]
+    x[10] = 3e38 * x[10].sign()  # (rstd is subnormal)
+    w = torch.randn(cols, generator=g, dtype=torch.float64) * 10.0 ** torch.randint(-30, 31, (cols,), generator=g).double()
+    x, w = x.to(TYPES[kind]), w.to(TYPES[kind])
+    h64, w64 = x.double().numpy(), w.double().numpy()
+    want = h64 / np.sqrt((h64 ** 2).mean(1))[:, None] * w64
+    for fmt in ("e4m3", "e2m1"):
+        q, y = gep.mx_empty(11, cols, fmt), torch.empty_like(x, device="cuda")
+        gep.rmsnorm(x.cuda(), w.cuda(), eps=0.0, y=y, q=q)
+        check_close(y, want, U, kind, "y")
+        check_mx(q, want, EXACT, fmt)
+    y = gep.rmsnorm(x.cuda(), w.cuda(), eps=0.0)
+    check_close(y, want, U, kind, "y alone")
