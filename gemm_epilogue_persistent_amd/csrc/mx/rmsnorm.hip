@@ -73,7 +73,8 @@ __device__ __forceinline__ V row_sum(V v, V* red) {
 // ---- y = h rstd w. A quantised value flips to its neighbour where an error carries y over the
 // border between them, so y is the rounding of the exact product: squares are summed in 64 bits,
 // rstd is held as hi + lo, h w is exact for 16-bit h and w (22 bits) or held as hi + lo too, and a y
-// that falls on a border of the element type is moved to the side of it that the product lies on.
+// that falls on a border of the element type is moved to the side of it that the product lies on
+// before it is quantised (y itself is stored as it is, the nearest fp32 number).
 // (With fp32 sums and two fp32 products 56 of 69 million values flipped, and now none.) h w may leave
 // fp32's range where h rstd w does not: chunks with a y that is not finite and rows of a very large or
 // small rstd are computed again in 64 bits, as are those with a y on a border.
@@ -95,9 +96,11 @@ __device__ __forceinline__ Rstd reciprocal_root(double mean_eps) {
   s.far = !(s.hi >= 0x1p-32f && s.hi <= 0x1p20f);
   return s;
 }
+// Returns which y lie on a border beside their product: bit e, the product has the larger magnitude; bit 8 + e,
+// the smaller.
 template <typename T>
-__device__ __forceinline__ void scale8(const float h[8], const float w[8], const Rstd& r, float y[8]) {
-  uint32_t low = ~0u;
+__device__ __forceinline__ uint32_t scale8(const float h[8], const float w[8], const Rstd& r, float y[8]) {
+  uint32_t low = ~0u, move = 0;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const float hw = h[e] * w[e];
@@ -117,23 +120,24 @@ __device__ __forceinline__ void scale8(const float h[8], const float w[8], const
       const uint32_t b = __float_as_uint(y[e]);
       again |= (b << 13) == 0 && (b << 1) != 0;
     }
-    if (__ballot(again) == 0) return;
+    if (__ballot(again) == 0) return 0;
     float hr[8], wr[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) hr[e] = h[e], wr[e] = w[e];
 #pragma unroll 1
     for (int i = 0; i < 8; ++i) {  // element i is at place 0, and its result goes to place 7
       const double p = (double)hr[0] * (double)wr[0] * r.r;
-      float v = (float)p;
+      const float v = (float)p;
       const double rest = p - (double)v;
       const uint32_t b = __float_as_uint(v);
-      if ((b << 13) == 0 && (b << 1) != 0 && rest != 0 && __builtin_isfinite(rest))
-        v = __uint_as_float((rest > 0) == (v > 0.f) ? b + 1 : b - 1);
+      const bool border = (b << 13) == 0 && (b << 1) != 0 && rest != 0 && __builtin_isfinite(rest);
+      move = (move >> 1) | (border ? ((rest > 0) == (v > 0.f) ? 1u << 7 : 1u << 15) : 0u);
 #pragma unroll
       for (int e = 0; e < 7; ++e) hr[e] = hr[e + 1], wr[e] = wr[e + 1], y[e] = y[e + 1];
       y[7] = v;
     }
   }
+  return move;
 }
 // Sum of squares of a chunk.
 __device__ __forceinline__ double squares(const float v[8]) {
@@ -143,13 +147,17 @@ __device__ __forceinline__ double squares(const float v[8]) {
   return s;
 }
 
-// Output chunk `ch` of a row: y in its type and / or (FMT an mx_format, or kNoMx) quantised.
+// Output chunk `ch` of a row: y in its type and / or (FMT an mx_format, or kNoMx) quantised. move: by scale8.
 constexpr int kNoMx = -1;
 template <typename T, int FMT, bool WHOLE, int STREAM = 0>
 __device__ __forceinline__ void norm_out(const NormParams& p, T* y_row, uint8_t* code_row, uint8_t* scale_row, int ch,
-                                         const float y[8]) {
+                                         float y[8], uint32_t move) {
   if (p.y) store_chunk<WHOLE, STREAM != 0>(y_row, ch * 8, p.cols, pack<T>(y));
   if constexpr (FMT != kNoMx) {
+    if (__builtin_expect(__ballot(move != 0) != 0, 0)) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = __uint_as_float(__float_as_uint(y[e]) + ((move >> e) & 1) - ((move >> (8 + e)) & 1));
+    }
     if (ch < p.nb * 4) mx_store_chunk<FMT>(y, ch, p.nb, p.nsb, code_row, scale_row);
   }
 }
@@ -208,8 +216,8 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void rmsnorm_kernel(const NormPa
     forget(h[j]);
     unpack(h[j], a);
     load8<WHOLE>((const T*)p.w, ch * 8, p.cols, w);
-    scale8<T>(a, w, rstd, y);
-    norm_out<T, FMT, WHOLE, STREAM>(p, y_row, code_row, scale_row, ch, y);
+    const uint32_t move = scale8<T>(a, w, rstd, y);
+    norm_out<T, FMT, WHOLE, STREAM>(p, y_row, code_row, scale_row, ch, y, move);
   }
 }
 
@@ -245,8 +253,8 @@ __global__ __launch_bounds__(1024) void rmsnorm_long_kernel(const NormParams p) 
     // (h may be x or the residual: every element is read again by the thread that replaces it)
     if (r && p.h) store_chunk<false>((T*)p.h + row * p.ldh, ch * 8, p.cols, pack<T>(v));
     load8<false>((const T*)p.w, ch * 8, p.cols, w);
-    scale8<T>(v, w, rstd, y);
-    norm_out<T, FMT, false>(p, (T*)p.y + row * p.ldy, mx_code_row<FMT>(p.codes, row, p.nb), mx_scale_row(p.scales, row, p.nsb), ch, y);
+    const uint32_t move = scale8<T>(v, w, rstd, y);
+    norm_out<T, FMT, false>(p, (T*)p.y + row * p.ldy, mx_code_row<FMT>(p.codes, row, p.nb), mx_scale_row(p.scales, row, p.nsb), ch, y, move);
   }
 }
 

@@ -311,3 +311,29 @@ def test_products_past_the_range(cols, kind):
         check_mx(q, want, EXACT, fmt)
     y = gep.rmsnorm(x.cuda(), w.cuda(), eps=0.0)
     check_close(y, want, U, kind, "y alone")
+
+
+@pytest.mark.parametrize("cols", [300, 5000, 17000])
+def test_fp32_output_on_borders(cols):
+    """Products next to the border between two codes: the fp32 y is the nearest fp32 number to each of them,
+    and the codes are those of the product."""
+    announce(f"rmsnorm fp32 output on borders {cols}")
+    rng = np.random.RandomState(cols)
+    x = torch.from_numpy(rng.randn(1, cols).astype(np.float32))
+    h64 = x.double().numpy()
+    r = 1 / np.sqrt((h64 ** 2).mean())
+    # (numbers of five significant bits: borders of e4m3 and, some, of e2m1)
+    border = rng.randint(16, 32, cols) * np.exp2(rng.randint(-6, 2, cols)) * np.sign(rng.randn(cols))
+    w = (border / (h64[0] * r)).astype(np.float32)
+    want = h64 * r * w.astype(np.float64)
+    near = np.spacing(np.abs(want).astype(np.float32)).astype(np.float64) / 2 + EXACT * np.abs(want)
+    assert (want.astype(np.float32) == border).sum() > cols // 4 and (want != border).all()
+    xd, wd = x.cuda(), torch.from_numpy(w).cuda()
+    for fmt in ("e4m3", "e2m1", None):
+        q = gep.mx_empty(1, cols, fmt) if fmt else None
+        y = torch.empty_like(xd)
+        gep.rmsnorm(xd, wd, eps=0.0, y=y, q=q)
+        err = np.abs(y.double().cpu().numpy() - want)
+        assert (err <= near).all(), f"{fmt}: {(err > near).sum()} of {cols} are not the nearest"
+        if fmt:
+            check_mx(q, want, EXACT, fmt)
