@@ -557,7 +557,8 @@ gemm_status rmsnorm_forward(const rmsnorm_args* a, void* stream) {
   if (!a) return fail(GEMM_ERR_INVALID_ARG, "%s: NULL args", fn);
   CHECK(check_sizes(fn, a->rows, a->cols, a->type));
   if (!(a->eps >= 0.f)) return fail(GEMM_ERR_INVALID_ARG, "%s: eps must be >= 0", fn);
-  if (!a->y && !a->q_codes) return fail(GEMM_ERR_INVALID_ARG, "%s: neither y nor q_codes given", fn);
+  // (the address of an empty matrix is NULL)
+  if (a->rows > 0 && !a->y && !a->q_codes) return fail(GEMM_ERR_INVALID_ARG, "%s: neither y nor q_codes given", fn);
   if ((a->q_codes != nullptr) != (a->q_scales != nullptr)) return fail(GEMM_ERR_INVALID_ARG, "%s: q_codes and q_scales come together", fn);
   if (a->h_out && !a->residual) return fail(GEMM_ERR_INVALID_ARG, "%s: h_out without a residual (h is x)", fn);
   if (a->q_codes && a->q_format != MX_E2M1 && a->q_format != MX_E4M3) return fail(GEMM_ERR_INVALID_ARG, "%s: unknown format %d", fn, a->q_format);

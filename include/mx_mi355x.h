@@ -64,7 +64,8 @@ gemm_status mx_dequantize(int32_t rows, int32_t k, int32_t format, const void* c
  * x, residual, h, y and weight share `type` (F16, BF16, F32); each matrix has its own leading
  * dimension. h_out may be NULL (required NULL without a residual: h is x) and may be x or
  * residual itself; y may not overlap x, residual or h. rstd (fp32[rows]) may be NULL. At least
- * one of y and q_codes is given; q_codes and q_scales come together. 1 <= cols <= 2^24, rows <= 2^30. */
+ * one of y and q_codes is given unless rows = 0, which launches nothing; q_codes and q_scales come
+ * together. 1 <= cols <= 2^24, rows <= 2^30. */
 typedef struct {
   int32_t rows, cols;
   int32_t type;     /* gemm_dtype */

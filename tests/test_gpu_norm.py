@@ -337,3 +337,15 @@ def test_fp32_output_on_borders(cols):
         assert (err <= near).all(), f"{fmt}: {(err > near).sum()} of {cols} are not the nearest"
         if fmt:
             check_mx(q, want, EXACT, fmt)
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+def test_no_rows(kind):
+    """A matrix without rows gives one, with any of the outputs."""
+    announce(f"rmsnorm without rows {kind}")
+    x, w = torch.empty(0, 64, dtype=TYPES[kind], device="cuda"), torch.ones(64, dtype=TYPES[kind], device="cuda")
+    assert gep.rmsnorm(x, w).shape == (0, 64)
+    q = gep.mx_empty(0, 64, "e4m3")
+    assert gep.rmsnorm(x, w, q=q) is q
+    y, h, rstd = torch.empty_like(x), torch.empty_like(x), torch.empty(0, device="cuda")
+    assert gep.rmsnorm(x, w, residual=x, h=h, y=y, q=q, rstd=rstd) is y

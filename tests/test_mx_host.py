@@ -304,3 +304,15 @@ def test_plan_choice_is_that_of_the_device_asked_for(lib):
         for cus, want in zip(counts, fresh):
             assert ask(h, cus) == want and ask(h, cus) == want
     lib.mx_gemm_destroy(h)
+
+
+def test_norm_without_rows(lib):
+    """No rows: every matrix may be NULL, as the address of an empty one is; sizes, type, eps and format are
+    looked at all the same."""
+    a = _abi.RmsnormArgs(rows=0, cols=64, type=2, eps=1e-5, ldx=64, ldy=64)
+    assert lib.rmsnorm_forward(ctypes.byref(a), None) == _abi.OK
+    for kw in (dict(cols=0), dict(type=4), dict(eps=-1.0)):
+        b = _abi.RmsnormArgs.from_buffer_copy(a)
+        for k, v in kw.items():
+            setattr(b, k, v)
+        assert lib.rmsnorm_forward(ctypes.byref(b), None) == _abi.INVALID_ARG
