@@ -206,9 +206,10 @@ class MxPlan:
     bytes; at least one of D, PostAct. tile, split: "auto" and 0, or the kernel to use ("256", "128",
     "32x64", "32", "16x32", "16") and over how many workgroups it shares out a tile's K.
 
-    Where K is shared out, the plan keeps the workspace for the partial sums: runs of one plan on
-    several streams that may overlap need a workspace each (a uint8 tensor of
-    plan.workspace_bytes), and the plan has to outlive a graph that captured its run."""
+    Where K is shared out, a run needs a workspace for the partial sums: workspace_bytes of memory that is
+    the run's stream's own. The plan keeps one for each stream that it has run on (allocated by the first
+    run there, and freed with the plan); a run that is captured into a graph takes one from the graph's
+    memory."""
 
     def __init__(self, a, b, C=None, D=None, PostAct=None, act="none", cu_seqlens_m=None, tile="auto",
                  split=0):
@@ -248,8 +249,7 @@ class MxPlan:
         n = ctypes.c_int64()
         _abi.check(self._lib.mx_gemm_workspace(h, self._cus(), ctypes.byref(n)))
         self.workspace_bytes = n.value
-        self._workspace = torch.empty(n.value, dtype=torch.uint8, device=a.device) if n.value else None
-        self._streams = {_raw_stream(a.device.index)}  # those the workspace is known to be used on
+        self._workspaces, self._workspace = {}, None  # by stream pointer; that of the run before
 
     def __del__(self):
         h = getattr(self, "handle", None)
@@ -274,13 +274,13 @@ class MxPlan:
 
     def run(self, a, b, C=None, D=None, PostAct=None, cu_seqlens_m=None, stream=None, workspace=None):
         """Enqueue on `stream` (default: torch's current stream of the operands' device). The
-        tensors are laid out as those the plan was made for. workspace: instead of the plan's own."""
+        tensors are laid out as those the plan was made for. workspace: instead of the plan's own, a
+        uint8 tensor of plan.workspace_bytes that nothing else uses meanwhile."""
         if self._signature(a, b, C, D, PostAct, cu_seqlens_m) != self._sig:
             raise ValueError("the operands are not laid out as those this plan was made for")
         if workspace is None:
-            workspace = self._workspace
-            if workspace is not None:
-                self._hold(stream)
+            if self.workspace_bytes:
+                workspace = self._stream_workspace(stream)
         elif workspace.device != self.device or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
             raise ValueError("workspace: contiguous uint8 tensor on the operands' GPU expected")
         args = _abi.MX_GEMM_ARGS.pack(a.codes.data_ptr(), a.scales.data_ptr(), b.codes.data_ptr(), b.scales.data_ptr(),
@@ -288,12 +288,22 @@ class MxPlan:
                                       0 if workspace is None else workspace.numel())
         _launch(self.device, stream, self._lib.mx_gemm_run, self.handle, args)
 
-    def _hold(self, stream):
-        """The allocator is told of another stream that the workspace is used on, once."""
-        raw = _raw_stream(self.device.index) if stream is None else stream.cuda_stream
-        if raw not in self._streams:
-            self._workspace.record_stream(torch.cuda.current_stream(self.device) if stream is None else stream)
-            self._streams.add(raw)
+    def _stream_workspace(self, stream):
+        """The workspace of a run on `stream`. It is allocated on that very stream: a block that the
+        allocator hands out on another one may still be in use by what was enqueued there before."""
+        if self.device.index != _current_device():
+            with torch.cuda.device(self.device):
+                return self._stream_workspace(stream)
+        with _allocating(stream):
+            if torch.cuda.is_current_stream_capturing():  # (not kept: a later graph may outlive this one)
+                return torch.empty(self.workspace_bytes, dtype=torch.uint8, device=self.device)
+            raw = _raw_stream(self.device.index)
+            workspace = self._workspaces.get(raw)
+            if workspace is None:
+                workspace = torch.empty(self.workspace_bytes, dtype=torch.uint8, device=self.device)
+                self._workspaces[raw] = workspace
+        self._workspace = workspace
+        return workspace
 
     def tile(self, num_cus=None):
         """(kernel, split) this plan runs with on a device with num_cus compute units."""
@@ -306,7 +316,7 @@ def mx_gemm(a, b, D=None, C=None, PostAct=None, act="none", cu_seqlens_m=None, s
             split=0):
     """One-shot product: plan and enqueue. Without D and PostAct, D is allocated in bf16. Returns
     D, or PostAct without D."""
-    with _allocating(stream):  # (the plan's workspace too)
+    with _allocating(stream):
         if D is None and PostAct is None:
             D = torch.empty((a.rows, b.rows), dtype=torch.bfloat16, device=a.device)
         plan = MxPlan(a, b, C, D, PostAct, act, cu_seqlens_m, tile, split)

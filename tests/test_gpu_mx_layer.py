@@ -223,3 +223,62 @@ def test_norm_output_refusals():
     for kw in (dict(y=x), dict(residual=r, y=r), dict(residual=r, h=h, y=h)):
         with pytest.raises(gep.GemmError):
             gep.rmsnorm(x, w, **kw)
+
+
+def test_plan_workspace_of_a_busy_stream():
+    """A plan made on a stream that still writes into a block freed there runs on another stream: its
+    partial sums lie elsewhere."""
+    announce("workspace beside a busy stream")
+    a = gep.mx_quantize(torch.randn(40, 4096, device="cuda"), "e4m3")
+    b = gep.mx_quantize(torch.randn(64, 4096, device="cuda"), "e4m3")
+    D, E = torch.empty(40, 64, device="cuda"), torch.empty(40, 64, device="cuda")
+    nbytes = 8 * 40 * 64 * 4
+    gep.MxPlan(a, b, None, D, tile="32", split=8).run(a, b, None, D)
+    s = torch.cuda.Stream()
+    block = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    torch.cuda._sleep(int(2e7))
+    block.fill_(255)
+    del block
+    plan = gep.MxPlan(a, b, None, D, tile="32", split=8)
+    assert plan.workspace_bytes == nbytes
+    for _ in range(50):
+        plan.run(a, b, None, E, stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(D, E)
+
+
+def test_plan_workspaces_overlap():
+    """Runs of one plan on two streams at once, and two graphs of it replayed at once, after the plan is gone."""
+    announce("one plan on two streams and in two graphs")
+    a = [gep.mx_quantize(torch.randn(40, 4096, device="cuda"), "e4m3") for _ in range(2)]
+    b = gep.mx_quantize(torch.randn(64, 4096, device="cuda"), "e4m3")
+    want, got = [torch.empty(40, 64, device="cuda") for _ in range(2)], [torch.empty(40, 64, device="cuda") for _ in range(2)]
+    plan = gep.MxPlan(a[0], b, None, want[0], tile="32", split=8)
+    for i in range(2):
+        plan.run(a[i], b, None, want[i])
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(50):
+        for i in range(2):
+            plan.run(a[i], b, None, got[i], stream=streams[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert torch.equal(got[i], want[i])
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for i in range(2):
+        with torch.cuda.graph(graphs[i]):
+            for _ in range(20):
+                plan.run(a[i], b, None, got[i])
+    del plan
+    for _ in range(3):
+        for t in got:
+            t.fill_(-1)
+        torch.cuda.synchronize()
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                graphs[i].replay()
+        torch.cuda.synchronize()
+        torch.full((1 << 20,), 255, dtype=torch.uint8, device="cuda")
+        for i in range(2):
+            assert torch.equal(got[i], want[i])

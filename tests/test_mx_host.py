@@ -316,3 +316,73 @@ def test_norm_without_rows(lib):
         for k, v in kw.items():
             setattr(b, k, v)
         assert lib.rmsnorm_forward(ctypes.byref(b), None) == _abi.INVALID_ARG
+
+
+class OnGpu(torch.Tensor):
+    """A CPU tensor that passes the checks for one on the GPU."""
+    is_cuda = True
+
+
+def test_workspace_is_the_streams_own(lib, monkeypatch):
+    """A plan's workspace comes from the allocator under the stream that the run goes to, whichever was
+    current when the plan was made: one for each stream, and one a run in a capture."""
+    import contextlib
+    from gemm_epilogue_persistent_amd import mx
+    current, capturing, made, used = ["first"], [False], {}, []
+    pointer = {"first": 11, "second": 12, "third": 13}
+
+    class Stream:
+        def __init__(self, name):
+            self.name, self.cuda_stream = name, pointer[name]
+
+    @contextlib.contextmanager
+    def under(stream):
+        before, current[0] = current[0], stream.name
+        yield
+        current[0] = before
+
+    def launch(device, stream, function, plan, args):
+        used.append((current[0] if stream is None else stream.name, _abi.MX_GEMM_ARGS.unpack(args)[8]))
+
+    empty = torch.empty
+
+    def allocate(*args, **kw):
+        t = empty(*args, **kw)
+        made.setdefault(t.data_ptr(), []).append((current[0], t))  # (kept: no address comes twice)
+        return t
+
+    monkeypatch.setattr(torch.cuda, "stream", under)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device: None)
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda self, stream: None)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing[0])
+    monkeypatch.setattr(mx, "_current_device", lambda: None)
+    monkeypatch.setattr(mx, "_raw_stream", lambda index: pointer[current[0]])
+    monkeypatch.setattr(mx, "_launch", launch)
+    monkeypatch.setattr(gep.MxPlan, "_cus", lambda self: 256)
+
+    def operand(rows):
+        q = gep.mx_empty(rows, 4096, "e4m3", device="cpu")
+        return gep.MxTensor(q.codes.as_subclass(OnGpu), q.scales, "e4m3", 4096)
+
+    a, b, D = operand(40), operand(64), torch.zeros(40, 64).as_subclass(OnGpu)
+    plan = gep.MxPlan(a, b, None, D, tile="32", split=4)
+    assert plan.workspace_bytes == 4 * 40 * 64 * 4
+    monkeypatch.setattr(torch, "empty", allocate)
+    plan.run(a, b, None, D, stream=Stream("second"))
+    plan.run(a, b, None, D)
+    current[0] = "third"
+    plan.run(a, b, None, D)
+    plan.run(a, b, None, D, stream=Stream("first"))
+    plan.run(a, b, None, D, stream=Stream("second"))
+    kept = [p for _, p in used]
+    for stream, p in used:
+        assert [s for s, t in made.get(p, [])] == [stream] and made[p][0][1].numel() == plan.workspace_bytes
+    assert [s for s, _ in used] == ["second", "first", "third", "first", "second"]
+    assert kept[3] == kept[1] and kept[4] == kept[0] and len(set(kept)) == 3
+    capturing[0] = True
+    plan.run(a, b, None, D)
+    plan.run(a, b, None, D)
+    capturing[0] = False
+    plan.run(a, b, None, D)
+    captured = [p for _, p in used[5:7]]
+    assert len({*captured, *kept}) == 5 and used[7] == ("third", kept[2])
