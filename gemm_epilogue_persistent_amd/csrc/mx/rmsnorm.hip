@@ -600,7 +600,7 @@ gemm_status rmsnorm_forward(const rmsnorm_args* a, void* stream) {
 }
 
 int64_t rmsnorm_backward_workspace(int32_t rows, int32_t cols) {
-  if (rows < 0 || cols < 0) return -1;
+  if (rows < 0 || cols < 0 || rows > kMaxExtent || cols > kMaxCols) return -1;
   return (int64_t)grad_parts(rows, cols, 16) * cols * 4;
 }
 

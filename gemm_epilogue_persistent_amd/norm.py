@@ -59,7 +59,7 @@ def rmsnorm_backward_workspace(rows, cols):
     """Bytes of device memory that rmsnorm_backward takes as its workspace."""
     n = _abi.load().rmsnorm_backward_workspace(int(rows), int(cols))
     if n < 0:
-        raise ValueError("negative size")
+        raise ValueError("negative size, or more than 2^30 rows or 2^24 columns")
     return n
 
 

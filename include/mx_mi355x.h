@@ -105,7 +105,7 @@ typedef struct {
   int64_t lddy, ldh, lddres, lddx;
 } rmsnorm_backward_args;
 gemm_status rmsnorm_backward(const rmsnorm_backward_args* args, void* stream);
-/* Bytes of workspace (-1 for a negative size). */
+/* Bytes of workspace (-1 for a negative size, or one that rmsnorm_backward refuses as too large). */
 int64_t rmsnorm_backward_workspace(int32_t rows, int32_t cols);
 
 /* Product of MX operands with a fused epilogue, fp32 accumulation:

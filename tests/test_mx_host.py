@@ -386,3 +386,15 @@ def test_workspace_is_the_streams_own(lib, monkeypatch):
     plan.run(a, b, None, D)
     captured = [p for _, p in used[5:7]]
     assert len({*captured, *kept}) == 5 and used[7] == ("third", kept[2])
+
+
+@pytest.mark.parametrize("rows,cols,ok", [
+    (1 << 30, 1 << 24, True), ((1 << 30) + 1, 64, False), (1, (1 << 24) + 1, False), (1, 2 ** 31 - 1, False),
+    (2 ** 31 - 1, 2 ** 31 - 1, False), (0, 2 ** 31 - 1, False), (5, 0, True)])
+def test_backward_workspace_limits(lib, rows, cols, ok):
+    """The sizes that rmsnorm_backward refuses have no workspace."""
+    assert (lib.rmsnorm_backward_workspace(rows, cols) >= 0) == ok
+    if not ok:
+        assert lib.rmsnorm_backward_workspace(rows, cols) == -1
+        with pytest.raises(ValueError):
+            gep.rmsnorm_backward_workspace(rows, cols)
