@@ -20,6 +20,7 @@ int out_bytes(int32_t dt) {
   }
 }
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t blocks_of(int64_t a, int64_t b) { return a / b + (a % b != 0); }  // (cdiv of any size)
 
 gemm_status check_out(const char* name, int32_t dt, int64_t ld, int32_t M, int32_t N) {
   if (dt == GEMM_DT_NONE) return GEMM_OK;
@@ -155,13 +156,21 @@ extern "C" {
 
 int64_t mx_code_bytes(int64_t rows, int64_t k, int32_t format) {
   if (rows < 0 || k < 0 || (format != MX_E2M1 && format != MX_E4M3)) return -1;
-  return rows * ((k + MX_BLOCK - 1) / MX_BLOCK) * (format == MX_E2M1 ? 16 : 32);
+  if (rows == 0) return 0;
+  int64_t row, all;
+  if (__builtin_mul_overflow(blocks_of(k, MX_BLOCK), (int64_t)(format == MX_E2M1 ? 16 : 32), &row) ||
+      __builtin_mul_overflow(rows, row, &all))
+    return -1;
+  return all;
 }
 
 int64_t mx_scale_bytes(int64_t rows, int64_t k) {
   if (rows < 0 || k < 0) return -1;
-  const int64_t nb = (k + MX_BLOCK - 1) / MX_BLOCK;
-  return cdiv(rows, 64) * cdiv(nb, 16) * 64 * 16;
+  int64_t tiles, all;
+  if (__builtin_mul_overflow(blocks_of(rows, 64), blocks_of(blocks_of(k, MX_BLOCK), 16), &tiles) ||
+      __builtin_mul_overflow(tiles, (int64_t)(64 * 16), &all))
+    return -1;
+  return all;
 }
 
 gemm_status mx_gemm_create(const mx_gemm_desc* d, mx_gemm_plan** out) {

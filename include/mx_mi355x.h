@@ -33,7 +33,7 @@ extern "C" {
 typedef enum { MX_E2M1 = 0, MX_E4M3 = 1 } mx_format;
 
 /* Bytes of the codes and of the scales of a (rows, k) MX matrix (0 for an empty one, -1 for a
- * negative size or an unknown format). */
+ * negative size, an unknown format or a number past 63 bits). */
 int64_t mx_code_bytes(int64_t rows, int64_t k, int32_t format);
 int64_t mx_scale_bytes(int64_t rows, int64_t k);
 

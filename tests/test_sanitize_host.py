@@ -41,3 +41,13 @@ def test_plan_builder_under_asan_ubsan(tmp_path):
     out = _build_and_run(tmp_path, "g++", [os.path.join(ROOT, "gemm_epilogue_persistent_amd", "csrc", "plan.cpp"),
                                            os.path.join(HERE, "plan_fuzz.cpp")], ["-std=c++17"], "plan_fuzz")
     assert "plans accepted" in out
+
+
+@pytest.mark.skipif(shutil.which("g++") is None, reason="g++ not available")
+def test_mx_plan_under_asan_ubsan(tmp_path):
+    """The MX product's plans and the storage sizes (csrc/mx/mx_plan.cpp), by a seeded fuzz of 100000 descriptors
+    and of sizes up to the largest; plan.cpp holds the error messages."""
+    csrc = os.path.join(ROOT, "gemm_epilogue_persistent_amd", "csrc")
+    out = _build_and_run(tmp_path, "g++", [os.path.join(csrc, "mx", "mx_plan.cpp"), os.path.join(csrc, "plan.cpp"),
+                                           os.path.join(HERE, "mx_plan_fuzz.cpp")], ["-std=c++17"], "mx_plan_fuzz")
+    assert "mx plans accepted" in out
