@@ -72,6 +72,14 @@ RMSNORM_ARGS = struct.Struct("@4if8P4q")
 RMSNORM_BACKWARD_ARGS = struct.Struct("@3i8P5q")
 
 
+def int32(name, value):
+    """value as an int32 field takes it (ctypes would cut it to 32 bits without a word)."""
+    value = int(value)
+    if not -(1 << 31) <= value < 1 << 31:
+        raise ValueError(f"{name} = {value} does not fit 32 bits")
+    return value
+
+
 class GemmError(RuntimeError):
     def __init__(self, status, message):
         super().__init__(f"{message} (status {status})")

@@ -21,6 +21,7 @@ from . import _abi
 from ._abi import ACT, DT, MX_FORMAT, MX_TILE
 
 BLOCK = 32
+_MOST = (1 << 31) - 1  # sizes of the C ABI are int32
 _FLOAT_DT = {torch.float16: DT["f16"], torch.bfloat16: DT["bf16"], torch.float32: DT["f32"]}
 _FLOAT_BYTES = {torch.float16: 2, torch.bfloat16: 2, torch.float32: 4}
 
@@ -66,6 +67,8 @@ def _matrix(name, t, dtypes, shape=None, device=None):
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     rows, cols = have
+    if rows > _MOST or cols > _MOST:
+        raise ValueError(f"{name}: more than 2^31 - 1 rows or columns")
     if rows == 0 or cols == 0:
         return cols
     ld, step = t.stride()
@@ -234,13 +237,14 @@ class MxPlan:
         if tile not in MX_TILE:
             raise ValueError(f"unknown tile {tile!r}")
         d = _abi.MxGemmDesc()
-        d.M, d.N, d.K, d.groups = a.rows, b.rows, a.k, b.groups or 0
+        d.M, d.N, d.K, d.groups = (_abi.int32(n, v) for n, v in (
+            ("rows of a", a.rows), ("rows of b", b.rows), ("k", a.k), ("groups", b.groups or 0)))
         d.a_format, d.b_format = MX_FORMAT[a.fmt], MX_FORMAT[b.fmt]
         shape = (a.rows, b.rows)
         d.c, d.ldc = _out("C", C, shape, a.device)
         d.d, d.ldd = _out("D", D, shape, a.device)
         d.post, d.ldp = _out("PostAct", PostAct, shape, a.device)
-        d.act, d.tile, d.split = ACT[act], MX_TILE[tile], int(split)
+        d.act, d.tile, d.split = ACT[act], MX_TILE[tile], _abi.int32("split", split)
         self.desc, self.device = d, a.device
         self._lib = _abi.load()
         h = ctypes.c_void_p()
@@ -308,7 +312,7 @@ class MxPlan:
     def tile(self, num_cus=None):
         """(kernel, split) this plan runs with on a device with num_cus compute units."""
         t, n = ctypes.c_int32(), ctypes.c_int32()
-        _abi.check(self._lib.mx_gemm_plan_tile(self.handle, int(num_cus or self._cus()), ctypes.byref(t), ctypes.byref(n)))
+        _abi.check(self._lib.mx_gemm_plan_tile(self.handle, _abi.int32("num_cus", num_cus or self._cus()), ctypes.byref(t), ctypes.byref(n)))
         return next(k for k, v in MX_TILE.items() if v == t.value), n.value
 
 

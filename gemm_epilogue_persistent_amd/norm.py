@@ -57,7 +57,7 @@ def rmsnorm(x, weight, residual=None, eps=1e-5, h=None, y=None, q=None, rstd=Non
 
 def rmsnorm_backward_workspace(rows, cols):
     """Bytes of device memory that rmsnorm_backward takes as its workspace."""
-    n = _abi.load().rmsnorm_backward_workspace(int(rows), int(cols))
+    n = _abi.load().rmsnorm_backward_workspace(_abi.int32("rows", rows), _abi.int32("cols", cols))
     if n < 0:
         raise ValueError("negative size, or more than 2^30 rows or 2^24 columns")
     return n

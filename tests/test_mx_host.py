@@ -398,3 +398,39 @@ def test_backward_workspace_limits(lib, rows, cols, ok):
         assert lib.rmsnorm_backward_workspace(rows, cols) == -1
         with pytest.raises(ValueError):
             gep.rmsnorm_backward_workspace(rows, cols)
+
+
+def test_sizes_past_32_bits(lib, monkeypatch):
+    """Sizes and counts that do not fit the C ABI's 32-bit fields are refused: cut to 32 bits, 2^32 rows would be
+    none, and the call would return without having written anything."""
+    from gemm_epilogue_persistent_amd import mx, norm
+    launch = lambda device, stream, function, *args: _abi.check(function(*args, None))  # noqa: E731
+    monkeypatch.setattr(mx, "_launch", launch)
+    monkeypatch.setattr(norm, "_launch", launch)
+    monkeypatch.setattr(gep.MxPlan, "_cus", lambda self: 256)
+    big = 1 << 32
+
+    def matrix(*shape, dtype=torch.float16):
+        return torch.empty(shape, dtype=dtype, device="meta").as_subclass(OnGpu)
+
+    def operand(rows, k, groups=None):
+        q = gep.mx_empty(rows, k, "e4m3", groups=groups, device="meta")
+        return gep.MxTensor(q.codes.as_subclass(OnGpu), q.scales, "e4m3", k)
+
+    for shape in ((big, 32), (32, big), (big + 1, 1), (1, big)):
+        q = operand(*shape)
+        for call in (lambda: gep.mx_quantize(matrix(*shape), "e4m3", out=q),
+                     lambda: gep.mx_quantize(matrix(*shape[::-1]), "e4m3", out=q, transpose=True),
+                     lambda: gep.mx_dequantize(q, out=matrix(*shape)),
+                     lambda: gep.rmsnorm(matrix(*shape), matrix(shape[1]).reshape(-1), y=matrix(*shape)),
+                     lambda: gep.rmsnorm_backward_workspace(*shape)):
+            with pytest.raises(ValueError):
+                call()
+    small = operand(16, 64)
+    for call in (lambda: gep.MxPlan(operand(big, 64), small, None, matrix(big, 16)),
+                 lambda: gep.MxPlan(small, operand(big, 64), None, matrix(16, big)),
+                 lambda: gep.MxPlan(operand(16, big), operand(16, big), None, matrix(16, 16)),
+                 lambda: gep.MxPlan(small, small, None, matrix(16, 16), split=big),
+                 lambda: gep.MxPlan(small, small, None, matrix(16, 16)).tile(big + 256)):
+        with pytest.raises(ValueError):
+            call()
