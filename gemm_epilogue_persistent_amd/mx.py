@@ -201,6 +201,12 @@ def _out(name, t, shape, device):
     return _FLOAT_DT[t.dtype], ld
 
 
+def _operands(a, b):
+    for name, q in (("a", a), ("b", b)):
+        if not isinstance(q, MxTensor):
+            raise TypeError(f"{name}: an MxTensor expected")
+
+
 class MxPlan:
     """A validated plan of D = a b^T + C and PostAct = act(a b^T + C) for one problem shape (host
     memory; reusable, from several streams too). a (m, k); b (n, k), or (G, n, k) with
@@ -217,10 +223,9 @@ class MxPlan:
     def __init__(self, a, b, C=None, D=None, PostAct=None, act="none", cu_seqlens_m=None, tile="auto",
                  split=0):
         self.handle = None
-        self._sig = self._signature(a, b, C, D, PostAct, cu_seqlens_m)
+        _operands(a, b)
         _plain_mx("a", a)
-        if not isinstance(b, MxTensor):
-            raise TypeError("b: an MxTensor expected")
+        self._sig = self._signature(a, b, C, D, PostAct, cu_seqlens_m)
         if b.device != a.device or not a.codes.is_cuda:
             raise ValueError("a and b must be on one GPU")
         if a.k != b.k:
@@ -320,6 +325,7 @@ def mx_gemm(a, b, D=None, C=None, PostAct=None, act="none", cu_seqlens_m=None, s
             split=0):
     """One-shot product: plan and enqueue. Without D and PostAct, D is allocated in bf16. Returns
     D, or PostAct without D."""
+    _operands(a, b)
     with _allocating(stream):
         if D is None and PostAct is None:
             D = torch.empty((a.rows, b.rows), dtype=torch.bfloat16, device=a.device)

@@ -434,3 +434,17 @@ def test_sizes_past_32_bits(lib, monkeypatch):
                  lambda: gep.MxPlan(small, small, None, matrix(16, 16)).tile(big + 256)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_plain_tensors_are_no_mx_operands():
+    """A tensor in the place of an MX operand is a TypeError that names it."""
+    q, x = gep.mx_empty(4, 32, "e4m3", device="cpu"), torch.zeros(4, 32)
+    for call in (gep.MxPlan, gep.mx_gemm):
+        with pytest.raises(TypeError, match="a: an MxTensor expected"):
+            call(x, q, D=x)
+        with pytest.raises(TypeError, match="b: an MxTensor expected"):
+            call(q, x, D=x)
+    with pytest.raises(TypeError, match="b: an MxTensor expected"):
+        gep.mx_gemm(q, x)
+    with pytest.raises(TypeError, match="a: an MxTensor expected"):
+        gep.mx_gemm(None, q)
