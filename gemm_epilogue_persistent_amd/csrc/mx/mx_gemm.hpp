@@ -14,12 +14,13 @@
 //            through LDS (global -> LDS transfers, two to four stages), persistent tile loop.
 //   MxDirect few rows. 16x16 to 32x64 outputs per workgroup, whose waves share out K and read
 //            their fragments from global memory themselves; one join in LDS at the end.
-// MxRing 8192^3 e2m1 x e2m1: 245 us, 4.49 PFLOP/s; the matrix pipes are busy 61% of the cycles, and the
-// chip holds 1.75 GHz of its 2.4 under that load (power). 16768 x 4096 x 4096 e4m3 x e2m1 over 8 experts: 237
-// to 241 us, 2.35 PFLOP/s, 60% busy at 2.0 GHz; a library product of e4m3 8192^3 reaches 2.66 here.
-// MxDirect 1 x 8192 x 8192 e4m3 x e2m1: 7.8 us for 35.7 MB, of which 2.5 are the launch. 256x128 tiles
-// were measured and are not kept: 4096 x 2048 x 4096 e4m3 34 us as with 128x128, one round either way,
-// 2048 x 2048 x 4096 28 us and 22.
+// MxRing 8192^3 e2m1 x e2m1: 246 us, 4.47 PFLOP/s (in short bursts 233, in long runs 254); the matrix pipes
+// are busy 62% of the cycles, and the chip holds 1.79 GHz of its 2.4 under that load. LDS is busy 37% of the
+// cycles; 18% of those are conflicts of the scale bytes' reads (see Lane). 16768 x 4096 x 4096 e4m3 x e2m1 over
+// 8 experts: 237 to 241 us, 2.35 PFLOP/s, 59% busy at 2.04 GHz; a library product of e4m3 8192^3 reaches 2.66.
+// MxDirect 1 x 8192 x 8192 e4m3 x e2m1: 8.0 us in a graph, 8.4 between other kernels, for 35.7 MB, of which 2.5
+// us are the launch. 256x128 tiles were measured and are not kept: as fast as 128x128 at 4096 x 2048 x 4096 e4m3,
+// one round either way, and 28 us for 22 at 2048 x 2048 x 4096.
 #pragma once
 #include "../gemm_kernel.hpp"
 #include "mx_common.hpp"
@@ -213,9 +214,9 @@ __host__ __device__ __forceinline__ int mx_epilogue_kind(const MxParams& mp) {
 // next step.
 //
 // EPI: the epilogues of the kernel, all kinds (0), kind 1 (1) or the others (2). Kind 1 has a kernel of
-// its own where the larger code costs it something: in 128x128 tiles (4096 x 2048 x 4096 e4m3 36.9 us
-// instead of 35.6) and in 256x256 tiles of two E2M1 operands (8192^3 230.4 and 227.8), but not in
-// those with an E4M3 operand (16384 x 4096 x 4096 192.8 in one kernel, 194.3 in two).
+// its own where the larger code costs it something: in 128x128 tiles (4096 x 2048 x 4096 e4m3, 4%) and in
+// 256x256 tiles of two E2M1 operands (8192^3, 1%), but not in those with an E4M3 operand (16384 x 4096 x
+// 4096, 1% faster in one kernel than in two).
 template <int BM, int BN, int NW, int NS, int FA, int FB, bool VM, int EPI>
 struct MxRing {
   static constexpr int kThreads = NW * 64;
@@ -241,7 +242,7 @@ struct MxRing {
   static constexpr int kAhead = (NS - 2) * kPer;  // transfers that may be outstanding at a barrier
   static constexpr int kN = kMI * kNI, kLastP = kN - kNI;
   // (What the registers hold next to the accumulators. With two stages an earlier barrier leaves the
-  // transfers less time: E4M3 x E4M3, 128x128 tiles, 8192^3: 521 us instead of 490.)
+  // transfers less time: E4M3 x E4M3, 128x128 tiles, 8192^3, 6% slower.)
   static constexpr int kRA = kDeep || (BM == 128 && NS > 2) ? 4 : 2;
   static constexpr bool kDB = FB == MX_E2M1 || (BM == 128 && NS > 2);
   // The barrier's position: past the last read of the step's own fragments, and past the head's
@@ -342,7 +343,9 @@ struct MxRing {
     __builtin_amdgcn_sched_barrier(0);
   }
 
-  // Lane offsets of the fragments in a stage, and of the scale bytes from kSOff on.
+  // Lane offsets of the fragments in a stage, and of the scale bytes from kSOff on. (The keys are the
+  // fragments'. A scale is a byte or two of a row of 16 bytes, so 16 rows of a read meet in pairs in 32
+  // banks: two conflict cycles a read, 18 to 20% of the LDS cycles.)
   struct Lane {
     int a, b, sa, sb;
   };
@@ -536,8 +539,8 @@ struct MxRing {
   // last), through 4 KB a wave of the last stage. One 16-bit output without C: the values are final in the
   // accumulators, so they are converted there and pass through LDS as 16-bit rows (32 rows a
   // pass); a 16-bit C is then loaded four or eight rows a lane ahead, the first of them before the next
-  // tile's transfers (16384 x 4096 x 4096 e4m3 x e2m1 with C 217 us, each row's load waited for in its
-  // turn 237, without C 193; 8192 x 8192 x 2048 e2m1 with C 99 and 124). Either way a lane then holds 8
+  // tile's transfers (16384 x 4096 x 4096 e4m3 x e2m1 with C 218 us, each row's load waited for in its
+  // turn 237, without C 196; 8192 x 8192 x 2048 e2m1 with C 102 and 124, without 81). Either way a lane then holds 8
   // consecutive columns, and C, D and PostAct are accessed 16 bytes or more at a time, 128 bytes a
   // row. Chunks are XOR-swizzled by the row as in gemm_kernel.hpp's 16x16 epilogues.
   static constexpr int kRegion = 4096;
@@ -1008,7 +1011,7 @@ constexpr int mx_stages() {
 }
 // 128x128 tiles run two workgroups a compute unit, or with no more workgroups than compute units
 // one with all of LDS: 512 x 4096 x 16384 (128 tiles) e4m3 x e4m3 56 us with four stages, 78 with
-// two; 8192^3 (many tiles) 564 and 490.
+// two; 8192^3 (many tiles) 15% slower with one workgroup than with two, 475 us.
 template <int BM, int NW, int WG, int FA, int FB, bool VM, int EPI>
 __global__ __launch_bounds__(NW * 64, WG) void mx_ring_kernel(const MxParams p) {
   MxRing<BM, BM, NW, mx_stages<BM, FA, FB, WG>(), FA, FB, VM, EPI>::run(p);
@@ -1020,8 +1023,8 @@ void mx_launch_ring(const MxParams& p, dim3 grid, hipStream_t s) {
   else mx_ring_kernel<BM, NW, WG, FA, FB, VM, 2><<<grid, NW * 64, 0, s>>>(p);
 }
 // Direct kernels: fragments two steps ahead. (Four steps, or twice the waves, are slower everywhere:
-// 1 x 8192 x 8192 e4m3 x e2m1 in 16x32 tiles 7.8 us, with four steps 8.6, with 16 waves 8.9; in 16x16
-// tiles 8.7 on four waves, 9.4 on eight, 11.2 on 16.)
+// 1 x 8192 x 8192 e4m3 x e2m1 in 16x32 tiles 8.0 us, four steps or 16 waves 10% more; in 16x16 tiles 9.0 on
+// four waves, on eight 8% more, on 16 29%.)
 template <int MB, int NB, int NW, int D, int FA, int FB, bool VM>
 __global__ __launch_bounds__(NW * 64) void mx_direct_kernel(const MxParams p) {
   MxDirect<MB, NB, NW, D, FA, FB, VM>::run(p);

@@ -58,16 +58,16 @@ int64_t mx_row_blocks(const mx_gemm_plan& p, int32_t bm) {
 // pairs of formats:
 //   direct kernels: 2.7 to 3.4 us, and a step of 128 along K moves the tile's rows of both operands at 33
 //     KB a microsecond and compute unit, whether one workgroup runs there or several, each for 1.6
-//     us at least (32x64: 2.2) (128x4096x4096 e4m3 x e2m1 in 32x64 tiles 12.0 measured, 11.2 estimated)
+//     us at least (32x64: 2.2) (128x4096x4096 e4m3 x e2m1 in 32x64 tiles 10.7 measured, 11.2 estimated)
 //   128x128: 7 us, and 74 KB a microsecond alone on a compute unit, 56 for two workgroups
-//     (512x4096x4096 19.0, 17.4; 16384x4096x4096 226, 234)
-//   256x256: 6 us, a round 5 us and 1.36 a step with an e4m3 operand, 0.85 without (4096^3 51.6, 54.5;
-//     16384x4096x4096 197, 200), the quarters of a last round 4 us and 1.3 times their share of one
+//     (512x4096x4096 18.3, 17.4; 16384x4096x4096 230, 234)
+//   256x256: 6 us, a round 5 us and 1.36 a step with an e4m3 operand, 0.85 without (4096^3 53.2, 54.5;
+//     16384x4096x4096 196, 200), the quarters of a last round 4 us and 1.3 times their share of one
 //   a split adds 3 us and the sums' way to memory and back at 4.2 MB a microsecond
-//     (1024x1024x8192 in 128x128 tiles over four workgroups 23.7, 23.2; over one 30.1)
-// so 16-row tiles serve few rows (1x8192x8192 10.5; in 32x64 tiles 13.5), 32x64 up to 128 or 256 rows,
+//     (1024x1024x8192 in 128x128 tiles over four workgroups 22.3, 23.2; over one 29.4)
+// so 16-row tiles serve few rows (1x8192x8192 8.0; in 32x64 tiles 13.8), 32x64 up to 128 or 256 rows,
 // 128x128 up to one round of 256x256 tiles, and deep products with few tiles are split
-// (128x512x8192: 9.9 in 32x32 tiles over four workgroups, 14.9 over one).
+// (128x512x8192: 8.3 in 32x32 tiles over four workgroups, 13.8 over one).
 static double estimate(const mx_gemm_plan& p, int32_t cus, int32_t tile, int32_t split) {
   int32_t bm, bn;
   mx_tile_extent(tile, &bm, &bn);

@@ -1,8 +1,8 @@
 // MX quantiser and its inverse (mx_quantize, mx_dequantize of the public header).
 //
 // Both are bound by memory: the input is read once, codes and scales (8.25 or 4.25 bits a value)
-// are written once, and a value costs about ten vector instructions. 8192 x 8192 bf16 to e2m1: 32.9 us
-// (170 MB, 5.2 TB/s); back to bf16 25.8 us (6.6 TB/s, part of it from the last-level cache). A torch copy of 4
+// are written once, and a value costs about ten vector instructions. 8192 x 8192 bf16 to e2m1: 33 us
+// (172 MB, 5.2 TB/s); back to bf16 26 us (6.6 TB/s, part of it from the last-level cache). A torch copy of 4
 // GiB reaches 4.7 TB/s.
 #include <type_traits>
 
@@ -38,9 +38,11 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(const T* x, int
 // 16-bit columns or one fp32 column) of one block in registers, kTB neighbouring lanes the kTB
 // blocks of a column, so that they write kTB x 32 (E4M3) or 16 (E2M1) contiguous bytes of an
 // output row. Each block starts 64 / kTB dwords further in LDS, so the 64 / kTB dword columns x kTB
-// blocks that a wave reads lie in 64 distinct banks. 5001 x 4104 f16 to e4m3: 15.9 us (62 MB, 3.9 TB/s);
-// 4096 x 4096 bf16 with nothing cached 14.1 us: its 1024 workgroups all run at once, so that the card
-// first only reads and then only writes.
+// blocks that a wave reads are distinct modulo 64 dwords. (Not modulo 32: two blocks' columns meet there, and
+// each read is counted with two conflict cycles, 0.33 M of the 0.99 M LDS cycles of the first call below.) 5001
+// x 4104 f16 to e4m3: 14.7 us in a graph of such calls (62 MB, 4.2 TB/s), 16 us with other kernels between them;
+// 4096 x 4096 bf16 10.3 and 12.8 us: its 1024 workgroups all run at once, so that the card first only reads
+// and then only writes.
 template <typename T, int FMT, int kTB, int kRowDw>
 __global__ __launch_bounds__(kTB* kRowDw) void quantize_cols_kernel(const T* x, int64_t ldx, int rows, int cols, int nb,
                                                                  int nsb, uint32_t first, uint32_t tiles, FastDiv fd_ty,
@@ -232,8 +234,8 @@ gemm_status mx_quantize(int32_t rows, int32_t cols, const void* x, int32_t x_typ
     using T = std::remove_pointer_t<decltype(t)>;
     if (transpose) {
       // 16-bit: 256 rows x 64 columns, the longest runs of the output (5001 x 4104 f16 to e4m3 14.7 us;
-      // 128 x 128 15.2, 64 x 128 16.1); fp32: 128 x 64, the longest of the input (8192 x 8192 to e2m1
-      // 59.8 us; 256 x 32 65.0).
+      // 128 x 128 15.3, 64 x 128 15.7); fp32: 128 x 64, the longest of the input (8192 x 8192 to e2m1
+      // 69 us; 256 x 32 77).
       constexpr int kTB = sizeof(T) == 2 ? 8 : 4, kRowDw = sizeof(T) == 2 ? 32 : 64, tc = kRowDw * 4 / (int)sizeof(T);
       const int64_t ty = (nb + kTB - 1) / kTB, tx = ((int64_t)cols + tc - 1) / tc;
       if (ty * tx > 0x7FFFFF00) { st = fail(GEMM_ERR_UNSUPPORTED, "mx_quantize: more than 2^31 tiles"); return; }

@@ -7,10 +7,10 @@
 // Both are bound by memory. A row is held in registers from its single read to its last use:
 // threads x CH chunks of 8 elements, chunk j of thread t at column (t + j threads) 8. Four
 // adjacent lanes hold an MX block. Rows too long for registers take a kernel that reads them
-// twice. All sums run in a fixed order. 16768 x 4096 bf16 with residual, h and e4m3 output: 78.5 us (483
-// MB, 6.2 TB/s); gradients 8192 x 8192 bf16 with dres: 94.9 us (537 MB and 17 MB of column sums written and
-// read, 6.0 TB/s; 90 and 5 us of it in the two kernels); one row of 4096: 3 us, the launch and two
-// rounds of memory latency.
+// twice. All sums run in a fixed order. 16768 x 4096 bf16 with residual, h and e4m3 output: 80 us (483
+// MB, 6.0 TB/s); gradients 8192 x 8192 bf16 with dres: 95 us (537 MB and 17 MB of column sums written and
+// read, 6.0 TB/s; 91 and 5 us of it in the two kernels); one row of 4096: 3 us, the launch and two
+// rounds of memory latency. (Times in these comments: calls in a graph, one after the other.)
 #include <type_traits>
 
 #include "mx_common.hpp"
@@ -112,7 +112,7 @@ __device__ __forceinline__ uint32_t scale8(const float h[8], const float w[8], c
   // Borders between values of at most four significant bits: the last 19 bits of y are zero there. So
   // they are in an infinity, and in the NaN that inf * hi + inf * lo gives.
   // (Branches of the whole wave, and a loop: rare code lies past the end of the common one and is short.
-  // One row of 4096 bf16: 3.1 us; with eight copies of it in line 3.6.)
+  // One row of 4096 bf16: 3.2 us; with eight copies of it in line 3.6.)
   if (__builtin_expect(__ballot((low == 0) | r.far) != 0, 0)) {
     bool again = r.far;
 #pragma unroll
@@ -279,7 +279,7 @@ template <typename T, bool WAVE, int CH, bool WHOLE, int STREAM>
 __global__ __launch_bounds__(WAVE ? 64 : 1024) void rmsnorm_grad_kernel(const NormGradParams p) {
   __shared__ float red[WAVE ? 1 : 16];
   // The next row is on its way while this one meets at the barriers and is stored, where its registers
-  // fit (fp32 rows, or chunks to be moved into place: 333 x 2050 fp32 8.9 us, ahead 15.0).
+  // fit (fp32 rows, or chunks to be moved into place: 333 x 2050 fp32 9.5 us, ahead 14.6).
   constexpr bool kAhead = rows_ahead<T, WHOLE>();
   const int t = threadIdx.x, threads = blockDim.x;
   float dw[CH][8];
@@ -415,8 +415,8 @@ __global__ __launch_bounds__(1024) void rmsnorm_grad_long_kernel(const NormGradP
 }
 
 // dw = sum of `n` rows of partial sums: 32 columns (whole lines) a workgroup, 32 threads a column.
-// (8192 x 8192 bf16, 512 rows of sums: both kernels 107.0 us; 16 columns 109.5, and with fewer
-// rows 64 columns are slower than 32: 8192 x 512 15.8 and 13.6.)
+// (8192 x 8192 bf16, 512 rows of sums: both kernels 95.9 us; 16 columns 98.8, 64 columns 95.6; with fewer
+// columns 64 are slower than 32: 8192 x 512 15.9 and 13.6.)
 constexpr int kSumCols = 32, kSumRows = 32;
 __global__ __launch_bounds__(kSumCols* kSumRows) void column_sum_kernel(const float* part, int n, int cols, float* dw) {
   __shared__ float s[kSumRows][kSumCols];
@@ -440,9 +440,8 @@ int cdiv(int a, int b) { return (a + b - 1) / b; }
 
 // Threads of a row and chunks of a thread: a wave up to 128 chunks (1024 columns), else two chunks
 // a thread and as many waves as that takes, up to 16384 columns. (16768 x 4096 bf16 with residual
-// and e4m3 output: 256 threads x 2 chunks 95 us, 512 x 1 103; one wave x 8 too many registers for
-// enough waves, 138.)
-// With few rows one chunk a thread: the row's time is its latency (1 x 4096: 3.1 us, with two 3.9).
+// and e4m3 output: 256 threads x 2 chunks 80 us, 512 x 1 93, 128 x 4 80.)
+// With few rows one chunk a thread: the row's time is its latency (1 x 4096: 3.2 us, with two 3.7).
 constexpr int kFewRows = 256;
 template <typename F>
 bool with_shape(int rows, int chunks, F&& f) {
@@ -456,9 +455,9 @@ bool with_shape(int rows, int chunks, F&& f) {
 
 // How a call's rows pass the caches (STREAM): 0 through them; past them, where it moves more bytes than
 // they hold, 2 both ways or 1 only what it writes. 2 needs rows of whole lines: past the caches a line
-// that two waves share is fetched twice (norm gradients 8192 x 5000 f16: 69 us with 1, 82 with 2, 81
-// with 0; 16768 x 4096 bf16: 103, 100, 107; norm 16768 x 4096 bf16 84, 78, 87). An fp32 chunk is two
-// 16-byte accesses to one line: 0 (norm 16384 x 4096: 199 us, with 2 204).
+// that two waves share is fetched twice (norm gradients 8192 x 5000 f16: 70 us with 1, 75 with 2, 82
+// with 0; norm 16768 x 4096 bf16 to e4m3: 84 with 1, 80 with 2, 88 with 0). An fp32 chunk is two
+// 16-byte accesses to one line: 0 (norm 16384 x 4096: 189 us, with 2 203).
 int stream_mode(int64_t elements, int bytes, int64_t strides) {
   if (bytes != 2 || elements * bytes <= kCacheBytes) return 0;
   return strides % 64 ? 1 : 2;
@@ -499,8 +498,10 @@ void launch_norm(NormParams p, int stream, hipStream_t s) {
 }
 
 // Rows of partial sums: the workgroups that run at once, with `waves` waves a compute unit, at most 16
-// MB of sums up to 16384 columns. 16 waves, or 8 where the next row is loaded ahead
-// (16768 x 4096 bf16: 8 waves 103 us, 16 waves 112; 8192 x 8192: 104, 107).
+// MB of sums up to 16384 columns. 8 waves where the next row is loaded ahead and rows are read through the
+// caches (4096 x 4096 bf16 with dres 28.3 us, 16 waves 30.1; 8192 x 4096 without 37.5 and 39.4), else 16: past the
+// caches that is 95.9 us at 8192 x 8192 bf16 with dres (8 waves 102), though 8 would be a little faster
+// without dres (75.4 and 73.8) and in shorter rows (16768 x 4096 with dres 102 and 97).
 int grad_parts(int rows, int cols, int waves) {
   int n = 256;
   with_shape(rows, cdiv(cols, 8), [&](auto, auto, int threads) { n = 256 * (waves * 64 > threads ? waves * 64 / threads : 1); });

@@ -215,10 +215,14 @@ class MxPlan:
     bytes; at least one of D, PostAct. tile, split: "auto" and 0, or the kernel to use ("256", "128",
     "32x64", "32", "16x32", "16") and over how many workgroups it shares out a tile's K.
 
+    Sums are held in fp32, but with an e4m3 operand the matrix instruction keeps the products of a block
+    of 32 only to 2^-13 of the block's largest: a float32 output is off by about 1e-5 (e2m1 on both sides:
+    as an fp32 product).
+
     Where K is shared out, a run needs a workspace for the partial sums: workspace_bytes of memory that is
     the run's stream's own. The plan keeps one for each stream that it has run on (allocated by the first
     run there, and freed with the plan); a run that is captured into a graph takes one from the graph's
-    memory."""
+    memory. (Threads that run one plan on one stream at the same time need workspaces of their own.)"""
 
     def __init__(self, a, b, C=None, D=None, PostAct=None, act="none", cu_seqlens_m=None, tile="auto",
                  split=0):

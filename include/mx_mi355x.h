@@ -83,7 +83,7 @@ typedef struct {
 } rmsnorm_args;
 gemm_status rmsnorm_forward(const rmsnorm_args* args, void* stream);
 
-/* Gradients of that norm. With n = h * rstd and p = dy * weight:
+/* Gradients of that norm, in fp32. With n = h * rstd and p = dy * weight:
  *   dx = rstd * (p - n * mean(p * n)) + dres     dw = sum over rows of dy * n
  * dx (the gradient with respect to h, hence to x and to the residual) has the type of h; dres
  * (the gradient that reaches h past the norm) may be NULL; dw is fp32[cols]. dx may be dy or
@@ -108,16 +108,23 @@ gemm_status rmsnorm_backward(const rmsnorm_backward_args* args, void* stream);
 /* Bytes of workspace (-1 for a negative size, or one that rmsnorm_backward refuses as too large). */
 int64_t rmsnorm_backward_workspace(int32_t rows, int32_t cols);
 
-/* Product of MX operands with a fused epilogue, fp32 accumulation:
+/* Product of MX operands with a fused epilogue:
  *   D       = A x B^T + C        PostAct = act(A x B^T + C)   (before D's rounding)
+ * Sums are held in fp32. With an E4M3 operand the matrix instruction itself keeps the products of a
+ * block of 32 only to 2^-13 of the block's largest (1 + 2^-13 is exact, 1 + 2^-14 gives 1), so an F32
+ * output has fewer good bits than an fp32 product of the same values: of normal values, K = 4096, it is off
+ * by 4e-6 (E4M3 x E2M1) or 1.5e-5 (E4M3 x E4M3) in the Frobenius norm, where fp32 sums are by 5e-8 and the
+ * rounding to BF16 by 1.7e-3. E2M1 x E2M1 products are exact before the sum.
  * A (M, K), B (N, K) MX matrices of any of the two formats each; C, D, PostAct row-major (M, N)
  * of type F16 / BF16 / F32 with their own leading dimensions (in elements). Grouped (groups > 0):
  * B is (groups, N, K) and row r of A / C / D / PostAct belongs to group g with
  * cu_seqlens_m[g] <= r < cu_seqlens_m[g+1] (device int32[groups+1], 0 .. M, never decreasing;
  * an array that breaks this runs nothing and writes nothing).
  * At least one of d, post is present. N is a multiple of 8, every leading dimension one of 16
- * bytes, K at most 2^22, and every pointer is 16-byte aligned. K = 0 gives D = C (or 0). C may be
- * D or PostAct itself (of its type and leading dimension); D and PostAct are two matrices. tile: 0 lets the library choose; otherwise one of the MX_TILE values. */
+ * bytes, K at most 2^22, and every pointer is 16-byte aligned. K = 0 gives D = C (or 0). The activations
+ * are those of gemm_run (ReLU of a NaN is 0). C may be D or PostAct itself (of its type and leading
+ * dimension); D and PostAct are two matrices. tile: 0 lets the library choose; otherwise one of the
+ * MX_TILE values. */
 typedef enum {
   MX_TILE_AUTO = 0,
   MX_TILE_256 = 1,   /* 256x256 outputs a workgroup, operands staged through LDS         */
