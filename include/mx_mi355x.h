@@ -58,8 +58,8 @@ gemm_status mx_dequantize(int32_t rows, int32_t k, int32_t format, const void* c
 /* Fused RMS norm over the rows of x (rows, cols):
  *   h    = x + residual, rounded to the type of x   (h = x without a residual)
  *   rstd = 1 / sqrt(mean(h^2) + eps)                (fp32, from the rounded h)
- *   y    = h * rstd * weight, rounded to fp32 (to half a step wherever it lies in fp32's normal
- *          range, whatever h * weight and rstd are), written rounded to the type of x and / or as an
+ *   y    = h * rstd * weight, rounded to fp32 (to half a step for magnitudes from 2^-90 on, smaller
+ *          ones to 2^-130; whatever h * weight is), written rounded to the type of x and / or as an
  *          MX matrix (rows, cols) quantised from the unrounded value.
  * x, residual, h, y and weight share `type` (F16, BF16, F32); each matrix has its own leading
  * dimension. h_out may be NULL (required NULL without a residual: h is x) and may be x or
