@@ -12,8 +12,8 @@ Six kinds of case, by case["op"]:
                quantised along columns for the weight's gradient
   balance      per-expert counts, a router's balance loss and its gradient
 
-Format: codes are OCP e4m3; scale = max |x| / 448 of the block in fp32, 2^-126 at least; a code is x / scale
-rounded to nearest even, the value code * scale. Storage: codes row-major, rows padded with zero codes to 16
+Format: codes are OCP e4m3. Of a block, r = 448 / max |x| in fp32, 2^126 at most, cut to 13 significant bits (so that x r is
+exact in fp32 for 16-bit x); a code is x r rounded to nearest even, scale = 1 / r in fp32, the value code * scale. Storage: codes row-major, rows padded with zero codes to 16
 bytes; scales in fp32, (rows / 64, blocks / 4, 64, 4) rounded up, or of tiles (rows / 128, blocks) with the blocks
 rounded up to a multiple of 4.
 """
@@ -27,7 +27,7 @@ own = False
 TYPES = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
 BLOCK = 128
 TOP = 448.0
-LEAST = 2.0**-126
+MOST = 2.0**126
 
 
 def listed():
@@ -155,12 +155,18 @@ def e4m3(v):
     return torch.round(v / step) * step
 
 
+def factor(top):
+    """What a block of largest magnitude `top` is multiplied with: quotient in 64 bits, rounded to 32, cut."""
+    r = torch.full_like(top, TOP, dtype=torch.float64).div(top.double()).float().clamp(max=MOST)
+    return r.view(torch.int32).bitwise_and(-(1 << 11)).view(torch.float32).double()
+
+
 def to_blocks(x, tiles):
-    """x (..., rows, k): its elements and scales, both in whole blocks. Quotients in 64 bits: a rounded one could
+    """x (..., rows, k): its elements and scales, both in whole blocks. Products in 64 bits: a rounded one could
     pass the border between two elements, which many 16-bit values lie on."""
     b = whole_blocks(x.float(), tiles)
-    scale = (b.abs().amax((-3, -1), keepdim=True).double() / TOP).float().clamp(min=LEAST)
-    return e4m3((b.double() / scale.double()).clamp(-TOP, TOP)), scale
+    r = factor(b.abs().amax((-3, -1), keepdim=True))
+    return e4m3((b.double() * r).clamp(-TOP, TOP)), (1 / r).float()
 
 
 def values_of(x, tiles=False):
@@ -420,7 +426,7 @@ def representable(device):
 
 
 def nearest(x, tiles=False):
-    """x (rows, k) in 64 bits as the nearest values of the format: ties to the even code. The scale is a number of 32 bits."""
+    """x (rows, k) in 64 bits as the nearest values of the format: ties to the even code. Factor and scale are numbers of 32 bits."""
     mags = representable(x.device)
     between = (mags[1:] + mags[:-1]) / 2
     rows, k = x.shape
@@ -431,8 +437,11 @@ def nearest(x, tiles=False):
         b[:r, :k] = part
         b = b.reshape(-1, tall, b.shape[1] // BLOCK, BLOCK)
         top = b.abs().permute(0, 2, 1, 3).flatten(2).max(-1).values[:, None, :, None]
-        scale = (top / TOP).float().clamp(min=LEAST).double()
-        v = b.abs() / scale
+        f = (torch.full_like(top, TOP) / top).float().clamp(max=MOST).double()
+        m, e = torch.frexp(f)
+        f = torch.floor(m * 8192) / 8192 * torch.exp2(e.double())
+        scale = torch.reciprocal(f).float().double()
+        v = b.abs() * f
         below, above = torch.bucketize(v, between), torch.bucketize(v, between, right=True)
         at = torch.where(below == above, below, below + below % 2)  # on a border: the even one of the two
         out.append((mags[at] * scale * torch.sign(b)).reshape(-1, b.shape[2] * BLOCK)[:r, :k])
