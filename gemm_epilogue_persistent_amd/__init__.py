@@ -26,13 +26,16 @@ from ._abi import GemmError, DT, ACT, ROW, COL
 _TORCH_DT = {torch.float16: "f16", torch.bfloat16: "bf16", torch.float32: "f32",
              torch.float8_e4m3fn: "e4m3", torch.float8_e5m2: "e5m2"}
 
+from .fp8 import (Fp8Plan, Fp8Tensor, fp8_act, fp8_act_backward, fp8_dequantize, fp8_empty, fp8_gemm,
+                  fp8_quantize)
 from .mx import MxPlan, MxTensor, mx_dequantize, mx_empty, mx_gemm, mx_quantize
 from .norm import rmsnorm, rmsnorm_backward, rmsnorm_backward_workspace
 
 __all__ = ["Plan", "gemm", "gemm_dact", "gemm_create", "gemm_run", "plan_grid", "configs", "tune", "fastdivmod_params",
            "fastdivmod_check", "check_cu_seqlens", "tuned_config", "GemmError", "library_path",
            "MxTensor", "MxPlan", "mx_empty", "mx_quantize", "mx_dequantize", "mx_gemm",
-           "rmsnorm", "rmsnorm_backward", "rmsnorm_backward_workspace"]
+           "rmsnorm", "rmsnorm_backward", "rmsnorm_backward_workspace",
+           "Fp8Tensor", "Fp8Plan", "fp8_empty", "fp8_quantize", "fp8_dequantize", "fp8_gemm", "fp8_act", "fp8_act_backward"]
 
 
 def library_path():

@@ -13,7 +13,9 @@ ROW, COL = 0, 1
 ACT = {"none": 0, "relu": 1, "relu_sq": 2, "gelu_tanh": 3, "silu": 4}
 MX_FORMAT = {"e2m1": 0, "e4m3": 1}
 MX_TILE = {"auto": 0, "256": 1, "128": 2, "32x64": 3, "32": 4, "16x32": 5, "16": 6}
+FP8_TILE = {"auto": 0, "256": 1, "128": 2, "32x64": 3, "32": 4, "16x32": 5, "16": 6}
 MX_HEADER = os.path.join(os.path.dirname(HERE), "include", "mx_mi355x.h")
+FP8_HEADER = os.path.join(os.path.dirname(HERE), "include", "fp8_mi355x.h")
 
 
 class GemmDesc(ctypes.Structure):
@@ -53,6 +55,29 @@ class MxGemmArgs(ctypes.Structure):
         ("workspace_bytes", ctypes.c_int64)]
 
 
+class Fp8GemmDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("M", "N", "K", "groups", "b_scaling", "c", "d", "post", "act", "tile",
+                                              "split")] + [
+        (n, ctypes.c_int64) for n in ("ldc", "ldd", "ldp")]
+
+
+class Fp8GemmArgs(ctypes.Structure):
+    _fields_ = MxGemmArgs._fields_
+
+
+class Fp8ActArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("rows", "cols", "type", "act")] + [
+        (n, ctypes.c_void_p) for n in ("x", "saved_codes", "saved_scales", "q_codes", "q_scales", "y")] + [
+        (n, ctypes.c_int64) for n in ("ldx", "ldy")]
+
+
+class Fp8ActBackwardArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("rows", "cols", "type", "act")] + [
+        (n, ctypes.c_void_p) for n in ("dy", "saved_codes", "saved_scales", "dx", "q_codes", "q_scales", "qt_codes", "qt_scales",
+                                       "y", "yt_codes", "yt_scales")] + [
+        (n, ctypes.c_int64) for n in ("lddy", "lddx", "ldy")]
+
+
 class RmsnormArgs(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("rows", "cols", "type", "q_format")] + [("eps", ctypes.c_float)] + [
         (n, ctypes.c_void_p) for n in ("x", "residual", "weight", "h_out", "y", "q_codes", "q_scales", "rstd")] + [
@@ -70,6 +95,8 @@ class RmsnormBackwardArgs(ctypes.Structure):
 MX_GEMM_ARGS = struct.Struct("@9Pq")
 RMSNORM_ARGS = struct.Struct("@4if8P4q")
 RMSNORM_BACKWARD_ARGS = struct.Struct("@3i8P5q")
+FP8_ACT_ARGS = struct.Struct("@4i6P2q")
+FP8_ACT_BACKWARD_ARGS = struct.Struct("@4i11P3q")
 
 
 def int32(name, value):
@@ -147,6 +174,28 @@ def load():
         lib.mx_gemm_plan_tile.argtypes = [vp, i32, ctypes.POINTER(i32), ctypes.POINTER(i32)]
         lib.mx_gemm_workspace.restype = ctypes.c_int
         lib.mx_gemm_workspace.argtypes = [vp, i32, ctypes.POINTER(i64)]
+        lib.fp8_code_bytes.restype = i64
+        lib.fp8_code_bytes.argtypes = [i64, i64]
+        lib.fp8_scale_bytes.restype = i64
+        lib.fp8_scale_bytes.argtypes = [i64, i64, i32]
+        lib.fp8_quantize.restype = ctypes.c_int
+        lib.fp8_quantize.argtypes = [i32, i32, vp, i32, i64, i32, vp, vp, vp, vp, vp]
+        lib.fp8_dequantize.restype = ctypes.c_int
+        lib.fp8_dequantize.argtypes = [i32, i32, i32, vp, vp, vp, i32, i64, vp]
+        lib.fp8_act_forward.restype = ctypes.c_int
+        lib.fp8_act_forward.argtypes = [vp, vp]
+        lib.fp8_act_backward.restype = ctypes.c_int
+        lib.fp8_act_backward.argtypes = [vp, vp]
+        lib.fp8_gemm_create.restype = ctypes.c_int
+        lib.fp8_gemm_create.argtypes = [ctypes.POINTER(Fp8GemmDesc), ctypes.POINTER(vp)]
+        lib.fp8_gemm_run.restype = ctypes.c_int
+        lib.fp8_gemm_run.argtypes = [vp, vp, vp]
+        lib.fp8_gemm_destroy.restype = ctypes.c_int
+        lib.fp8_gemm_destroy.argtypes = [vp]
+        lib.fp8_gemm_plan_tile.restype = ctypes.c_int
+        lib.fp8_gemm_plan_tile.argtypes = [vp, i32, ctypes.POINTER(i32), ctypes.POINTER(i32)]
+        lib.fp8_gemm_workspace.restype = ctypes.c_int
+        lib.fp8_gemm_workspace.argtypes = [vp, i32, ctypes.POINTER(i64)]
         lib.gemm_status_string.restype = ctypes.c_char_p
         lib.gemm_status_string.argtypes = [ctypes.c_int]
         lib.gemm_last_error.restype = ctypes.c_char_p

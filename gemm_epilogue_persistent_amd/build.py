@@ -22,6 +22,10 @@ UNITS = ["plan.cpp", "gemm_api.hip"] + [
 UNITS += [os.path.join("mx", u) for u in ["mx_plan.cpp", "mx_api.hip", "mx_quant.hip", "rmsnorm.hip"] + [
     f"mx_inst_{a}_{b}_{v}.hip" for a in ("e2m1", "e4m3") for b in ("e2m1", "e4m3") for v in ("dense", "vm")]]
 
+# FP8 operators with a scale per 128 values
+UNITS += [os.path.join("fp8", u) for u in ["fp8_quant.hip"] + [
+    f"fp8_inst_{b}_{v}.hip" for b in ("rows", "tiles") for v in ("dense", "vm")]]
+
 
 def hipcc() -> str:
     for c in (os.environ.get("HIPCC"), "/opt/rocm/bin/hipcc", shutil.which("hipcc")):

@@ -1,0 +1,4 @@
+#include "fp8_gemm.hpp"
+namespace gep {
+GEP_FP8_LAUNCH(true, false)
+}

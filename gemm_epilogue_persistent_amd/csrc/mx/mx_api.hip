@@ -1,7 +1,8 @@
-// mx_gemm_run (C ABI): the launch of an MX product.
+// mx_gemm_run and fp8_gemm_run (C ABI): the launch of a product of block-scaled operands.
 #include <atomic>
 #include <utility>
 
+#include "../fp8/fp8_gemm.hpp"
 #include "mx_gemm.hpp"
 #include "mx_plan.hpp"
 
@@ -17,8 +18,16 @@ GEP_MX_DECLARE(MX_E2M1, MX_E4M3)
 GEP_MX_DECLARE(MX_E4M3, MX_E2M1)
 GEP_MX_DECLARE(MX_E4M3, MX_E4M3)
 
+template <> hipError_t fp8_launch<false, false>(int32_t, const MxParams&, dim3, hipStream_t);
+template <> hipError_t fp8_launch<false, true>(int32_t, const MxParams&, dim3, hipStream_t);
+template <> hipError_t fp8_launch<true, false>(int32_t, const MxParams&, dim3, hipStream_t);
+template <> hipError_t fp8_launch<true, true>(int32_t, const MxParams&, dim3, hipStream_t);
+
 template <bool VM>
-static hipError_t launch(const mx_gemm_desc& d, int32_t tile, const MxParams& p, dim3 g, hipStream_t s) {
+static hipError_t launch(const mx_gemm_plan& plan, int32_t tile, const MxParams& p, dim3 g, hipStream_t s) {
+  const mx_gemm_desc& d = plan.d;
+  if (plan.b_scaling == FP8_ROWS) return fp8_launch<true, VM>(tile, p, g, s);
+  if (plan.b_scaling == FP8_TILES) return fp8_launch<false, VM>(tile, p, g, s);
   if (d.a_format == MX_E2M1)
     return d.b_format == MX_E2M1 ? mx_launch<MX_E2M1, MX_E2M1, VM>(tile, p, g, s) : mx_launch<MX_E2M1, MX_E4M3, VM>(tile, p, g, s);
   return d.b_format == MX_E2M1 ? mx_launch<MX_E4M3, MX_E2M1, VM>(tile, p, g, s) : mx_launch<MX_E4M3, MX_E4M3, VM>(tile, p, g, s);
@@ -64,27 +73,23 @@ static gemm_status compute_units(int32_t* cus) {
   return GEMM_OK;
 }
 
-}  // namespace gep
-
-using namespace gep;
-
-extern "C" gemm_status mx_gemm_run(const mx_gemm_plan* plan, const mx_gemm_args* a, void* stream) {
-  if (!plan || !a) return fail(GEMM_ERR_INVALID_ARG, "mx_gemm_run: NULL plan or args");
+gemm_status block_gemm_run(const char* fn, const mx_gemm_plan* plan, const mx_gemm_args* a, void* stream) {
+  if (!plan || !a) return fail(GEMM_ERR_INVALID_ARG, "%s: NULL plan or args", fn);
   const mx_gemm_desc& d = plan->d;
   if (d.M == 0 || d.N == 0) { clear_error(); return GEMM_OK; }
   if (d.K > 0 && (!a->a_codes || !a->a_scales || ((!a->b_codes || !a->b_scales))))
-    return fail(GEMM_ERR_INVALID_ARG, "mx_gemm_run: A and B are required");
-  if ((d.c != GEMM_DT_NONE) != (a->C != nullptr)) return fail(GEMM_ERR_INVALID_ARG, "mx_gemm_run: C must be given iff the plan has a C type");
-  if ((d.d != GEMM_DT_NONE) != (a->D != nullptr)) return fail(GEMM_ERR_INVALID_ARG, "mx_gemm_run: D must be given iff the plan has a D type");
-  if ((d.post != GEMM_DT_NONE) != (a->PostAct != nullptr)) return fail(GEMM_ERR_INVALID_ARG, "mx_gemm_run: PostAct must be given iff the plan has a PostAct type");
-  if ((d.groups > 0) != (a->cu_seqlens_m != nullptr)) return fail(GEMM_ERR_INVALID_ARG, "mx_gemm_run: cu_seqlens_m must be given iff the plan is grouped");
+    return fail(GEMM_ERR_INVALID_ARG, "%s: A and B are required", fn);
+  if ((d.c != GEMM_DT_NONE) != (a->C != nullptr)) return fail(GEMM_ERR_INVALID_ARG, "%s: C must be given iff the plan has a C type", fn);
+  if ((d.d != GEMM_DT_NONE) != (a->D != nullptr)) return fail(GEMM_ERR_INVALID_ARG, "%s: D must be given iff the plan has a D type", fn);
+  if ((d.post != GEMM_DT_NONE) != (a->PostAct != nullptr)) return fail(GEMM_ERR_INVALID_ARG, "%s: PostAct must be given iff the plan has a PostAct type", fn);
+  if ((d.groups > 0) != (a->cu_seqlens_m != nullptr)) return fail(GEMM_ERR_INVALID_ARG, "%s: cu_seqlens_m must be given iff the plan is grouped", fn);
   for (const void* p : {a->a_codes, a->a_scales, a->b_codes, a->b_scales, a->C, (const void*)a->D, (const void*)a->PostAct})
-    if ((uintptr_t)p & 15) return fail(GEMM_ERR_ALIGNMENT, "mx_gemm_run: pointers must be 16-byte aligned");
-  if ((uintptr_t)a->cu_seqlens_m & 3) return fail(GEMM_ERR_ALIGNMENT, "mx_gemm_run: cu_seqlens_m not 4-byte aligned");
+    if ((uintptr_t)p & 15) return fail(GEMM_ERR_ALIGNMENT, "%s: pointers must be 16-byte aligned", fn);
+  if ((uintptr_t)a->cu_seqlens_m & 3) return fail(GEMM_ERR_ALIGNMENT, "%s: cu_seqlens_m not 4-byte aligned", fn);
   for (const auto& o : {std::pair<const void*, std::pair<int32_t, int64_t>>{a->D, {d.d, d.ldd}}, {a->PostAct, {d.post, d.ldp}}})
     if (a->C && a->C == o.first && (d.c != o.second.first || (d.M > 1 && d.ldc != o.second.second)))
-      return fail(GEMM_ERR_INVALID_ARG, "mx_gemm_run: C in the place of an output needs its type and leading dimension");
-  if (a->D && a->D == a->PostAct) return fail(GEMM_ERR_INVALID_ARG, "mx_gemm_run: D and PostAct are one matrix");
+      return fail(GEMM_ERR_INVALID_ARG, "%s: C in the place of an output needs its type and leading dimension", fn);
+  if (a->D && a->D == a->PostAct) return fail(GEMM_ERR_INVALID_ARG, "%s: D and PostAct are one matrix", fn);
   int32_t cus = 0;
   const gemm_status st = compute_units(&cus);
   if (st != GEMM_OK) return st;
@@ -93,8 +98,8 @@ extern "C" gemm_status mx_gemm_run(const mx_gemm_plan* plan, const mx_gemm_args*
   if (choice.split > 1) {
     const int64_t need = mx_workspace_bytes(*plan, choice);
     if (!a->workspace) choice = mx_choice(*plan, cus, false);
-    else if (a->workspace_bytes < need) return fail(GEMM_ERR_INVALID_ARG, "mx_gemm_run: workspace of %lld bytes expected", (long long)need);
-    else if ((uintptr_t)a->workspace & 15) return fail(GEMM_ERR_ALIGNMENT, "mx_gemm_run: workspace not 16-byte aligned");
+    else if (a->workspace_bytes < need) return fail(GEMM_ERR_INVALID_ARG, "%s: workspace of %lld bytes expected", fn, (long long)need);
+    else if ((uintptr_t)a->workspace & 15) return fail(GEMM_ERR_ALIGNMENT, "%s: workspace not 16-byte aligned", fn);
   }
   const int32_t tile = choice.tile;
   int32_t bm, bn;
@@ -115,7 +120,7 @@ extern "C" gemm_status mx_gemm_run(const mx_gemm_plan* plan, const mx_gemm_args*
   p.split = choice.split;
   p.per = choice.per;
   p.sums = (float*)a->workspace;
-  if (p.split > 1 && (int64_t)d.M * (d.N / 8) > 0x7FFFFF00) return fail(GEMM_ERR_UNSUPPORTED, "mx_gemm_run: too many outputs to share out K");
+  if (p.split > 1 && (int64_t)d.M * (d.N / 8) > 0x7FFFFF00) return fail(GEMM_ERR_UNSUPPORTED, "%s: too many outputs to share out K", fn);
   const int64_t tm = mx_row_blocks(*plan, bm), tn = (d.N + bn - 1) / bn;
   dim3 grid;
   int32_t tail_grid = 0;  // workgroups of the split tail's launch
@@ -142,11 +147,11 @@ extern "C" gemm_status mx_gemm_run(const mx_gemm_plan* plan, const mx_gemm_args*
       }
     }
   } else {
-    if (!mx_direct_fits(*plan, tile)) return fail(GEMM_ERR_UNSUPPORTED, "mx_gemm_run: too many rows or columns for the tile asked for");
+    if (!mx_direct_fits(*plan, tile)) return fail(GEMM_ERR_UNSUPPORTED, "%s: too many rows or columns for the tile asked for", fn);
     grid = dim3((unsigned)tn, (unsigned)tm, (unsigned)p.split);
   }
   hipStream_t s = (hipStream_t)stream;
-  auto run = [&](int32_t t, dim3 g) { return d.groups ? launch<true>(d, t, p, g, s) : launch<false>(d, t, p, g, s); };
+  auto run = [&](int32_t t, dim3 g) { return d.groups ? launch<true>(*plan, t, p, g, s) : launch<false>(*plan, t, p, g, s); };
   hipError_t e = run(tile, grid);
   if (e == hipSuccess && tail_grid > 0) {
     k.tail = 2;
@@ -158,7 +163,21 @@ extern "C" gemm_status mx_gemm_run(const mx_gemm_plan* plan, const mx_gemm_args*
     mx_join_kernel<<<(n + 255) / 256, 256, 0, s>>>(p, n, make_fastdiv((uint32_t)d.N / 8));
     e = hipGetLastError();
   }
-  if (e != hipSuccess) return fail(GEMM_ERR_HIP, "mx_gemm_run launch: %s", hipGetErrorString(e));
+  if (e != hipSuccess) return fail(GEMM_ERR_HIP, "%s launch: %s", fn, hipGetErrorString(e));
   clear_error();
   return GEMM_OK;
+}
+
+}  // namespace gep
+
+using namespace gep;
+
+extern "C" gemm_status mx_gemm_run(const mx_gemm_plan* plan, const mx_gemm_args* a, void* stream) {
+  return block_gemm_run("mx_gemm_run", plan, a, stream);
+}
+
+extern "C" gemm_status fp8_gemm_run(const fp8_gemm_plan* plan, const fp8_gemm_args* a, void* stream) {
+  if (!a) return fail(GEMM_ERR_INVALID_ARG, "fp8_gemm_run: NULL plan or args");
+  const mx_gemm_args m{a->a_codes, a->a_scales, a->b_codes, a->b_scales, a->C, a->D, a->PostAct, a->cu_seqlens_m, a->workspace, a->workspace_bytes};
+  return block_gemm_run("fp8_gemm_run", plan, &m, stream);
 }

@@ -213,6 +213,9 @@ __host__ __device__ __forceinline__ int mx_epilogue_kind(const MxParams& mp) {
 // half of the transfers into the freed stage goes out; the second half follows at the head of the
 // next step.
 //
+// The parts that depend on how operands are scaled are the class's that derives from this one (Self; MxRing itself
+// for MX operands): Src, Lane, Frags, scale_source, dma_scales, lane_offsets, first_reads, positions, sched, drain.
+//
 // EPI: the epilogues of the kernel, all kinds (0), kind 1 (1) or the others (2). Kind 1 has a kernel of
 // its own where the larger code costs it something: in 128x128 tiles (4096 x 2048 x 4096 e4m3, 4%) and in
 // 256x256 tiles of two E2M1 operands (8192^3, 1%), but not in those with an E4M3 operand (16384 x 4096 x
@@ -487,51 +490,63 @@ struct MxRing {
     }
   }
 
+  // The first step's fragments, before the main loop; what is left to add behind it.
+  static __device__ __forceinline__ void first_reads(Frags& f, const GEP_LDS char* smem, const Lane& o) {
+    const At x = at<0>(o, 0, 0);
+#pragma unroll
+    for (int r = 0; r < kRA - 1; ++r) read_a<0>(f, smem, x, r);
+#pragma unroll
+    for (int c = 0; c < kNI; ++c) read_b<0>(f, smem, x, c);
+  }
+  static __device__ __forceinline__ void drain(f32x4 (&)[kMI][kNI], Frags&) {}
+
   // stores: the stores x kStores16 stores of the previous tile's epilogue lie between this tile's transfers
   // of stage NS - 2 and NS - 1, and need not be waited for before those.
-  template <bool MM, int T>
-  static __device__ __forceinline__ void step(f32x4 (&acc)[kMI][kNI], Frags& f, GEP_LDS char* smem, const Lane& lo,
-                                              const Src& s, int q, Stages& st, int stores, int wave) {
+  template <class Self, bool MM, int T>
+  static __device__ __forceinline__ void step(f32x4 (&acc)[kMI][kNI], typename Self::Frags& f, GEP_LDS char* smem,
+                                              const typename Self::Lane& lo, const typename Self::Src& s, int q, Stages& st,
+                                              int stores, int wave) {
     const int so = (q & 1) * kSBytes, so_next = T == 3 ? ((q + 1) & 1) * kSBytes : so;
     const At x = at<T>(lo, st.cur, so), y = at<(T + 1) & 3>(lo, last_step(T) ? st.next : st.cur, so_next);
     if constexpr (MM) {
       __builtin_amdgcn_sched_barrier(0);
       __builtin_amdgcn_s_setprio(1);
       __builtin_amdgcn_sched_barrier(0);
-      positions<true, T, 0, kPrioP>(acc, f, smem, x, y, s, q, st, wave);
-      sched<T, 0, kPrioP>();
+      Self::template positions<true, T, 0, kPrioP>(acc, f, smem, x, y, s, q, st, wave);
+      Self::template sched<T, 0, kPrioP>();
       __builtin_amdgcn_sched_barrier(0);
       __builtin_amdgcn_s_setprio(0);
       __builtin_amdgcn_sched_barrier(0);
     }
-    positions<MM, T, MM ? kPrioP : 0, kBarP>(acc, f, smem, x, y, s, q, st, wave);
-    if constexpr (MM) sched<T, kPrioP, kBarP>();
+    Self::template positions<MM, T, MM ? kPrioP : 0, kBarP>(acc, f, smem, x, y, s, q, st, wave);
+    if constexpr (MM) Self::template sched<T, kPrioP, kBarP>();
     if constexpr (last_step(T)) {
       if constexpr (T / kSPS <= NS - 3) ring_barrier(stores);
       else ring_barrier();
     }
-    positions<MM, T, kBarP, kN>(acc, f, smem, x, y, s, q, st, wave);
+    Self::template positions<MM, T, kBarP, kN>(acc, f, smem, x, y, s, q, st, wave);
     if constexpr (MM) {
-      sched<T, kBarP, kN>();
+      Self::template sched<T, kBarP, kN>();
       __builtin_amdgcn_sched_barrier(0);
     }
     if constexpr (last_step(T)) st.advance();
   }
-  template <bool MM>
-  static __device__ __forceinline__ void mainloop(f32x4 (&acc)[kMI][kNI], Frags& f, GEP_LDS char* smem, const Lane& o,
-                                                  const Src& s, int steps, int stores, int wave) {
+  template <class Self, bool MM>
+  static __device__ __forceinline__ void mainloop(f32x4 (&acc)[kMI][kNI], typename Self::Frags& f, GEP_LDS char* smem,
+                                                  const typename Self::Lane& o, const typename Self::Src& s, int steps,
+                                                  int stores, int wave) {
     Stages st{(NS - 1) * kStage, 0, kStage};
     int q = 0;
     for (; q * 4 + 2 < steps; ++q) {
-      step<MM, 0>(acc, f, smem, o, s, q, st, stores, wave);
-      step<MM, 1>(acc, f, smem, o, s, q, st, stores, wave);
-      step<MM, 2>(acc, f, smem, o, s, q, st, stores, wave);
-      step<MM, 3>(acc, f, smem, o, s, q, st, stores, wave);
+      step<Self, MM, 0>(acc, f, smem, o, s, q, st, stores, wave);
+      step<Self, MM, 1>(acc, f, smem, o, s, q, st, stores, wave);
+      step<Self, MM, 2>(acc, f, smem, o, s, q, st, stores, wave);
+      step<Self, MM, 3>(acc, f, smem, o, s, q, st, stores, wave);
       stores = 0;
     }
     if (q * 4 < steps) {
-      step<MM, 0>(acc, f, smem, o, s, q, st, stores, wave);
-      step<MM, 1>(acc, f, smem, o, s, q, st, stores, wave);
+      step<Self, MM, 0>(acc, f, smem, o, s, q, st, stores, wave);
+      step<Self, MM, 1>(acc, f, smem, o, s, q, st, stores, wave);
     }
   }
 
@@ -736,7 +751,23 @@ struct MxRing {
     return ti;
   }
 
-  static __device__ __forceinline__ void run(const MxParams& mp) {
+  // Where this lane's scales come from: row i of the tile's A rows, then of its B rows, a wave 64 of them.
+  static __device__ __forceinline__ void scale_source(Src& s, const MxParams& mp, const MxTileInfo& ti, int q0, int wave, int lane) {
+    const KParams& p = mp.k;
+    s.nsb = mp.nsb - q0;
+    const bool is_a = wave < BM / 64;  // (waves past (BM + BN) / 64 move no scales)
+    const int first = is_a ? ti.m0 : ti.n0;  // row of the tile's first scale
+    const int i = (is_a ? wave : wave - BM / 64) * 64 + lane;  // row of the tile
+    const int64_t so = ((int64_t)(first >> 6) * mp.nsb + q0) * 1024;
+    s.s = make_rsrc(is_a ? mp.sa + so : mp.sb + (int64_t)ti.g * mp.sb_bytes + so,
+                    (is_a ? mp.sa_bytes : mp.sb_bytes) - so);
+    const int rr = (first & 63) + i;
+    s.s_off = first + i < (is_a ? ti.row_end : p.N) ? (uint32_t)((rr >> 6) * mp.nsb * 1024 + (rr & 63) * 16) : kOOB;
+  }
+
+  static __device__ __forceinline__ void run(const MxParams& mp) { run_as<MxRing>(mp); }
+  template <class Self>
+  static __device__ __forceinline__ void run_as(const MxParams& mp) {
     const KParams& p = mp.k;
     __shared__ __attribute__((aligned(1024))) char smem_raw[kLdsBytes];
     GEP_LDS char* smem = (GEP_LDS char*)smem_raw;
@@ -769,7 +800,7 @@ struct MxRing {
     }
 
     MxTileInfo ti;
-    Src s;
+    typename Self::Src s;
     int steps;
     // The tile's operands, and its first transfers: the first scales and all stages but the last.
     auto begin_tile = [&](int t) {
@@ -784,16 +815,8 @@ struct MxRing {
       const int64_t ao = (int64_t)ti.m0 * p.lda + ka, bo = (int64_t)ti.n0 * p.ldb + kb;
       s.a = make_rsrc((const char*)p.A + ao, p.a_bytes - ao);
       s.b = make_rsrc((const char*)p.B + (int64_t)ti.g * p.b_bytes + bo, p.b_bytes - bo);
-      s.nsb = mp.nsb - q0;
-      const bool is_a = wave < BM / 64;  // (waves past (BM + BN) / 64 move no scales)
-      const int first = is_a ? ti.m0 : ti.n0;  // row of the tile's first scale
-      const int i = (is_a ? wave : wave - BM / 64) * 64 + lane;  // row of the tile
-      const int64_t so = ((int64_t)(first >> 6) * mp.nsb + q0) * 1024;
-      s.s = make_rsrc(is_a ? mp.sa + so : mp.sb + (int64_t)ti.g * mp.sb_bytes + so,
-                      (is_a ? mp.sa_bytes : mp.sb_bytes) - so);
-      const int rr = (first & 63) + i;
-      s.s_off = first + i < (is_a ? ti.row_end : p.N) ? (uint32_t)((rr >> 6) * mp.nsb * 1024 + (rr & 63) * 16) : kOOB;
-      dma_scales(s, 0, smem, 0, wave);
+      Self::scale_source(s, mp, ti, q0, wave, lane);
+      Self::dma_scales(s, 0, smem, 0, wave);
 #pragma unroll
       for (int i = 0; i < NS - 1; ++i) {
         dma<0, kInstrA>(s.la, s.a, i * kRowA, smem + i * kStage, wave);
@@ -818,18 +841,15 @@ struct MxRing {
       dma<0, kInstrB / 2>(s.lb, s.b, (NS - 1) * kRowB, smem + (NS - 1) * kStage + kABytes, wave);
       int lane = lane_id;
       asm volatile("" : "+v"(lane));
-      const Lane o = lane_offsets(lane, wm0, wn0);
-      Frags f;
+      const typename Self::Lane o = Self::lane_offsets(lane, wm0, wn0);
+      typename Self::Frags f;
       if (idle) {
         __builtin_amdgcn_s_setprio(0);
-        mainloop<false>(acc, f, smem, o, s, steps, stores, wave);
+        mainloop<Self, false>(acc, f, smem, o, s, steps, stores, wave);
       } else {
-        const At x = at<0>(o, 0, 0);
-#pragma unroll
-        for (int r = 0; r < kRA - 1; ++r) read_a<0>(f, smem, x, r);
-#pragma unroll
-        for (int c = 0; c < kNI; ++c) read_b<0>(f, smem, x, c);
-        mainloop<true>(acc, f, smem, o, s, steps, stores, wave);
+        Self::first_reads(f, smem, o);
+        mainloop<Self, true>(acc, f, smem, o, s, steps, stores, wave);
+        Self::drain(acc, f);
       }
       dma_barrier();  // transfers past K have landed and every wave has left the ring
       const MxTileInfo done = ti;
@@ -851,7 +871,8 @@ struct MxRing {
 // 16 MB x 16 NB outputs per workgroup of NW waves; wave w takes the scale tiles (512 values of
 // K) w, w + NW, ... and reads its fragments straight from global memory, D steps ahead. With one
 // row of activations the operand B is read once from HBM in 64-byte runs of 16 rows, and nothing
-// waits on a barrier. The waves' partial sums meet in LDS in a fixed order.
+// waits on a barrier. The waves' partial sums meet in LDS in a fixed order. What depends on how operands are scaled is
+// the class's that derives from this one (Self): Scales, Now, scale_source, fetch_scales, take, step.
 template <int MB, int NB, int NW, int D, int FA, int FB, bool VM>
 struct MxDirect {
   static constexpr int kBM = 16 * MB, kBN = 16 * NB;
@@ -898,19 +919,54 @@ struct MxDirect {
     return (int)(lo | (hi << 16));
   }
 
+  // The scales of the four steps that are multiplied.
+  struct Now {
+    int a[MB], b[NB];
+  };
+  static __device__ __forceinline__ void take(Now& now, const Scales& sc, int kg) {
+    const uint32_t sel = (uint32_t)kg | ((uint32_t)(4 + kg) << 8) | 0x0C0C0000u;  // (0x0C: a zero byte)
+#pragma unroll
+    for (int i = 0; i < MB; ++i) now.a[i] = gather_scale(sc.a[i], sel);
+#pragma unroll
+    for (int j = 0; j < NB; ++j) now.b[j] = gather_scale(sc.b[j], sel);
+  }
+  // This lane's scales: row r of each fragment.
+  static __device__ __forceinline__ void scale_source(Src& s, const MxParams& mp, int g, int m0, int n0, int row_end, int lane) {
+    const int r = lane & 15;
+    const int64_t sao = (int64_t)(m0 >> 6) * mp.nsb * 1024, sbo = (int64_t)(n0 >> 6) * mp.nsb * 1024;
+    s.sa = make_rsrc(mp.sa + sao, mp.sa_bytes - sao);
+    s.sb = make_rsrc(mp.sb + (int64_t)g * mp.sb_bytes + sbo, mp.sb_bytes - sbo);
+#pragma unroll
+    for (int i = 0; i < MB; ++i) {
+      const int q = (m0 & 63) + i * 16 + r;
+      s.sao[i] = m0 + i * 16 + r < row_end ? (uint32_t)((q >> 6) * mp.nsb * 1024 + (q & 63) * 16) : kOOB;
+    }
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      const int q = (n0 & 63) + j * 16 + r;
+      s.sbo[j] = n0 + j * 16 + r < mp.k.N ? (uint32_t)((q >> 6) * mp.nsb * 1024 + (q & 63) * 16) : kOOB;
+    }
+  }
   template <int T>
-  static __device__ __forceinline__ void step(f32x4 (&acc)[MB][NB], Buf (&buf)[D], const Src& s, const int (&sa)[MB],
-                                              const int (&sb)[NB], int tile) {
-    Buf& b = buf[T % D];
+  static __device__ __forceinline__ void multiply(f32x4 (&acc)[MB][NB], const Buf& b, const Now& now) {
 #pragma unroll
     for (int i = 0; i < MB; ++i)
 #pragma unroll
-      for (int j = 0; j < NB; ++j) acc[i][j] = mx_mma<FA, FB, T>(b.b[j], b.a[i], acc[i][j], sb[j], sa[i]);
+      for (int j = 0; j < NB; ++j) acc[i][j] = mx_mma<FA, FB, T>(b.b[j], b.a[i], acc[i][j], now.b[j], now.a[i]);
+  }
+
+  template <class Self, int T>
+  static __device__ __forceinline__ void step(f32x4 (&acc)[MB][NB], Buf (&buf)[D], const Src& s, const typename Self::Now& now,
+                                              int tile) {
+    Buf& b = buf[T % D];
+    Self::template multiply<T>(acc, b, now);
     // the step D further on, in this tile of scales or in the wave's next
     fetch(b, s, T + D < 4 ? tile * 4 + T + D : (tile + NW) * 4 + T + D - 4);
   }
 
-  static __device__ __forceinline__ void run(const MxParams& mp) {
+  static __device__ __forceinline__ void run(const MxParams& mp) { run_as<MxDirect>(mp); }
+  template <class Self>
+  static __device__ __forceinline__ void run_as(const MxParams& mp) {
     const KParams& p = mp.k;
     __shared__ __attribute__((aligned(16))) float sums[NW * kPlane];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -930,23 +986,19 @@ struct MxDirect {
     const int64_t ao = (int64_t)m0 * p.lda, bo = (int64_t)n0 * p.ldb;
     s.a = make_rsrc((const char*)p.A + ao, p.a_bytes - ao);
     s.b = make_rsrc((const char*)p.B + (int64_t)g * p.b_bytes + bo, p.b_bytes - bo);
-    const int64_t sao = (int64_t)(m0 >> 6) * mp.nsb * 1024, sbo = (int64_t)(n0 >> 6) * mp.nsb * 1024;
-    s.sa = make_rsrc(mp.sa + sao, mp.sa_bytes - sao);
-    s.sb = make_rsrc(mp.sb + (int64_t)g * mp.sb_bytes + sbo, mp.sb_bytes - sbo);
+    Self::scale_source(s, mp, g, m0, n0, row_end, lane);
     s.nsb = t1;
     s.ka = min((int)p.lda, t1 * 4 * MxFmt<FA>::kStepBytes) - kg * 16;
     s.kb = min((int)p.ldb, t1 * 4 * MxFmt<FB>::kStepBytes) - kg * 16;
 #pragma unroll
     for (int i = 0; i < MB; ++i) {
-      const int row = i * 16 + r, q = (m0 & 63) + row;
+      const int row = i * 16 + r;
       s.ao[i] = m0 + row < row_end ? (uint32_t)(row * (int)p.lda + kg * 16) : kOOB;
-      s.sao[i] = m0 + row < row_end ? (uint32_t)((q >> 6) * mp.nsb * 1024 + (q & 63) * 16) : kOOB;
     }
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
-      const int row = j * 16 + r, q = (n0 & 63) + row;
+      const int row = j * 16 + r;
       s.bo[j] = n0 + row < p.N ? (uint32_t)(row * (int)p.ldb + kg * 16) : kOOB;
-      s.sbo[j] = n0 + row < p.N ? (uint32_t)((q >> 6) * mp.nsb * 1024 + (q & 63) * 16) : kOOB;
     }
     f32x4 acc[MB][NB];
 #pragma unroll
@@ -955,23 +1007,19 @@ struct MxDirect {
       for (int j = 0; j < NB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
     if (t0 + wave < t1) {
-      const uint32_t sel = (uint32_t)kg | ((uint32_t)(4 + kg) << 8) | 0x0C0C0000u;  // (0x0C: a zero byte)
-      Scales sc;
-      fetch_scales(sc, s, t0 + wave);
+      typename Self::Scales sc;
+      Self::fetch_scales(sc, s, t0 + wave);
       Buf buf[D];
 #pragma unroll
       for (int t = 0; t < D; ++t) fetch(buf[t], s, (t0 + wave) * 4 + t);
       for (int tile = t0 + wave; tile < t1; tile += NW) {
-        int sa[MB], sb[NB];
-#pragma unroll
-        for (int i = 0; i < MB; ++i) sa[i] = gather_scale(sc.a[i], sel);
-#pragma unroll
-        for (int j = 0; j < NB; ++j) sb[j] = gather_scale(sc.b[j], sel);
-        fetch_scales(sc, s, tile + NW);
-        step<0>(acc, buf, s, sa, sb, tile);
-        step<1>(acc, buf, s, sa, sb, tile);
-        step<2>(acc, buf, s, sa, sb, tile);
-        step<3>(acc, buf, s, sa, sb, tile);
+        typename Self::Now now;
+        Self::take(now, sc, kg);
+        Self::fetch_scales(sc, s, tile + NW);
+        step<Self, 0>(acc, buf, s, now, tile);
+        step<Self, 1>(acc, buf, s, now, tile);
+        step<Self, 2>(acc, buf, s, now, tile);
+        step<Self, 3>(acc, buf, s, now, tile);
       }
     }
     // lane l of block (i, j) holds row l % 16, columns 4 (l / 16) + [0, 4)

@@ -1,4 +1,4 @@
-// Host side of the MX product's C ABI: validation of a description and the choice of the
+// Host side of the C ABI of the MX and FP8 products: validation of a description and the choice of the
 // kernel. No HIP call is made here.
 #include "mx_plan.hpp"
 
@@ -22,14 +22,14 @@ int out_bytes(int32_t dt) {
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t blocks_of(int64_t a, int64_t b) { return a / b + (a % b != 0); }  // (cdiv of any size)
 
-gemm_status check_out(const char* name, int32_t dt, int64_t ld, int32_t M, int32_t N) {
+gemm_status check_out(const char* fn, const char* name, int32_t dt, int64_t ld, int32_t M, int32_t N) {
   if (dt == GEMM_DT_NONE) return GEMM_OK;
   const int es = out_bytes(dt);
-  if (!es) return fail(GEMM_ERR_UNSUPPORTED, "mx_gemm_create: %s must be F16, BF16 or F32", name);
-  if (ld < 0) return fail(GEMM_ERR_INVALID_ARG, "mx_gemm_create: negative leading dimension of %s", name);
-  if (ld > ((int64_t)1 << 48)) return fail(GEMM_ERR_UNSUPPORTED, "mx_gemm_create: leading dimension of %s beyond 2^48", name);
-  if (M > 1 && ld < N) return fail(GEMM_ERR_INVALID_ARG, "mx_gemm_create: leading dimension of %s below N", name);
-  if (ld * es % 16) return fail(GEMM_ERR_ALIGNMENT, "mx_gemm_create: leading dimension of %s is not a multiple of 16 bytes", name);
+  if (!es) return fail(GEMM_ERR_UNSUPPORTED, "%s: %s must be F16, BF16 or F32", fn, name);
+  if (ld < 0) return fail(GEMM_ERR_INVALID_ARG, "%s: negative leading dimension of %s", fn, name);
+  if (ld > ((int64_t)1 << 48)) return fail(GEMM_ERR_UNSUPPORTED, "%s: leading dimension of %s beyond 2^48", fn, name);
+  if (M > 1 && ld < N) return fail(GEMM_ERR_INVALID_ARG, "%s: leading dimension of %s below N", fn, name);
+  if (ld * es % 16) return fail(GEMM_ERR_ALIGNMENT, "%s: leading dimension of %s is not a multiple of 16 bytes", fn, name);
   return GEMM_OK;
 }
 }  // namespace
@@ -148,6 +148,45 @@ int64_t mx_workspace_bytes(const mx_gemm_plan& p, const MxChoice& c) {
   return c.split > 1 ? (int64_t)c.split * p.d.M * p.d.N * 4 : 0;
 }
 
+gemm_status block_gemm_init(const char* fn, const mx_gemm_desc& d, int32_t b_scaling, mx_gemm_plan* p) {
+  if (d.M < 0 || d.N < 0 || d.K < 0) return fail(GEMM_ERR_INVALID_ARG, "%s: negative size", fn);
+  if (d.groups < 0) return fail(GEMM_ERR_INVALID_ARG, "%s: negative group count", fn);
+  if (d.groups > kMaxVarlenGroups) return fail(GEMM_ERR_UNSUPPORTED, "%s: more than %d groups", fn, kMaxVarlenGroups);
+  for (int32_t f : {d.a_format, d.b_format})
+    if (f != MX_E2M1 && f != MX_E4M3) return fail(GEMM_ERR_INVALID_ARG, "%s: unknown format %d", fn, f);
+  for (int32_t t : {d.c, d.d, d.post})
+    if (t < GEMM_DT_NONE || t > GEMM_DT_E5M2) return fail(GEMM_ERR_INVALID_ARG, "%s: unknown type %d", fn, t);
+  if (d.d == GEMM_DT_NONE && d.post == GEMM_DT_NONE) return fail(GEMM_ERR_INVALID_ARG, "%s: neither D nor PostAct", fn);
+  if (d.act < GEMM_ACT_NONE || d.act > GEMM_ACT_SILU) return fail(GEMM_ERR_INVALID_ARG, "%s: unknown activation %d", fn, d.act);
+  if (d.act != GEMM_ACT_NONE && d.post == GEMM_DT_NONE) return fail(GEMM_ERR_INVALID_ARG, "%s: an activation without PostAct", fn);
+  if (d.tile < MX_TILE_AUTO || d.tile > MX_TILE_16) return fail(GEMM_ERR_INVALID_ARG, "%s: unknown tile %d", fn, d.tile);
+  if (d.split < 0 || d.split > 64) return fail(GEMM_ERR_INVALID_ARG, "%s: split must lie in [0, 64]", fn);
+  if (d.split > 1 && (d.groups || d.tile == MX_TILE_256))
+    return fail(GEMM_ERR_UNSUPPORTED, "%s: a grouped plan and the 256x256 tile do not split K", fn);
+  if (d.N % 8) return fail(GEMM_ERR_ALIGNMENT, "%s: N = %d is not a multiple of 8", fn, d.N);
+  // (256 rows of codes stay below 2^31 bytes: the kernels' offsets inside a tile are 32-bit)
+  if (d.K > (1 << 22)) return fail(GEMM_ERR_UNSUPPORTED, "%s: K above 2^22", fn);
+  gemm_status st = check_out(fn, "C", d.c, d.ldc, d.M, d.N);
+  if (st == GEMM_OK) st = check_out(fn, "D", d.d, d.ldd, d.M, d.N);
+  if (st == GEMM_OK) st = check_out(fn, "PostAct", d.post, d.ldp, d.M, d.N);
+  if (st != GEMM_OK) return st;
+  p->d = d;
+  p->b_scaling = b_scaling;
+  const bool fp8 = b_scaling >= 0;
+  auto codes = [&](int64_t rows, int32_t format) { return fp8 ? fp8_code_bytes(rows, d.K) : mx_code_bytes(rows, d.K, format); };
+  p->lda = (int32_t)codes(1, d.a_format);
+  p->ldb = (int32_t)codes(1, d.b_format);
+  p->a_bytes = codes(d.M, d.a_format);
+  p->b_bytes = codes(d.N, d.b_format);
+  p->sa_bytes = fp8 ? fp8_scale_bytes(d.M, d.K, FP8_ROWS) : mx_scale_bytes(d.M, d.K);
+  p->sb_bytes = fp8 ? fp8_scale_bytes(d.N, d.K, b_scaling) : mx_scale_bytes(d.N, d.K);
+  int32_t bm, bn;
+  mx_tile_extent(MX_TILE_128, &bm, &bn);
+  if (mx_row_blocks(*p, bm) * cdiv(d.N, bn) > 0xFFFFFF) return fail(GEMM_ERR_UNSUPPORTED, "%s: too many output tiles", fn);
+  clear_error();
+  return GEMM_OK;
+}
+
 }  // namespace gep
 
 using namespace gep;
@@ -174,46 +213,17 @@ int64_t mx_scale_bytes(int64_t rows, int64_t k) {
 }
 
 gemm_status mx_gemm_create(const mx_gemm_desc* d, mx_gemm_plan** out) {
-  if (!out) return fail(GEMM_ERR_INVALID_ARG, "mx_gemm_create: NULL out");
+  const char* fn = "mx_gemm_create";
+  if (!out) return fail(GEMM_ERR_INVALID_ARG, "%s: NULL out", fn);
   *out = nullptr;
-  if (!d) return fail(GEMM_ERR_INVALID_ARG, "mx_gemm_create: NULL desc");
-  if (d->M < 0 || d->N < 0 || d->K < 0) return fail(GEMM_ERR_INVALID_ARG, "mx_gemm_create: negative size");
-  if (d->groups < 0) return fail(GEMM_ERR_INVALID_ARG, "mx_gemm_create: negative group count");
-  if (d->groups > kMaxVarlenGroups) return fail(GEMM_ERR_UNSUPPORTED, "mx_gemm_create: more than %d groups", kMaxVarlenGroups);
-  for (int32_t f : {d->a_format, d->b_format})
-    if (f != MX_E2M1 && f != MX_E4M3) return fail(GEMM_ERR_INVALID_ARG, "mx_gemm_create: unknown format %d", f);
-  for (int32_t t : {d->c, d->d, d->post})
-    if (t < GEMM_DT_NONE || t > GEMM_DT_E5M2) return fail(GEMM_ERR_INVALID_ARG, "mx_gemm_create: unknown type %d", t);
-  if (d->d == GEMM_DT_NONE && d->post == GEMM_DT_NONE) return fail(GEMM_ERR_INVALID_ARG, "mx_gemm_create: neither D nor PostAct");
-  if (d->act < GEMM_ACT_NONE || d->act > GEMM_ACT_SILU) return fail(GEMM_ERR_INVALID_ARG, "mx_gemm_create: unknown activation %d", d->act);
-  if (d->act != GEMM_ACT_NONE && d->post == GEMM_DT_NONE) return fail(GEMM_ERR_INVALID_ARG, "mx_gemm_create: an activation without PostAct");
-  if (d->tile < MX_TILE_AUTO || d->tile > MX_TILE_16) return fail(GEMM_ERR_INVALID_ARG, "mx_gemm_create: unknown tile %d", d->tile);
-  if (d->split < 0 || d->split > 64) return fail(GEMM_ERR_INVALID_ARG, "mx_gemm_create: split must lie in [0, 64]");
-  if (d->split > 1 && (d->groups || d->tile == MX_TILE_256))
-    return fail(GEMM_ERR_UNSUPPORTED, "mx_gemm_create: a grouped plan and MX_TILE_256 do not split K");
-  if (d->N % 8) return fail(GEMM_ERR_ALIGNMENT, "mx_gemm_create: N = %d is not a multiple of 8", d->N);
-  // (256 rows of codes stay below 2^31 bytes: the kernels' offsets inside a tile are 32-bit)
-  if (d->K > (1 << 22)) return fail(GEMM_ERR_UNSUPPORTED, "mx_gemm_create: K above 2^22");
-  gemm_status st = check_out("C", d->c, d->ldc, d->M, d->N);
-  if (st == GEMM_OK) st = check_out("D", d->d, d->ldd, d->M, d->N);
-  if (st == GEMM_OK) st = check_out("PostAct", d->post, d->ldp, d->M, d->N);
-  if (st != GEMM_OK) return st;
+  if (!d) return fail(GEMM_ERR_INVALID_ARG, "%s: NULL desc", fn);
   mx_gemm_plan* p = new (std::nothrow) mx_gemm_plan;
-  if (!p) return fail(GEMM_ERR_NO_MEMORY, "mx_gemm_create: out of memory");
-  p->d = *d;
-  p->lda = (int32_t)mx_code_bytes(1, d->K, d->a_format);
-  p->ldb = (int32_t)mx_code_bytes(1, d->K, d->b_format);
-  p->a_bytes = mx_code_bytes(d->M, d->K, d->a_format);
-  p->b_bytes = mx_code_bytes(d->N, d->K, d->b_format);
-  p->sa_bytes = mx_scale_bytes(d->M, d->K);
-  p->sb_bytes = mx_scale_bytes(d->N, d->K);
-  int32_t bm, bn;
-  mx_tile_extent(MX_TILE_128, &bm, &bn);
-  if (mx_row_blocks(*p, bm) * cdiv(d->N, bn) > 0xFFFFFF) {
+  if (!p) return fail(GEMM_ERR_NO_MEMORY, "%s: out of memory", fn);
+  const gemm_status st = block_gemm_init(fn, *d, -1, p);
+  if (st != GEMM_OK) {
     delete p;
-    return fail(GEMM_ERR_UNSUPPORTED, "mx_gemm_create: too many output tiles");
+    return st;
   }
-  clear_error();
   *out = p;
   return GEMM_OK;
 }
@@ -238,6 +248,64 @@ gemm_status mx_gemm_workspace(const mx_gemm_plan* plan, int32_t num_cus, int64_t
   *bytes = mx_workspace_bytes(*plan, mx_choice(*plan, num_cus, true));
   clear_error();
   return GEMM_OK;
+}
+
+// ---- FP8 products
+
+static_assert((int)FP8_TILE_AUTO == (int)MX_TILE_AUTO && (int)FP8_TILE_256 == (int)MX_TILE_256 && (int)FP8_TILE_128 == (int)MX_TILE_128 &&
+                  (int)FP8_TILE_32X64 == (int)MX_TILE_32X64 && (int)FP8_TILE_32 == (int)MX_TILE_32 &&
+                  (int)FP8_TILE_16X32 == (int)MX_TILE_16X32 && (int)FP8_TILE_16 == (int)MX_TILE_16,
+              "one numbering of the tiles");
+
+int64_t fp8_code_bytes(int64_t rows, int64_t k) {
+  if (rows < 0 || k < 0) return -1;
+  int64_t row, all;
+  if (__builtin_mul_overflow(blocks_of(k, 16), (int64_t)16, &row) || __builtin_mul_overflow(rows, row, &all)) return rows == 0 ? 0 : -1;
+  return all;
+}
+
+int64_t fp8_scale_bytes(int64_t rows, int64_t k, int32_t scaling) {
+  if (rows < 0 || k < 0 || (scaling != FP8_ROWS && scaling != FP8_TILES)) return -1;
+  int64_t quads, all;
+  const int64_t units = scaling == FP8_ROWS ? blocks_of(rows, 64) : blocks_of(rows, FP8_BLOCK);
+  if (__builtin_mul_overflow(units, blocks_of(blocks_of(k, FP8_BLOCK), 4), &quads) ||
+      __builtin_mul_overflow(quads, (int64_t)(scaling == FP8_ROWS ? 64 * 16 : 16), &all))
+    return -1;
+  return all;
+}
+
+gemm_status fp8_gemm_create(const fp8_gemm_desc* d, fp8_gemm_plan** out) {
+  const char* fn = "fp8_gemm_create";
+  if (!out) return fail(GEMM_ERR_INVALID_ARG, "%s: NULL out", fn);
+  *out = nullptr;
+  if (!d) return fail(GEMM_ERR_INVALID_ARG, "%s: NULL desc", fn);
+  if (d->b_scaling != FP8_ROWS && d->b_scaling != FP8_TILES) return fail(GEMM_ERR_INVALID_ARG, "%s: unknown scaling %d", fn, d->b_scaling);
+  fp8_gemm_plan* p = new (std::nothrow) fp8_gemm_plan;
+  if (!p) return fail(GEMM_ERR_NO_MEMORY, "%s: out of memory", fn);
+  const mx_gemm_desc m{d->M, d->N, d->K, d->groups, MX_E4M3, MX_E4M3, d->c, d->d, d->post, d->act, d->tile, d->split, d->ldc, d->ldd, d->ldp};
+  const gemm_status st = block_gemm_init(fn, m, d->b_scaling, p);
+  if (st != GEMM_OK) {
+    delete p;
+    return st;
+  }
+  *out = p;
+  return GEMM_OK;
+}
+
+gemm_status fp8_gemm_destroy(fp8_gemm_plan* plan) {
+  delete plan;
+  clear_error();
+  return GEMM_OK;
+}
+
+gemm_status fp8_gemm_plan_tile(const fp8_gemm_plan* plan, int32_t num_cus, int32_t* tile, int32_t* split) {
+  if (!plan || num_cus < 1) return fail(GEMM_ERR_INVALID_ARG, "fp8_gemm_plan_tile: NULL plan or no compute units");
+  return mx_gemm_plan_tile(plan, num_cus, tile, split);
+}
+
+gemm_status fp8_gemm_workspace(const fp8_gemm_plan* plan, int32_t num_cus, int64_t* bytes) {
+  if (!plan || !bytes || num_cus < 1) return fail(GEMM_ERR_INVALID_ARG, "fp8_gemm_workspace: NULL argument or no compute units");
+  return mx_gemm_workspace(plan, num_cus, bytes);
 }
 
 }  // extern "C"

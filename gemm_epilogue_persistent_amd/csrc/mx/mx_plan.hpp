@@ -1,14 +1,16 @@
-// Host-side plan of an MX product.
+// Host-side plan of a product of block-scaled operands: MX, or FP8 with a scale per 128 values.
 #pragma once
 #include <stdint.h>
 
 #include <atomic>
 
+#include "../../../include/fp8_mi355x.h"
 #include "../../../include/mx_mi355x.h"
 #include "../params.hpp"
 
 struct mx_gemm_plan {
-  mx_gemm_desc d;
+  mx_gemm_desc d;               // (FP8: both formats MX_E4M3)
+  int32_t b_scaling = -1;       // FP8 operands: the fp8_scaling of B; -1: MX operands
   int64_t a_bytes, b_bytes;    // codes (B: of one group)
   int64_t sa_bytes, sb_bytes;  // scales
   int32_t lda, ldb;            // bytes of a row of codes
@@ -17,7 +19,15 @@ struct mx_gemm_plan {
   mutable std::atomic<uint64_t> chosen[2] = {{0}, {0}};
 };
 
+// (An FP8 plan is the same thing under its own entry points.)
+struct fp8_gemm_plan : mx_gemm_plan {};
+
 namespace gep {
+// Validate `d` for the entry point `fn` and fill in `p`.
+gemm_status block_gemm_init(const char* fn, const mx_gemm_desc& d, int32_t b_scaling, mx_gemm_plan* p);
+// Launch a plan's product for the entry point `fn`.
+gemm_status block_gemm_run(const char* fn, const mx_gemm_plan* plan, const mx_gemm_args* a, void* stream);
+
 // How a plan runs on `cus` compute units: the tile (an mx_tile, never AUTO), over how many
 // workgroups a tile's K is shared out, and the scale tiles (512 values of K) of each.
 struct MxChoice {

@@ -207,29 +207,13 @@ def _operands(a, b):
             raise TypeError(f"{name}: an MxTensor expected")
 
 
-class MxPlan:
-    """A validated plan of D = a b^T + C and PostAct = act(a b^T + C) for one problem shape (host
-    memory; reusable, from several streams too). a (m, k); b (n, k), or (G, n, k) with
-    cu_seqlens_m: int32 of G + 1 row offsets on the GPU, whose values are read by each run. n is a
-    multiple of 8. C, D, PostAct: 16- or 32-bit floats, rows contiguous, row strides of whole 16
-    bytes; at least one of D, PostAct. tile, split: "auto" and 0, or the kernel to use ("256", "128",
-    "32x64", "32", "16x32", "16") and over how many workgroups it shares out a tile's K.
+class _PlanBase:
+    """What the plans of products of block-scaled operands share: the checks of a call, the handle and the
+    workspaces. The names of the library's functions stand in the classes."""
 
-    Sums are held in fp32, but with an e4m3 operand the matrix instruction keeps the products of a block
-    of 32 only to 2^-13 of the block's largest: a float32 output is off by about 1e-5 (e2m1 on both sides:
-    as an fp32 product).
+    handle = None
 
-    Where K is shared out, a run needs a workspace for the partial sums: workspace_bytes of memory that is
-    the run's stream's own. The plan keeps one for each stream that it has run on (allocated by the first
-    run there, and freed with the plan); a run that is captured into a graph takes one from the graph's
-    memory. (Threads that run one plan on one stream at the same time need workspaces of their own.)"""
-
-    def __init__(self, a, b, C=None, D=None, PostAct=None, act="none", cu_seqlens_m=None, tile="auto",
-                 split=0):
-        self.handle = None
-        _operands(a, b)
-        _plain_mx("a", a)
-        self._sig = self._signature(a, b, C, D, PostAct, cu_seqlens_m)
+    def _check_operands(self, a, b, cu_seqlens_m, act, tile):
         if b.device != a.device or not a.codes.is_cuda:
             raise ValueError("a and b must be on one GPU")
         if a.k != b.k:
@@ -243,31 +227,32 @@ class MxPlan:
                 raise ValueError("rows without a group")
         if act not in ACT:
             raise ValueError(f"unknown activation {act!r}")
-        if tile not in MX_TILE:
+        if tile not in self._tiles:
             raise ValueError(f"unknown tile {tile!r}")
-        d = _abi.MxGemmDesc()
-        d.M, d.N, d.K, d.groups = (_abi.int32(n, v) for n, v in (
-            ("rows of a", a.rows), ("rows of b", b.rows), ("k", a.k), ("groups", b.groups or 0)))
-        d.a_format, d.b_format = MX_FORMAT[a.fmt], MX_FORMAT[b.fmt]
+
+    def _finish(self, d, a, b, C, D, PostAct, act, cu_seqlens_m, tile, split):
+        """The outputs' part of the description `d`, and the plan itself."""
+        self._sig = self._signature(a, b, C, D, PostAct, cu_seqlens_m)
         shape = (a.rows, b.rows)
         d.c, d.ldc = _out("C", C, shape, a.device)
         d.d, d.ldd = _out("D", D, shape, a.device)
         d.post, d.ldp = _out("PostAct", PostAct, shape, a.device)
-        d.act, d.tile, d.split = ACT[act], MX_TILE[tile], _abi.int32("split", split)
+        d.act, d.tile, d.split = ACT[act], self._tiles[tile], _abi.int32("split", split)
         self.desc, self.device = d, a.device
         self._lib = _abi.load()
+        self._enqueue = getattr(self._lib, self._run)
         h = ctypes.c_void_p()
-        _abi.check(self._lib.mx_gemm_create(ctypes.byref(d), ctypes.byref(h)))
+        _abi.check(getattr(self._lib, self._create)(ctypes.byref(d), ctypes.byref(h)))
         self.handle = h
         n = ctypes.c_int64()
-        _abi.check(self._lib.mx_gemm_workspace(h, self._cus(), ctypes.byref(n)))
+        _abi.check(getattr(self._lib, self._workspace_size)(h, self._cus(), ctypes.byref(n)))
         self.workspace_bytes = n.value
         self._workspaces, self._workspace = {}, None  # by stream pointer; that of the run before
 
     def __del__(self):
         h = getattr(self, "handle", None)
         if h is not None and h.value:
-            self._lib.mx_gemm_destroy(h)
+            getattr(self._lib, self._destroy)(h)
             self.handle = None
 
     def _cus(self):
@@ -279,11 +264,6 @@ class MxPlan:
             raise ValueError("cu_seqlens_m: contiguous int32 vector on the operands' GPU expected")
         if cu.numel() != b.groups + 1:
             raise ValueError(f"cu_seqlens_m: {b.groups + 1} offsets expected")
-
-    @staticmethod
-    def _signature(a, b, C, D, PostAct, cu):
-        return (a.fmt, a.codes.shape, a.k, a.device, b.fmt, b.codes.shape, b.device) + tuple(
-            None if t is None else (t.dtype, t.shape, t.stride(), t.device) for t in (C, D, PostAct, cu))
 
     def run(self, a, b, C=None, D=None, PostAct=None, cu_seqlens_m=None, stream=None, workspace=None):
         """Enqueue on `stream` (default: torch's current stream of the operands' device). The
@@ -299,7 +279,7 @@ class MxPlan:
         args = _abi.MX_GEMM_ARGS.pack(a.codes.data_ptr(), a.scales.data_ptr(), b.codes.data_ptr(), b.scales.data_ptr(),
                                       *[0 if t is None else t.data_ptr() for t in (C, D, PostAct, cu_seqlens_m, workspace)],
                                       0 if workspace is None else workspace.numel())
-        _launch(self.device, stream, self._lib.mx_gemm_run, self.handle, args)
+        _launch(self.device, stream, self._enqueue, self.handle, args)
 
     def _stream_workspace(self, stream):
         """The workspace of a run on `stream`. It is allocated on that very stream: a block that the
@@ -321,8 +301,47 @@ class MxPlan:
     def tile(self, num_cus=None):
         """(kernel, split) this plan runs with on a device with num_cus compute units."""
         t, n = ctypes.c_int32(), ctypes.c_int32()
-        _abi.check(self._lib.mx_gemm_plan_tile(self.handle, _abi.int32("num_cus", num_cus or self._cus()), ctypes.byref(t), ctypes.byref(n)))
-        return next(k for k, v in MX_TILE.items() if v == t.value), n.value
+        _abi.check(getattr(self._lib, self._plan_tile)(self.handle, _abi.int32("num_cus", num_cus or self._cus()), ctypes.byref(t), ctypes.byref(n)))
+        return next(k for k, v in self._tiles.items() if v == t.value), n.value
+
+
+class MxPlan(_PlanBase):
+    """A validated plan of D = a b^T + C and PostAct = act(a b^T + C) for one problem shape (host
+    memory; reusable, from several streams too). a (m, k); b (n, k), or (G, n, k) with
+    cu_seqlens_m: int32 of G + 1 row offsets on the GPU, whose values are read by each run. n is a
+    multiple of 8. C, D, PostAct: 16- or 32-bit floats, rows contiguous, row strides of whole 16
+    bytes; at least one of D, PostAct. tile, split: "auto" and 0, or the kernel to use ("256", "128",
+    "32x64", "32", "16x32", "16") and over how many workgroups it shares out a tile's K.
+
+    Sums are held in fp32, but with an e4m3 operand the matrix instruction keeps the products of a block
+    of 32 only to 2^-13 of the block's largest: a float32 output is off by about 1e-5 (e2m1 on both sides:
+    as an fp32 product).
+
+    Where K is shared out, a run needs a workspace for the partial sums: workspace_bytes of memory that is
+    the run's stream's own. The plan keeps one for each stream that it has run on (allocated by the first
+    run there, and freed with the plan); a run that is captured into a graph takes one from the graph's
+    memory. (Threads that run one plan on one stream at the same time need workspaces of their own.)"""
+
+    _create, _destroy, _run, _plan_tile, _workspace_size = (
+        "mx_gemm_create", "mx_gemm_destroy", "mx_gemm_run", "mx_gemm_plan_tile", "mx_gemm_workspace")
+    _tiles = MX_TILE
+
+    def __init__(self, a, b, C=None, D=None, PostAct=None, act="none", cu_seqlens_m=None, tile="auto",
+                 split=0):
+        self.handle = None
+        _operands(a, b)
+        _plain_mx("a", a)
+        self._check_operands(a, b, cu_seqlens_m, act, tile)
+        d = _abi.MxGemmDesc()
+        d.M, d.N, d.K, d.groups = (_abi.int32(n, v) for n, v in (
+            ("rows of a", a.rows), ("rows of b", b.rows), ("k", a.k), ("groups", b.groups or 0)))
+        d.a_format, d.b_format = MX_FORMAT[a.fmt], MX_FORMAT[b.fmt]
+        self._finish(d, a, b, C, D, PostAct, act, cu_seqlens_m, tile, split)
+
+    @staticmethod
+    def _signature(a, b, C, D, PostAct, cu):
+        return (a.fmt, a.codes.shape, a.k, a.device, b.fmt, b.codes.shape, b.device) + tuple(
+            None if t is None else (t.dtype, t.shape, t.stride(), t.device) for t in (C, D, PostAct, cu))
 
 
 def mx_gemm(a, b, D=None, C=None, PostAct=None, act="none", cu_seqlens_m=None, stream=None, tile="auto",
