@@ -30,12 +30,14 @@ from .fp8 import (Fp8Plan, Fp8Tensor, fp8_act, fp8_act_backward, fp8_dequantize,
                   fp8_quantize)
 from .mx import MxPlan, MxTensor, mx_dequantize, mx_empty, mx_gemm, mx_quantize
 from .norm import rmsnorm, rmsnorm_backward, rmsnorm_backward_workspace
+from .router import RouterBalance, balance_empty, router_balance, router_balance_backward, router_balance_workspace
 
 __all__ = ["Plan", "gemm", "gemm_dact", "gemm_create", "gemm_run", "plan_grid", "configs", "tune", "fastdivmod_params",
            "fastdivmod_check", "check_cu_seqlens", "tuned_config", "GemmError", "library_path",
            "MxTensor", "MxPlan", "mx_empty", "mx_quantize", "mx_dequantize", "mx_gemm",
            "rmsnorm", "rmsnorm_backward", "rmsnorm_backward_workspace",
-           "Fp8Tensor", "Fp8Plan", "fp8_empty", "fp8_quantize", "fp8_dequantize", "fp8_gemm", "fp8_act", "fp8_act_backward"]
+           "Fp8Tensor", "Fp8Plan", "fp8_empty", "fp8_quantize", "fp8_dequantize", "fp8_gemm", "fp8_act", "fp8_act_backward",
+           "RouterBalance", "balance_empty", "router_balance", "router_balance_backward", "router_balance_workspace"]
 
 
 def library_path():

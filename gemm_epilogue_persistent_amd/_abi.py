@@ -16,6 +16,7 @@ MX_TILE = {"auto": 0, "256": 1, "128": 2, "32x64": 3, "32": 4, "16x32": 5, "16":
 FP8_TILE = {"auto": 0, "256": 1, "128": 2, "32x64": 3, "32": 4, "16x32": 5, "16": 6}
 MX_HEADER = os.path.join(os.path.dirname(HERE), "include", "mx_mi355x.h")
 FP8_HEADER = os.path.join(os.path.dirname(HERE), "include", "fp8_mi355x.h")
+ROUTER_HEADER = os.path.join(os.path.dirname(HERE), "include", "router_mi355x.h")
 
 
 class GemmDesc(ctypes.Structure):
@@ -78,6 +79,20 @@ class Fp8ActBackwardArgs(ctypes.Structure):
         (n, ctypes.c_int64) for n in ("lddy", "lddx", "ldy")]
 
 
+class RouterBalanceArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("batch", "tokens", "experts", "k", "type", "scores", "index_bytes")] + [
+        ("coef", ctypes.c_float)] + [
+        (n, ctypes.c_void_p) for n in ("logits", "chosen", "mask", "counts", "valid", "cu_seqlens", "probs", "loss", "workspace")] + [
+        (n, ctypes.c_int64) for n in ("workspace_bytes", "logits_ld", "logits_batch")]
+
+
+class RouterBalanceBackwardArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("batch", "tokens", "experts", "k", "type", "scores")] + [
+        ("coef", ctypes.c_float)] + [
+        (n, ctypes.c_void_p) for n in ("logits", "mask", "counts", "valid", "grad", "dlogits")] + [
+        (n, ctypes.c_int64) for n in ("logits_ld", "logits_batch", "dlogits_ld", "dlogits_batch")]
+
+
 class RmsnormArgs(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("rows", "cols", "type", "q_format")] + [("eps", ctypes.c_float)] + [
         (n, ctypes.c_void_p) for n in ("x", "residual", "weight", "h_out", "y", "q_codes", "q_scales", "rstd")] + [
@@ -97,6 +112,8 @@ RMSNORM_ARGS = struct.Struct("@4if8P4q")
 RMSNORM_BACKWARD_ARGS = struct.Struct("@3i8P5q")
 FP8_ACT_ARGS = struct.Struct("@4i6P2q")
 FP8_ACT_BACKWARD_ARGS = struct.Struct("@4i11P3q")
+ROUTER_BALANCE_ARGS = struct.Struct("@7if9P3q")
+ROUTER_BALANCE_BACKWARD_ARGS = struct.Struct("@6if6P4q")
 
 
 def int32(name, value):
@@ -196,6 +213,12 @@ def load():
         lib.fp8_gemm_plan_tile.argtypes = [vp, i32, ctypes.POINTER(i32), ctypes.POINTER(i32)]
         lib.fp8_gemm_workspace.restype = ctypes.c_int
         lib.fp8_gemm_workspace.argtypes = [vp, i32, ctypes.POINTER(i64)]
+        lib.router_balance.restype = ctypes.c_int
+        lib.router_balance.argtypes = [vp, vp]
+        lib.router_balance_backward.restype = ctypes.c_int
+        lib.router_balance_backward.argtypes = [vp, vp]
+        lib.router_balance_workspace.restype = i64
+        lib.router_balance_workspace.argtypes = [i32, i32, i32]
         lib.gemm_status_string.restype = ctypes.c_char_p
         lib.gemm_status_string.argtypes = [ctypes.c_int]
         lib.gemm_last_error.restype = ctypes.c_char_p

@@ -26,6 +26,9 @@ UNITS += [os.path.join("mx", u) for u in ["mx_plan.cpp", "mx_api.hip", "mx_quant
 UNITS += [os.path.join("fp8", u) for u in ["fp8_quant.hip"] + [
     f"fp8_inst_{b}_{v}.hip" for b in ("rows", "tiles") for v in ("dense", "vm")]]
 
+# the router's counts and balance loss
+UNITS += [os.path.join("router", "balance.hip")]
+
 
 def hipcc() -> str:
     for c in (os.environ.get("HIPCC"), "/opt/rocm/bin/hipcc", shutil.which("hipcc")):

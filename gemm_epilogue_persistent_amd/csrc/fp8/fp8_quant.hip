@@ -270,9 +270,10 @@ __global__ __launch_bounds__(kThreads) void act_backward_kernel(const BackArgs<T
       settle<false>(in[p], c, a.cols);
       unpack(in[p], v[p]);
       fp8_values8(w[p], scale[p], x);
+      const float nan = -0.f * scale[p];  // NaN for a NaN block, whose slopes are not; -0 changes no other product
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float d = v[p][e] * slope(a.act, x[e]);
+        const float d = __builtin_fmaf(v[p][e], slope(a.act, x[e]), nan);
         v[p][e] = r + p < a.rows && c + e < a.cols ? d : 0.f;
       }
       if (a.dx && r + p < a.rows) store_chunk<false>(a.dx + (int64_t)(r + p) * a.lddx, c, a.cols, pack<T>(v[p]));

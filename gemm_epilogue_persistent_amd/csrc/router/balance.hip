@@ -1,0 +1,570 @@
+// Per-expert counts, balance loss and its gradient (router_balance, router_balance_backward of the public header).
+//
+// Bound by memory: the logits are read once in each direction, a value costs two or three exponentials. G
+// neighbouring lanes hold a token's logits, 8 (or 16, 32) a lane, so that a row is one coalesced load and its sums stay in
+// registers; a workgroup takes a run of tokens of one sequence.
+#include <initializer_list>
+#include <type_traits>
+
+#include "../../../include/router_mi355x.h"
+#include "../mx/mx_common.hpp"
+
+namespace gep {
+gemm_status fail(gemm_status st, const char* fmt, ...);
+void clear_error();
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxExperts = 2048;
+
+// ---- exchange over the G lanes of a row (G a power of two; fixed order, the same result in every lane)
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), CTRL, 0xF, 0xF, true));
+}
+template <int G, typename F>
+__device__ __forceinline__ float reduce(float v, F&& f) {
+  if constexpr (G >= 2) v = f(v, dpp<0xB1>(v));   // lanes 1 0 3 2
+  if constexpr (G >= 4) v = f(v, dpp<0x4E>(v));   // lanes 2 3 0 1
+  if constexpr (G >= 8) v = f(v, dpp<0x141>(v));  // within 8: i <-> 7 - i
+  if constexpr (G >= 16) v = f(v, dpp<0x140>(v));  // within 16: i <-> 15 - i
+  if constexpr (G >= 32) v = f(v, __shfl_xor(v, 16));
+  if constexpr (G >= 64) v = f(v, __shfl_xor(v, 32));
+  return v;
+}
+template <int G>
+__device__ __forceinline__ float row_sum(float v) { return reduce<G>(v, [](float a, float b) { return a + b; }); }
+template <int G>
+__device__ __forceinline__ float row_max(float v) { return reduce<G>(v, [](float a, float b) { return fmaxf(a, b); }); }
+
+// e^x of x <= 0 to about an fp32 step: x log2 e in two parts, so that the error does not grow with x.
+__device__ __forceinline__ float exp_neg(float x) {
+  const float t = x * 1.44269502162933349609375f;
+  const float lo = __builtin_fmaf(x, 1.92596299112661e-8f, __builtin_fmaf(x, 1.44269502162933349609375f, -t));
+  const float e = __builtin_amdgcn_exp2f(t);
+  return t < -150.f ? 0.f : __builtin_fmaf(e, lo * 0.693147182464599609375f, e);  // (lo of -inf is NaN)
+}
+
+// The scores of a row: p (8 N a lane) from its logits x, -inf past the last expert. miss: 1 - s(x) (sigmoid). A row
+// of -inf alone gives zeros.
+template <int G, int N>
+__device__ __forceinline__ void row_scores(int scores, const float (&x)[N][8], float (&p)[N][8], float (&miss)[N][8]) {
+  float top = -__builtin_inff();
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = fmaxf(top, x[i][e]);
+  top = row_max<G>(top);
+  const bool none = top == -__builtin_inff();
+  float sum = 0.f;
+  if (scores == ROUTER_SOFTMAX) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        p[i][e] = none ? 0.f : exp_neg(x[i][e] - top);
+        p[i][e] = x[i][e] != x[i][e] ? x[i][e] : p[i][e];
+        sum += p[i][e];
+      }
+  } else {
+    // s(x) e^-m with m = min(top, 0), which the quotient cancels: logits that are all far below zero keep their digits
+    const float m = fminf(top, 0.f);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float v = x[i][e], a = exp_neg(-fabsf(v)), q = __builtin_amdgcn_rcpf(1.f + a);
+        p[i][e] = none ? 0.f : exp_neg(fminf(v, 0.f) - m) * q;
+        p[i][e] = v != v ? v : p[i][e];
+        miss[i][e] = v < 0.f ? q : a * q;
+        sum += p[i][e];
+      }
+  }
+  sum = row_sum<G>(sum);
+  const float inv = none ? 1.f : 1.f / sum;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) p[i][e] *= inv;
+}
+
+template <typename T, int G, int N>
+struct Rows {
+  static constexpr int kGroups = kThreads / G;  // rows a pass
+  Chunk<T> c[N];
+  // Lane l of the row's group takes chunks l, l + G, ...
+  __device__ __forceinline__ void load(const T* row, int experts, int lane) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) c[i] = load_chunk<false>(row, (i * G + lane) * 8, experts);
+  }
+  __device__ __forceinline__ void values(int experts, int lane, float (&x)[N][8]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int at = (i * G + lane) * 8;
+      settle<false>(c[i], at, experts);
+      unpack(c[i], x[i]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[i][e] = at + e < experts ? x[i][e] : -__builtin_inff();
+    }
+  }
+};
+
+struct Forward {
+  int batch, tokens, experts, k, scores, index_bytes;
+  float coef;
+  const void* logits;
+  const void* chosen;
+  const uint8_t* mask;
+  int32_t *counts, *valid, *cu_seqlens;
+  float *probs, *loss;
+  int64_t ld, ldb;
+  int per, wgs;  // tokens of a workgroup, workgroups of a sequence
+  // partial results of workgroup i of sequence b: part (b * wgs + i); and what the join shares
+  float* part_p;
+  int32_t *part_c, *part_n;
+  float* part_loss;
+  uint32_t* ticket;
+};
+
+// Expert e of sequence b is joined; its share of sum_e c_e P_e / n.
+__device__ __forceinline__ float finish_expert(const Forward& a, int b, int e, float p, int32_t c, int32_t n) {
+  const float mean = n > 0 ? p / (float)n : 0.f;
+  a.probs[(int64_t)b * a.experts + e] = mean;
+  a.counts[(int64_t)b * a.experts + e] = c;
+  return n > 0 ? (float)c / (float)n * mean : 0.f;
+}
+__device__ __forceinline__ float loss_factor(const Forward& a) { return a.coef * (float)a.experts / ((float)a.batch * (float)a.k); }
+
+// Sum over the workgroup in a fixed order, in every thread. buf: a float for each wave.
+__device__ __forceinline__ float block_sum(float v, float* buf) {
+  v = row_sum<64>(v);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) buf[threadIdx.x >> 6] = v;
+  __syncthreads();
+  return (buf[0] + buf[1]) + (buf[2] + buf[3]);
+}
+// cu[i + 1] = sum of the first i + 1 totals (total(e): a function); one workgroup.
+template <typename F>
+__device__ __forceinline__ void offsets(int32_t* cu, int experts, F&& total, int32_t* buf) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int32_t base = 0;
+  if (tid == 0) cu[0] = 0;
+  for (int e0 = 0; e0 < experts; e0 += kThreads) {
+    const int e = e0 + tid;
+    int32_t v = e < experts ? total(e) : 0;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int32_t u = __shfl_up(v, off);
+      if (lane >= off) v += u;
+    }
+    __syncthreads();
+    if (lane == 63) buf[wave] = v;
+    __syncthreads();
+    int32_t before = base;
+    for (int w = 0; w < wave; ++w) before += buf[w];
+    if (e < experts) cu[e + 1] = before + v;
+    base += buf[0] + buf[1] + buf[2] + buf[3];
+  }
+}
+
+// The tokens of one workgroup. ONE: they are all there are, and the results are finished here.
+template <typename T, int G, int N, bool ONE>
+__global__ __launch_bounds__(kThreads) void balance_kernel(const Forward a) {
+  constexpr int kCols = 8 * G * N;
+  __shared__ float psum[4][kCols];
+  __shared__ int32_t hist[kCols];
+  __shared__ int32_t tokens_seen;
+  __shared__ float red[4];
+  const int tid = threadIdx.x, lane = tid & (G - 1), group = tid / G, wave = tid >> 6;
+  const int b = blockIdx.y, wg = blockIdx.x;
+  const int t0 = wg * a.per, t1 = min(a.tokens, t0 + a.per);
+  const uint8_t* mask = a.mask ? a.mask + (int64_t)b * a.tokens : nullptr;
+  if (!ONE && tid == 0 && b == 0 && wg == 0) *a.ticket = 0;  // (for the join, the next launch)
+  for (int e = tid; e < kCols; e += kThreads) hist[e] = 0;
+  if (tid == 0) tokens_seen = 0;
+  __syncthreads();
+  // counts
+  const int64_t id0 = ((int64_t)b * a.tokens + t0) * a.k;
+  const uint32_t ids = (uint32_t)(t1 - t0) * (uint32_t)a.k;
+  for (uint32_t i = tid; i < ids; i += kThreads) {
+    const int64_t e = a.index_bytes == 8 ? ((const int64_t*)a.chosen)[id0 + i] : (int64_t)((const int32_t*)a.chosen)[id0 + i];
+    if (e >= 0 && e < a.experts && (!mask || mask[t0 + i / (uint32_t)a.k])) atomicAdd(&hist[(int)e], 1);
+  }
+  // scores
+  float acc[N][8];
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[i][e] = 0.f;
+  const T* logits = (const T*)a.logits + b * a.ldb;
+  int seen = 0;
+  constexpr int kGroups = Rows<T, G, N>::kGroups, kAhead = N == 1 ? 4 : (N == 2 ? 2 : 1);
+  for (int t = t0 + group; t < t1; t += kGroups * kAhead) {
+    Rows<T, G, N> rows[kAhead];
+    bool use[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int tt = t + u * kGroups, at = min(tt, t1 - 1);
+      use[u] = tt < t1 && (!mask || mask[at]);
+      rows[u].load(logits + at * a.ld, a.experts, lane);
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      float x[N][8], p[N][8], miss[N][8];
+      rows[u].values(a.experts, lane, x);
+      row_scores<G, N>(a.scores, x, p, miss);
+      seen += use[u];
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[i][e] += use[u] ? p[i][e] : 0.f;
+    }
+  }
+  if (lane == 0 && seen) atomicAdd(&tokens_seen, seen);
+  // over the row groups of the wave, then over the waves
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+#pragma unroll
+      for (int off = G; off < 64; off <<= 1) acc[i][e] += __shfl_xor(acc[i][e], off);
+  if ((tid & 63) < G) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) psum[wave][(i * G + lane) * 8 + e] = acc[i][e];
+  }
+  __syncthreads();
+  const int32_t n = tokens_seen;
+  float mine = 0.f;
+  for (int e = tid; e < a.experts; e += kThreads) {
+    const float p = (psum[0][e] + psum[1][e]) + (psum[2][e] + psum[3][e]);
+    if constexpr (ONE) {
+      mine += finish_expert(a, b, e, p, hist[e], n);
+    } else {
+      const int64_t at = ((int64_t)b * a.wgs + wg) * a.experts + e;
+      a.part_p[at] = p;
+      a.part_c[at] = hist[e];
+    }
+  }
+  if constexpr (ONE) {
+    const float all = block_sum(mine, red);
+    if (tid == 0) {
+      a.valid[0] = n;
+      *a.loss = all * loss_factor(a);
+    }
+    if (a.cu_seqlens) offsets(a.cu_seqlens, a.experts, [&](int e) { return hist[e]; }, (int32_t*)red);
+  } else if (tid == 0) {
+    a.part_n[(int64_t)b * a.wgs + wg] = n;
+  }
+}
+
+// Joins the workgroups' sums of one sequence for 64 experts, a quarter of them in each wave; the last workgroup of all
+// adds up the loss, in order, and the offsets.
+__global__ __launch_bounds__(kThreads) void balance_join_kernel(const Forward a) {
+  __shared__ float psum[4][64];
+  __shared__ int32_t csum[4][64], nsum[4];
+  __shared__ float red[4];
+  __shared__ uint32_t last;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, b = blockIdx.y;
+  const int e = blockIdx.x * 64 + lane;
+  const int64_t first = (int64_t)b * a.wgs;
+  int32_t n = 0;
+  for (int i = tid; i < a.wgs; i += kThreads) n += a.part_n[first + i];
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) n += __shfl_xor(n, off);
+  float p = 0.f;
+  int32_t c = 0;
+  if (e < a.experts) {
+#pragma unroll 8
+    for (int i = wave; i < a.wgs; i += 4) {
+      p += a.part_p[(first + i) * a.experts + e];
+      c += a.part_c[(first + i) * a.experts + e];
+    }
+  }
+  psum[wave][lane] = p;
+  csum[wave][lane] = c;
+  if (lane == 0) nsum[wave] = n;
+  __syncthreads();
+  n = nsum[0] + nsum[1] + nsum[2] + nsum[3];
+  if (wave == 0) {
+    float mine = 0.f;
+    if (e < a.experts)
+      mine = finish_expert(a, b, e, (psum[0][lane] + psum[1][lane]) + (psum[2][lane] + psum[3][lane]),
+                           csum[0][lane] + csum[1][lane] + csum[2][lane] + csum[3][lane], n);
+    mine = row_sum<64>(mine);
+    if (lane == 0) {
+      if (blockIdx.x == 0) a.valid[b] = n;
+      a.part_loss[(int64_t)b * gridDim.x + blockIdx.x] = mine;
+    }
+  }
+  __threadfence();
+  __syncthreads();
+  if (tid == 0) last = atomicAdd(a.ticket, 1u) == gridDim.x * gridDim.y - 1;
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  float v = 0.f;
+  for (uint32_t i = tid; i < gridDim.x * gridDim.y; i += kThreads) v += __hip_atomic_load(a.part_loss + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  v = block_sum(v, red);
+  if (tid == 0) *a.loss = v * loss_factor(a);
+  if (a.cu_seqlens)
+    offsets(a.cu_seqlens, a.experts, [&](int x) {
+      int32_t s = 0;
+      for (int y = 0; y < a.batch; ++y) s += __hip_atomic_load(a.counts + (int64_t)y * a.experts + x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      return s;
+    }, (int32_t*)red);
+}
+
+// No tokens: zeros.
+__global__ __launch_bounds__(kThreads) void balance_zero_kernel(const Forward a) {
+  const int64_t n = (int64_t)a.batch * a.experts;
+  const int64_t i0 = (int64_t)blockIdx.x * kThreads + threadIdx.x, step = (int64_t)gridDim.x * kThreads;
+  for (int64_t i = i0; i < n; i += step) a.counts[i] = 0, a.probs[i] = 0.f;
+  for (int64_t i = i0; i < a.batch; i += step) a.valid[i] = 0;
+  if (a.cu_seqlens)
+    for (int64_t i = i0; i <= a.experts; i += step) a.cu_seqlens[i] = 0;
+  if (i0 == 0) *a.loss = 0.f;
+}
+
+struct Backward {
+  int batch, tokens, experts, scores;
+  float factor;  // coef * experts / (batch * k)
+  const void* logits;
+  const uint8_t* mask;
+  const int32_t *counts, *valid;
+  const float* grad;
+  void* dlogits;
+  int64_t ld, ldb, ldd, lddb;
+  int per;
+};
+template <typename T, int G, int N>
+__global__ __launch_bounds__(kThreads) void balance_backward_kernel(const Backward a) {
+  const int tid = threadIdx.x, lane = tid & (G - 1), group = tid / G, b = blockIdx.y;
+  const int t0 = blockIdx.x * a.per, t1 = min(a.tokens, t0 + a.per);
+  const uint8_t* mask = a.mask ? a.mask + (int64_t)b * a.tokens : nullptr;
+  const T* logits = (const T*)a.logits + b * a.ldb;
+  T* out = (T*)a.dlogits + b * a.lddb;
+  const float n = (float)a.valid[b];
+  const float factor = n > 0.f ? (a.grad ? *a.grad : 1.f) * (a.factor / n / n) : 0.f;
+  // the counts less the smallest one, exact integers
+  int32_t c[N][8], least = 0x7FFFFFFF;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int at = (i * G + lane) * 8 + e;
+      c[i][e] = at < a.experts ? a.counts[(int64_t)b * a.experts + at] : 0x7FFFFFFF;
+      least = min(least, c[i][e]);
+    }
+#pragma unroll
+  for (int off = 1; off < G; off <<= 1) least = min(least, __shfl_xor(least, off));
+  float w[N][8];
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[i][e] = (i * G + lane) * 8 + e < a.experts ? (float)(c[i][e] - least) * factor : 0.f;
+  constexpr int kGroups = Rows<T, G, N>::kGroups, kAhead = N == 1 ? 4 : (N == 2 ? 2 : 1);
+  for (int t = t0 + group; t < t1; t += kGroups * kAhead) {
+    Rows<T, G, N> rows[kAhead];
+    bool use[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int tt = t + u * kGroups, at = min(tt, t1 - 1);
+      use[u] = !mask || mask[at];
+      rows[u].load(logits + at * a.ld, a.experts, lane);
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int tt = t + u * kGroups;
+      float x[N][8], p[N][8], miss[N][8];
+      rows[u].values(a.experts, lane, x);
+      row_scores<G, N>(a.scores, x, p, miss);
+      float mean = 0.f;
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) mean += p[i][e] * w[i][e];
+      mean = row_sum<G>(mean);
+      if (tt >= t1) continue;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        float d[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          d[e] = p[i][e] * (w[i][e] - mean);
+          if (a.scores == ROUTER_SIGMOID) d[e] *= miss[i][e];
+          d[e] = use[u] ? d[e] : 0.f;
+        }
+        store_chunk<false>(out + tt * a.ldd, (i * G + lane) * 8, a.experts, pack<T>(d));
+      }
+    }
+  }
+}
+
+// Call f(G, N) with the lanes of a row and the chunks of a lane.
+template <typename F>
+void with_rows(int experts, F&& f) {
+  using std::integral_constant;
+  auto go = [&](auto g, auto n) { f(g, n); };
+  const int chunks = (experts + 7) / 8;
+  integral_constant<int, 1> one;
+  if (chunks <= 1) go(one, one);
+  else if (chunks <= 2) go(integral_constant<int, 2>{}, one);
+  else if (chunks <= 4) go(integral_constant<int, 4>{}, one);
+  else if (chunks <= 8) go(integral_constant<int, 8>{}, one);
+  else if (chunks <= 16) go(integral_constant<int, 16>{}, one);
+  else if (chunks <= 32) go(integral_constant<int, 32>{}, one);
+  else if (chunks <= 64) go(integral_constant<int, 64>{}, one);
+  else if (chunks <= 128) go(integral_constant<int, 64>{}, integral_constant<int, 2>{});
+  else go(integral_constant<int, 64>{}, integral_constant<int, 4>{});
+}
+int lanes_of(int experts) {
+  int g = 1;
+  while (g < 64 && g * 8 < experts) g *= 2;
+  return g;
+}
+
+// How the tokens of a sequence are shared out: about 512 workgroups in all, of whole passes of rows.
+struct Share {
+  int per, wgs;
+};
+Share share(int32_t batch, int32_t tokens, int32_t experts, int32_t most) {
+  const int64_t pass = kThreads / lanes_of(experts);
+  const int64_t want = max((int64_t)1, (int64_t)most / max(batch, 1));
+  int64_t per = ((int64_t)tokens + want - 1) / want;
+  per = (per + pass - 1) / pass * pass;
+  per = max(per, pass);
+  return Share{(int)min(per, (int64_t)0x7FFFFFFF), (int)(((int64_t)tokens + per - 1) / per)};
+}
+constexpr int32_t kForwardWgs = 512, kBackwardWgs = 2048;
+
+int64_t round16(int64_t v) { return (v + 15) / 16 * 16; }
+struct Layout {
+  int64_t p, c, n, loss, ticket, bytes;
+};
+Layout layout(int32_t batch, int32_t wgs, int32_t experts) {
+  Layout l;
+  const int64_t parts = (int64_t)batch * wgs;
+  l.p = 0;
+  l.c = l.p + round16(parts * experts * 4);
+  l.n = l.c + round16(parts * experts * 4);
+  l.loss = l.n + round16(parts * 4);
+  l.ticket = l.loss + round16((int64_t)batch * ((experts + 63) / 64) * 4);
+  l.bytes = l.ticket + 16;
+  return l;
+}
+
+gemm_status check_sizes(const char* fn, int32_t batch, int32_t tokens, int32_t experts, int32_t k, int32_t type, int32_t scores) {
+  if (batch < 0 || tokens < 0) return fail(GEMM_ERR_INVALID_ARG, "%s: negative size", fn);
+  if (experts < 1 || k < 1 || k > experts) return fail(GEMM_ERR_INVALID_ARG, "%s: 1 <= k <= experts expected", fn);
+  if (experts > kMaxExperts) return fail(GEMM_ERR_UNSUPPORTED, "%s: more than %d experts", fn, kMaxExperts);
+  if (batch > 65535) return fail(GEMM_ERR_UNSUPPORTED, "%s: more than 65535 sequences", fn);
+  if ((int64_t)batch * tokens > 0x7FFFFFFF / k) return fail(GEMM_ERR_UNSUPPORTED, "%s: 2^31 choices or more", fn);
+  if (type != GEMM_DT_F16 && type != GEMM_DT_BF16 && type != GEMM_DT_F32) return fail(GEMM_ERR_INVALID_ARG, "%s: the logits must be F16, BF16 or F32", fn);
+  if (scores != ROUTER_SOFTMAX && scores != ROUTER_SIGMOID) return fail(GEMM_ERR_INVALID_ARG, "%s: unknown scores %d", fn, scores);
+  return GEMM_OK;
+}
+gemm_status check_logits(const char* fn, const char* name, int32_t batch, int32_t tokens, int32_t experts, int32_t type, const void* p,
+                         int64_t ld, int64_t ldb) {
+  const int64_t most = (int64_t)1 << 48;
+  if (ld < 0 || ld > most || ldb < 0 || ldb > most) return fail(GEMM_ERR_UNSUPPORTED, "%s: strides of %s outside [0, 2^48]", fn, name);
+  if (tokens > 1 && ld < experts) return fail(GEMM_ERR_INVALID_ARG, "%s: rows of %s overlap", fn, name);
+  if (batch > 1 && tokens > 0 && ldb < (tokens - 1) * ld + experts) return fail(GEMM_ERR_INVALID_ARG, "%s: sequences of %s overlap", fn, name);
+  if (!p) return fail(GEMM_ERR_INVALID_ARG, "%s: NULL %s", fn, name);
+  if ((uintptr_t)p % (type == GEMM_DT_F32 ? 4 : 2)) return fail(GEMM_ERR_ALIGNMENT, "%s: %s not aligned to its elements", fn, name);
+  return GEMM_OK;
+}
+gemm_status launched(const char* fn) {
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return fail(GEMM_ERR_HIP, "%s launch: %s", fn, hipGetErrorString(e));
+  return GEMM_OK;
+}
+
+}  // namespace
+}  // namespace gep
+
+using namespace gep;
+
+extern "C" {
+
+int64_t router_balance_workspace(int32_t batch, int32_t tokens, int32_t experts) {
+  if (batch < 0 || tokens < 0 || experts < 1 || experts > kMaxExperts || batch > 65535) return -1;
+  return layout(batch, share(batch, tokens, experts, kForwardWgs).wgs, experts).bytes;
+}
+
+gemm_status router_balance(const router_balance_args* a, void* stream) {
+  const char* fn = "router_balance";
+  if (!a) return fail(GEMM_ERR_INVALID_ARG, "%s: NULL args", fn);
+  gemm_status st = check_sizes(fn, a->batch, a->tokens, a->experts, a->k, a->type, a->scores);
+  if (st != GEMM_OK) return st;
+  if (a->index_bytes != 4 && a->index_bytes != 8) return fail(GEMM_ERR_INVALID_ARG, "%s: indices of 4 or 8 bytes expected", fn);
+  const bool empty = a->batch == 0 || a->tokens == 0;
+  if (!empty) {
+    st = check_logits(fn, "logits", a->batch, a->tokens, a->experts, a->type, a->logits, a->logits_ld, a->logits_batch);
+    if (st != GEMM_OK) return st;
+    if (!a->chosen) return fail(GEMM_ERR_INVALID_ARG, "%s: NULL chosen", fn);
+    if ((uintptr_t)a->chosen % a->index_bytes) return fail(GEMM_ERR_ALIGNMENT, "%s: chosen not aligned to its elements", fn);
+  }
+  if (!a->loss || (a->batch > 0 && (!a->counts || !a->valid || !a->probs))) return fail(GEMM_ERR_INVALID_ARG, "%s: NULL counts, valid, probs or loss", fn);
+  for (const void* p : {(const void*)a->counts, (const void*)a->valid, (const void*)a->cu_seqlens, (const void*)a->probs, (const void*)a->loss})
+    if ((uintptr_t)p & 3) return fail(GEMM_ERR_ALIGNMENT, "%s: outputs not 4-byte aligned", fn);
+  const Share sh = share(a->batch, a->tokens, a->experts, kForwardWgs);
+  const Layout l = layout(a->batch, sh.wgs, a->experts);
+  if (!a->workspace || a->workspace_bytes < l.bytes) return fail(GEMM_ERR_INVALID_ARG, "%s: workspace of %lld bytes expected", fn, (long long)l.bytes);
+  if ((uintptr_t)a->workspace & 15) return fail(GEMM_ERR_ALIGNMENT, "%s: workspace not 16-byte aligned", fn);
+  clear_error();
+  char* w = (char*)a->workspace;
+  Forward f{a->batch, a->tokens, a->experts, a->k, a->scores, a->index_bytes, a->coef, a->logits, a->chosen, a->mask,
+            a->counts, a->valid, a->cu_seqlens, a->probs, a->loss, a->logits_ld, a->logits_batch, sh.per, sh.wgs,
+            (float*)(w + l.p), (int32_t*)(w + l.c), (int32_t*)(w + l.n), (float*)(w + l.loss), (uint32_t*)(w + l.ticket)};
+  hipStream_t s = (hipStream_t)stream;
+  if (empty) {
+    balance_zero_kernel<<<256, kThreads, 0, s>>>(f);
+    return launched(fn);
+  }
+  const bool one = a->batch == 1 && sh.wgs == 1;
+  with_type(a->type, [&](auto* t) {
+    using T = std::remove_pointer_t<decltype(t)>;
+    with_rows(a->experts, [&](auto g, auto n) {
+      constexpr int G = decltype(g)::value, N = decltype(n)::value;
+      const dim3 grid((unsigned)sh.wgs, (unsigned)a->batch);
+      if (one) balance_kernel<T, G, N, true><<<grid, kThreads, 0, s>>>(f);
+      else balance_kernel<T, G, N, false><<<grid, kThreads, 0, s>>>(f);
+    });
+  });
+  if (!one) balance_join_kernel<<<dim3((unsigned)(a->experts + 63) / 64, (unsigned)a->batch), kThreads, 0, s>>>(f);
+  return launched(fn);
+}
+
+gemm_status router_balance_backward(const router_balance_backward_args* a, void* stream) {
+  const char* fn = "router_balance_backward";
+  if (!a) return fail(GEMM_ERR_INVALID_ARG, "%s: NULL args", fn);
+  gemm_status st = check_sizes(fn, a->batch, a->tokens, a->experts, a->k, a->type, a->scores);
+  if (st != GEMM_OK) return st;
+  if (a->batch == 0 || a->tokens == 0) { clear_error(); return GEMM_OK; }
+  st = check_logits(fn, "logits", a->batch, a->tokens, a->experts, a->type, a->logits, a->logits_ld, a->logits_batch);
+  if (st == GEMM_OK) st = check_logits(fn, "dlogits", a->batch, a->tokens, a->experts, a->type, a->dlogits, a->dlogits_ld, a->dlogits_batch);
+  if (st != GEMM_OK) return st;
+  if (!a->counts || !a->valid) return fail(GEMM_ERR_INVALID_ARG, "%s: NULL counts or valid", fn);
+  for (const void* p : {(const void*)a->counts, (const void*)a->valid, (const void*)a->grad})
+    if ((uintptr_t)p & 3) return fail(GEMM_ERR_ALIGNMENT, "%s: counts, valid or grad not 4-byte aligned", fn);
+  if (a->dlogits == a->logits && ((a->tokens > 1 && a->dlogits_ld != a->logits_ld) || (a->batch > 1 && a->dlogits_batch != a->logits_batch)))
+    return fail(GEMM_ERR_INVALID_ARG, "%s: dlogits in the place of the logits needs their strides", fn);
+  clear_error();
+  const Share sh = share(a->batch, a->tokens, a->experts, kBackwardWgs);
+  const Backward f{a->batch, a->tokens, a->experts, a->scores, a->coef * (float)a->experts / ((float)a->batch * (float)a->k),
+                   a->logits, a->mask, a->counts, a->valid, a->grad, a->dlogits, a->logits_ld, a->logits_batch,
+                   a->dlogits_ld, a->dlogits_batch, sh.per};
+  with_type(a->type, [&](auto* t) {
+    using T = std::remove_pointer_t<decltype(t)>;
+    with_rows(a->experts, [&](auto g, auto n) {
+      balance_backward_kernel<T, decltype(g)::value, decltype(n)::value>
+          <<<dim3((unsigned)sh.wgs, (unsigned)a->batch), kThreads, 0, (hipStream_t)stream>>>(f);
+    });
+  });
+  return launched(fn);
+}
+
+}  // extern "C"
