@@ -15,13 +15,13 @@ namespace gep {
 
 constexpr int kFp8Block = 128;
 
-// The block's factor r (0 for one with a NaN or an infinity, whose codes are zero) and its scale, from the
-// bits of its largest magnitude.
+// The block's factor r (0 for one with a NaN or an infinity, whose codes are zero) and its scale, from its largest
+// magnitude (NaN if there is one).
 struct Fp8Factor {
   float r, scale;
 };
-__device__ __forceinline__ float fp8_factor(uint32_t amax) {
-  const float r = fminf(448.f / __uint_as_float(amax), 0x1p126f);  // (correctly rounded; 448 / 0 is infinite)
+__device__ __forceinline__ float fp8_factor(float amax) {
+  const float r = fminf(448.f / amax, 0x1p126f);  // (correctly rounded; 448 / 0 is infinite)
   return __uint_as_float(__float_as_uint(r) & 0xFFFFF800u);
 }
 // 1 / r of a normal r of 13 bits, correctly rounded: one step from a reciprocal within one unit.
@@ -29,8 +29,8 @@ __device__ __forceinline__ float fp8_inverse(float r) {
   const float y = __builtin_amdgcn_rcpf(r);
   return __builtin_fmaf(__builtin_fmaf(-r, y, 1.f), y, y);
 }
-__device__ __forceinline__ Fp8Factor fp8_block(uint32_t amax) {
-  if (amax >= 0x7F800000u) return Fp8Factor{0.f, __uint_as_float(0x7FC00000u)};
+__device__ __forceinline__ Fp8Factor fp8_block(float amax) {
+  if (!(amax < __builtin_inff())) return Fp8Factor{0.f, __uint_as_float(0x7FC00000u)};
   const float r = fp8_factor(amax);
   return Fp8Factor{r, fp8_inverse(r)};
 }
@@ -47,13 +47,13 @@ __device__ __forceinline__ float fp8_scaled(float x, float r) {
   return e != 0.f ? __uint_as_float(cut) : q;
 }
 
-// Eight values of a block with factor r as codes. (v_cvt_pk_fp8_f32 does not saturate by itself; r times the largest
-// may pass 448 by the rounding of r.)
+// Eight values of a block with factor r as codes. (v_cvt_pk_fp8_f32 does not saturate by itself, and need not: r times the
+// largest value passes 448 by half an fp32 step at most, which rounds to 448.)
 template <bool EXACT>
 __device__ __forceinline__ uint2 fp8_codes8(const float v[8], float r) {
   float c[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) c[e] = __builtin_amdgcn_fmed3f(fp8_scaled<EXACT>(v[e], r), -448.f, 448.f);
+  for (int e = 0; e < 8; ++e) c[e] = fp8_scaled<EXACT>(v[e], r);
   int x = __builtin_amdgcn_cvt_pk_fp8_f32(c[0], c[1], 0, false);
   x = __builtin_amdgcn_cvt_pk_fp8_f32(c[2], c[3], x, true);
   int y = __builtin_amdgcn_cvt_pk_fp8_f32(c[4], c[5], 0, false);
@@ -69,11 +69,24 @@ __device__ __forceinline__ void fp8_values8(uint2 w, float scale, float v[8]) {
   for (int e = 0; e < 8; ++e) v[e] = p[e >> 1][e & 1] * scale;
 }
 
-// Maximum over 16 neighbouring lanes (a block, 8 values a lane), in each of them.
-__device__ __forceinline__ uint32_t row_max16(uint32_t a) {
-  a = quad_max(a);
-  a = max(a, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)a, 0x141, 0xF, 0xF, true));  // within 8: i <-> 7 - i
-  return max(a, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)a, 0x140, 0xF, 0xF, true));  // within 16: i <-> 15 - i
+// The larger magnitude, NaN if either is one (v_maximum3_f32 takes three operands and their magnitudes).
+__device__ __forceinline__ float larger(float a, float b) { return __builtin_elementwise_maximum(__builtin_fabsf(a), __builtin_fabsf(b)); }
+__device__ __forceinline__ float largest8(const float v[8]) {
+  float a = larger(v[0], v[1]);
+#pragma unroll
+  for (int e = 2; e < 8; e += 2) a = larger(larger(a, v[e]), v[e + 1]);
+  return a;
+}
+// Largest magnitude over 16 neighbouring lanes (a block, 8 values a lane), in each of them.
+template <int CTRL>
+__device__ __forceinline__ float lanes(float a) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(a), CTRL, 0xF, 0xF, true));
+}
+__device__ __forceinline__ float row_max16(float a) {
+  a = larger(a, lanes<0xB1>(a));   // lanes 1 0 3 2
+  a = larger(a, lanes<0x4E>(a));   // lanes 2 3 0 1
+  a = larger(a, lanes<0x141>(a));  // within 8: i <-> 7 - i
+  return larger(a, lanes<0x140>(a));  // within 16: i <-> 15 - i
 }
 
 // ---- storage. nb blocks a row, nq = ceil(nb / 4), kp bytes of codes a row.

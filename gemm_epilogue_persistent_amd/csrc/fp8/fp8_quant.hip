@@ -31,26 +31,30 @@ __device__ __forceinline__ void act8(int act, float v[8]) {
     }
   }
 }
-// s (1 + x (1 - s) z') with s = 1 / (1 + e^-z): the slope of x s(z). 1 - s = e^-z s keeps its digits for large
-// z. Beyond |x| = 80 (GELU: 12) the slope is 0 or 1 in fp32, and x kept to that finite.
-__device__ __forceinline__ float sigmoid_slope(float x, float z, float dz) {
-  const float e = fast_exp(-z), s = __builtin_amdgcn_rcpf(1.f + e);
-  return s * (1.f + x * (e * s) * dz);
-}
-__device__ __forceinline__ float slope(int act, float x) {
-  switch (act) {
-    case ACT_RELU: return x > 0.f ? 1.f : 0.f;
-    case ACT_RELU_SQ: return x > 0.f ? 2.f * x : 0.f;
-    case ACT_GELU_TANH: {
-      const float c = __builtin_amdgcn_fmed3f(x, -12.f, 12.f), c2 = c * c;
-      const float z = __builtin_amdgcn_fmed3f(1.5957691216057308f * (c + 0.044715f * c2 * c), -80.f, 80.f);
-      return sigmoid_slope(c, z, 1.5957691216057308f * (1.f + 0.134145f * c2));
-    }
-    case ACT_SILU: {
-      const float c = __builtin_amdgcn_fmed3f(x, -80.f, 80.f);
-      return sigmoid_slope(c, c, 1.f);
-    }
-    default: return 1.f;
+// act(x) and its slope. Both smooth activations are x s with s = 1 / (1 + 2^-u), and their slope is s (1 + x (1 - s) z')
+// with z = u log 2; 1 - s = 2^-u s keeps its digits for large z. Beyond |x| = 12 (GELU) and 80 (SiLU) x is kept to
+// that, and 2^-u below infinity, so that all factors are finite: there s is 0 or 1 to within 2^-115.
+template <int ACT>
+__device__ __forceinline__ void act_and_slope(float x, float& y, float& d) {
+  if constexpr (ACT == ACT_RELU) {
+    y = act_fn<ACT_RELU>(x);
+    d = x > 0.f ? 1.f : 0.f;
+  } else if constexpr (ACT == ACT_RELU_SQ) {
+    y = act_fn<ACT_RELU_SQ>(x);
+    d = x > 0.f ? 2.f * x : 0.f;
+  } else if constexpr (ACT == ACT_GELU_TANH || ACT == ACT_SILU) {
+    constexpr bool gelu = ACT == ACT_GELU_TANH;
+    constexpr float top = gelu ? 12.f : 80.f, log2e = 1.4426950408889634f;
+    const float c = __builtin_amdgcn_fmed3f(x, -top, top), c2 = c * c;
+    // -u, and z' = dz / dx with z = 2 sqrt(2 / pi) (x + 0.044715 x^3)
+    const float u = gelu ? c * __builtin_fmaf(c2, -0.044715f * 1.5957691216057308f * log2e, -1.5957691216057308f * log2e) : c * -log2e;
+    const float e = __builtin_amdgcn_exp2f(fminf(u, 120.f)), s = __builtin_amdgcn_rcpf(1.f + e);
+    const float cz = gelu ? c * __builtin_fmaf(c2, 0.134145f * 1.5957691216057308f, 1.5957691216057308f) : c;
+    d = s * __builtin_fmaf(cz, e * s, 1.f);
+    y = fmaxf(x, -top) * s;
+  } else {
+    y = x;
+    d = 1.f;
   }
 }
 
@@ -63,7 +67,7 @@ struct Mat {
 // Quantise and store chunk ch (8 values) of row r, blocks along the row. In each of the 16 lanes of a block.
 template <bool EXACT>
 __device__ __forceinline__ void store_row_chunk(const Mat& m, const Fp8Geometry& g, int64_t r, int ch, const float v[8]) {
-  const Fp8Factor f = fp8_block(row_max16(amax_bits(v)));
+  const Fp8Factor f = fp8_block(row_max16(largest8(v)));
   const uint2 w = fp8_codes8<EXACT>(v, f.r);
   if (ch * 8 < g.kp) *(uint2*)(m.codes + r * g.kp + ch * 8) = w;
   if ((ch & 15) == 0) fp8_store_scale(m.scales + fp8_row_scale(r, ch >> 4, g.nq), ch >> 4, g, f.scale);
@@ -99,7 +103,10 @@ __global__ __launch_bounds__(kThreads) void rows_kernel(const T* x, int64_t ldx,
 // that 16 neighbouring lanes hold a block of a row, and the 8 codes of a thread in one column are neighbours in
 // the transposed matrix.
 struct TileShared {
-  __attribute__((aligned(16))) uint32_t codes[kTile * kTile / 4];  // and before that 16 partial maxima of each column
+  union {
+    __attribute__((aligned(16))) uint32_t codes[kTile * kTile / 4];
+    __attribute__((aligned(16))) float part[16 * kTile];  // before that: 16 partial maxima of each column
+  };
   __attribute__((aligned(16))) float factor[kTile];
 };
 
@@ -132,21 +139,22 @@ template <bool EXACT>
 __device__ __forceinline__ void store_columns(const Mat& m, const Fp8Geometry& gt, int r0, int c0, int cols, const float (&v)[8][8],
                                               TileShared& s) {
   const int tid = threadIdx.x, g = tid >> 4, cl = tid & 15;
-  uint32_t a[8];
+  float a[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    a[j] = 0;
+    float w[8];
 #pragma unroll
-    for (int p = 0; p < 8; ++p) a[j] = max(a[j], __float_as_uint(v[p][j]) & 0x7FFFFFFFu);
+    for (int p = 0; p < 8; ++p) w[p] = v[p][j];
+    a[j] = largest8(w);
   }
-  uint4* part = (uint4*)(s.codes + g * kTile + cl * 8);
-  part[0] = uint4{a[0], a[1], a[2], a[3]};
-  part[1] = uint4{a[4], a[5], a[6], a[7]};
+  f32x4* part = (f32x4*)(s.part + g * kTile + cl * 8);
+  part[0] = f32x4{a[0], a[1], a[2], a[3]};
+  part[1] = f32x4{a[4], a[5], a[6], a[7]};
   __syncthreads();
   if (tid < kTile) {
-    uint32_t top = 0;
+    float top = s.part[tid];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) top = max(top, s.codes[i * kTile + tid]);
+    for (int i = 1; i < 16; ++i) top = larger(top, s.part[i * kTile + tid]);
     const Fp8Factor f = fp8_block(top);
     s.factor[tid] = f.r;
     const int b = r0 / kFp8Block;
@@ -198,15 +206,15 @@ __global__ __launch_bounds__(kThreads) void quantize_tiles_kernel(const T* x, in
     }
   }
   if constexpr (TILES) {
-    uint32_t a = 0;
+    float a = largest8(v[0]);
 #pragma unroll
-    for (int p = 0; p < 8; ++p) a = max(a, amax_bits(v[p]));
+    for (int p = 1; p < 8; ++p) a = larger(a, largest8(v[p]));
     a = row_max16(a);
-    if (cl == 0) s.codes[g] = a;
+    if (cl == 0) s.part[g] = a;
     __syncthreads();
-    a = 0;
+    a = s.part[0];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) a = max(a, s.codes[i]);
+    for (int i = 1; i < 16; ++i) a = larger(a, s.part[i]);
     const Fp8Factor f = fp8_block(a);
     const int i = at.r0 / kTile, b = at.c0 / kTile;
     if (q.codes) {
@@ -236,7 +244,7 @@ __global__ __launch_bounds__(kThreads) void quantize_tiles_kernel(const T* x, in
 // ---- the backward pass of an activation from its checkpoint.
 template <typename T>
 struct BackArgs {
-  int rows, cols, act;
+  int rows, cols;
   const T* dy;
   const uint8_t* codes;
   const float* scales;
@@ -244,7 +252,7 @@ struct BackArgs {
   Mat q, qt, yt;
   int64_t lddy, lddx, ldy;
 };
-template <typename T>
+template <typename T, int ACT>
 __global__ __launch_bounds__(kThreads) void act_backward_kernel(const BackArgs<T> a, uint32_t first, uint32_t tiles, FastDiv fd_ty) {
   __shared__ TileShared sx, sy;
   TileAt at;
@@ -262,35 +270,42 @@ __global__ __launch_bounds__(kThreads) void act_backward_kernel(const BackArgs<T
     w[p] = *(const uint2*)(a.codes + row * geo.kp + min(c, geo.kp - 8));
     scale[p] = a.scales[fp8_row_scale(row, at.c0 / kFp8Block, geo.nq)];
   }
-  float v[8][8];
-  if (a.dy) {
+  const bool edge = at.r0 + kTile > a.rows || at.c0 + kTile > a.cols;
+  // Values past the matrix are zero in both results.
+  auto inside = [&](float (&v)[8], int p) {
+    if (!edge) return;
 #pragma unroll
-    for (int p = 0; p < 8; ++p) {
-      float x[8];
-      settle<false>(in[p], c, a.cols);
-      unpack(in[p], v[p]);
-      fp8_values8(w[p], scale[p], x);
-      const float nan = -0.f * scale[p];  // NaN for a NaN block, whose slopes are not; -0 changes no other product
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float d = __builtin_fmaf(v[p][e], slope(a.act, x[e]), nan);
-        v[p][e] = r + p < a.rows && c + e < a.cols ? d : 0.f;
-      }
-      if (a.dx && r + p < a.rows) store_chunk<false>(a.dx + (int64_t)(r + p) * a.lddx, c, a.cols, pack<T>(v[p]));
-      if (a.q.codes && r + p < a.rows) store_row_chunk<false>(a.q, geo, r + p, c >> 3, v[p]);
-    }
-    if (a.qt.codes) store_columns<false>(a.qt, geo_t, at.r0, at.c0, a.cols, v, sx);
-  }
-  if (!a.y && !a.yt.codes) return;
+    for (int e = 0; e < 8; ++e) v[e] = r + p < a.rows && c + e < a.cols ? v[e] : 0.f;
+  };
+  float v[8][8], y[8][8];
 #pragma unroll
   for (int p = 0; p < 8; ++p) {
-    fp8_values8(w[p], scale[p], v[p]);
-    act8(a.act, v[p]);
+    float x[8], d[8];
+    fp8_values8(w[p], scale[p], x);
+    if (a.dy) {
+      settle<false>(in[p], c, a.cols);
+      unpack(in[p], v[p]);
+    }
+    const float nan = -0.f * scale[p];  // NaN for a NaN block, whose slopes are not; -0 changes no other product
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[p][e] = r + p < a.rows && c + e < a.cols ? v[p][e] : 0.f;
-    if (a.y && r + p < a.rows) store_chunk<false>(a.y + (int64_t)(r + p) * a.ldy, c, a.cols, pack<T>(v[p]));
+    for (int e = 0; e < 8; ++e) {
+      act_and_slope<ACT>(x[e], y[p][e], d[e]);
+      if (ACT == ACT_GELU_TANH || ACT == ACT_SILU) y[p][e] += nan;
+    }
+    inside(y[p], p);
+    if (a.dy) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[p][e] = __builtin_fmaf(v[p][e], d[e], nan);
+      inside(v[p], p);
+    }
+    if (r + p < a.rows) {
+      if (a.y) store_chunk<false>(a.y + (int64_t)(r + p) * a.ldy, c, a.cols, pack<T>(y[p]));
+      if (a.dx) store_chunk<false>(a.dx + (int64_t)(r + p) * a.lddx, c, a.cols, pack<T>(v[p]));
+      if (a.q.codes) store_row_chunk<false>(a.q, geo, r + p, c >> 3, v[p]);
+    }
   }
-  if (a.yt.codes) store_columns<false>(a.yt, geo_t, at.r0, at.c0, a.cols, v, sy);
+  if (a.qt.codes) store_columns<false>(a.qt, geo_t, at.r0, at.c0, a.cols, v, sx);
+  if (a.yt.codes) store_columns<false>(a.yt, geo_t, at.r0, at.c0, a.cols, y, sy);
 }
 
 // ---- values of the codes. A thread takes 8 codes and writes 8 values.
@@ -488,12 +503,19 @@ gemm_status fp8_act_backward(const fp8_act_backward_args* a, void* stream) {
   bool fits = true;
   with_type(a->type, [&](auto* t) {
     using T = std::remove_pointer_t<decltype(t)>;
-    const BackArgs<T> b{a->rows, a->cols, a->act, (const T*)a->dy, (const uint8_t*)a->saved_codes, (const float*)a->saved_scales,
+    const BackArgs<T> b{a->rows, a->cols, (const T*)a->dy, (const uint8_t*)a->saved_codes, (const float*)a->saved_scales,
                         (T*)a->dx, (T*)a->y, Mat{(uint8_t*)a->q_codes, (float*)a->q_scales},
                         Mat{(uint8_t*)a->qt_codes, (float*)a->qt_scales}, Mat{(uint8_t*)a->yt_codes, (float*)a->yt_scales},
                         a->lddy, a->lddx, a->ldy};
     fits = tile_ranges(a->rows, a->cols, [&](uint32_t first, uint32_t tiles, uint32_t grid, FastDiv fd) {
-      act_backward_kernel<T><<<grid, kThreads, 0, (hipStream_t)stream>>>(b, first, tiles, fd);
+      auto go = [&](auto act) { act_backward_kernel<T, decltype(act)::value><<<grid, kThreads, 0, (hipStream_t)stream>>>(b, first, tiles, fd); };
+      switch (a->act) {
+        case GEMM_ACT_RELU: go(std::integral_constant<int, ACT_RELU>{}); break;
+        case GEMM_ACT_RELU_SQ: go(std::integral_constant<int, ACT_RELU_SQ>{}); break;
+        case GEMM_ACT_GELU_TANH: go(std::integral_constant<int, ACT_GELU_TANH>{}); break;
+        case GEMM_ACT_SILU: go(std::integral_constant<int, ACT_SILU>{}); break;
+        default: go(std::integral_constant<int, ACT_NONE>{}); break;
+      }
     });
   });
   if (!fits) return fail(GEMM_ERR_UNSUPPORTED, "%s: more than 2^31 tiles", fn);

@@ -38,72 +38,80 @@ __device__ __forceinline__ float row_sum(float v) { return reduce<G>(v, [](float
 template <int G>
 __device__ __forceinline__ float row_max(float v) { return reduce<G>(v, [](float a, float b) { return fmaxf(a, b); }); }
 
-// e^x of x <= 0 to about an fp32 step: x log2 e in two parts, so that the error does not grow with x.
+// e^x of x <= 0 to about an fp32 step: what the rounding of x log2 e leaves is put back, so that the error does not grow
+// with x. (Not for NaN: see row_scores.)
 __device__ __forceinline__ float exp_neg(float x) {
-  const float t = x * 1.44269502162933349609375f;
-  const float lo = __builtin_fmaf(x, 1.92596299112661e-8f, __builtin_fmaf(x, 1.44269502162933349609375f, -t));
+  constexpr float log2e = 1.44269502162933349609375f;
+  const float c = fmaxf(x, -104.f);  // (e^-104 is below fp32)
+  const float t = c * log2e, lo = __builtin_fmaf(c, log2e, -t);
   const float e = __builtin_amdgcn_exp2f(t);
-  return t < -150.f ? 0.f : __builtin_fmaf(e, lo * 0.693147182464599609375f, e);  // (lo of -inf is NaN)
+  return __builtin_fmaf(e * lo, 0.693147182464599609375f, e);
 }
 
-// The scores of a row: p (8 N a lane) from its logits x, -inf past the last expert. miss: 1 - s(x) (sigmoid). A row
-// of -inf alone gives zeros.
-template <int G, int N>
-__device__ __forceinline__ void row_scores(int scores, const float (&x)[N][8], float (&p)[N][8], float (&miss)[N][8]) {
-  float top = -__builtin_inff();
+// The scores of a row from its logits x, -inf past the last expert: p = u inv (8 N a lane). miss: 1 - s(x) (sigmoid). A
+// row of -inf alone has inv = 0; a NaN makes inv NaN.
+template <int G, int N, int SCORES>
+__device__ __forceinline__ float row_scores(const float (&x)[N][8], float (&u)[N][8], float (&miss)[N][8]) {
+  float top = -__builtin_inff(), sum = 0.f;
+  bool nan = false;
 #pragma unroll
   for (int i = 0; i < N; ++i)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) top = fmaxf(top, x[i][e]);
+    for (int e = 0; e < 8; ++e) {
+      top = fmaxf(top, x[i][e]);
+      nan |= x[i][e] != x[i][e];
+    }
   top = row_max<G>(top);
-  const bool none = top == -__builtin_inff();
-  float sum = 0.f;
-  if (scores == ROUTER_SOFTMAX) {
+  if constexpr (SCORES == ROUTER_SOFTMAX) {
+    const float m = fmaxf(top, -3.402823466e38f);  // (-inf less -inf is no number)
 #pragma unroll
     for (int i = 0; i < N; ++i)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        p[i][e] = none ? 0.f : exp_neg(x[i][e] - top);
-        p[i][e] = x[i][e] != x[i][e] ? x[i][e] : p[i][e];
-        sum += p[i][e];
-      }
+      for (int e = 0; e < 8; ++e) u[i][e] = exp_neg(x[i][e] - m), sum += u[i][e];
+    nan |= top == __builtin_inff();
   } else {
-    // s(x) e^-m with m = min(top, 0), which the quotient cancels: logits that are all far below zero keep their digits
-    const float m = fminf(top, 0.f);
+    // s(x) = a q or q with a = e^-|x|, q = 1 / (1 + a); 1 - s(x) is the other one
 #pragma unroll
     for (int i = 0; i < N; ++i)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float v = x[i][e], a = exp_neg(-fabsf(v)), q = __builtin_amdgcn_rcpf(1.f + a);
-        p[i][e] = none ? 0.f : exp_neg(fminf(v, 0.f) - m) * q;
-        p[i][e] = v != v ? v : p[i][e];
-        miss[i][e] = v < 0.f ? q : a * q;
-        sum += p[i][e];
+        const float a = exp_neg(-fabsf(x[i][e])), q = __builtin_amdgcn_rcpf(1.f + a), aq = a * q;
+        u[i][e] = x[i][e] < 0.f ? aq : q;
+        miss[i][e] = x[i][e] < 0.f ? q : aq;
+        sum += u[i][e];
       }
+    // Logits that are all far below zero: times e^-top, which the quotient cancels, so that they keep their digits.
+    // (From -40 on what e^x loses is below e^-60 of the sum.)
+    if (top < -40.f) {
+      const float m = fmaxf(top, -3.402823466e38f);
+      sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) u[i][e] = exp_neg(x[i][e] - m) * miss[i][e], sum += u[i][e];
+    }
   }
+  if (nan) sum = __uint_as_float(0x7FC00000u);
   sum = row_sum<G>(sum);
-  const float inv = none ? 1.f : 1.f / sum;
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) p[i][e] *= inv;
+  return top == -__builtin_inff() && sum == sum ? 0.f : 1.f / sum;
 }
 
-template <typename T, int G, int N>
+// WHOLE: the experts fill the lanes.
+template <typename T, int G, int N, bool WHOLE>
 struct Rows {
-  static constexpr int kGroups = kThreads / G;  // rows a pass
   Chunk<T> c[N];
   // Lane l of the row's group takes chunks l, l + G, ...
   __device__ __forceinline__ void load(const T* row, int experts, int lane) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) c[i] = load_chunk<false>(row, (i * G + lane) * 8, experts);
+    for (int i = 0; i < N; ++i) c[i] = load_chunk<WHOLE>(row, (i * G + lane) * 8, experts);
   }
   __device__ __forceinline__ void values(int experts, int lane, float (&x)[N][8]) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int at = (i * G + lane) * 8;
-      settle<false>(c[i], at, experts);
+      if (!WHOLE) settle<false>(c[i], at, experts);
       unpack(c[i], x[i]);
+      if (WHOLE) continue;
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[i][e] = at + e < experts ? x[i][e] : -__builtin_inff();
     }
@@ -137,20 +145,24 @@ __device__ __forceinline__ float finish_expert(const Forward& a, int b, int e, f
 __device__ __forceinline__ float loss_factor(const Forward& a) { return a.coef * (float)a.experts / ((float)a.batch * (float)a.k); }
 
 // Sum over the workgroup in a fixed order, in every thread. buf: a float for each wave.
+template <int TH>
 __device__ __forceinline__ float block_sum(float v, float* buf) {
   v = row_sum<64>(v);
   __syncthreads();
   if ((threadIdx.x & 63) == 0) buf[threadIdx.x >> 6] = v;
   __syncthreads();
-  return (buf[0] + buf[1]) + (buf[2] + buf[3]);
+  v = buf[0];
+#pragma unroll
+  for (int w = 1; w < TH / 64; ++w) v += buf[w];
+  return v;
 }
 // cu[i + 1] = sum of the first i + 1 totals (total(e): a function); one workgroup.
-template <typename F>
+template <int TH, typename F>
 __device__ __forceinline__ void offsets(int32_t* cu, int experts, F&& total, int32_t* buf) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   int32_t base = 0;
   if (tid == 0) cu[0] = 0;
-  for (int e0 = 0; e0 < experts; e0 += kThreads) {
+  for (int e0 = 0; e0 < experts; e0 += TH) {
     const int e = e0 + tid;
     int32_t v = e < experts ? total(e) : 0;
 #pragma unroll
@@ -162,64 +174,71 @@ __device__ __forceinline__ void offsets(int32_t* cu, int experts, F&& total, int
     if (lane == 63) buf[wave] = v;
     __syncthreads();
     int32_t before = base;
-    for (int w = 0; w < wave; ++w) before += buf[w];
+#pragma unroll
+    for (int w = 0; w < TH / 64; ++w) {
+      before += w < wave ? buf[w] : 0;
+      base += buf[w];
+    }
     if (e < experts) cu[e + 1] = before + v;
-    base += buf[0] + buf[1] + buf[2] + buf[3];
   }
 }
 
-// The tokens of one workgroup. ONE: they are all there are, and the results are finished here.
-template <typename T, int G, int N, bool ONE>
-__global__ __launch_bounds__(kThreads) void balance_kernel(const Forward a) {
-  constexpr int kCols = 8 * G * N;
-  __shared__ float psum[4][kCols];
+// The tokens of one workgroup of TH threads. ONE: they are all there are, and the results are finished here.
+template <typename T, int G, int N, int SCORES, bool WHOLE, bool ONE, int TH>
+__global__ __launch_bounds__(TH) void balance_kernel(const Forward a) {
+  constexpr int kCols = 8 * G * N, kWaves = TH / 64, kGroups = TH / G, kAhead = N == 1 ? 4 : (N == 2 ? 2 : 1);
+  __shared__ float psum[kWaves][kCols];
   __shared__ int32_t hist[kCols];
   __shared__ int32_t tokens_seen;
-  __shared__ float red[4];
+  __shared__ float red[kWaves];
   const int tid = threadIdx.x, lane = tid & (G - 1), group = tid / G, wave = tid >> 6;
   const int b = blockIdx.y, wg = blockIdx.x;
   const int t0 = wg * a.per, t1 = min(a.tokens, t0 + a.per);
   const uint8_t* mask = a.mask ? a.mask + (int64_t)b * a.tokens : nullptr;
-  if (!ONE && tid == 0 && b == 0 && wg == 0) *a.ticket = 0;  // (for the join, the next launch)
-  for (int e = tid; e < kCols; e += kThreads) hist[e] = 0;
-  if (tid == 0) tokens_seen = 0;
-  __syncthreads();
-  // counts
-  const int64_t id0 = ((int64_t)b * a.tokens + t0) * a.k;
-  const uint32_t ids = (uint32_t)(t1 - t0) * (uint32_t)a.k;
-  for (uint32_t i = tid; i < ids; i += kThreads) {
-    const int64_t e = a.index_bytes == 8 ? ((const int64_t*)a.chosen)[id0 + i] : (int64_t)((const int32_t*)a.chosen)[id0 + i];
-    if (e >= 0 && e < a.experts && (!mask || mask[t0 + i / (uint32_t)a.k])) atomicAdd(&hist[(int)e], 1);
-  }
-  // scores
-  float acc[N][8];
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) acc[i][e] = 0.f;
   const T* logits = (const T*)a.logits + b * a.ldb;
-  int seen = 0;
-  constexpr int kGroups = Rows<T, G, N>::kGroups, kAhead = N == 1 ? 4 : (N == 2 ? 2 : 1);
-  for (int t = t0 + group; t < t1; t += kGroups * kAhead) {
-    Rows<T, G, N> rows[kAhead];
-    bool use[kAhead];
+  Rows<T, G, N, WHOLE> rows[kAhead];
+  bool use[kAhead];
+  auto fetch = [&](int t) {
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       const int tt = t + u * kGroups, at = min(tt, t1 - 1);
       use[u] = tt < t1 && (!mask || mask[at]);
       rows[u].load(logits + at * a.ld, a.experts, lane);
     }
+  };
+  fetch(t0 + group);  // (under way while the choices are counted)
+  if (!ONE && tid == 0 && b == 0 && wg == 0) *a.ticket = 0;  // (for the join, the next launch)
+  for (int e = tid; e < kCols; e += TH) hist[e] = 0;
+  if (tid == 0) tokens_seen = 0;
+  __syncthreads();
+  const int64_t id0 = ((int64_t)b * a.tokens + t0) * a.k;
+  const uint32_t ids = (uint32_t)(t1 - t0) * (uint32_t)a.k;
+  for (uint32_t i = tid; i < ids; i += TH) {
+    const int64_t e = a.index_bytes == 8 ? ((const int64_t*)a.chosen)[id0 + i] : (int64_t)((const int32_t*)a.chosen)[id0 + i];
+    if (e >= 0 && e < a.experts && (!mask || mask[t0 + i / (uint32_t)a.k])) atomicAdd(&hist[(int)e], 1);
+  }
+  float acc[N][8];
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[i][e] = 0.f;
+  int seen = 0;
+  for (int t = t0 + group;;) {
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      float x[N][8], p[N][8], miss[N][8];
+      if (!use[u]) continue;
+      float x[N][8], s[N][8], miss[N][8];
       rows[u].values(a.experts, lane, x);
-      row_scores<G, N>(a.scores, x, p, miss);
-      seen += use[u];
+      const float inv = row_scores<G, N, SCORES>(x, s, miss);
+      ++seen;
 #pragma unroll
       for (int i = 0; i < N; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) acc[i][e] += use[u] ? p[i][e] : 0.f;
+        for (int e = 0; e < 8; ++e) acc[i][e] = __builtin_fmaf(s[i][e], inv, acc[i][e]);
     }
+    t += kGroups * kAhead;
+    if (t >= t1) break;
+    fetch(t);
   }
   if (lane == 0 && seen) atomicAdd(&tokens_seen, seen);
   // over the row groups of the wave, then over the waves
@@ -238,8 +257,10 @@ __global__ __launch_bounds__(kThreads) void balance_kernel(const Forward a) {
   __syncthreads();
   const int32_t n = tokens_seen;
   float mine = 0.f;
-  for (int e = tid; e < a.experts; e += kThreads) {
-    const float p = (psum[0][e] + psum[1][e]) + (psum[2][e] + psum[3][e]);
+  for (int e = tid; e < a.experts; e += TH) {
+    float p = psum[0][e];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) p += psum[w][e];
     if constexpr (ONE) {
       mine += finish_expert(a, b, e, p, hist[e], n);
     } else {
@@ -249,12 +270,12 @@ __global__ __launch_bounds__(kThreads) void balance_kernel(const Forward a) {
     }
   }
   if constexpr (ONE) {
-    const float all = block_sum(mine, red);
+    const float all = block_sum<TH>(mine, red);
     if (tid == 0) {
       a.valid[0] = n;
       *a.loss = all * loss_factor(a);
     }
-    if (a.cu_seqlens) offsets(a.cu_seqlens, a.experts, [&](int e) { return hist[e]; }, (int32_t*)red);
+    if (a.cu_seqlens) offsets<TH>(a.cu_seqlens, a.experts, [&](int e) { return hist[e]; }, (int32_t*)red);
   } else if (tid == 0) {
     a.part_n[(int64_t)b * a.wgs + wg] = n;
   }
@@ -307,10 +328,10 @@ __global__ __launch_bounds__(kThreads) void balance_join_kernel(const Forward a)
   __threadfence();
   float v = 0.f;
   for (uint32_t i = tid; i < gridDim.x * gridDim.y; i += kThreads) v += __hip_atomic_load(a.part_loss + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  v = block_sum(v, red);
+  v = block_sum<kThreads>(v, red);
   if (tid == 0) *a.loss = v * loss_factor(a);
   if (a.cu_seqlens)
-    offsets(a.cu_seqlens, a.experts, [&](int x) {
+    offsets<kThreads>(a.cu_seqlens, a.experts, [&](int x) {
       int32_t s = 0;
       for (int y = 0; y < a.batch; ++y) s += __hip_atomic_load(a.counts + (int64_t)y * a.experts + x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       return s;
@@ -339,13 +360,25 @@ struct Backward {
   int64_t ld, ldb, ldd, lddb;
   int per;
 };
-template <typename T, int G, int N>
+template <typename T, int G, int N, int SCORES, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void balance_backward_kernel(const Backward a) {
+  constexpr int kGroups = kThreads / G, kAhead = N == 1 ? 4 : (N == 2 ? 2 : 1);
   const int tid = threadIdx.x, lane = tid & (G - 1), group = tid / G, b = blockIdx.y;
   const int t0 = blockIdx.x * a.per, t1 = min(a.tokens, t0 + a.per);
   const uint8_t* mask = a.mask ? a.mask + (int64_t)b * a.tokens : nullptr;
   const T* logits = (const T*)a.logits + b * a.ldb;
   T* out = (T*)a.dlogits + b * a.lddb;
+  Rows<T, G, N, WHOLE> rows[kAhead];
+  bool use[kAhead];
+  auto fetch = [&](int t) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int at = min(t + u * kGroups, t1 - 1);
+      use[u] = !mask || mask[at];
+      rows[u].load(logits + at * a.ld, a.experts, lane);
+    }
+  };
+  fetch(t0 + group);  // (under way while the weights are formed)
   const float n = (float)a.valid[b];
   const float factor = n > 0.f ? (a.grad ? *a.grad : 1.f) * (a.factor / n / n) : 0.f;
   // the counts less the smallest one, exact integers
@@ -355,7 +388,7 @@ __global__ __launch_bounds__(kThreads) void balance_backward_kernel(const Backwa
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const int at = (i * G + lane) * 8 + e;
-      c[i][e] = at < a.experts ? a.counts[(int64_t)b * a.experts + at] : 0x7FFFFFFF;
+      c[i][e] = WHOLE || at < a.experts ? a.counts[(int64_t)b * a.experts + at] : 0x7FFFFFFF;
       least = min(least, c[i][e]);
     }
 #pragma unroll
@@ -364,42 +397,41 @@ __global__ __launch_bounds__(kThreads) void balance_backward_kernel(const Backwa
 #pragma unroll
   for (int i = 0; i < N; ++i)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) w[i][e] = (i * G + lane) * 8 + e < a.experts ? (float)(c[i][e] - least) * factor : 0.f;
-  constexpr int kGroups = Rows<T, G, N>::kGroups, kAhead = N == 1 ? 4 : (N == 2 ? 2 : 1);
-  for (int t = t0 + group; t < t1; t += kGroups * kAhead) {
-    Rows<T, G, N> rows[kAhead];
-    bool use[kAhead];
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int tt = t + u * kGroups, at = min(tt, t1 - 1);
-      use[u] = !mask || mask[at];
-      rows[u].load(logits + at * a.ld, a.experts, lane);
-    }
+    for (int e = 0; e < 8; ++e) w[i][e] = WHOLE || (i * G + lane) * 8 + e < a.experts ? (float)(c[i][e] - least) * factor : 0.f;
+  for (int t = t0 + group; t < t1;) {
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       const int tt = t + u * kGroups;
-      float x[N][8], p[N][8], miss[N][8];
-      rows[u].values(a.experts, lane, x);
-      row_scores<G, N>(a.scores, x, p, miss);
-      float mean = 0.f;
-#pragma unroll
-      for (int i = 0; i < N; ++i)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) mean += p[i][e] * w[i][e];
-      mean = row_sum<G>(mean);
       if (tt >= t1) continue;
+      float d[N][8];
+      if (use[u]) {
+        float x[N][8], s[N][8], miss[N][8];
+        rows[u].values(a.experts, lane, x);
+        const float inv = row_scores<G, N, SCORES>(x, s, miss);
+        float mean = 0.f;
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        float d[8];
+        for (int i = 0; i < N; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          d[e] = p[i][e] * (w[i][e] - mean);
-          if (a.scores == ROUTER_SIGMOID) d[e] *= miss[i][e];
-          d[e] = use[u] ? d[e] : 0.f;
-        }
-        store_chunk<false>(out + tt * a.ldd, (i * G + lane) * 8, a.experts, pack<T>(d));
+          for (int e = 0; e < 8; ++e) mean = __builtin_fmaf(s[i][e], w[i][e], mean);
+        mean = row_sum<G>(mean) * inv;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            d[i][e] = (s[i][e] * inv) * (w[i][e] - mean);
+            if (SCORES == ROUTER_SIGMOID) d[i][e] *= miss[i][e];
+          }
+      } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) d[i][e] = 0.f;
       }
+#pragma unroll
+      for (int i = 0; i < N; ++i) store_chunk<WHOLE>(out + tt * a.ldd, (i * G + lane) * 8, a.experts, pack<T>(d[i]));
     }
+    t += kGroups * kAhead;
+    if (t < t1) fetch(t);
   }
 }
 
@@ -420,25 +452,41 @@ void with_rows(int experts, F&& f) {
   else if (chunks <= 128) go(integral_constant<int, 64>{}, integral_constant<int, 2>{});
   else go(integral_constant<int, 64>{}, integral_constant<int, 4>{});
 }
+template <typename F>
+void with_case(int scores, bool whole, F&& f) {
+  std::integral_constant<int, ROUTER_SOFTMAX> softmax;
+  std::integral_constant<int, ROUTER_SIGMOID> sigmoid;
+  if (scores == ROUTER_SOFTMAX) whole ? f(softmax, std::true_type{}) : f(softmax, std::false_type{});
+  else whole ? f(sigmoid, std::true_type{}) : f(sigmoid, std::false_type{});
+}
 int lanes_of(int experts) {
   int g = 1;
   while (g < 64 && g * 8 < experts) g *= 2;
   return g;
 }
 
-// How the tokens of a sequence are shared out: about 512 workgroups in all, of whole passes of rows.
+// How the tokens of a sequence are shared out: about `most` workgroups in all, of whole passes of `threads`.
 struct Share {
   int per, wgs;
 };
-Share share(int32_t batch, int32_t tokens, int32_t experts, int32_t most) {
-  const int64_t pass = kThreads / lanes_of(experts);
+Share share(int32_t batch, int32_t tokens, int32_t experts, int32_t threads, int32_t most) {
+  const int64_t pass = threads / lanes_of(experts);
   const int64_t want = max((int64_t)1, (int64_t)most / max(batch, 1));
   int64_t per = ((int64_t)tokens + want - 1) / want;
   per = (per + pass - 1) / pass * pass;
   per = max(per, pass);
   return Share{(int)min(per, (int64_t)0x7FFFFFFF), (int)(((int64_t)tokens + per - 1) / per)};
 }
-constexpr int32_t kForwardWgs = 512, kBackwardWgs = 2048;
+// Forward: as many threads a workgroup as the registers of a lane allow, since every workgroup leaves sums of all
+// experts behind; backward: many small ones.
+int forward_threads(int32_t experts) { return experts <= 512 ? 1024 : 256; }
+Share forward_share(int32_t batch, int32_t tokens, int32_t experts) {
+  // (few enough for one workgroup: 256 threads, and no join)
+  const Share small = share(batch, tokens, experts, kThreads, 1);
+  if (batch == 1 && small.per <= 4 * kThreads / lanes_of(experts)) return small;
+  return share(batch, tokens, experts, forward_threads(experts), 256);
+}
+Share backward_share(int32_t batch, int32_t tokens, int32_t experts) { return share(batch, tokens, experts, kThreads, 1024); }
 
 int64_t round16(int64_t v) { return (v + 15) / 16 * 16; }
 struct Layout {
@@ -491,7 +539,7 @@ extern "C" {
 
 int64_t router_balance_workspace(int32_t batch, int32_t tokens, int32_t experts) {
   if (batch < 0 || tokens < 0 || experts < 1 || experts > kMaxExperts || batch > 65535) return -1;
-  return layout(batch, share(batch, tokens, experts, kForwardWgs).wgs, experts).bytes;
+  return layout(batch, forward_share(batch, tokens, experts).wgs, experts).bytes;
 }
 
 gemm_status router_balance(const router_balance_args* a, void* stream) {
@@ -510,7 +558,7 @@ gemm_status router_balance(const router_balance_args* a, void* stream) {
   if (!a->loss || (a->batch > 0 && (!a->counts || !a->valid || !a->probs))) return fail(GEMM_ERR_INVALID_ARG, "%s: NULL counts, valid, probs or loss", fn);
   for (const void* p : {(const void*)a->counts, (const void*)a->valid, (const void*)a->cu_seqlens, (const void*)a->probs, (const void*)a->loss})
     if ((uintptr_t)p & 3) return fail(GEMM_ERR_ALIGNMENT, "%s: outputs not 4-byte aligned", fn);
-  const Share sh = share(a->batch, a->tokens, a->experts, kForwardWgs);
+  const Share sh = forward_share(a->batch, a->tokens, a->experts);
   const Layout l = layout(a->batch, sh.wgs, a->experts);
   if (!a->workspace || a->workspace_bytes < l.bytes) return fail(GEMM_ERR_INVALID_ARG, "%s: workspace of %lld bytes expected", fn, (long long)l.bytes);
   if ((uintptr_t)a->workspace & 15) return fail(GEMM_ERR_ALIGNMENT, "%s: workspace not 16-byte aligned", fn);
@@ -528,10 +576,15 @@ gemm_status router_balance(const router_balance_args* a, void* stream) {
   with_type(a->type, [&](auto* t) {
     using T = std::remove_pointer_t<decltype(t)>;
     with_rows(a->experts, [&](auto g, auto n) {
-      constexpr int G = decltype(g)::value, N = decltype(n)::value;
+      constexpr int G = decltype(g)::value, N = decltype(n)::value, TH = N == 1 ? 1024 : 256;
       const dim3 grid((unsigned)sh.wgs, (unsigned)a->batch);
-      if (one) balance_kernel<T, G, N, true><<<grid, kThreads, 0, s>>>(f);
-      else balance_kernel<T, G, N, false><<<grid, kThreads, 0, s>>>(f);
+      auto go = [&](auto scores, auto whole) {
+        constexpr int S = decltype(scores)::value;
+        constexpr bool W = decltype(whole)::value;
+        if (one) balance_kernel<T, G, N, S, W, true, kThreads><<<grid, kThreads, 0, s>>>(f);
+        else balance_kernel<T, G, N, S, W, false, TH><<<grid, TH, 0, s>>>(f);
+      };
+      with_case(a->scores, a->experts == 8 * G * N, go);
     });
   });
   if (!one) balance_join_kernel<<<dim3((unsigned)(a->experts + 63) / 64, (unsigned)a->batch), kThreads, 0, s>>>(f);
@@ -553,15 +606,18 @@ gemm_status router_balance_backward(const router_balance_backward_args* a, void*
   if (a->dlogits == a->logits && ((a->tokens > 1 && a->dlogits_ld != a->logits_ld) || (a->batch > 1 && a->dlogits_batch != a->logits_batch)))
     return fail(GEMM_ERR_INVALID_ARG, "%s: dlogits in the place of the logits needs their strides", fn);
   clear_error();
-  const Share sh = share(a->batch, a->tokens, a->experts, kBackwardWgs);
+  const Share sh = backward_share(a->batch, a->tokens, a->experts);
   const Backward f{a->batch, a->tokens, a->experts, a->scores, a->coef * (float)a->experts / ((float)a->batch * (float)a->k),
                    a->logits, a->mask, a->counts, a->valid, a->grad, a->dlogits, a->logits_ld, a->logits_batch,
                    a->dlogits_ld, a->dlogits_batch, sh.per};
   with_type(a->type, [&](auto* t) {
     using T = std::remove_pointer_t<decltype(t)>;
     with_rows(a->experts, [&](auto g, auto n) {
-      balance_backward_kernel<T, decltype(g)::value, decltype(n)::value>
-          <<<dim3((unsigned)sh.wgs, (unsigned)a->batch), kThreads, 0, (hipStream_t)stream>>>(f);
+      constexpr int G = decltype(g)::value, N = decltype(n)::value;
+      const dim3 grid((unsigned)sh.wgs, (unsigned)a->batch);
+      with_case(a->scores, a->experts == 8 * G * N, [&](auto scores, auto whole) {
+        balance_backward_kernel<T, G, N, decltype(scores)::value, decltype(whole)::value><<<grid, kThreads, 0, (hipStream_t)stream>>>(f);
+      });
     });
   });
   return launched(fn);
