@@ -167,54 +167,68 @@ __device__ __forceinline__ void store_columns(const Mat& m, const Fp8Geometry& g
   write_transposed<EXACT>(v, r, r0, c0, cols, gt, m.codes, s);
 }
 
+// Tile i of the matrix: along the rows, or (down) down the columns.
+struct TileMap {
+  uint32_t first;
+  FastDiv fd;  // by the tiles of a row, or of a column
+  int32_t down;
+};
 struct TileAt {
   int r0, c0;
 };
-// Workgroups go to the eight XCDs in turn; each XCD takes a run of tiles down the rows, so that lines of the
-// transposed matrices that two tiles share are put together in one L2. False: no tile.
-__device__ __forceinline__ bool tile_of(uint32_t first, uint32_t tiles, const FastDiv& fd_ty, TileAt& t) {
-  const uint32_t per = (tiles + 7) >> 3, i = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-  if (i >= tiles) return false;  // (the grid is 8 per)
-  uint32_t bx, by;
-  fd_divmod(fd_ty, first + i, bx, by);
-  t = TileAt{(int)by * kTile, (int)bx * kTile};
-  return true;
+__device__ __forceinline__ TileAt tile_at(const TileMap& m, uint32_t i) {
+  uint32_t q, r;
+  fd_divmod(m.fd, m.first + i, q, r);
+  return m.down ? TileAt{(int)r * kTile, (int)q * kTile} : TileAt{(int)q * kTile, (int)r * kTile};
 }
 
-// ---- the quantiser of a whole matrix in both directions, or by tiles.
-template <typename T, bool TILES>
-__global__ __launch_bounds__(kThreads) void quantize_tiles_kernel(const T* x, int64_t ldx, int rows, int cols, uint32_t first,
-                                                                  uint32_t tiles, FastDiv fd_ty, Mat q, Mat qt) {
-  constexpr bool kExact = sizeof(T) == 4;
-  __shared__ TileShared s;
-  TileAt at;
-  if (!tile_of(first, tiles, fd_ty, at)) return;
-  const int tid = threadIdx.x, g = tid >> 4, cl = tid & 15;
-  const int r = at.r0 + g * 8, c = at.c0 + cl * 8;
-  const Fp8Geometry geo = fp8_geometry(cols), geo_t = fp8_geometry(rows);
+// A thread's rows of one matrix of the tile: the chunks of rows r + [0, 8) at column c. Rows past the end load the last
+// one, so that no load has a branch.
+template <typename T, bool WHOLE>
+struct TileRows {
   Chunk<T> in[8];
+  __device__ __forceinline__ void load(const T* x, int64_t ld, int r, int c, int rows, int cols) {
 #pragma unroll
-  for (int p = 0; p < 8; ++p) in[p] = load_chunk<false>(x + (int64_t)min(r + p, rows - 1) * ldx, c, cols);
-  float v[8][8];
+    for (int p = 0; p < 8; ++p) in[p] = load_chunk<WHOLE>(x + (int64_t)min(r + p, rows - 1) * ld, c, cols);
+  }
+  // Row p, zeros past the matrix (edge: the tile reaches there).
+  __device__ __forceinline__ void values(int p, int r, int c, int rows, int cols, bool edge, float (&v)[8]) {
+    if (edge) {
+      settle<WHOLE>(in[p], c, cols);
+      unpack(in[p], v);
 #pragma unroll
-  for (int p = 0; p < 8; ++p) {
-    settle<false>(in[p], c, cols);
-    unpack(in[p], v[p]);
-    if (r + p >= rows) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[p][e] = 0.f;
+      for (int e = 0; e < 8; ++e) v[e] = r + p < rows ? v[e] : 0.f;
+    } else {
+      unpack(in[p], v);
     }
   }
+};
+
+// ---- the quantiser of a whole matrix in both directions, or by tiles.
+template <typename T, bool TILES, bool WHOLE>
+__global__ __launch_bounds__(kThreads) void quantize_tiles_kernel(const T* x, int64_t ldx, int rows, int cols, TileMap map, Mat q, Mat qt) {
+  constexpr bool kExact = sizeof(T) == 4;
+  __shared__ TileShared s;
+  const int tid = threadIdx.x, g = tid >> 4, cl = tid & 15;
+  const Fp8Geometry geo = fp8_geometry(cols), geo_t = fp8_geometry(rows);
+  const TileAt at = tile_at(map, blockIdx.x);
+  const int r = at.r0 + g * 8, c = at.c0 + cl * 8;
+  const bool edge = at.r0 + kTile > rows || at.c0 + kTile > cols;
+  TileRows<T, WHOLE> in;
+  in.load(x, ldx, r, c, rows, cols);
+  float v[8][8];
+#pragma unroll
+  for (int p = 0; p < 8; ++p) in.values(p, r, c, rows, cols, edge, v[p]);
   if constexpr (TILES) {
     float a = largest8(v[0]);
 #pragma unroll
     for (int p = 1; p < 8; ++p) a = larger(a, largest8(v[p]));
     a = row_max16(a);
-    if (cl == 0) s.part[g] = a;
+    if (cl == 0) s.factor[g] = a;
     __syncthreads();
-    a = s.part[0];
+    a = s.factor[0];
 #pragma unroll
-    for (int i = 1; i < 16; ++i) a = larger(a, s.part[i]);
+    for (int j = 1; j < 16; ++j) a = larger(a, s.factor[j]);
     const Fp8Factor f = fp8_block(a);
     const int i = at.r0 / kTile, b = at.c0 / kTile;
     if (q.codes) {
@@ -228,7 +242,6 @@ __global__ __launch_bounds__(kThreads) void quantize_tiles_kernel(const T* x, in
       float all[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) all[j] = f.r;
-      __syncthreads();  // (the maxima have been read)
       write_transposed<kExact>(v, all, at.r0, at.c0, cols, geo_t, qt.codes, s);
     }
   } else {
@@ -252,55 +265,48 @@ struct BackArgs {
   Mat q, qt, yt;
   int64_t lddy, lddx, ldy;
 };
-template <typename T, int ACT>
-__global__ __launch_bounds__(kThreads) void act_backward_kernel(const BackArgs<T> a, uint32_t first, uint32_t tiles, FastDiv fd_ty) {
+template <typename T, int ACT, bool WHOLE>
+__global__ __launch_bounds__(kThreads) void act_backward_kernel(const BackArgs<T> a, TileMap map) {
   __shared__ TileShared sx, sy;
-  TileAt at;
-  if (!tile_of(first, tiles, fd_ty, at)) return;
   const int tid = threadIdx.x, g = tid >> 4, cl = tid & 15;
-  const int r = at.r0 + g * 8, c = at.c0 + cl * 8;
   const Fp8Geometry geo = fp8_geometry(a.cols), geo_t = fp8_geometry(a.rows);
-  Chunk<T> in[8];
+  const TileAt at = tile_at(map, blockIdx.x);
+  const int r = at.r0 + g * 8, c = at.c0 + cl * 8;
+  const bool edge = at.r0 + kTile > a.rows || at.c0 + kTile > a.cols;
+  TileRows<T, WHOLE> in;
   uint2 w[8];
   float scale[8];
+  if (a.dy) in.load(a.dy, a.lddy, r, c, a.rows, a.cols);
 #pragma unroll
   for (int p = 0; p < 8; ++p) {
     const int64_t row = min(r + p, a.rows - 1);
-    if (a.dy) in[p] = load_chunk<false>(a.dy + row * a.lddy, c, a.cols);
     w[p] = *(const uint2*)(a.codes + row * geo.kp + min(c, geo.kp - 8));
     scale[p] = a.scales[fp8_row_scale(row, at.c0 / kFp8Block, geo.nq)];
   }
-  const bool edge = at.r0 + kTile > a.rows || at.c0 + kTile > a.cols;
-  // Values past the matrix are zero in both results.
-  auto inside = [&](float (&v)[8], int p) {
-    if (!edge) return;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = r + p < a.rows && c + e < a.cols ? v[e] : 0.f;
-  };
   float v[8][8], y[8][8];
 #pragma unroll
   for (int p = 0; p < 8; ++p) {
     float x[8], d[8];
     fp8_values8(w[p], scale[p], x);
-    if (a.dy) {
-      settle<false>(in[p], c, a.cols);
-      unpack(in[p], v[p]);
-    }
+    if (a.dy) in.values(p, r, c, a.rows, a.cols, edge, v[p]);
     const float nan = -0.f * scale[p];  // NaN for a NaN block, whose slopes are not; -0 changes no other product
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       act_and_slope<ACT>(x[e], y[p][e], d[e]);
       if (ACT == ACT_GELU_TANH || ACT == ACT_SILU) y[p][e] += nan;
+      if (a.dy) v[p][e] = __builtin_fmaf(v[p][e], d[e], nan);
     }
-    inside(y[p], p);
-    if (a.dy) {
+    if (edge) {  // (rows past the end are copies of the last one)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[p][e] = __builtin_fmaf(v[p][e], d[e], nan);
-      inside(v[p], p);
+      for (int e = 0; e < 8; ++e) {
+        const bool inside = r + p < a.rows && c + e < a.cols;
+        y[p][e] = inside ? y[p][e] : 0.f;
+        v[p][e] = inside ? v[p][e] : 0.f;
+      }
     }
     if (r + p < a.rows) {
-      if (a.y) store_chunk<false>(a.y + (int64_t)(r + p) * a.ldy, c, a.cols, pack<T>(y[p]));
-      if (a.dx) store_chunk<false>(a.dx + (int64_t)(r + p) * a.lddx, c, a.cols, pack<T>(v[p]));
+      if (a.y) store_chunk<WHOLE>(a.y + (int64_t)(r + p) * a.ldy, c, a.cols, pack<T>(y[p]));
+      if (a.dx) store_chunk<WHOLE>(a.dx + (int64_t)(r + p) * a.lddx, c, a.cols, pack<T>(v[p]));
       if (a.q.codes) store_row_chunk<false>(a.q, geo, r + p, c >> 3, v[p]);
     }
   }
@@ -323,23 +329,34 @@ __global__ __launch_bounds__(kThreads) void dequantize_kernel(const uint8_t* cod
   store_chunk<false>(out + r * ldo, (int)ch * 8, g.k, pack<T>(v));
 }
 
+gemm_status launched(const char* fn) {
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return fail(GEMM_ERR_HIP, "%s launch: %s", fn, hipGetErrorString(e));
+  return GEMM_OK;
+}
+
 // Launch `f(r0, n)` over ranges of rows whose chunks number below 2^31.
 template <typename F>
 void row_ranges(int32_t rows, uint32_t cpr, F&& f) {
   const int64_t per = max((int64_t)1, (int64_t)0x7FFFFF00 / cpr);
   for (int64_t r0 = 0; r0 < rows; r0 += per) f(r0, (uint32_t)(min((int64_t)rows - r0, per) * cpr));
 }
-// Launch `f(first, tiles, grid, fd_ty)` over ranges of the 128 x 128 tiles. False: too many.
+// Launch `f(grid, map)` over the 128 x 128 tiles. Tiles follow each other along the
+// rows, so that the lines of all matrices that the card works on at a time lie together; where rows of a transposed matrix
+// are no whole lines, down the columns, so that the lines that two tiles share are put together in a cache.
 template <typename F>
-bool tile_ranges(int32_t rows, int32_t cols, F&& f) {
+gemm_status tile_ranges(const char* fn, int32_t rows, int32_t cols, bool transposed, F&& f) {
   const int64_t ty = ((int64_t)rows + kTile - 1) / kTile, tx = ((int64_t)cols + kTile - 1) / kTile;
-  if (ty * tx > 0x7FFFFF00) return false;
+  if (ty * tx > 0x7FFFFF00) return fail(GEMM_ERR_UNSUPPORTED, "%s: more than 2^31 tiles", fn);
+  TileMap m;
+  m.down = transposed && rows % kTile != 0;
+  m.fd = make_fastdiv((uint32_t)(m.down ? ty : tx));
   constexpr int64_t most = 1 << 22;  // (a grid has below 2^32 threads)
   for (int64_t first = 0; first < ty * tx; first += most) {
-    const uint32_t tiles = (uint32_t)min(ty * tx - first, most);
-    f((uint32_t)first, tiles, (tiles + 7) / 8 * 8, make_fastdiv((uint32_t)ty));
+    m.first = (uint32_t)first;
+    f((uint32_t)min(ty * tx - first, most), m);
   }
-  return true;
+  return launched(fn);
 }
 
 constexpr int32_t kMaxExtent = 1 << 30;
@@ -365,12 +382,6 @@ gemm_status check_fp8(const char* fn, const char* name, const void* codes, const
   if ((uintptr_t)scales & 3) return fail(GEMM_ERR_ALIGNMENT, "%s: scales of %s not 4-byte aligned", fn, name);
   return GEMM_OK;
 }
-gemm_status launched(const char* fn) {
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return fail(GEMM_ERR_HIP, "%s launch: %s", fn, hipGetErrorString(e));
-  return GEMM_OK;
-}
-
 template <typename T>
 void run_rows(const T* x, int64_t ldx, int32_t rows, int32_t cols, int act, Mat saved, Mat q, T* y, int64_t ldy, hipStream_t s) {
   const Fp8Geometry g = fp8_geometry(cols);
@@ -404,20 +415,22 @@ gemm_status fp8_quantize(int32_t rows, int32_t cols, const void* x, int32_t x_ty
   clear_error();
   hipStream_t s = (hipStream_t)stream;
   const Mat q{(uint8_t*)codes, (float*)scales}, qt{(uint8_t*)codes_t, (float*)scales_t};
-  bool fits = true;
   with_type(x_type, [&](auto* t) {
     using T = std::remove_pointer_t<decltype(t)>;
     if (scaling == FP8_ROWS && !codes_t) {
       run_rows<T>((const T*)x, ldx, rows, cols, ACT_NONE, q, Mat{nullptr, nullptr}, nullptr, 0, s);
+      st = launched(fn);
       return;
     }
-    fits = tile_ranges(rows, cols, [&](uint32_t first, uint32_t tiles, uint32_t grid, FastDiv fd) {
-      if (scaling == FP8_ROWS) quantize_tiles_kernel<T, false><<<grid, kThreads, 0, s>>>((const T*)x, ldx, rows, cols, first, tiles, fd, q, qt);
-      else quantize_tiles_kernel<T, true><<<grid, kThreads, 0, s>>>((const T*)x, ldx, rows, cols, first, tiles, fd, q, qt);
+    st = tile_ranges(fn, rows, cols, codes_t != nullptr, [&](uint32_t grid, const TileMap& m) {
+      auto go = [&](auto by_tiles, auto whole) {
+        quantize_tiles_kernel<T, decltype(by_tiles)::value, decltype(whole)::value><<<grid, kThreads, 0, s>>>((const T*)x, ldx, rows, cols, m, q, qt);
+      };
+      if (scaling == FP8_ROWS) cols % 8 == 0 ? go(std::false_type{}, std::true_type{}) : go(std::false_type{}, std::false_type{});
+      else cols % 8 == 0 ? go(std::true_type{}, std::true_type{}) : go(std::true_type{}, std::false_type{});
     });
   });
-  if (!fits) return fail(GEMM_ERR_UNSUPPORTED, "%s: more than 2^31 tiles", fn);
-  return launched(fn);
+  return st;
 }
 
 gemm_status fp8_dequantize(int32_t rows, int32_t k, int32_t scaling, const void* codes, const void* scales, void* out,
@@ -500,15 +513,17 @@ gemm_status fp8_act_backward(const fp8_act_backward_args* a, void* stream) {
   }
   if (a->y && a->y == a->dy) return fail(GEMM_ERR_INVALID_ARG, "%s: y in the place of dy", fn);
   clear_error();
-  bool fits = true;
   with_type(a->type, [&](auto* t) {
     using T = std::remove_pointer_t<decltype(t)>;
     const BackArgs<T> b{a->rows, a->cols, (const T*)a->dy, (const uint8_t*)a->saved_codes, (const float*)a->saved_scales,
                         (T*)a->dx, (T*)a->y, Mat{(uint8_t*)a->q_codes, (float*)a->q_scales},
                         Mat{(uint8_t*)a->qt_codes, (float*)a->qt_scales}, Mat{(uint8_t*)a->yt_codes, (float*)a->yt_scales},
                         a->lddy, a->lddx, a->ldy};
-    fits = tile_ranges(a->rows, a->cols, [&](uint32_t first, uint32_t tiles, uint32_t grid, FastDiv fd) {
-      auto go = [&](auto act) { act_backward_kernel<T, decltype(act)::value><<<grid, kThreads, 0, (hipStream_t)stream>>>(b, first, tiles, fd); };
+    st = tile_ranges(fn, a->rows, a->cols, qt || yt, [&](uint32_t grid, const TileMap& m) {
+      auto go = [&](auto act) {
+        if (a->cols % 8 == 0) act_backward_kernel<T, decltype(act)::value, true><<<grid, kThreads, 0, (hipStream_t)stream>>>(b, m);
+        else act_backward_kernel<T, decltype(act)::value, false><<<grid, kThreads, 0, (hipStream_t)stream>>>(b, m);
+      };
       switch (a->act) {
         case GEMM_ACT_RELU: go(std::integral_constant<int, ACT_RELU>{}); break;
         case GEMM_ACT_RELU_SQ: go(std::integral_constant<int, ACT_RELU_SQ>{}); break;
@@ -518,8 +533,7 @@ gemm_status fp8_act_backward(const fp8_act_backward_args* a, void* stream) {
       }
     });
   });
-  if (!fits) return fail(GEMM_ERR_UNSUPPORTED, "%s: more than 2^31 tiles", fn);
-  return launched(fn);
+  return st;
 }
 
 }  // extern "C"

@@ -56,7 +56,7 @@ __global__ __launch_bounds__(256) void mx_join_kernel(const MxParams p, uint32_t
 }
 
 // Compute units of the current device, looked up once per device.
-static gemm_status compute_units(int32_t* cus) {
+gemm_status compute_units(int32_t* cus) {
   static std::atomic<int32_t> cache[64];
   int dev = 0, n = 0;
   hipError_t e = hipGetDevice(&dev);
