@@ -68,6 +68,14 @@ int64_t mx_row_blocks(const mx_gemm_plan& p, int32_t bm) {
 // so 16-row tiles serve few rows (1x8192x8192 8.0; in 32x64 tiles 13.8), 32x64 up to 128 or 256 rows,
 // 128x128 up to one round of 256x256 tiles, and deep products with few tiles are split
 // (128x512x8192: 8.3 in 32x32 tiles over four workgroups, 13.8 over one).
+// FP8 products run in the same kernels with more vector arithmetic, B's scales by tiles (or by rows), fitted to 60
+// shapes each from 1x1024x1024 to 4096x8192x8192 (4% from the best kernel in the mean, 12% at most):
+//   256x256: 1.66 (2.07) a step (4096^3 63.5 measured, 64.1 estimated; 2048x8192x8192 115.9, 117)
+//   128x128: 55 (43) KB a microsecond alone on a compute unit, 65 (55) for two workgroups (256x4096x4096 over
+//     one 25.8, 25.6, over four 21.8, 22.7; 2048x4096x4096 38.3, 38.5), and B at 7 MB a microsecond at most
+//     (64x8192x8192 over four 23.1, 23.6)
+//   16x16, 16x32, 32x32: B's bytes, from memory, at 25, 19.5 and 18.5 KB a microsecond, A's, from a cache, at 50, 100
+//     and 95 (16x16 and 16x32: 1x8192x8192 13.3, 13.3 and 16.1, 16.0; 16x8192x8192 18.1, 18.1 and 16.4, 17.2)
 static double estimate(const mx_gemm_plan& p, int32_t cus, int32_t tile, int32_t split) {
   int32_t bm, bn;
   mx_tile_extent(tile, &bm, &bn);
@@ -78,17 +86,24 @@ static double estimate(const mx_gemm_plan& p, int32_t cus, int32_t tile, int32_t
   const double steps = split > 1 ? 4.0 * (double)cdiv(nsb, split) : (double)cdiv(p.d.K, 128);
   const double rows_a = p.d.M < bm ? p.d.M : bm, rows_b = p.d.N < bn ? p.d.N : bn;
   const double kb = (rows_a * (p.d.a_format == MX_E4M3 ? 128 : 64) + rows_b * (p.d.b_format == MX_E4M3 ? 128 : 64)) / 1024;
+  const bool fp8 = p.b_scaling >= 0, fp8_rows = p.b_scaling == FP8_ROWS;
   double t;
   if (tile == MX_TILE_256) {
     // (a last round of at most half the card runs in 128x128 quarters)
-    const double step = p.d.a_format == MX_E2M1 && p.d.b_format == MX_E2M1 ? 0.85 : 1.36;
+    const double step = fp8 ? (fp8_rows ? 2.07 : 1.66) : p.d.a_format == MX_E2M1 && p.d.b_format == MX_E2M1 ? 0.85 : 1.36;
     const double full = (double)((int64_t)wgs / cus), rest = wgs / cus - full;
     const bool quarters = full > 0 && rest > 0 && rest <= 0.5;
     t = 6 + (full + (quarters ? rest * 1.3 : rest > 0)) * (steps * step + 5) + (quarters ? 4 : 0);
   } else if (tile == MX_TILE_128) {
-    t = 7 + (wgs <= cus ? steps * kb / 74 : (double)cdiv((int64_t)wgs, 2 * (int64_t)cus) * (steps * 2 * kb / 56 + 1) - 1);
+    const double alone = fp8 ? (fp8_rows ? 43 : 55) : 74, two = fp8 ? (fp8_rows ? 55 : 65) : 56;
+    const double memory = fp8 ? (double)p.d.N * p.d.K / 7e6 : 0;  // (B's bytes)
+    t = 7 + (wgs <= cus ? (steps * kb / alone > memory ? steps * kb / alone : memory) : (double)cdiv((int64_t)wgs, 2 * (int64_t)cus) * (steps * 2 * kb / two + 1) - 1);
   } else {
-    const double load = wgs / cus, one = steps * kb / 33;
+    const double load = wgs / cus;
+    double one = steps * kb / 33;
+    if (fp8 && tile == MX_TILE_16) one = steps * (rows_b / 8 / 25 + rows_a / 8 / 50);
+    if (fp8 && tile == MX_TILE_32) one = steps * (rows_b / 8 / 18.5 + rows_a / 8 / 95);
+    if (fp8 && tile == MX_TILE_16X32) one = steps * (rows_b / 8 / 19.5 + rows_a / 8 / 100);
     const double start = tile == MX_TILE_16 ? 2.7 : tile == MX_TILE_16X32 ? 2.8 : tile == MX_TILE_32 ? 3.0 : 3.4;
     const double least = tile == MX_TILE_32X64 ? 2.2 : 1.6;
     t = start + (one > least ? one : least) * (load > 1 ? load : 1);
