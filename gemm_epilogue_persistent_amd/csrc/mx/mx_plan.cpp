@@ -97,7 +97,8 @@ static double estimate(const mx_gemm_plan& p, int32_t cus, int32_t tile, int32_t
   } else if (tile == MX_TILE_128) {
     const double alone = fp8 ? (fp8_rows ? 43 : 55) : 74, two = fp8 ? (fp8_rows ? 55 : 65) : 56;
     const double memory = fp8 ? (double)p.d.N * p.d.K / 7e6 : 0;  // (B's bytes)
-    t = 7 + (wgs <= cus ? (steps * kb / alone > memory ? steps * kb / alone : memory) : (double)cdiv((int64_t)wgs, 2 * (int64_t)cus) * (steps * 2 * kb / two + 1) - 1);
+    const double work = wgs <= cus ? steps * kb / alone : (double)cdiv((int64_t)wgs, 2 * (int64_t)cus) * (steps * 2 * kb / two + 1) - 1;
+    t = 7 + (work > memory ? work : memory);
   } else {
     const double load = wgs / cus;
     double one = steps * kb / 33;
