@@ -326,14 +326,17 @@ __global__ __launch_bounds__(kThreads) void balance_join_kernel(const Forward a)
   __syncthreads();
   if (!last) return;
   __threadfence();
+  // (the fences order the others' stores before these loads; eight are under way at a time)
   float v = 0.f;
-  for (uint32_t i = tid; i < gridDim.x * gridDim.y; i += kThreads) v += __hip_atomic_load(a.part_loss + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll 8
+  for (uint32_t i = tid; i < gridDim.x * gridDim.y; i += kThreads) v += a.part_loss[i];
   v = block_sum<kThreads>(v, red);
   if (tid == 0) *a.loss = v * loss_factor(a);
   if (a.cu_seqlens)
     offsets<kThreads>(a.cu_seqlens, a.experts, [&](int x) {
       int32_t s = 0;
-      for (int y = 0; y < a.batch; ++y) s += __hip_atomic_load(a.counts + (int64_t)y * a.experts + x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll 8
+      for (int y = 0; y < a.batch; ++y) s += a.counts[(int64_t)y * a.experts + x];
       return s;
     }, (int32_t*)red);
 }
