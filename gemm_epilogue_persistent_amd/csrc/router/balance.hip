@@ -489,7 +489,7 @@ Share forward_share(int32_t batch, int32_t tokens, int32_t experts) {
   if (batch == 1 && small.per <= 4 * kThreads / lanes_of(experts)) return small;
   return share(batch, tokens, experts, forward_threads(experts), 256);
 }
-Share backward_share(int32_t batch, int32_t tokens, int32_t experts) { return share(batch, tokens, experts, kThreads, 1024); }
+Share backward_share(int32_t batch, int32_t tokens, int32_t experts) { return share(batch, tokens, experts, kThreads, 2048); }
 
 int64_t round16(int64_t v) { return (v + 15) / 16 * 16; }
 struct Layout {
