@@ -3,6 +3,7 @@
 // Bound by memory: the logits are read once in each direction, a value costs two or three exponentials. G
 // neighbouring lanes hold a token's logits, 8 (or 16, 32) a lane, so that a row is one coalesced load and its sums stay in
 // registers; a workgroup takes a run of tokens of one sequence.
+#include <algorithm>
 #include <initializer_list>
 #include <type_traits>
 
@@ -17,6 +18,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxExperts = 2048;
+__device__ __forceinline__ uint32_t lesser(uint32_t a, uint32_t b) { return a < b ? a : b; }
 
 // ---- exchange over the G lanes of a row (G a power of two; fixed order, the same result in every lane)
 template <int CTRL>
@@ -193,15 +195,15 @@ __global__ __launch_bounds__(TH) void balance_kernel(const Forward a) {
   __shared__ float red[kWaves];
   const int tid = threadIdx.x, lane = tid & (G - 1), group = tid / G, wave = tid >> 6;
   const int b = blockIdx.y, wg = blockIdx.x;
-  const int t0 = wg * a.per, t1 = min(a.tokens, t0 + a.per);
+  const uint32_t t0 = (uint32_t)wg * a.per, t1 = lesser((uint32_t)a.tokens, t0 + a.per);  // (a token's number may pass the last one)
   const uint8_t* mask = a.mask ? a.mask + (int64_t)b * a.tokens : nullptr;
   const T* logits = (const T*)a.logits + b * a.ldb;
   Rows<T, G, N, WHOLE> rows[kAhead];
   bool use[kAhead];
-  auto fetch = [&](int t) {
+  auto fetch = [&](uint32_t t) {
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      const int tt = t + u * kGroups, at = min(tt, t1 - 1);
+      const uint32_t tt = t + u * kGroups, at = lesser(tt, t1 - 1);
       use[u] = tt < t1 && (!mask || mask[at]);
       rows[u].load(logits + at * a.ld, a.experts, lane);
     }
@@ -212,7 +214,7 @@ __global__ __launch_bounds__(TH) void balance_kernel(const Forward a) {
   if (tid == 0) tokens_seen = 0;
   __syncthreads();
   const int64_t id0 = ((int64_t)b * a.tokens + t0) * a.k;
-  const uint32_t ids = (uint32_t)(t1 - t0) * (uint32_t)a.k;
+  const uint32_t ids = (t1 - t0) * (uint32_t)a.k;
   for (uint32_t i = tid; i < ids; i += TH) {
     const int64_t e = a.index_bytes == 8 ? ((const int64_t*)a.chosen)[id0 + i] : (int64_t)((const int32_t*)a.chosen)[id0 + i];
     if (e >= 0 && e < a.experts && (!mask || mask[t0 + i / (uint32_t)a.k])) atomicAdd(&hist[(int)e], 1);
@@ -223,7 +225,7 @@ __global__ __launch_bounds__(TH) void balance_kernel(const Forward a) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[i][e] = 0.f;
   int seen = 0;
-  for (int t = t0 + group;;) {
+  for (uint32_t t = t0 + group;;) {
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       if (!use[u]) continue;
@@ -367,16 +369,16 @@ template <typename T, int G, int N, int SCORES, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void balance_backward_kernel(const Backward a) {
   constexpr int kGroups = kThreads / G, kAhead = N == 1 ? 4 : (N == 2 ? 2 : 1);
   const int tid = threadIdx.x, lane = tid & (G - 1), group = tid / G, b = blockIdx.y;
-  const int t0 = blockIdx.x * a.per, t1 = min(a.tokens, t0 + a.per);
+  const uint32_t t0 = blockIdx.x * (uint32_t)a.per, t1 = lesser((uint32_t)a.tokens, t0 + a.per);
   const uint8_t* mask = a.mask ? a.mask + (int64_t)b * a.tokens : nullptr;
   const T* logits = (const T*)a.logits + b * a.ldb;
   T* out = (T*)a.dlogits + b * a.lddb;
   Rows<T, G, N, WHOLE> rows[kAhead];
   bool use[kAhead];
-  auto fetch = [&](int t) {
+  auto fetch = [&](uint32_t t) {
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      const int at = min(t + u * kGroups, t1 - 1);
+      const uint32_t at = lesser(t + u * kGroups, t1 - 1);
       use[u] = !mask || mask[at];
       rows[u].load(logits + at * a.ld, a.experts, lane);
     }
@@ -401,10 +403,10 @@ __global__ __launch_bounds__(kThreads) void balance_backward_kernel(const Backwa
   for (int i = 0; i < N; ++i)
 #pragma unroll
     for (int e = 0; e < 8; ++e) w[i][e] = WHOLE || (i * G + lane) * 8 + e < a.experts ? (float)(c[i][e] - least) * factor : 0.f;
-  for (int t = t0 + group; t < t1;) {
+  for (uint32_t t = t0 + group; t < t1;) {
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      const int tt = t + u * kGroups;
+      const uint32_t tt = t + u * kGroups;
       if (tt >= t1) continue;
       float d[N][8];
       if (use[u]) {
@@ -474,11 +476,11 @@ struct Share {
 };
 Share share(int32_t batch, int32_t tokens, int32_t experts, int32_t threads, int32_t most) {
   const int64_t pass = threads / lanes_of(experts);
-  const int64_t want = max((int64_t)1, (int64_t)most / max(batch, 1));
+  const int64_t want = std::max((int64_t)1, (int64_t)most / std::max(batch, 1));
   int64_t per = ((int64_t)tokens + want - 1) / want;
   per = (per + pass - 1) / pass * pass;
-  per = max(per, pass);
-  return Share{(int)min(per, (int64_t)0x7FFFFFFF), (int)(((int64_t)tokens + per - 1) / per)};
+  per = std::max(per, pass);
+  return Share{(int)std::min(per, (int64_t)0x7FFFFFFF), (int)(((int64_t)tokens + per - 1) / per)};
 }
 // Forward: as many threads a workgroup as the registers of a lane allow, since every workgroup leaves sums of all
 // experts behind; backward: many small ones.
@@ -522,7 +524,9 @@ gemm_status check_logits(const char* fn, const char* name, int32_t batch, int32_
   const int64_t most = (int64_t)1 << 48;
   if (ld < 0 || ld > most || ldb < 0 || ldb > most) return fail(GEMM_ERR_UNSUPPORTED, "%s: strides of %s outside [0, 2^48]", fn, name);
   if (tokens > 1 && ld < experts) return fail(GEMM_ERR_INVALID_ARG, "%s: rows of %s overlap", fn, name);
-  if (batch > 1 && tokens > 0 && ldb < (tokens - 1) * ld + experts) return fail(GEMM_ERR_INVALID_ARG, "%s: sequences of %s overlap", fn, name);
+  const __int128 l = ld, b = ldb;
+  const bool apart = b >= (tokens - 1) * l + experts, alternate = ldb >= experts && l >= (batch - 1) * b + experts;
+  if (batch > 1 && tokens > 0 && !apart && !(alternate && tokens > 1)) return fail(GEMM_ERR_INVALID_ARG, "%s: sequences of %s overlap", fn, name);
   if (!p) return fail(GEMM_ERR_INVALID_ARG, "%s: NULL %s", fn, name);
   if ((uintptr_t)p % (type == GEMM_DT_F32 ? 4 : 2)) return fail(GEMM_ERR_ALIGNMENT, "%s: %s not aligned to its elements", fn, name);
   return GEMM_OK;

@@ -35,7 +35,8 @@ typedef enum { ROUTER_SOFTMAX = 0, ROUTER_SIGMOID = 1 } router_scores;
  * grouped products take it for rows in the order of their experts (wrong past 2^31 choices).
  * workspace: router_balance_workspace bytes, 16-byte aligned; its contents need no preparation, and calls that
  * follow each other on a stream may share it. 1 <= experts <= 2048, 1 <= k <= experts, batch <= 65535, batch * tokens
- * * k below 2^31. batch = 0 or tokens = 0 gives zeros. */
+ * * k below 2^31. Rows do not overlap; sequences follow each other or alternate row by row (tokens
+ * outermost). batch = 0 or tokens = 0 gives zeros. */
 typedef struct {
   int32_t batch, tokens, experts, k;
   int32_t type;   /* gemm_dtype of the logits */

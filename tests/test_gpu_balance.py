@@ -278,3 +278,33 @@ def test_refusals():
         gep.router_balance_backward(x, x)
     with pytest.raises(ValueError):
         gep.balance_empty(0)
+
+
+@pytest.mark.parametrize("experts,dtype", [(8, torch.float32), (60, torch.bfloat16)])
+def test_tokens_outermost(experts, dtype):
+    """Logits (tokens, batch, experts), whose sequences alternate row by row, give what contiguous ones give."""
+    announce(f"balance with alternating sequences {experts}")
+    base = torch.randn(70, 3, experts, device="cuda").to(dtype)
+    logits = base.transpose(0, 1)
+    chosen = torch.randint(0, experts, (3, 70, 2), device="cuda")
+    want = gep.router_balance(logits.contiguous(), chosen)
+    got = gep.router_balance(logits, chosen)
+    for name in ("loss", "probs", "counts", "cu_seqlens", "valid"):
+        assert torch.equal(getattr(got, name), getattr(want, name))
+    d = gep.router_balance_backward(logits, got, dlogits=torch.empty_like(base).transpose(0, 1))
+    assert torch.equal(d, gep.router_balance_backward(logits.contiguous(), want))
+
+
+def test_most_tokens():
+    """2^31 - 1 tokens of one choice each: numbers past the last token pass 31 bits."""
+    announce("balance of 2^31 - 1 tokens")
+    n = 2 ** 31 - 1
+    logits, chosen = torch.zeros(n, 1, dtype=torch.bfloat16, device="cuda"), torch.zeros(n, 1, dtype=torch.int32, device="cuda")
+    b = gep.router_balance(logits, chosen)
+    assert b.counts.item() == n and b.valid.item() == n and b.cu_seqlens.tolist() == [0, n]
+    # (a workgroup adds 2^23 ones, which fp32 holds; the 256 workgroups' sums are added in four chains of 64, each sum rounded by
+    # 2^-24 of itself at most and all but the last one's exact; P, f and their product are rounded once each)
+    assert abs(b.loss.item() - 1) <= 2.0 ** -20
+    logits.fill_(1)
+    gep.router_balance_backward(logits, b, dlogits=logits)
+    assert not logits.any()
