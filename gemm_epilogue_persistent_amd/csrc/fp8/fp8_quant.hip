@@ -5,6 +5,7 @@
 //   rows   blocks along rows only. A thread takes 8 values, 16 lanes a block; the maximum crosses lanes by DPP.
 //   tiles  anything with blocks along columns, or tiles. A workgroup takes 128 x 128 values, which hold whole
 //          blocks of both directions, in registers.
+#include <algorithm>
 #include <type_traits>
 
 #include "../gemm_kernel.hpp"
@@ -338,8 +339,8 @@ gemm_status launched(const char* fn) {
 // Launch `f(r0, n)` over ranges of rows whose chunks number below 2^31.
 template <typename F>
 void row_ranges(int32_t rows, uint32_t cpr, F&& f) {
-  const int64_t per = max((int64_t)1, (int64_t)0x7FFFFF00 / cpr);
-  for (int64_t r0 = 0; r0 < rows; r0 += per) f(r0, (uint32_t)(min((int64_t)rows - r0, per) * cpr));
+  const int64_t per = std::max((int64_t)1, (int64_t)0x7FFFFF00 / cpr);
+  for (int64_t r0 = 0; r0 < rows; r0 += per) f(r0, (uint32_t)(std::min((int64_t)rows - r0, per) * cpr));
 }
 // Launch `f(grid, map)` over the 128 x 128 tiles. Tiles follow each other along the
 // rows, so that the lines of all matrices that the card works on at a time lie together; where rows of a transposed matrix
@@ -354,7 +355,7 @@ gemm_status tile_ranges(const char* fn, int32_t rows, int32_t cols, bool transpo
   constexpr int64_t most = 1 << 22;  // (a grid has below 2^32 threads)
   for (int64_t first = 0; first < ty * tx; first += most) {
     m.first = (uint32_t)first;
-    f((uint32_t)min(ty * tx - first, most), m);
+    f((uint32_t)std::min(ty * tx - first, most), m);
   }
   return launched(fn);
 }
@@ -412,6 +413,7 @@ gemm_status fp8_quantize(int32_t rows, int32_t cols, const void* x, int32_t x_ty
   if (st == GEMM_OK && (codes || scales)) st = check_fp8(fn, "x", codes, scales);
   if (st == GEMM_OK && (codes_t || scales_t)) st = check_fp8(fn, "x^T", codes_t, scales_t);
   if (st != GEMM_OK) return st;
+  if (codes == codes_t) return fail(GEMM_ERR_INVALID_ARG, "%s: x and x^T are one matrix", fn);
   clear_error();
   hipStream_t s = (hipStream_t)stream;
   const Mat q{(uint8_t*)codes, (float*)scales}, qt{(uint8_t*)codes_t, (float*)scales_t};
@@ -474,6 +476,7 @@ gemm_status fp8_act_forward(const fp8_act_args* a, void* stream) {
   if (st == GEMM_OK && saved) st = check_fp8(fn, "saved", a->saved_codes, a->saved_scales);
   if (st == GEMM_OK && q) st = check_fp8(fn, "q", a->q_codes, a->q_scales);
   if (st != GEMM_OK) return st;
+  if (saved && a->saved_codes == a->q_codes) return fail(GEMM_ERR_INVALID_ARG, "%s: saved and q are one matrix", fn);
   if (a->y == a->x && a->rows > 1 && a->ldy != a->ldx) return fail(GEMM_ERR_INVALID_ARG, "%s: y in the place of x needs its leading dimension", fn);
   clear_error();
   with_type(a->type, [&](auto* t) {

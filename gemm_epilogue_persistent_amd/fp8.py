@@ -142,6 +142,8 @@ def fp8_quantize(x, out=None, out_t=None, tiles=None, stream=None):
 def fp8_dequantize(q, out=None, dtype=torch.bfloat16, stream=None):
     """The values of an FP8 matrix in `out` (allocated in `dtype` if None), rounded to nearest."""
     codes, scales = _plain("q", q)
+    if q is None:
+        raise TypeError("q: an Fp8Tensor expected")
     if out is None:
         with _allocating(stream):
             out = torch.empty((q.rows, q.k), dtype=dtype, device=q.device)

@@ -112,7 +112,8 @@ gemm_status fp8_act_backward(const fp8_act_backward_args* args, void* stream);
  * The matrix instruction sums the 128 products of a block, and the blocks are scaled and added in fp32. The
  * instruction keeps the products of 32 values only to 2^-13 of their largest, so an F32 output has
  * fewer good bits than an fp32 product of the same values. sa * sb is formed in fp32: blocks whose product
- * of scales lies below 2^-126 lose bits, and one past fp32's range gives infinities.
+ * of scales lies below 2^-126 lose bits, and one past fp32's range gives infinities or, where the block's products sum
+ * to 0, NaN.
  * A (M, K) is FP8_ROWS; B (N, K) FP8_TILES (weights) or FP8_ROWS (the weight's gradient: dW = dY^T x X^T^T
  * of two matrices with blocks along the tokens). C, D, PostAct row-major (M, N) of type F16 / BF16 / F32
  * with their own leading dimensions (in elements). Grouped (groups > 0): B is (groups, N, K) and row r

@@ -334,3 +334,29 @@ def test_sizes_past_32_bits(lib, monkeypatch):
     with pytest.raises(ValueError):
         gep.router_balance(torch.empty((0, many, 8)).as_subclass(OnGpu), torch.empty((0, many, 2), dtype=torch.int64))
     del x
+
+
+def test_one_matrix_twice(lib):
+    """Two outputs at one address are refused."""
+    assert lib.fp8_quantize(128, 128, P, 2, 128, 0, 2 * P, 2 * P, 2 * P, 2 * P, None) == _abi.INVALID_ARG
+    assert lib.fp8_act_forward(ctypes.byref(act_args(q_codes=2 * P, saved_codes=2 * P)), None) == _abi.INVALID_ARG
+    with pytest.raises(TypeError):
+        gep.fp8_dequantize(None)
+
+
+def test_sequence_strides(lib):
+    """Sequences that overlap are refused, whatever their strides' product; those that alternate row by row are not (the
+    refusal here is that of the workspace, which comes later)."""
+    big = 1 << 48
+    for kw in (dict(logits_ld=big, logits_batch=big), dict(logits_ld=15, logits_batch=8), dict(logits_ld=16, logits_batch=7),
+               dict(tokens=2 ** 30 - 1, batch=2, k=1, logits_ld=big, logits_batch=big)):
+        assert lib.router_balance(ctypes.byref(balance_args(**kw)), None) == _abi.INVALID_ARG
+        assert b"sequences of logits overlap" in lib.gemm_last_error() or b"rows of logits" in lib.gemm_last_error()
+    for kw in (dict(logits_ld=16, logits_batch=8), dict(logits_ld=8, logits_batch=40)):
+        assert lib.router_balance(ctypes.byref(balance_args(workspace=None, **kw)), None) == _abi.INVALID_ARG
+        assert b"workspace" in lib.gemm_last_error()
+
+
+def test_workspace_of_many_tokens():
+    """Sharing out 2^31 - 1 tokens is 64-bit arithmetic: 256 workgroups' sums, not one for each 256 tokens."""
+    assert gep.router_balance_workspace(1, 2 ** 31 - 1, 8) < 1 << 20
