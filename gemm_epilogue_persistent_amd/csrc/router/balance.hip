@@ -283,25 +283,27 @@ __global__ __launch_bounds__(TH) void balance_kernel(const Forward a) {
   }
 }
 
-// Joins the workgroups' sums of one sequence for 64 experts, a quarter of them in each wave; the last workgroup of all
+// Joins the workgroups' sums of one sequence for 64 experts, a share of them in each wave of TH threads; the last workgroup of all
 // adds up the loss, in order, and the offsets.
-__global__ __launch_bounds__(kThreads) void balance_join_kernel(const Forward a) {
-  __shared__ float psum[4][64];
-  __shared__ int32_t csum[4][64], nsum[4];
-  __shared__ float red[4];
+template <int TH>
+__global__ __launch_bounds__(TH) void balance_join_kernel(const Forward a) {
+  constexpr int kWaves = TH / 64;
+  __shared__ float psum[kWaves][64];
+  __shared__ int32_t csum[kWaves][64], nsum[kWaves];
+  __shared__ float red[kWaves];
   __shared__ uint32_t last;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, b = blockIdx.y;
   const int e = blockIdx.x * 64 + lane;
   const int64_t first = (int64_t)b * a.wgs;
   int32_t n = 0;
-  for (int i = tid; i < a.wgs; i += kThreads) n += a.part_n[first + i];
+  for (int i = tid; i < a.wgs; i += TH) n += a.part_n[first + i];
 #pragma unroll
   for (int off = 1; off < 64; off <<= 1) n += __shfl_xor(n, off);
   float p = 0.f;
   int32_t c = 0;
   if (e < a.experts) {
 #pragma unroll 8
-    for (int i = wave; i < a.wgs; i += 4) {
+    for (int i = wave; i < a.wgs; i += kWaves) {
       p += a.part_p[(first + i) * a.experts + e];
       c += a.part_c[(first + i) * a.experts + e];
     }
@@ -310,32 +312,32 @@ __global__ __launch_bounds__(kThreads) void balance_join_kernel(const Forward a)
   csum[wave][lane] = c;
   if (lane == 0) nsum[wave] = n;
   __syncthreads();
-  n = nsum[0] + nsum[1] + nsum[2] + nsum[3];
   if (wave == 0) {
-    float mine = 0.f;
-    if (e < a.experts)
-      mine = finish_expert(a, b, e, (psum[0][lane] + psum[1][lane]) + (psum[2][lane] + psum[3][lane]),
-                           csum[0][lane] + csum[1][lane] + csum[2][lane] + csum[3][lane], n);
+    n = nsum[0], p = psum[0][lane], c = csum[0][lane];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) n += nsum[w], p += psum[w][lane], c += csum[w][lane];
+    float mine = e < a.experts ? finish_expert(a, b, e, p, c, n) : 0.f;
     mine = row_sum<64>(mine);
     if (lane == 0) {
       if (blockIdx.x == 0) a.valid[b] = n;
       a.part_loss[(int64_t)b * gridDim.x + blockIdx.x] = mine;
     }
   }
-  __threadfence();
-  __syncthreads();
-  if (tid == 0) last = atomicAdd(a.ticket, 1u) == gridDim.x * gridDim.y - 1;
+  if (wave == 0) {  // (all stores are its own; a fence of every wave costs 0.5 us each)
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
+    if (lane == 0) last = atomicAdd(a.ticket, 1u) == gridDim.x * gridDim.y - 1;
+  }
   __syncthreads();
   if (!last) return;
-  __threadfence();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
   // (the fences order the others' stores before these loads; eight are under way at a time)
   float v = 0.f;
 #pragma unroll 8
-  for (uint32_t i = tid; i < gridDim.x * gridDim.y; i += kThreads) v += a.part_loss[i];
-  v = block_sum<kThreads>(v, red);
+  for (uint32_t i = tid; i < gridDim.x * gridDim.y; i += TH) v += a.part_loss[i];
+  v = block_sum<TH>(v, red);
   if (tid == 0) *a.loss = v * loss_factor(a);
   if (a.cu_seqlens)
-    offsets<kThreads>(a.cu_seqlens, a.experts, [&](int x) {
+    offsets<TH>(a.cu_seqlens, a.experts, [&](int x) {
       int32_t s = 0;
 #pragma unroll 8
       for (int y = 0; y < a.batch; ++y) s += a.counts[(int64_t)y * a.experts + x];
@@ -493,6 +495,10 @@ Share forward_share(int32_t batch, int32_t tokens, int32_t experts) {
 }
 Share backward_share(int32_t batch, int32_t tokens, int32_t experts) { return share(batch, tokens, experts, kThreads, 2048); }
 
+// Of more sums than these the join takes 512 threads (256 sums of 512 experts 9.0 us in 256 threads, 7.3 in 512; of 2048
+// experts 13.6 and 10.3), else 256 (128 sums of 64 experts 5.4 and 5.8; 32 of 256 experts, 8 sequences, 6.3 and 7.5).
+constexpr int kManySums = 128;
+
 int64_t round16(int64_t v) { return (v + 15) / 16 * 16; }
 struct Layout {
   int64_t p, c, n, loss, ticket, bytes;
@@ -594,7 +600,11 @@ gemm_status router_balance(const router_balance_args* a, void* stream) {
       with_case(a->scores, a->experts == 8 * G * N, go);
     });
   });
-  if (!one) balance_join_kernel<<<dim3((unsigned)(a->experts + 63) / 64, (unsigned)a->batch), kThreads, 0, s>>>(f);
+  if (!one) {
+    const dim3 grid((unsigned)(a->experts + 63) / 64, (unsigned)a->batch);
+    if (sh.wgs > kManySums) balance_join_kernel<512><<<grid, 512, 0, s>>>(f);
+    else balance_join_kernel<256><<<grid, 256, 0, s>>>(f);
+  }
   return launched(fn);
 }
 
