@@ -41,36 +41,36 @@ template <int G>
 __device__ __forceinline__ float row_max(float v) { return reduce<G>(v, [](float a, float b) { return fmaxf(a, b); }); }
 
 // e^x of x <= 0 to about an fp32 step: what the rounding of x log2 e leaves is put back, so that the error does not grow
-// with x. (Not for NaN: see row_scores.)
+// with x. NaN for NaN.
 __device__ __forceinline__ float exp_neg(float x) {
   constexpr float log2e = 1.44269502162933349609375f;
-  const float c = fmaxf(x, -104.f);  // (e^-104 is below fp32)
+  const float c = __builtin_elementwise_maximum(x, -104.f);  // (e^-104 is below fp32)
   const float t = c * log2e, lo = __builtin_fmaf(c, log2e, -t);
   const float e = __builtin_amdgcn_exp2f(t);
   return __builtin_fmaf(e * lo, 0.693147182464599609375f, e);
 }
-
-// The scores of a row from its logits x, -inf past the last expert: p = u inv (8 N a lane). miss: 1 - s(x) (sigmoid). A
-// row of -inf alone has inv = 0; a NaN makes inv NaN.
-template <int G, int N, int SCORES>
-__device__ __forceinline__ float row_scores(const float (&x)[N][8], float (&u)[N][8], float (&miss)[N][8]) {
-  float top = -__builtin_inff(), sum = 0.f;
-  bool nan = false;
+template <int G, int N>
+__device__ __forceinline__ float row_top(const float (&x)[N][8]) {
+  float top = -__builtin_inff();
 #pragma unroll
   for (int i = 0; i < N; ++i)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      top = fmaxf(top, x[i][e]);
-      nan |= x[i][e] != x[i][e];
-    }
-  top = row_max<G>(top);
+    for (int e = 0; e < 8; ++e) top = fmaxf(top, x[i][e]);
+  return row_max<G>(top);
+}
+
+// The scores of a row from its logits x, -inf past the last expert: p = u inv (8 N a lane). miss: 1 - s(x) (sigmoid). A
+// row of -inf alone has inv = 0; a NaN, and an infinity under a softmax, make the sum and inv NaN.
+template <int G, int N, int SCORES>
+__device__ __forceinline__ float row_scores(const float (&x)[N][8], float (&u)[N][8], float (&miss)[N][8]) {
+  float sum = 0.f;
   if constexpr (SCORES == ROUTER_SOFTMAX) {
-    const float m = fmaxf(top, -3.402823466e38f);  // (-inf less -inf is no number)
+    const float m = fmaxf(row_top<G, N>(x), -3.402823466e38f);  // (-inf less -inf is no number)
 #pragma unroll
     for (int i = 0; i < N; ++i)
 #pragma unroll
       for (int e = 0; e < 8; ++e) u[i][e] = exp_neg(x[i][e] - m), sum += u[i][e];
-    nan |= top == __builtin_inff();
+    sum = row_sum<G>(sum);
   } else {
     // s(x) = a q or q with a = e^-|x|, q = 1 / (1 + a); 1 - s(x) is the other one
 #pragma unroll
@@ -82,20 +82,23 @@ __device__ __forceinline__ float row_scores(const float (&x)[N][8], float (&u)[N
         miss[i][e] = x[i][e] < 0.f ? q : aq;
         sum += u[i][e];
       }
+    sum = row_sum<G>(sum);
     // Logits that are all far below zero: times e^-top, which the quotient cancels, so that they keep their digits.
-    // (From -40 on what e^x loses is below e^-60 of the sum.)
-    if (top < -40.f) {
-      const float m = fmaxf(top, -3.402823466e38f);
-      sum = 0.f;
+    // (From -40 on what e^x loses is below e^-60 of the sum, and 2048 of e^-40 are below 1e-14.)
+    if (sum < 1e-14f) {
+      const float top = row_top<G, N>(x);
+      if (top < -40.f) {
+        const float m = fmaxf(top, -3.402823466e38f);
+        sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < N; ++i)
+        for (int i = 0; i < N; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) u[i][e] = exp_neg(x[i][e] - m) * miss[i][e], sum += u[i][e];
+          for (int e = 0; e < 8; ++e) u[i][e] = exp_neg(x[i][e] - m) * miss[i][e], sum += u[i][e];
+        sum = row_sum<G>(sum);
+      }
     }
   }
-  if (nan) sum = __uint_as_float(0x7FC00000u);
-  sum = row_sum<G>(sum);
-  return top == -__builtin_inff() && sum == sum ? 0.f : 1.f / sum;
+  return sum == 0.f ? 0.f : 1.f / sum;
 }
 
 // WHOLE: the experts fill the lanes.
