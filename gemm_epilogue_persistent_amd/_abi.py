@@ -13,7 +13,7 @@ ROW, COL = 0, 1
 ACT = {"none": 0, "relu": 1, "relu_sq": 2, "gelu_tanh": 3, "silu": 4}
 MX_FORMAT = {"e2m1": 0, "e4m3": 1}
 MX_TILE = {"auto": 0, "256": 1, "128": 2, "32x64": 3, "32": 4, "16x32": 5, "16": 6}
-FP8_TILE = {"auto": 0, "256": 1, "128": 2, "32x64": 3, "32": 4, "16x32": 5, "16": 6}
+FP8_TILE = {"auto": 0, "256": 1, "128": 2, "64": 3, "32": 4, "16x32": 5, "16": 6}
 MX_HEADER = os.path.join(os.path.dirname(HERE), "include", "mx_mi355x.h")
 FP8_HEADER = os.path.join(os.path.dirname(HERE), "include", "fp8_mi355x.h")
 ROUTER_HEADER = os.path.join(os.path.dirname(HERE), "include", "router_mi355x.h")

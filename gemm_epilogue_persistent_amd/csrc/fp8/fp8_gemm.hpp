@@ -232,6 +232,140 @@ struct Fp8Direct : MxDirect<MB, NB, NW, D, MX_E4M3, MX_E4M3, VM> {
   static __device__ __forceinline__ void run(const MxParams& mp) { R::template run_as<Fp8Direct>(mp); }
 };
 
+// 64 x 64 outputs a workgroup of four waves that share out K, as in MxDirect, but each wave's operands come through LDS in
+// a ring of its own, two steps ahead: whole lines of 128 bytes (fragments read from memory directly take 64 bytes of
+// each of 16 rows at a time), and no barrier. Wave w takes step w of every quad of steps.
+template <bool VM, bool BROWS>
+struct Fp8Staged : MxDirect<4, 4, 4, 1, MX_E4M3, MX_E4M3, VM> {
+  using R = MxDirect<4, 4, 4, 1, MX_E4M3, MX_E4M3, VM>;
+  static constexpr int kWaves = 4, kPart = 64 * 128, kScales = 2 * kPart, kStage = kScales + 2048, kRing = 2 * kStage;
+  static constexpr int kLag = 2;
+  static constexpr int kPer = 18;  // transfers of a stage: A, B, and the scales of their rows
+  static_assert(R::kPlane * 4 <= kRing, "the waves' sums lie in their rings");
+  struct Src {
+    __amdgpu_buffer_rsrc_t a, b, sa, sb;
+    uint32_t ao[8], bo[8];  // this lane's chunk of row 8 q + lane / 8 (kOOB past the operand)
+    int ka[2], kb[2];       // bytes of a row past that chunk, for even and odd q
+    uint32_t sao, sbo;      // the scales of row `lane`
+    int sb_step;            // bytes from a row's quad of B's scales to the next
+    int t1;                 // quads up to here
+  };
+  static __device__ __forceinline__ void move(__amdgpu_buffer_rsrc_t rs, uint32_t off, GEP_LDS char* lds) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (GEP_LDS void*)lds, 16, off, 0, 0, 0);
+#endif
+  }
+  static __device__ __forceinline__ void transfer(const Src& s, int quad, int wave, GEP_LDS char* lds) {
+    const int kb = (quad * 4 + wave) * 128;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) move(s.b, kb < s.kb[q & 1] ? s.bo[q] + kb : kOOB, lds + kPart + q * 1024);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) move(s.a, kb < s.ka[q & 1] ? s.ao[q] + kb : kOOB, lds + q * 1024);
+    // (past the last quad: zeros, as its codes)
+    move(s.sa, quad < s.t1 ? s.sao + quad * 1024 : kOOB, lds + kScales);
+    move(s.sb, quad < s.t1 ? s.sbo + quad * s.sb_step : kOOB, lds + kScales + 1024);
+  }
+  static __device__ __forceinline__ Fp8Frag fragment(const GEP_LDS char* lds, int at, int r) {
+    return Fp8Frag{*(const GEP_LDS i32x4*)(lds + at + r * 2048), *(const GEP_LDS i32x4*)(lds + (at ^ 64) + r * 2048)};
+  }
+  // The step whose stage is `lds`, and the transfers of the step two behind it.
+  static __device__ __forceinline__ void step(f32x4 (&acc)[4][4], const Src& s, int quad, int wave, GEP_LDS char* lds, int at, int lane) {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kPer) : "memory");  // (outstanding: the next step's)
+    __builtin_amdgcn_sched_barrier(0);
+    Fp8Frag a[4], b[4];
+    float sa[4];
+    f32x4 sb[BROWS ? 4 : 1];
+    const GEP_LDS char* sp = lds + kScales + wave * 4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      b[i] = fragment(lds + kPart, at, i);
+      a[i] = fragment(lds, at, i);
+      sa[i] = *(const GEP_LDS float*)(sp + (i * 16 + (lane & 15)) * 16);
+      if constexpr (BROWS) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sb[i][e] = *(const GEP_LDS float*)(sp + 1024 + (i * 16 + 4 * (lane >> 4) + e) * 16);
+      }
+    }
+    if constexpr (!BROWS) sb[0][0] = *(const GEP_LDS float*)(sp + 1024);
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the stage is free
+    __builtin_amdgcn_sched_barrier(0);
+    transfer(s, quad + 2, wave, lds);
+    if constexpr (!BROWS) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sa[i] *= sb[0][0];
+    }
+    f32x4 t[4];
+#pragma unroll
+    for (int q = 0; q < 16 + kLag; ++q) {  // the FMAs two matrix instructions behind
+      if (q < 16) t[q & 3] = fp8_mma(b[q & 3], a[q >> 2]);
+      if (q < kLag) continue;
+      const int i = (q - kLag) >> 2, j = (q - kLag) & 3;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float v = t[(q - kLag) & 3][e];
+        acc[i][j][e] = __builtin_fmaf(BROWS ? v * sb[BROWS ? j : 0][e] : v, sa[i], acc[i][j][e]);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < 16; ++q) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x002, BROWS ? 8 : 4, 0);
+    }
+  }
+  static __device__ __forceinline__ void run(const MxParams& mp) {
+    const KParams& p = mp.k;
+    __shared__ __attribute__((aligned(1024))) char smem[kWaves * kRing];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    typename R::Place pl;
+    if (!R::place(pl, mp, lane)) return;
+    Src s;
+    const int64_t ao = (int64_t)pl.m0 * p.lda, bo = (int64_t)pl.n0 * p.ldb;
+    s.a = make_rsrc((const char*)p.A + ao, p.a_bytes - ao);
+    s.b = make_rsrc((const char*)p.B + (int64_t)pl.g * p.b_bytes + bo, p.b_bytes - bo);
+    // (chunk c of row r lies at chunk c ^ kswz(r), a key that repeats every 16 rows)
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const int row = q * 8 + (lane >> 3), c = (lane & 7) ^ kswz(row);
+      s.ao[q] = pl.m0 + row < pl.row_end ? (uint32_t)(row * (int)p.lda + c * 16) : kOOB;
+      s.bo[q] = pl.n0 + row < p.N ? (uint32_t)(row * (int)p.ldb + c * 16) : kOOB;
+      if (q < 2) {
+        s.ka[q] = min((int)p.lda, pl.t1 * 512) - c * 16;
+        s.kb[q] = min((int)p.ldb, pl.t1 * 512) - c * 16;
+      }
+    }
+    {
+      const int64_t so = (int64_t)(pl.m0 >> 6) * mp.nsb * 1024;
+      const int q = (pl.m0 & 63) + lane;
+      s.sa = make_rsrc(mp.sa + so, mp.sa_bytes - so);
+      s.sao = pl.m0 + lane < pl.row_end ? (uint32_t)((q >> 6) * mp.nsb * 1024 + (q & 63) * 16) : kOOB;
+    }
+    const int64_t so = BROWS ? (int64_t)(pl.n0 >> 6) * mp.nsb * 1024 : (int64_t)(pl.n0 >> 7) * mp.nsb * 16;
+    s.sb = make_rsrc(mp.sb + (int64_t)pl.g * mp.sb_bytes + so, mp.sb_bytes - so);
+    s.sbo = !BROWS ? 0 : (pl.n0 + lane < p.N ? (uint32_t)lane * 16 : kOOB);
+    s.sb_step = BROWS ? 1024 : 16;
+    s.t1 = pl.t1;
+    const int at = (lane & 15) * 128 + (((lane >> 4) ^ kswz(lane & 15)) << 4);
+    f32x4 acc[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    GEP_LDS char* ring = (GEP_LDS char*)smem + wave * kRing;
+    if (pl.t0 < pl.t1) {
+      transfer(s, pl.t0, wave, ring);
+      transfer(s, pl.t0 + 1, wave, ring + kStage);
+      for (int quad = pl.t0; quad < pl.t1; quad += 2) {
+        step(acc, s, quad, wave, ring, at, lane);
+        step(acc, s, quad + 1, wave, ring + kStage, at, lane);
+      }
+    }
+    dma_barrier();  // transfers past K have landed: the sums take the rings' place
+    R::join(mp, pl, acc, (float*)smem);
+  }
+};
+
 template <int BM, int NW, int WG, bool VM, int EPI, bool BROWS>
 __global__ __launch_bounds__(NW * 64, WG) void fp8_ring_kernel(const MxParams p) {
   Fp8Ring<BM, BM, NW, mx_stages<BM, MX_E4M3, MX_E4M3, WG>(), VM, EPI, BROWS>::run(p);
@@ -247,6 +381,12 @@ __global__ __launch_bounds__(NW * 64) void fp8_direct_kernel(const MxParams p) {
   Fp8Direct<MB, NB, NW, D, VM, BROWS>::run(p);
 }
 
+// (Bounds of 512 threads for its 256: the compiler then keeps to 256 registers, and results out of the accumulation ones.)
+template <bool VM, bool BROWS>
+__global__ __launch_bounds__(512) void fp8_staged_kernel(const MxParams p) {
+  Fp8Staged<VM, BROWS>::run(p);
+}
+
 // The kernels (launch configuration by mx_plan.cpp; the tiles are numbered as the MX product's).
 template <bool BROWS, bool VM>
 hipError_t fp8_launch(int32_t tile, const MxParams& p, dim3 grid, hipStream_t s);
@@ -260,7 +400,7 @@ hipError_t fp8_launch(int32_t tile, const MxParams& p, dim3 grid, hipStream_t s)
         if (p.k.P <= p.cus) fp8_launch_ring<128, 4, 1, VM, BROWS>(p, grid, s);                        \
         else fp8_launch_ring<128, 4, 2, VM, BROWS>(p, grid, s);                                       \
         break;                                                                                        \
-      case MX_TILE_32X64: fp8_direct_kernel<2, 4, 4, 2, VM, BROWS><<<grid, 256, 0, s>>>(p); break;    \
+      case FP8_TILE_64: fp8_staged_kernel<VM, BROWS><<<grid, 256, 0, s>>>(p); break;                  \
       case MX_TILE_32: fp8_direct_kernel<2, 2, 4, 2, VM, BROWS><<<grid, 256, 0, s>>>(p); break;       \
       case MX_TILE_16X32: fp8_direct_kernel<1, 2, 8, 2, VM, BROWS><<<grid, 512, 0, s>>>(p); break;    \
       case MX_TILE_16: fp8_direct_kernel<1, 1, 4, 2, VM, BROWS><<<grid, 256, 0, s>>>(p); break;       \

@@ -103,7 +103,7 @@ gemm_status block_gemm_run(const char* fn, const mx_gemm_plan* plan, const mx_ge
   }
   const int32_t tile = choice.tile;
   int32_t bm, bn;
-  mx_tile_extent(tile, &bm, &bn);
+  mx_tile_extent(*plan, tile, &bm, &bn);
   MxParams p{};
   KParams& k = p.k;
   k.A = a->a_codes; k.B = a->b_codes; k.C = a->C; k.D = a->D; k.Post = a->PostAct;

@@ -965,28 +965,67 @@ struct MxDirect {
   }
 
   static __device__ __forceinline__ void run(const MxParams& mp) { run_as<MxDirect>(mp); }
+  // The workgroup's tile and scale tiles [t0, t1). False: there is no such tile (the same in every wave).
+  struct Place {
+    int g, m0, n0, row_end, slice, t0, t1;
+  };
+  static __device__ __forceinline__ bool place(Place& at, const MxParams& mp, int lane) {
+    const KParams& p = mp.k;
+    const int slice = VM ? 0 : blockIdx.z, t0 = VM ? 0 : slice * mp.per;
+    at = Place{0, (int)blockIdx.y * kBM, (int)blockIdx.x * kBN, p.M, slice, t0, VM ? mp.nsb : min(mp.nsb, t0 + mp.per)};
+    if constexpr (VM) {
+      const MxGroup found = mx_find_group(p, (int)blockIdx.y, kBM, 1, lane);
+      if (found.index < 0) return false;
+      at.g = found.index;
+      at.m0 = found.begin + ((int)blockIdx.y - found.first) * kBM;
+      at.row_end = found.end;
+    }
+    return true;
+  }
+  // Adds up the waves' sums in LDS, in order, and finishes the tile.
+  static __device__ __forceinline__ void join(const MxParams& mp, const Place& at, const f32x4 (&acc)[MB][NB], float* sums) {
+    const KParams& p = mp.k;
+    const int tid = threadIdx.x, r = tid & 15, kg = (tid & 63) >> 4, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    // lane l of block (i, j) holds row l % 16, columns 4 (l / 16) + [0, 4)
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+        *(f32x4*)(sums + wave * kPlane + (i * 16 + r) * kPitch + j * 16 + kg * 4) = acc[i][j];
+    __syncthreads();
+    for (int u = tid; u < kBM * kBN / 8; u += NW * 64) {
+      const int row = u / (kBN / 8), col = u % (kBN / 8) * 8;
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = 0.f;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        const float* q = sums + w * kPlane + row * kPitch + col;
+        const f32x4 x = *(const f32x4*)q, y = *(const f32x4*)(q + 4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] += x[e], v[4 + e] += y[e];
+      }
+      if (at.m0 + row < at.row_end && at.n0 + col < p.N) {
+        if (!VM && mp.split > 1) mx_slice8(mp, at.slice, at.m0 + row, at.n0 + col, v);
+        else mx_finish8(p, at.m0 + row, at.n0 + col, v);
+      }
+    }
+  }
+
   template <class Self>
   static __device__ __forceinline__ void run_as(const MxParams& mp) {
     const KParams& p = mp.k;
     __shared__ __attribute__((aligned(16))) float sums[NW * kPlane];
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    int g = 0, m0 = blockIdx.y * kBM, row_end = p.M;
-    // this workgroup's scale tiles [t0, t1)
-    const int slice = VM ? 0 : blockIdx.z, t0 = VM ? 0 : slice * mp.per, t1 = VM ? mp.nsb : min(mp.nsb, t0 + mp.per);
-    const int n0 = blockIdx.x * kBN;
-    if constexpr (VM) {
-      const MxGroup found = mx_find_group(p, (int)blockIdx.y, kBM, 1, lane);
-      if (found.index < 0) return;  // (the same in every wave)
-      g = found.index;
-      m0 = found.begin + ((int)blockIdx.y - found.first) * kBM;
-      row_end = found.end;
-    }
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    Place at;
+    if (!place(at, mp, lane)) return;
+    const int m0 = at.m0, n0 = at.n0, row_end = at.row_end, t0 = at.t0, t1 = at.t1;
     const int r = lane & 15, kg = lane >> 4;
     Src s;
     const int64_t ao = (int64_t)m0 * p.lda, bo = (int64_t)n0 * p.ldb;
     s.a = make_rsrc((const char*)p.A + ao, p.a_bytes - ao);
-    s.b = make_rsrc((const char*)p.B + (int64_t)g * p.b_bytes + bo, p.b_bytes - bo);
-    Self::scale_source(s, mp, g, m0, n0, row_end, lane);
+    s.b = make_rsrc((const char*)p.B + (int64_t)at.g * p.b_bytes + bo, p.b_bytes - bo);
+    Self::scale_source(s, mp, at.g, m0, n0, row_end, lane);
     s.nsb = t1;
     s.ka = min((int)p.lda, t1 * 4 * MxFmt<FA>::kStepBytes) - kg * 16;
     s.kb = min((int)p.ldb, t1 * 4 * MxFmt<FB>::kStepBytes) - kg * 16;
@@ -1022,30 +1061,7 @@ struct MxDirect {
         step<Self, 3>(acc, buf, s, now, tile);
       }
     }
-    // lane l of block (i, j) holds row l % 16, columns 4 (l / 16) + [0, 4)
-#pragma unroll
-    for (int i = 0; i < MB; ++i)
-#pragma unroll
-      for (int j = 0; j < NB; ++j)
-        *(f32x4*)(sums + wave * kPlane + (i * 16 + r) * kPitch + j * 16 + kg * 4) = acc[i][j];
-    __syncthreads();
-    for (int u = tid; u < kBM * kBN / 8; u += NW * 64) {
-      const int row = u / (kBN / 8), col = u % (kBN / 8) * 8;
-      float v[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = 0.f;
-#pragma unroll
-      for (int w = 0; w < NW; ++w) {
-        const float* q = sums + w * kPlane + row * kPitch + col;
-        const f32x4 x = *(const f32x4*)q, y = *(const f32x4*)(q + 4);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] += x[e], v[4 + e] += y[e];
-      }
-      if (m0 + row < row_end && n0 + col < p.N) {
-        if (!VM && mp.split > 1) mx_slice8(mp, slice, m0 + row, n0 + col, v);
-        else mx_finish8(p, m0 + row, n0 + col, v);
-      }
-    }
+    join(mp, at, acc, sums);
   }
 };
 

@@ -34,11 +34,11 @@ gemm_status check_out(const char* fn, const char* name, int32_t dt, int64_t ld, 
 }
 }  // namespace
 
-void mx_tile_extent(int32_t tile, int32_t* bm, int32_t* bn) {
+void mx_tile_extent(const mx_gemm_plan& p, int32_t tile, int32_t* bm, int32_t* bn) {
   switch (tile) {
     case MX_TILE_256: *bm = *bn = 256; break;
     case MX_TILE_128: *bm = *bn = 128; break;
-    case MX_TILE_32X64: *bm = 32; *bn = 64; break;
+    case MX_TILE_32X64: *bm = p.b_scaling >= 0 ? 64 : 32; *bn = 64; break;
     case MX_TILE_32: *bm = *bn = 32; break;
     case MX_TILE_16X32: *bm = 16; *bn = 32; break;
     default: *bm = *bn = 16; break;
@@ -68,17 +68,22 @@ int64_t mx_row_blocks(const mx_gemm_plan& p, int32_t bm) {
 // so 16-row tiles serve few rows (1x8192x8192 8.0; in 32x64 tiles 13.8), 32x64 up to 128 or 256 rows,
 // 128x128 up to one round of 256x256 tiles, and deep products with few tiles are split
 // (128x512x8192: 8.3 in 32x32 tiles over four workgroups, 13.8 over one).
-// FP8 products run in the same kernels with more vector arithmetic, B's scales by tiles (or by rows), fitted to 60
-// shapes each from 1x1024x1024 to 4096x8192x8192 (4% from the best kernel in the mean, 12% at most):
+// FP8 products run in the same kernels with more vector arithmetic, B's scales by tiles (or by rows), fitted to 108
+// shapes each from 1x1024x1024 to 4096x8192x8192 (1% from the best kernel in
+// the mean, 18% at most):
 //   256x256: 1.66 (2.07) a step (4096^3 63.5 measured, 64.1 estimated; 2048x8192x8192 115.9, 117)
 //   128x128: 55 (43) KB a microsecond alone on a compute unit, 65 (55) for two workgroups (256x4096x4096 over
 //     one 25.8, 25.6, over four 21.8, 22.7; 2048x4096x4096 38.3, 38.5), and B at 7 MB a microsecond at most
 //     (64x8192x8192 over four 23.1, 23.6)
+//   64x64: 2.8 (2.3) us, a round 1.8 (2.6) and 0.55 (0.72) a quad of steps, up to 0.35 (0.22) more with the card
+//     full; B at 6 (5.6) MB a microsecond at most (256x4096x4096 11.6, 11.7; 64x8192x8192 17.0, 16.5; 512x4096x4096 21.0,
+//     20.6). Direct 32x64 tiles, which MX products have in their place, were nowhere the fastest (256x4096x4096 25.6, 128 rows
+//     14.8 and 10.5, 64x8192x8192 25.5 and 17.0)
 //   16x16, 16x32, 32x32: B's bytes, from memory, at 25, 19.5 and 18.5 KB a microsecond, A's, from a cache, at 50, 100
 //     and 95 (16x16 and 16x32: 1x8192x8192 13.3, 13.3 and 16.1, 16.0; 16x8192x8192 18.1, 18.1 and 16.4, 17.2)
 static double estimate(const mx_gemm_plan& p, int32_t cus, int32_t tile, int32_t split) {
   int32_t bm, bn;
-  mx_tile_extent(tile, &bm, &bn);
+  mx_tile_extent(p, tile, &bm, &bn);
   // (grouped: half a partial row block for each group)
   const double blocks = p.d.groups ? (double)p.d.M / bm + 0.5 * (p.d.M < p.d.groups ? p.d.M : p.d.groups) : (double)mx_row_blocks(p, bm);
   const double wgs = blocks * (double)cdiv(p.d.N, bn) * split;
@@ -99,6 +104,13 @@ static double estimate(const mx_gemm_plan& p, int32_t cus, int32_t tile, int32_t
     const double memory = fp8 ? (double)p.d.N * p.d.K / 7e6 : 0;  // (B's bytes)
     const double work = wgs <= cus ? steps * kb / alone : (double)cdiv((int64_t)wgs, 2 * (int64_t)cus) * (steps * 2 * kb / two + 1) - 1;
     t = 7 + (work > memory ? work : memory);
+  } else if (fp8 && tile == FP8_TILE_64) {
+    const double load = wgs / cus, full = load < 1 ? load : 1;
+    const double rounds = load <= 2 ? (double)cdiv((int64_t)wgs, cus) : load;
+    const double memory = (double)p.d.N * p.d.K / (fp8_rows ? 5.6e6 : 6e6);
+    const double quad = fp8_rows ? 0.72 + 0.22 * full * kb / 16 : 0.55 + 0.35 * full * kb / 16;
+    const double work = rounds * (steps / 4 * quad + (fp8_rows ? 2.6 : 1.8));
+    t = (fp8_rows ? 2.3 : 2.8) + (work > memory ? work : memory);
   } else {
     const double load = wgs / cus;
     double one = steps * kb / 33;
@@ -121,7 +133,7 @@ MxChoice mx_choose(const mx_gemm_plan& p, int32_t cus, bool workspace) {
   for (int32_t tile = MX_TILE_256; tile <= MX_TILE_16; ++tile) {
     if (p.d.tile != MX_TILE_AUTO && p.d.tile != tile) continue;
     int32_t bm, bn;
-    mx_tile_extent(tile, &bm, &bn);
+    mx_tile_extent(p, tile, &bm, &bn);
     if (p.d.tile == MX_TILE_AUTO && !mx_direct_fits(p, tile)) continue;
     for (int32_t split = 1; split <= 64; ++split) {
       const bool wanted = p.d.split > 0 ? split == p.d.split : (split & (split - 1)) == 0 && split <= 16;
@@ -156,7 +168,7 @@ MxChoice mx_choice(const mx_gemm_plan& p, int32_t cus, bool workspace) {
 bool mx_direct_fits(const mx_gemm_plan& p, int32_t tile) {
   if (tile == MX_TILE_256 || tile == MX_TILE_128) return true;
   int32_t bm, bn;
-  mx_tile_extent(tile, &bm, &bn);
+  mx_tile_extent(p, tile, &bm, &bn);
   return mx_row_blocks(p, bm) <= 65535 && cdiv(p.d.N, bn) < (1 << 23);
 }
 
@@ -197,7 +209,7 @@ gemm_status block_gemm_init(const char* fn, const mx_gemm_desc& d, int32_t b_sca
   p->sa_bytes = fp8 ? fp8_scale_bytes(d.M, d.K, FP8_ROWS) : mx_scale_bytes(d.M, d.K);
   p->sb_bytes = fp8 ? fp8_scale_bytes(d.N, d.K, b_scaling) : mx_scale_bytes(d.N, d.K);
   int32_t bm, bn;
-  mx_tile_extent(MX_TILE_128, &bm, &bn);
+  mx_tile_extent(*p, MX_TILE_128, &bm, &bn);
   if (mx_row_blocks(*p, bm) * cdiv(d.N, bn) > 0xFFFFFF) return fail(GEMM_ERR_UNSUPPORTED, "%s: too many output tiles", fn);
   clear_error();
   return GEMM_OK;
@@ -269,7 +281,7 @@ gemm_status mx_gemm_workspace(const mx_gemm_plan* plan, int32_t num_cus, int64_t
 // ---- FP8 products
 
 static_assert((int)FP8_TILE_AUTO == (int)MX_TILE_AUTO && (int)FP8_TILE_256 == (int)MX_TILE_256 && (int)FP8_TILE_128 == (int)MX_TILE_128 &&
-                  (int)FP8_TILE_32X64 == (int)MX_TILE_32X64 && (int)FP8_TILE_32 == (int)MX_TILE_32 &&
+                  (int)FP8_TILE_64 == (int)MX_TILE_32X64 && (int)FP8_TILE_32 == (int)MX_TILE_32 &&
                   (int)FP8_TILE_16X32 == (int)MX_TILE_16X32 && (int)FP8_TILE_16 == (int)MX_TILE_16,
               "one numbering of the tiles");
 

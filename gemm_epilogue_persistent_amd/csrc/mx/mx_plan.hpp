@@ -36,10 +36,11 @@ struct MxChoice {
 MxChoice mx_choose(const mx_gemm_plan& p, int32_t cus, bool workspace);
 // The same, kept in the plan for the next run.
 MxChoice mx_choice(const mx_gemm_plan& p, int32_t cus, bool workspace);
-void mx_tile_extent(int32_t tile, int32_t* bm, int32_t* bn);
+// (Tile 3 is 32x64 of an MX plan and 64x64 of an FP8 one; the others are alike.)
+void mx_tile_extent(const mx_gemm_plan& p, int32_t tile, int32_t* bm, int32_t* bn);
 // Upper bound of the row blocks of a tile of bm rows over all groups (exact for a dense plan).
 int64_t mx_row_blocks(const mx_gemm_plan& p, int32_t bm);
-// Whether the grid of a direct kernel (tiles of at most 32 rows) can be launched: row blocks in 16 bits,
+// Whether the grid of a direct kernel (tiles of at most 64 rows) can be launched: row blocks in 16 bits,
 // columns of up to 512 threads in 32. True for the other tiles.
 bool mx_direct_fits(const mx_gemm_plan& p, int32_t tile);
 int64_t mx_workspace_bytes(const mx_gemm_plan& p, const MxChoice& c);

@@ -229,7 +229,7 @@ class Fp8Plan(_PlanBase):
     tiles (weights) or of rows (the gradient of a weight: a = dY^T, b = X^T, blocks along the tokens).
     n is a multiple of 8. C, D, PostAct: 16- or 32-bit floats, rows contiguous, row strides of whole 16
     bytes; at least one of D, PostAct. tile, split: "auto" and 0, or the kernel to use ("256", "128",
-    "32x64", "32", "16x32", "16") and over how many workgroups it shares out a tile's K.
+    "64", "32", "16x32", "16") and over how many workgroups it shares out a tile's K.
 
     The matrix instruction sums a block's 128 products (each kept to 2^-13 of the largest of 32), and blocks are
     scaled and added in fp32: a float32 output is off by about 1e-5.

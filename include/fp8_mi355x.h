@@ -127,8 +127,8 @@ typedef enum {
   FP8_TILE_AUTO = 0,
   FP8_TILE_256 = 1,   /* 256x256 outputs a workgroup, operands staged through LDS       */
   FP8_TILE_128 = 2,   /* 128x128, the same                                              */
-  FP8_TILE_32X64 = 3, /* 32 rows x 64 columns, the waves of a workgroup share out K     */
-  FP8_TILE_32 = 4,    /* 32x32, the same                                                */
+  FP8_TILE_64 = 3,    /* 64x64, the same, and the waves of a workgroup share out K      */
+  FP8_TILE_32 = 4,    /* 32x32, the waves share out K and read their operands directly  */
   FP8_TILE_16X32 = 5, /* 16 rows x 32 columns, the same                                 */
   FP8_TILE_16 = 6     /* 16x16, the same                                                */
 } fp8_tile;

@@ -281,7 +281,7 @@ def run_product(M, N, K, tile, tiles=True, c=None, d="f32", post=None, act="none
         check_product(P, R.act(x, act), bound, post, act, x)
 
 
-TILES = ["256", "128", "32x64", "32", "16x32", "16"]
+TILES = ["256", "128", "64", "32", "16x32", "16"]
 
 
 @pytest.mark.parametrize("tile", TILES)
@@ -520,3 +520,19 @@ def test_python_refusals():
         gep.fp8_dequantize(a, out=torch.empty(16, 63, device="cuda"))
     with pytest.raises(ValueError):
         gep.fp8_dequantize(g)
+
+
+@pytest.mark.parametrize("tiles", [True, False])
+@pytest.mark.parametrize("tile", TILES)
+@pytest.mark.parametrize("K", [128, 512, 640, 1536])
+def test_nan_stays_in_its_rows(tile, tiles, K):
+    """A NaN block of A makes its row NaN and no other, one of B its columns: the scales behind a row's last quad, which are
+    another row's, never meet it."""
+    announce(f"fp8 product NaN rows {tile} {tiles} {K}")
+    A, B = torch.randn(200, K, device="cuda"), torch.randn(264, K, device="cuda")
+    A[64:, 0] = float("nan")
+    B[128:, K - 1] = float("inf")
+    a, b = gep.fp8_quantize(A), gep.fp8_quantize(B, tiles=tiles)
+    D = torch.zeros(200, 264, device="cuda")
+    gep.Fp8Plan(a, b, None, D, tile=tile, split=1).run(a, b, None, D)
+    assert D[:64, :128].isfinite().all() and D[64:].isnan().all() and D[:, 128:].isnan().all()
