@@ -2,6 +2,7 @@
 // kernel. No HIP call is made here.
 #include "mx_plan.hpp"
 
+#include <cmath>
 #include <initializer_list>
 #include <new>
 
@@ -68,19 +69,6 @@ int64_t mx_row_blocks(const mx_gemm_plan& p, int32_t bm) {
 // so 16-row tiles serve few rows (1x8192x8192 8.0; in 32x64 tiles 13.8), 32x64 up to 128 or 256 rows,
 // 128x128 up to one round of 256x256 tiles, and deep products with few tiles are split
 // (128x512x8192: 8.3 in 32x32 tiles over four workgroups, 13.8 over one).
-// FP8 products run in the same kernels with more vector arithmetic, B's scales by tiles (or by rows), fitted to 108
-// shapes each from 1x1024x1024 to 4096x8192x8192 (1% from the best kernel in
-// the mean, 18% at most):
-//   256x256: 1.66 (2.07) a step (4096^3 63.5 measured, 64.1 estimated; 2048x8192x8192 115.9, 117)
-//   128x128: 55 (43) KB a microsecond alone on a compute unit, 65 (55) for two workgroups (256x4096x4096 over
-//     one 25.8, 25.6, over four 21.8, 22.7; 2048x4096x4096 38.3, 38.5), and B at 7 MB a microsecond at most
-//     (64x8192x8192 over four 23.1, 23.6)
-//   64x64: 2.8 (2.3) us, a round 1.8 (2.6) and 0.55 (0.72) a quad of steps, up to 0.35 (0.22) more with the card
-//     full; B at 6 (5.6) MB a microsecond at most (256x4096x4096 11.6, 11.7; 64x8192x8192 17.0, 16.5; 512x4096x4096 21.0,
-//     20.6). Direct 32x64 tiles, which MX products have in their place, were nowhere the fastest (256x4096x4096 25.6, 128 rows
-//     14.8 and 10.5, 64x8192x8192 25.5 and 17.0)
-//   16x16, 16x32, 32x32: B's bytes, from memory, at 25, 19.5 and 18.5 KB a microsecond, A's, from a cache, at 50, 100
-//     and 95 (16x16 and 16x32: 1x8192x8192 13.3, 13.3 and 16.1, 16.0; 16x8192x8192 18.1, 18.1 and 16.4, 17.2)
 static double estimate(const mx_gemm_plan& p, int32_t cus, int32_t tile, int32_t split) {
   int32_t bm, bn;
   mx_tile_extent(p, tile, &bm, &bn);
@@ -91,36 +79,86 @@ static double estimate(const mx_gemm_plan& p, int32_t cus, int32_t tile, int32_t
   const double steps = split > 1 ? 4.0 * (double)cdiv(nsb, split) : (double)cdiv(p.d.K, 128);
   const double rows_a = p.d.M < bm ? p.d.M : bm, rows_b = p.d.N < bn ? p.d.N : bn;
   const double kb = (rows_a * (p.d.a_format == MX_E4M3 ? 128 : 64) + rows_b * (p.d.b_format == MX_E4M3 ? 128 : 64)) / 1024;
-  const bool fp8 = p.b_scaling >= 0, fp8_rows = p.b_scaling == FP8_ROWS;
   double t;
   if (tile == MX_TILE_256) {
     // (a last round of at most half the card runs in 128x128 quarters)
-    const double step = fp8 ? (fp8_rows ? 2.07 : 1.66) : p.d.a_format == MX_E2M1 && p.d.b_format == MX_E2M1 ? 0.85 : 1.36;
+    const double step = p.d.a_format == MX_E2M1 && p.d.b_format == MX_E2M1 ? 0.85 : 1.36;
     const double full = (double)((int64_t)wgs / cus), rest = wgs / cus - full;
     const bool quarters = full > 0 && rest > 0 && rest <= 0.5;
     t = 6 + (full + (quarters ? rest * 1.3 : rest > 0)) * (steps * step + 5) + (quarters ? 4 : 0);
   } else if (tile == MX_TILE_128) {
-    const double alone = fp8 ? (fp8_rows ? 43 : 55) : 74, two = fp8 ? (fp8_rows ? 55 : 65) : 56;
-    const double memory = fp8 ? (double)p.d.N * p.d.K / 7e6 : 0;  // (B's bytes)
-    const double work = wgs <= cus ? steps * kb / alone : (double)cdiv((int64_t)wgs, 2 * (int64_t)cus) * (steps * 2 * kb / two + 1) - 1;
-    t = 7 + (work > memory ? work : memory);
-  } else if (fp8 && tile == FP8_TILE_64) {
-    const double load = wgs / cus, full = load < 1 ? load : 1;
-    const double rounds = load <= 2 ? (double)cdiv((int64_t)wgs, cus) : load;
-    const double memory = (double)p.d.N * p.d.K / (fp8_rows ? 5.6e6 : 6e6);
-    const double quad = fp8_rows ? 0.72 + 0.22 * full * kb / 16 : 0.55 + 0.35 * full * kb / 16;
-    const double work = rounds * (steps / 4 * quad + (fp8_rows ? 2.6 : 1.8));
-    t = (fp8_rows ? 2.3 : 2.8) + (work > memory ? work : memory);
+    t = 7 + (wgs <= cus ? steps * kb / 74 : (double)cdiv((int64_t)wgs, 2 * (int64_t)cus) * (steps * 2 * kb / 56 + 1) - 1);
   } else {
-    const double load = wgs / cus;
-    double one = steps * kb / 33;
-    if (fp8 && tile == MX_TILE_16) one = steps * (rows_b / 8 / 25 + rows_a / 8 / 50);
-    if (fp8 && tile == MX_TILE_32) one = steps * (rows_b / 8 / 18.5 + rows_a / 8 / 95);
-    if (fp8 && tile == MX_TILE_16X32) one = steps * (rows_b / 8 / 19.5 + rows_a / 8 / 100);
+    const double load = wgs / cus, one = steps * kb / 33;
     const double start = tile == MX_TILE_16 ? 2.7 : tile == MX_TILE_16X32 ? 2.8 : tile == MX_TILE_32 ? 3.0 : 3.4;
     const double least = tile == MX_TILE_32X64 ? 2.2 : 1.6;
     t = start + (one > least ? one : least) * (load > 1 ? load : 1);
   }
+  if (split > 1) t += 3 + (double)split * p.d.M * p.d.N * 8 / 4.2e6;
+  return t;
+}
+
+// The same of FP8 products, whose kernels have more vector arithmetic (256x256, 128x128, 32x32 and less) or are their own
+// (64x64). Dense: fits to 108 shapes each with B's scales by tiles and (in brackets) by rows from 1x1024x1024 to 4096x8192x8192;
+// the choice is 1% slower than the best kernel in the mean, 18% at most.
+//   256x256: 6 us, a round 5 us and 1.66 (2.07) a step (4096^3 63.5 measured, 64.1 estimated; 2048x8192x8192 115.9, 117)
+//   128x128: 7 us, and 55 (43) KB a microsecond alone on a compute unit, 65 (55) for two workgroups (256x4096x4096 over
+//     one 25.8, 25.6, over four 21.8, 22.7; 2048x4096x4096 38.3, 38.5), and B at 7 MB a microsecond at most
+//     (64x8192x8192 over four 23.1, 23.6)
+//   64x64: 2.8 (2.3) us, a round 1.8 (2.6) and 0.55 (0.72) a quad of steps, up to 0.35 (0.22) more with the card
+//     full; B at 6 (5.6) MB a microsecond at most (256x4096x4096 11.6, 11.7; 64x8192x8192 17.0, 16.5; 512x4096x4096 21.0,
+//     20.6). Direct 32x64 tiles, which MX products have in their place, were nowhere the fastest (256x4096x4096 25.6, 128 rows
+//     14.8 and 10.5, 64x8192x8192 25.5 and 17.0)
+//   16x16, 16x32, 32x32: 2.7 to 3 us, B's bytes, from memory, at 25, 19.5 and 18.5 KB a microsecond, A's, from a cache,
+//     at 50, 100 and 95 (16x16 and 16x32: 1x8192x8192 13.3, 13.3 and 16.1, 16.0; 16x8192x8192 18.1, 18.1 and 16.4, 17.2)
+// Grouped: the groups that have rows are those of a choice at random, with as many each, and their B come from HBM; fits to 60
+// shapes of 8 to 8192 rows over 8 and 64 groups (2% slower than the best in the mean, 21% at most). A workgroup looks its
+// group up first, 1.8 us a round in 64x64 tiles and as much before the first of a direct kernel; B at 4.5 MB a microsecond
+// in 128x128 and 64x64 tiles, 6.1 in direct ones, 3.6 in 256x256 (512 rows over 64 experts of 4096x4096: 246, 230, 207 in
+// 32x32, 269; 8192 rows 305, 471, 1067, 295).
+static double estimate_fp8(const mx_gemm_plan& p, int32_t cus, int32_t tile, int32_t split) {
+  int32_t bm, bn;
+  mx_tile_extent(p, tile, &bm, &bn);
+  const bool grouped = p.d.groups > 0, rows = p.b_scaling == FP8_ROWS;
+  const double groups = grouped ? p.d.groups * (1 - std::exp(-(double)p.d.M / p.d.groups)) : 1, m = p.d.M / (groups > 0 ? groups : 1);
+  double blocks = grouped ? (double)p.d.M / bm + 0.5 * groups : (double)mx_row_blocks(p, bm);
+  if (blocks < groups) blocks = groups;
+  const double wgs = blocks * (double)cdiv(p.d.N, bn) * split, load = wgs / cus, full = load < 1 ? load : 1;
+  const int64_t nsb = cdiv(p.d.K, 512);
+  const double steps = split > 1 ? 4.0 * (double)cdiv(nsb, split) : (double)cdiv(p.d.K, 128);
+  const double kb_a = (m < bm ? m : bm) / 8, kb_b = (double)(p.d.N < bn ? p.d.N : bn) / 8;  // KB of a step
+  const double bytes_b = groups * p.d.N * p.d.K;
+  double start, work, rate;  // us before the first step and behind it, us of the work, B's bytes a us at most
+  if (tile == FP8_TILE_256) {
+    // (a last round of at most half the card runs in 128x128 quarters)
+    const double rounds = (double)(int64_t)load, rest = load - rounds;
+    const bool quarters = rounds > 0 && rest > 0 && rest <= 0.5;
+    start = 6;
+    work = (rounds + (quarters ? rest * 1.3 : rest > 0)) * (steps * (rows ? 2.07 : 1.66) + 5) + (quarters ? 4 : 0);
+    rate = grouped ? 3.6e6 : 1e9;
+  } else if (tile == FP8_TILE_128) {
+    start = grouped ? 9.3 : 7;
+    work = load <= 1 ? steps * (kb_a + kb_b) / (rows ? 43 : 55)
+                     : (double)cdiv((int64_t)wgs, 2 * (int64_t)cus) * (steps * 2 * (kb_a + kb_b) / (rows ? 55 : 65) + 1) - 1;
+    rate = grouped ? 4.55e6 : 7e6;
+  } else if (tile == FP8_TILE_64) {
+    const double rounds = load <= 2 ? (double)cdiv((int64_t)wgs, cus) : load, fill = full * (kb_a + kb_b) / 16;
+    const double quad = rows ? 0.72 + 0.22 * fill : 0.55 + 0.35 * fill;
+    start = grouped ? 4.2 : (rows ? 2.3 : 2.8);
+    work = rounds * (steps / 4 * quad + (grouped ? 3.6 : (rows ? 2.6 : 1.8)));
+    rate = grouped ? 4.5e6 : (rows ? 5.6e6 : 6e6);
+  } else {
+    const int i = tile == FP8_TILE_16 ? 0 : (tile == FP8_TILE_16X32 ? 1 : 2);
+    const double first[] = {2.7, 2.8, 3.0}, kb_us_a[] = {50, 100, 95};
+    const double kb_us_b[] = {25, 19.5, 18.5}, grouped_b[] = {19.2, 17.6, 18.2}, each[] = {0.15, 0.4, 0.23};
+    double one = steps * (kb_b / (grouped ? grouped_b : kb_us_b)[i] + kb_a / kb_us_a[i]);
+    if (grouped) one += each[i];
+    else if (one < 1.6) one = 1.6;
+    start = first[i] + (grouped ? 1.9 : 0);
+    work = one * (load > 1 ? load : 1);
+    rate = grouped ? 6.1e6 : 1e9;
+  }
+  double t = start + (work > bytes_b / rate ? work : bytes_b / rate);
   if (split > 1) t += 3 + (double)split * p.d.M * p.d.N * 8 / 4.2e6;
   return t;
 }
@@ -140,7 +178,7 @@ MxChoice mx_choose(const mx_gemm_plan& p, int32_t cus, bool workspace) {
       if (!wanted && split > 1) continue;
       if (split > 1 && (!may_split || tile == MX_TILE_256 || split > nsb)) continue;
       if (p.d.split == 1 && split > 1) continue;
-      const double t = estimate(p, cus, tile, split) - (p.d.split > 1 && split == p.d.split ? 1e9 : 0);
+      const double t = (p.b_scaling >= 0 ? estimate_fp8 : estimate)(p, cus, tile, split) - (p.d.split > 1 && split == p.d.split ? 1e9 : 0);
       if (t < best) {
         best = t;
         best_tile = tile;

@@ -214,7 +214,8 @@ def test_plan_tile(lib):
     wide = dict(ldc=8192, ldd=8192, ldp=8192)
     assert choice(M=8192, N=8192, K=8192, **wide) == (_abi.FP8_TILE["256"], 1)
     assert choice(M=1, N=8192, K=8192, **wide) == (_abi.FP8_TILE["16"], 1)
-    assert choice(M=256, N=4096, K=4096, **wide)[1] > 1 and choice(M=256, N=4096, K=4096, groups=4, **wide)[1] == 1
+    assert choice(M=256, N=4096, K=4096, **wide) == (_abi.FP8_TILE["64"], 1)
+    assert choice(M=512, N=512, K=8192, **wide)[1] > 1 and choice(M=512, N=512, K=8192, groups=4, **wide)[1] == 1
 
 
 def balance_args(**kw):
