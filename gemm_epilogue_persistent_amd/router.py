@@ -11,7 +11,7 @@ the logits or their sigmoids divided by the sum of them.
 import torch
 
 from . import _abi
-from .mx import _FLOAT_DT, _allocating, _launch
+from .mx import _FLOAT_DT, _MOST, _allocating, _launch
 
 SCORES = {"softmax": 0, "sigmoid": 1}
 
@@ -28,12 +28,15 @@ class RouterBalance:
 
 
 def balance_empty(experts, batch=1, device="cuda"):
-    """Storage of the results of router_balance."""
-    experts, batch = int(experts), int(batch)
+    """Storage of the results of router_balance, zeros."""
+    return _storage(int(experts), int(batch), device, torch.zeros)
+
+
+def _storage(experts, batch, device, fill):
     if experts < 1 or batch < 0:
         raise ValueError("at least one expert and no negative batch expected")
     b = RouterBalance()
-    new = lambda shape, dtype: torch.zeros(shape, dtype=dtype, device=device)  # noqa: E731
+    new = lambda shape, dtype: fill(shape, dtype=dtype, device=device)  # noqa: E731
     b.loss, b.counts, b.cu_seqlens = new((), torch.float32), new((batch, experts), torch.int32), new((experts + 1,), torch.int32)
     b.probs, b.valid = new((batch, experts), torch.float32), new((batch,), torch.int32)
     b.batch, b.experts, b.device, b.call = batch, experts, b.loss.device, None
@@ -50,23 +53,24 @@ def router_balance_workspace(batch, tokens, experts):
 
 def _logits(name, t, shape=None, device=None, dtype=None):
     """Checks of logits (tokens, experts) or (batch, tokens, experts); (batch, tokens, experts) and both strides."""
-    if t.dim() not in (2, 3) or not t.is_cuda:
+    have = t.shape
+    if len(have) not in (2, 3) or not t.is_cuda:
         raise ValueError(f"{name}: (tokens, experts) or (batch, tokens, experts) on the GPU expected")
     if t.dtype not in _FLOAT_DT or (dtype is not None and t.dtype != dtype):
         raise TypeError(f"{name}: unsupported dtype {t.dtype}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if shape is not None and have != shape:
+        raise ValueError(f"{name} has shape {tuple(have)}, expected {tuple(shape)}")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.dim() == 2:
-        t = t.unsqueeze(0)
-    b, n, e = t.shape
+    b, n, e = have if len(have) == 3 else (1, *have)
+    if b > _MOST or n > _MOST or e > _MOST:
+        raise ValueError(f"{name}: more than 2^31 - 1 sequences, tokens or experts")
     if e < 1:
         raise ValueError(f"{name}: no experts")
-    if e > 1 and t.stride(2) != 1:
+    step = t.stride()
+    if e > 1 and step[-1] != 1:
         raise ValueError(f"{name}: rows must be contiguous")
-    ld = t.stride(1) if n > 1 else e
-    return (b, n, e), ld, t.stride(0) if b > 1 else 0
+    return (b, n, e), step[-2] if n > 1 else e, step[0] if b > 1 else 0
 
 
 def router_balance(logits, chosen, out=None, scores="softmax", coef=1.0, mask=None, workspace=None, stream=None):
@@ -91,11 +95,10 @@ def router_balance(logits, chosen, out=None, scores="softmax", coef=1.0, mask=No
             raise TypeError(f"mask: bool expected, not {mask.dtype}")
         if mask.shape != lead or mask.device != dev or not mask.is_contiguous():
             raise ValueError(f"mask: contiguous {tuple(lead)} on {dev} expected")
-    need = router_balance_workspace(b, n, e)
     if out is None or workspace is None:
         with _allocating(stream), torch.cuda.device(dev):
-            out = balance_empty(e, b, dev) if out is None else out
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev) if workspace is None else workspace
+            out = _storage(e, b, dev, torch.empty) if out is None else out
+            workspace = torch.empty(router_balance_workspace(b, n, e), dtype=torch.uint8, device=dev) if workspace is None else workspace
     if not isinstance(out, RouterBalance):
         raise TypeError("out: a RouterBalance expected")
     if out.batch != b or out.experts != e or out.device != dev:
@@ -103,8 +106,7 @@ def router_balance(logits, chosen, out=None, scores="softmax", coef=1.0, mask=No
     if workspace.device != dev or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise ValueError("workspace: contiguous uint8 tensor on the logits' GPU expected")
     a = _abi.ROUTER_BALANCE_ARGS.pack(
-        _abi.int32("batch", b), _abi.int32("tokens", n), _abi.int32("experts", e), _abi.int32("k", k), _FLOAT_DT[logits.dtype],
-        SCORES[scores], chosen.element_size(), float(coef), logits.data_ptr(), chosen.data_ptr(),
+        b, n, e, _abi.int32("k", k), _FLOAT_DT[logits.dtype], SCORES[scores], chosen.element_size(), float(coef), logits.data_ptr(), chosen.data_ptr(),
         mask.data_ptr() if mask is not None else 0, out.counts.data_ptr(), out.valid.data_ptr(), out.cu_seqlens.data_ptr(),
         out.probs.data_ptr(), out.loss.data_ptr(), workspace.data_ptr(), workspace.numel(), ld, ldb)
     _launch(dev, stream, _abi.load().router_balance, a)
