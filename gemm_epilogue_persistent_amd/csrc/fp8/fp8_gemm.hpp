@@ -9,7 +9,17 @@
 // multiplications). The FMAs run kLag matrix instructions behind, so that none waits for a result.
 //
 // The kernels are those of the MX product (MxRing, MxDirect) with these parts in the place of the scale operands of
-// the matrix instruction; four scales of a row are 16 bytes, as 16 MX scales are, and take the same way.
+// the matrix instruction; four scales of a row are 16 bytes, as 16 MX scales are, and take the same way. For 64 to some
+// hundred rows there is one more, Fp8Staged.
+//
+// Measured: 8192^3 with B's scales by tiles 425 to 475 us, 2.3 to 2.6 PFLOP/s (bursts and long runs), matrix pipes 63%
+// busy at 1.95 GHz; MxRing with e4m3 operands, without the FMAs, 368 to 386, a library product with one scale 363.
+// (The pipes and the FMAs alone, from registers, reach 3.7 to 3.9 PFLOP/s, without FMAs 4.0 to 4.3: the clock falls
+// under their load.) By rows 524: with 8 vector instructions a matrix instruction the FMAs are the bound. 16768 x 4096 x 4096 over 8
+// experts with SiLU 302: four rounds of 65, of which SiLU is 3.5, and a last partial round of 42 in 128x128 quarters.
+// Measured at 8192^3 and not kept: a ring of four A fragments (436 to 454 where this took 425 to 442), all transfers behind the
+// barrier, the two waves of a SIMD taking turns (451), FMAs one instruction behind (2% slower) or three, other
+// priorities. 128x128 tiles for the experts: 338 for 302.
 #pragma once
 #include "../mx/mx_gemm.hpp"
 #include "fp8_common.hpp"
@@ -234,7 +244,11 @@ struct Fp8Direct : MxDirect<MB, NB, NW, D, MX_E4M3, MX_E4M3, VM> {
 
 // 64 x 64 outputs a workgroup of four waves that share out K, as in MxDirect, but each wave's operands come through LDS in
 // a ring of its own, two steps ahead: whole lines of 128 bytes (fragments read from memory directly take 64 bytes of
-// each of 16 rows at a time), and no barrier. Wave w takes step w of every quad of steps.
+// each of 16 rows at a time), and no barrier. Wave w takes step w of every quad of steps. 85 KB a microsecond and compute
+// unit, where direct kernels move 33 and 128x128 tiles 55 to 65 between their barriers. 256 x 4096 x 4096 11.6 us (direct
+// 64x64 tiles 20.4, 32x64 25.6, 128x128 over four workgroups 21.7), 64 x 8192 x 8192 17.0 for 67 MB (25.5 and 23.0), 512 x
+// 4096 x 4096 21.0 (38, 45, 25.6). Whole quads for each wave, with their scales in registers: 12.7, and 7.2 instead of 6.0 at
+// 512 x 1024 x 1024, where two waves had none.
 template <bool VM, bool BROWS>
 struct Fp8Staged : MxDirect<4, 4, 4, 1, MX_E4M3, MX_E4M3, VM> {
   using R = MxDirect<4, 4, 4, 1, MX_E4M3, MX_E4M3, VM>;
