@@ -308,3 +308,13 @@ def test_most_tokens():
     logits.fill_(1)
     gep.router_balance_backward(logits, b, dlogits=logits)
     assert not logits.any()
+
+
+@pytest.mark.parametrize("E,T", [(8, 1024), (8, 1025), (8, 4096), (8, 4097), (64, 128), (64, 129), (64, 512), (64, 513), (512, 17), (512, 64),
+                                 (512, 65), (600, 16), (600, 17)])
+def test_one_workgroup(E, T):
+    """Around the numbers of tokens up to which one workgroup of 256 or 1024 threads takes them."""
+    announce(f"balance one workgroup {T} over {E}")
+    x, chosen, mask = inputs(E + T, 1, T, E, 3, "f32", True, torch.int32)
+    b, d = run(x, chosen, mask, "softmax", coef=1.0)
+    check(b, d, definition(x.double(), chosen, mask, "softmax", 1.0), "f32", T, 3)
