@@ -44,6 +44,8 @@ template <int G>
 __device__ __forceinline__ float row_sum(float v) { return reduce<G>(v, [](float a, float b) { return a + b; }); }
 template <int G>
 __device__ __forceinline__ float row_max(float v) { return reduce<G>(v, [](float a, float b) { return fmaxf(a, b); }); }
+template <int G>
+__device__ __forceinline__ float row_min(float v) { return reduce<G>(v, [](float a, float b) { return fminf(a, b); }); }
 
 // e^x of x <= 0 to about an fp32 step: what the roundings of x log2 e and of log2 e itself leave is put back, so that the error does
 // not grow with x (1.2e-7 of the value down to -87, 0 below; without log2 e's own rest 1.2e-6 at -80). NaN for NaN.
@@ -64,8 +66,8 @@ __device__ __forceinline__ float row_top(const float (&x)[N][8]) {
   return row_max<G>(top);
 }
 
-// The scores of a row from its logits x, -inf past the last expert: p = u inv (8 N a lane). miss: 1 - s(x) (sigmoid). A
-// row of -inf alone has inv = 0; a NaN, and an infinity under a softmax, make the sum and inv NaN.
+// The scores of a row from its logits x, -inf past the last expert: p = u inv (8 N a lane), 0 where p is below fp32's normal
+// numbers. miss: 1 - s(x) (sigmoid). A row of -inf alone has inv = 0; a NaN, and an infinity under a softmax, make the sum and inv NaN.
 template <int G, int N, int SCORES>
 __device__ __forceinline__ float row_scores(const float (&x)[N][8], float (&u)[N][8], float (&miss)[N][8]) {
   float sum = 0.f;
@@ -88,12 +90,16 @@ __device__ __forceinline__ float row_scores(const float (&x)[N][8], float (&u)[N
         sum += u[i][e];
       }
     sum = row_sum<G>(sum);
-    // Logits that are all far below zero: times e^-top, which the quotient cancels, so that they keep their digits.
-    // (From -40 on what e^x loses is below e^-60 of the sum, and 2048 of e^-40 are below 1e-14.)
-    if (sum < 1e-14f) {
-      const float top = row_top<G, N>(x);
-      if (top < -40.f) {
-        const float m = fmaxf(top, -3.402823466e38f);
+    // e^x ends at 2^-126 = e^-87.3, p only where s(x) / sum does: a row whose sum is below 1 and that has a logit further down
+    // takes s(x) = e^x (1 - s(x)) times e^-top, which the quotient cancels.
+    if (sum < 1.f) {
+      float low = 0.f;  // (of the finite ones)
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) low = fminf(low, x[i][e] > -__builtin_inff() ? x[i][e] : 0.f);
+      if (row_min<G>(low) < -87.f) {
+        const float m = row_top<G, N>(x);
         sum = 0.f;
 #pragma unroll
         for (int i = 0; i < N; ++i)

@@ -2,12 +2,15 @@
 
 Tolerances, in half steps h = 2^-24. A score p = e^d / sum, d a difference that fp32 holds: the exponential 3 (one step of the
 instruction, and its own last rounding), the sum of a row whose other terms are below e^-20 1, the quotient 1, their product
-1: 6. A sigmoid's e^x / (1 + e^x) 3 more: a reciprocal within a step and a product: 9. The mean of one token is that. A
+1: 6. A sigmoid's e^x / (1 + e^x) 3 more: a reciprocal within a step and a product: 9; where a row is scaled by its largest
+logit, the product with 1 - s(x), which has 3 of the exponential, 1 of the sum and 2 of the reciprocal: 12. The mean of one token is that. A
 gradient p (w - sum p w) of a weight that is exact: the score's, those of the sum, which is a score's, and 6 for its four products and differences.
 """
+import numpy as np
 import pytest
 import torch
 
+import test_gpu_balance as balance
 from test_gpu_balance import definition, run
 from test_gpu_fp8 import announce
 
@@ -44,3 +47,43 @@ def test_far_below_the_largest(E, scores):
         # (of a sigmoid of 100, 1 - s is e^-100: below fp32)
         others = torch.ones_like(x, dtype=torch.bool).scatter(2, top, False)
         assert relative(got[others], want["d"][others]) <= (18 if scores == "softmax" else 24) * H
+
+
+@pytest.mark.parametrize("top", [-0.5, -5.0, -12.0, -20.0, -30.0, -36.0, -39.5, -41.0, -70.0, -86.0])
+def test_small_sigmoids_beside_smaller_ones(top):
+    """Sigmoid rows whose largest logit is small and whose others lie below e^-87, where fp32 ends: the scores are e^(x - top)
+    all the same. Multiples of 1 / 4: differences are exact."""
+    announce(f"balance small sigmoids {top}")
+    low = [v / 4 for v in range(-4 * 110, -4 * 80) if v / 4 > top - 85]
+    for E in (2, 24, 260):
+        rows = []
+        for i, v in enumerate(low):
+            row = np.full(E, v)
+            row[i % E] = top
+            row[(i + 1) % E] = v
+            if E > 2:
+                row[(i + 2) % E] = -np.inf
+            rows.append(row)
+        x = torch.tensor(np.array(rows))[:, None, :]
+        chosen = (torch.arange(len(low)) + 1).remainder(E)[:, None, None]
+        want = definition(x, chosen, None, "sigmoid", 1.0)
+        b, d = run(x.float(), chosen, None, "sigmoid", coef=1.0, grad=float(len(low)))
+        # (a row's sum: 8 values of a lane one after another, and 6 levels of the tree)
+        levels = 14 * H
+        assert relative(b.probs.double().cpu(), want["probs"]) <= 12 * H + levels
+        # (relative to p (w + sum p w): two scores, 6 as above, 6 of 1 - s(x), and 4 of the weight, coef experts / (batch k))
+        want = definition(x, chosen, None, "sigmoid", 1.0, float(len(low)))
+        assert ((d.double().cpu() - want["d"]).abs() <= (40 * H + 2 * levels) * want["size"] + 2.0 ** -124).all()
+
+
+def test_negative_infinity_beside_small_sigmoids():
+    announce("balance -inf beside small sigmoids")
+    x = torch.full((3, 4, 9), -np.inf, dtype=torch.float64)
+    x[0, 0, 3] = -100.0
+    x[0, 1, 3], x[0, 1, 4] = -30.0, -np.inf
+    x[1, 2] = -95.0
+    x[2, 3, :2] = torch.tensor([-0.25, -99.0])
+    chosen = torch.randint(0, 9, (3, 4, 2), generator=torch.Generator().manual_seed(1))
+    b, d = run(x.float(), chosen, None, "sigmoid", coef=1.0, grad=64.0)
+    balance.check(b, d, definition(x, chosen, None, "sigmoid", 1.0, 64.0), "f32", 4, 2)
+    assert (d[0, 2] == 0).all() and b.probs[0, 3].item() == 0.5
