@@ -581,7 +581,7 @@ using namespace gep;
 extern "C" {
 
 int64_t router_balance_workspace(int32_t batch, int32_t tokens, int32_t experts) {
-  if (batch < 0 || tokens < 0 || experts < 1 || experts > kMaxExperts || batch > 65535) return -1;
+  if (batch < 0 || tokens < 0 || experts < 1 || experts > kMaxExperts || batch > 65535 || (int64_t)batch * tokens > 0x7FFFFFFF) return -1;
   return layout(batch, forward_share(batch, tokens, experts).wgs, experts).bytes;
 }
 
