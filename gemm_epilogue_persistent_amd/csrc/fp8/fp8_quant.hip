@@ -45,28 +45,29 @@ __device__ __forceinline__ void act8(int act, float v[8]) {
 }
 // act(x) and its slope. Both smooth activations are x s with s = 1 / (1 + 2^-u), and their slope is s (1 + x (1 - s) z')
 // with z = u log 2; 1 - s = 2^-u s keeps its digits for large z. Beyond |x| = 12 (GELU) and 80 (SiLU) x is kept to
-// that, and 2^-u below infinity, so that all factors are finite: there s is 0 or 1 to within 2^-115.
+// that, and 2^-u below infinity, so that all factors are finite: there s is 0 or 1 to within 2^-115. The slope at a NaN (of a block
+// or of a code) is NaN, and so are the smooth ones' values: their clamps are v_minimum and v_maximum, which pass it on.
 template <int ACT>
 __device__ __forceinline__ void act_and_slope(float x, float& y, float& d) {
   if constexpr (ACT == ACT_RELU) {
     y = act_fn<ACT_RELU>(x);
-    d = x > 0.f ? 1.f : 0.f;
+    d = x > 0.f ? 1.f : (x <= 0.f ? 0.f : x);
   } else if constexpr (ACT == ACT_RELU_SQ) {
     y = act_fn<ACT_RELU_SQ>(x);
-    d = x > 0.f ? 2.f * x : 0.f;
+    d = 2.f * __builtin_elementwise_maximum(x, 0.f);
   } else if constexpr (ACT == ACT_GELU_TANH || ACT == ACT_SILU) {
     constexpr bool gelu = ACT == ACT_GELU_TANH;
     constexpr float top = gelu ? 12.f : 80.f, log2e = 1.4426950408889634f;
-    const float c = __builtin_amdgcn_fmed3f(x, -top, top), c2 = c * c;
+    const float up = __builtin_elementwise_maximum(x, -top), c = __builtin_elementwise_minimum(up, top), c2 = c * c;
     // -u, and z' = dz / dx with z = 2 sqrt(2 / pi) (x + 0.044715 x^3)
     const float u = gelu ? c * __builtin_fmaf(c2, -0.044715f * 1.5957691216057308f * log2e, -1.5957691216057308f * log2e) : c * -log2e;
-    const float e = __builtin_amdgcn_exp2f(fminf(u, 120.f)), s = __builtin_amdgcn_rcpf(1.f + e);
+    const float e = __builtin_amdgcn_exp2f(__builtin_elementwise_minimum(u, 120.f)), s = __builtin_amdgcn_rcpf(1.f + e);
     const float cz = gelu ? c * __builtin_fmaf(c2, 0.134145f * 1.5957691216057308f, 1.5957691216057308f) : c;
     d = s * __builtin_fmaf(cz, e * s, 1.f);
-    y = fmaxf(x, -top) * s;
+    y = up * s;
   } else {
     y = x;
-    d = 1.f;
+    d = x == x ? 1.f : x;
   }
 }
 
@@ -301,12 +302,10 @@ __global__ __launch_bounds__(kThreads) void act_backward_kernel(const BackArgs<T
     float x[8], d[8];
     fp8_values8(w[p], scale[p], x);
     if (a.dy) in.values(p, r, c, a.rows, a.cols, edge, v[p]);
-    const float nan = -0.f * scale[p];  // NaN for a NaN block, whose slopes are not; -0 changes no other product
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       act_and_slope<ACT>(x[e], y[p][e], d[e]);
-      if (ACT == ACT_GELU_TANH || ACT == ACT_SILU) y[p][e] += nan;
-      if (a.dy) v[p][e] = __builtin_fmaf(v[p][e], d[e], nan);
+      if (a.dy) v[p][e] *= d[e];
     }
     if (edge) {  // (rows past the end are copies of the last one)
 #pragma unroll

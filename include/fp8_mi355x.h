@@ -86,7 +86,7 @@ gemm_status fp8_act_forward(const fp8_act_args* args, void* stream);
  *                        the weight behind the activation)
  * Each output may be NULL, not all of them; dy is needed for the first three and NULL without them
  * (act NONE then transposes a checkpoint: yt has its blocks along the other axis). act' of ReLU is 0 at 0; a NaN
- * block of `saved` makes dx NaN. dx may be dy itself. All FP8 matrices are FP8_ROWS. */
+ * block or code of `saved` makes its dx NaN (and y but for the ReLUs'). dx may be dy itself. All FP8 matrices are FP8_ROWS. */
 typedef struct {
   int32_t rows, cols;
   int32_t type; /* gemm_dtype of dy, dx and y */
