@@ -44,8 +44,13 @@ template <int G>
 __device__ __forceinline__ float row_sum(float v) { return reduce<G>(v, [](float a, float b) { return a + b; }); }
 template <int G>
 __device__ __forceinline__ float row_max(float v) { return reduce<G>(v, [](float a, float b) { return fmaxf(a, b); }); }
+// Whether v holds in any lane of the row.
 template <int G>
-__device__ __forceinline__ float row_min(float v) { return reduce<G>(v, [](float a, float b) { return fminf(a, b); }); }
+__device__ __forceinline__ bool row_any(bool v) {
+  const uint64_t all = __ballot(v);
+  if constexpr (G == 64) return all != 0;
+  else return (all >> (threadIdx.x & (64 - G)) & (((uint64_t)1 << G) - 1)) != 0;
+}
 
 // e^x of x <= 0 to about an fp32 step: what the roundings of x log2 e and of log2 e itself leave is put back, so that the error does
 // not grow with x (1.2e-7 of the value down to -87, 0 below; without log2 e's own rest 1.2e-6 at -80). NaN for NaN.
@@ -91,14 +96,15 @@ __device__ __forceinline__ float row_scores(const float (&x)[N][8], float (&u)[N
       }
     sum = row_sum<G>(sum);
     // e^x ends at 2^-126 = e^-87.3, p only where s(x) / sum does: a row whose sum is below 1 and that has a logit further down
-    // takes s(x) = e^x (1 - s(x)) times e^-top, which the quotient cancels.
+    // takes s(x) = e^x (1 - s(x)) times e^-top, which the quotient cancels. (Looking for one where all sums are below 1: 8 x 4096
+    // tokens over 256 experts bf16, forward 16.6 to 17.5 us, backward 13.2 to 13.5.)
     if (sum < 1.f) {
       float low = 0.f;  // (of the finite ones)
 #pragma unroll
       for (int i = 0; i < N; ++i)
 #pragma unroll
         for (int e = 0; e < 8; ++e) low = fminf(low, x[i][e] > -__builtin_inff() ? x[i][e] : 0.f);
-      if (row_min<G>(low) < -87.f) {
+      if (row_any<G>(low < -87.f)) {
         const float m = row_top<G, N>(x);
         sum = 0.f;
 #pragma unroll
