@@ -1,4 +1,5 @@
-"""The balance loss's scores far below a row's largest one.
+"""The balance loss's scores far below a row's largest one, its sums row by row, and its mean scores under bounds that follow
+from how the tokens are shared out.
 
 Tolerances, in half steps h = 2^-24. A score p = e^d / sum, d a difference that fp32 holds: the exponential 3 (one step of the
 instruction, and its own last rounding), the sum of a row whose other terms are below e^-20 1, the quotient 1, their product
@@ -10,8 +11,9 @@ import numpy as np
 import pytest
 import torch
 
+import gemm_epilogue_persistent_amd as gep
 import test_gpu_balance as balance
-from test_gpu_balance import definition, run
+from test_gpu_balance import definition, inputs, run
 from test_gpu_fp8 import announce
 
 pytestmark = pytest.mark.gpu
@@ -87,3 +89,67 @@ def test_negative_infinity_beside_small_sigmoids():
     b, d = run(x.float(), chosen, None, "sigmoid", coef=1.0, grad=64.0)
     balance.check(b, d, definition(x, chosen, None, "sigmoid", 1.0, 64.0), "f32", 4, 2)
     assert (d[0, 2] == 0).all() and b.probs[0, 3].item() == 0.5
+
+
+SHARED = [(1, 20000, 64, 6), (8, 3001, 128, 8), (70, 33, 8, 2), (1, 5000, 8, 1), (2, 1500, 2048, 3), (300, 77, 16, 2), (1, 70000, 8, 2),
+          (1, 1025, 512, 2), (3, 4097, 257, 4), (1, 64, 64, 2)]
+
+
+@pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("B,T,E,k", SHARED)
+def test_every_row_once(B, T, E, k, scores):
+    """Each token has one expert of score 1, all others 0: the sums are whole numbers, which fp32 adds exactly, so that a row
+    taken twice, left out or taken for its neighbour changes a mean."""
+    announce(f"balance every row once {B}x{T} over {E} {scores}")
+    g = torch.Generator().manual_seed(B + T)
+    best = torch.randint(0, E, (B, T), generator=g)
+    mask = torch.rand(B, T, generator=g) < 0.8 if B > 1 else None
+    x = torch.full((B, T, E), -200.0).scatter_(2, best[..., None], 100.0)
+    chosen = torch.randint(0, E, (B, T, k), generator=g)
+    b, d = run(x, chosen, mask, scores)
+    keep = torch.ones(B, T, dtype=torch.bool) if mask is None else mask
+    for s in range(B):
+        n = keep[s].sum()
+        want = torch.bincount(best[s][keep[s]], minlength=E).float() / n.float()
+        assert torch.equal(b.probs[s].cpu(), want)
+        assert torch.equal(b.counts[s].cpu().long(), torch.bincount(chosen[s][keep[s]].flatten(), minlength=E))
+    assert not d.any()
+
+
+def chain(B, T, E):
+    """Additions that a mean score passes through: the tokens of a group of lanes one after another, the groups of a wave, the waves of a
+    workgroup; the workgroups that a wave of the join adds, and its eight waves."""
+    lanes = 1
+    while lanes < 64 and lanes * 8 < E:
+        lanes *= 2
+    threads = 1024 if E <= 512 else 256
+    groups = threads // lanes
+    per = -(-(-(-T // max(1, 256 // B))) // groups) * groups
+    if B == 1 and T <= 4 * groups:
+        return 16 + 6 + 16  # (one workgroup of 256 or 1024 threads: four tokens a group, or sixteen)
+    return per // groups + 6 + threads // 64 + -(-(-(-T // per)) // 4) + 8
+
+
+@pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("B,T,E,k", SHARED)
+def test_mean_scores(B, T, E, k, scores):
+    """The error of a score (the file of the other tests: 46 half steps, and the difference to the largest logit, which lies below 32
+    in magnitude: 32 more, its half step relative to e^d), then a half step for each addition on the way and 2 for the mean."""
+    announce(f"balance mean scores {B}x{T} over {E} {scores}")
+    x, chosen, mask = inputs(B + T, B, T, E, k, "f32", B > 1, torch.int64)
+    want = definition(x.double(), chosen, mask, scores, 1.0)
+    b, _ = run(x, chosen, mask, scores, coef=1.0)
+    tol = (80 + chain(B, T, E)) * H
+    assert ((b.probs.double().cpu() - want["probs"]).abs() <= tol * want["probs"]).all()
+    # (the loss: the factors f, their products and 2048 sums in a tree of 9 levels and 64 workgroups' shares)
+    assert abs(b.loss.double().item() - want["loss"].item()) <= (tol + (8 + 9 + -(-B * (-(-E // 64)) // 256) + 16) * H) * want["loss"].item()
+
+
+@pytest.mark.parametrize("B,T,E", [(4096, 3, 8), (65535, 1, 8), (3000, 2, 130), (1000, 5, 2048)])
+def test_many_sequences(B, T, E):
+    """Counts, offsets and losses of thousands of short sequences."""
+    announce(f"balance of {B} sequences of {T} tokens over {E}")
+    x, chosen, mask = inputs(B, B, T, E, 2, "f32", True, torch.int32)
+    want = definition(x.double(), chosen, mask, "softmax", 0.01, 64.0)
+    b, d = run(x, chosen, mask, "softmax", grad=64.0)
+    balance.check(b, d, want, "f32", T, 2)
