@@ -539,9 +539,9 @@ int forward_threads(int32_t experts) { return experts <= 512 ? 1024 : 256; }
 int one_threads(int32_t tokens, int32_t experts) {
   return tokens <= 4 * kThreads / lanes_of(experts) ? kThreads : forward_threads(experts);
 }
-// Tokens that one workgroup takes instead of several and their join, a group of lanes: four, which are under way at once (2048
-// tokens over 8 experts 7.9 us for 10.7, 256 over 64 6.4 for 9.2, 64 over 512 7.6 for 10.1); with eight, 1024 over 64 11.2
-// for 9.4.
+// Tokens that one workgroup takes instead of several and their join, a group of lanes: four, which are under way at once. (Over 8 to 512
+// experts, fp32 and bf16, softmax and sigmoids: with two a group 6.0 to 8.5 us for 9.0 to 11.3, with four 7.5 to 10.6 for 8.8 to
+// 11.4; with five a softmax takes as long either way or 8% less, sigmoids 3 to 13% longer; with six 1 to 27% longer.)
 constexpr int kOne = 4;
 Share forward_share(int32_t batch, int32_t tokens, int32_t experts) {
   if (batch == 1 && tokens <= kOne * forward_threads(experts) / lanes_of(experts))  // (one workgroup, and no join)
@@ -550,9 +550,10 @@ Share forward_share(int32_t batch, int32_t tokens, int32_t experts) {
 }
 Share backward_share(int32_t batch, int32_t tokens, int32_t experts) { return share(batch, tokens, experts, kThreads, 2048); }
 
-// Of more sums than these the join takes 512 threads (256 sums of 512 experts 9.0 us in 256 threads, 7.3 in 512; of 2048
-// experts 13.6 and 10.3), else 256 (128 sums of 64 experts 5.4 and 5.8; 32 of 256 experts, 8 sequences, 6.3 and 7.5).
-constexpr int kManySums = 128;
+// Of more sums than these the join takes 512 threads, else 256. (Forward passes over 8 to 2048 experts: of 8 to 64 sums 256 threads are
+// 1 to 10% faster, 4096 tokens over 64 experts 9.4 us for 10.3; of 128 512 threads by 0 to 7%, 2048 over 512 10.9 for 11.6; of 256 by 8 to
+// 17%, 8192 over 512 13.1 for 15.0.)
+constexpr int kManySums = 64;
 
 int64_t round16(int64_t v) { return (v + 15) / 16 * 16; }
 struct Layout {
