@@ -12,11 +12,11 @@
 // the matrix instruction; four scales of a row are 16 bytes, as 16 MX scales are, and take the same way. For 64 to some
 // hundred rows there is one more, Fp8Staged.
 //
-// Measured: 8192^3 with B's scales by tiles 425 to 475 us, 2.3 to 2.6 PFLOP/s (bursts and long runs), matrix pipes 63%
+// Measured: 8192^3 with B's scales by tiles 425 to 490 us, 2.2 to 2.6 PFLOP/s (by card, bursts and long runs), matrix pipes 63%
 // busy at 1.95 GHz; MxRing with e4m3 operands, without the FMAs, 368 to 386, a library product with one scale 363.
 // (The pipes and the FMAs alone, from registers, reach 3.7 to 3.9 PFLOP/s, without FMAs 4.0 to 4.3: the clock falls
-// under their load.) By rows 524: with 8 vector instructions a matrix instruction the FMAs are the bound. 16768 x 4096 x 4096 over 8
-// experts with SiLU 302: four rounds of 65, of which SiLU is 3.5, and a last partial round of 42 in 128x128 quarters.
+// under their load.) By rows 524 to 557: with 8 vector instructions a matrix instruction the FMAs are the bound. 16768 x 4096 x 4096 over 8
+// experts with SiLU 302 to 323: four rounds of 65, of which SiLU is 3.5, and a last partial round of 42 in 128x128 quarters.
 // Measured at 8192^3 and not kept: a ring of four A fragments (436 to 454 where this took 425 to 442), all transfers behind the
 // barrier, the two waves of a SIMD taking turns (451), FMAs one instruction behind (2% slower) or three, other
 // priorities. 128x128 tiles for the experts: 338 for 302.

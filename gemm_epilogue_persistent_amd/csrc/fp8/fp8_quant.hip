@@ -10,10 +10,14 @@
 //   16 x 4096 bf16 along rows, and its inverse                 2.6 and 2.4 us, which are the launch
 //   16768 x 4096 bf16, SiLU, saved and q                       62 us, 283 MB: 4.6 TB/s
 //   8192 x 8192 bf16 by tiles, both ways                       56 to 62 us, 269 MB: 4.3 to 4.8 TB/s
-//   5001 x 4104 f16 along rows and columns                     19.1 us, 82 MB; 24.7 from far memory
-//   8192 x 8192 bf16 GELU backward, q, qt, yt                  102 us, 403 MB and 17 of scales: 4.1 TB/s (ReLU 93; q alone
-//                                                              57.6, q and qt 75)
+//   5001 x 4104 f16 along rows and columns                     26 to 29 us, 82 MB; 19.2 from a cache
+//   8192 x 8192 bf16 GELU backward, q, qt, yt                  98 to 103 us, 403 MB and 17 of scales: 4.1 TB/s (SiLU 93, the
+//                                                              ReLUs 89; q alone 71)
 //   8192 x 8192 inverse to bf16                                35 us, 201 MB: 5.7 TB/s
+// q, qt and yt of a computed value round its product with the block's factor to fp32 before the rounding to a code, so that near a border
+// of two codes the other one may be taken (also for an fp32 x or dy as it is: act NONE, ReLU); rounding to odd first, as for saved,
+// takes 68 us for 60 of 16768 x 4096 bf16 SiLU with saved and q, 121 for 99 of the GELU backward pass, and in fp32 80 to 82 for 74
+// and 133 for 118.
 // What was measured and is not kept: workgroups that stay and load the next tile ahead (the compiler spills: 120 us for
 // 56 by tiles); bounds of 4 or 6 workgroups a compute unit (backward 126 for 101, by tiles 80 for 56).
 #include <algorithm>

@@ -5,7 +5,7 @@
 //
 // Three kernels: sums of a workgroup, their join, the gradient. Bound by the launches and by the latency of what follows
 // on each other: 16 tokens over 8 experts 3.7 us (one workgroup, no join) and 2.1; 8 x 4096 tokens over 256 experts bf16
-// with sigmoids 9.3 to 10.4, 6.1 and 10.9 us, of which memory needs 3.5, 0 and 7 and the about 20 vector instructions a value
+// with sigmoids 9.2 to 10.3, 6.2 to 6.6 and 9.6 to 11.4 us, of which memory needs 3.5, 0 and 7 and the about 21 vector instructions a value
 // 5 in each direction; 8192 tokens over 2048 experts 14, 10 and 17 for 34 MB in and 34 out. Forward workgroups
 // of 512 threads are no faster than of 1024; backward, up to 2048 workgroups in all instead of 1024 save 2 us in 31.
 #include <algorithm>

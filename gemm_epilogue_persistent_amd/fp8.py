@@ -38,7 +38,7 @@ class Fp8Tensor:
     codes: uint8 (e4m3), (rows, bytes) or (G, rows, bytes), contiguous; bytes = k rounded up to 16, the codes
     past k zero. scales: float32, contiguous; a scale per 128 values of a row: (rows / 64, blocks / 4, 64, 4)
     rounded up; per tile of 128 x 128 (tiles): (rows / 128, blocks rounded up to a multiple of 4). Each with a
-    leading G for grouped ones; finite past the row's last block. A value is code * scale; a NaN scale
+    leading G for grouped ones; below 2^63 past the row's last block. A value is code * scale; a NaN scale
     makes its block NaN."""
 
     __slots__ = ("codes", "scales", "k", "rows", "groups", "tiles", "device")

@@ -9,7 +9,8 @@
  *   ROUTER_SOFTMAX   p_e = exp(x_e) / sum_j exp(x_j)
  *   ROUTER_SIGMOID   p_e = s(x_e) / sum_j s(x_j),   s(x) = 1 / (1 + exp(-x))
  * A token whose mask is 0 (padding) counts nowhere, whatever its logits hold; one whose logits are all -inf has
- * p = 0. With n_b the unmasked tokens of sequence b, c_be how often they chose expert e, and k choices a token:
+ * p = 0, and scores below 2^-126 may be 0. With n_b the unmasked tokens of sequence b, c_be how often they chose
+ * expert e, and k choices a token:
  *   P_be = sum over its tokens of p_e / n_b     f_be = experts * c_be / (k * n_b)
  *   loss = coef / batch * sum over b, e of f_be * P_be         (a sequence without tokens adds 0)
  * so that an even choice gives coef. batch = 1: one loss over all tokens; more: one for each sequence. Sums are held in
