@@ -124,9 +124,10 @@ gemm_status fp8_act_backward(const fp8_act_backward_args* args, void* stream);
  * int32[groups+1], 0 .. M, never decreasing; an array that breaks this runs nothing and writes
  * nothing). The groups share out rows only: sums over a group's tokens, the gradients of the experts' weights, are
  * gemm_mi355x.h's variable-K products of 16-bit operands (blocks of 128 tokens run over the groups' borders). At
- * least one of d, post is present. N is a multiple of 8, every leading dimension one of 16 bytes, K at most 2^22, and every pointer is 16-byte aligned. K = 0 gives D = C (or 0). The
- * activations are those of gemm_run. C may be D or PostAct itself (of its type and leading dimension); D
- * and PostAct are two matrices. tile: 0 lets the library choose; otherwise one of the FP8_TILE values. */
+ * least one of d, post is present. N is a multiple of 8, every leading dimension one of 16 bytes, K at most 2^22, and
+ * every pointer is 16-byte aligned. K = 0 gives D = C (or 0). The activations are those of gemm_run. C may be D or
+ * PostAct itself (of its type and leading dimension); D and PostAct are two matrices. tile: 0 lets the library choose;
+ * otherwise one of the FP8_TILE values. */
 typedef enum {
   FP8_TILE_AUTO = 0,
   FP8_TILE_256 = 1,   /* 256x256 outputs a workgroup, operands staged through LDS       */
